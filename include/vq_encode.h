@@ -254,6 +254,146 @@ vq_status vq_attention_decode_static(const void *q, const uint8_t *k_codes,
                                      float scale, vq_dtype dtype, void *out, vq_stream_t stream);
 
 /*
+ * The paged code cache.  A serving loop holds the codes of requests of
+ * different lengths in one pool of pages of page_size tokens:
+ *   k_codes, v_codes   page p at p * page_stride bytes (the same stride for
+ *                      both; at least heads_kv * page_size * ns), each
+ *                      [heads_kv][page_size][ns] uint8, ns = head_dim/sub_dim
+ *   block_table        [requests][max_blocks] int32: the page of tokens
+ *                      [b * page_size, (b + 1) * page_size) of a request;
+ *                      entries at or past ceil(length / page_size) are
+ *                      unspecified
+ *   free_pages         [num_pages] int32, a stack: the first *free_count
+ *                      entries are the pages nobody holds
+ *   lens               [requests] int32: tokens in the cache
+ * and packs the new tokens of a step, request after request, into rows
+ * [tokens]; request r's are rows cu_new[r] .. cu_new[r + 1] - 1.  A step is
+ * vq_paged_reserve (pages and slots for the new tokens), vq_paged_append
+ * (their keys and values, encoded into the slots) and vq_paged_attention;
+ * vq_paged_trim takes tokens back.  All lengths stay on the device: none of
+ * the calls synchronises, and all can be captured in a CUDA graph.
+ *
+ * Limits: page_size a power of two up to VQ_PAGED_MAX_PAGE; rows, and
+ * max_blocks * page_size, up to VQ_PAGED_MAX_TOKENS; head_dim up to
+ * VQ_PAGED_MAX_HEAD_DIM; heads up to VQ_PAGED_MAX_HEADS; n_centroids up to
+ * 256; sub_dim up to 32 for the append; up to 8192 requests for reserve and
+ * trim (VQ_ERR_UNSUPPORTED beyond).
+ */
+#define VQ_PAGED_MAX_PAGE 1024
+#define VQ_PAGED_MAX_TOKENS 0x40000000
+#define VQ_PAGED_MAX_HEAD_DIM 512
+#define VQ_PAGED_MAX_HEADS 1024
+
+/*
+ * vq_paged_reserve -- pages and slots for new_lens[r] more tokens of each
+ * request.  A request needs the pages its longer length has more than its
+ * present one.  It is granted if its length fits the table and, where it
+ * needs pages, if its need and that of every request before it (refused
+ * for want of pages or not) are within *free_count.  The pages of the granted
+ * requests are popped from the stack in request order, then block order.
+ *   lens, new_lens  [requests]  device; negative values count as 0
+ *   block_table     the entries of the new pages are written
+ *   total_new       rows of `slots` (known to the host: the rows of the packed
+ *                   new tokens; may exceed the sum of new_lens)
+ *   lens_out        [requests]  device, written: lens + new_lens where granted,
+ *                   lens where refused.  May be lens.
+ *   free_count_out  [1]  device, written.  May be free_count.
+ *   cu_new          [requests + 1]  device, written: exclusive sums of new_lens
+ *                   (refused requests keep their rows)
+ *   slots           [total_new] int64, device, written: page * page_size +
+ *                   offset of each new token; -1 for tokens of refused
+ *                   requests and for rows past the last
+ * Asynchronous on `stream`.
+ */
+vq_status vq_paged_reserve(const int32_t *lens, const int32_t *new_lens, int64_t requests,
+                           const int32_t *free_pages, const int32_t *free_count, int64_t num_pages,
+                           int32_t *block_table, int64_t max_blocks, int32_t page_size,
+                           int64_t total_new, int32_t *lens_out, int32_t *free_count_out,
+                           int32_t *cu_new, int64_t *slots, vq_stream_t stream);
+
+/*
+ * vq_paged_trim -- cut each request to keep_lens[r] tokens (rejected drafts:
+ * a few less; a finished request: 0) and push the pages it no longer needs
+ * on the stack, in request order, then block order.  keep_lens is taken within
+ * [0, lens[r]].  The block table is read only.
+ *   free_pages      entries from *free_count on are written
+ *   lens_out        [requests]  device, written.  May be lens.
+ *   free_count_out  [1]  device, written.  May be free_count.
+ * Asynchronous on `stream`.
+ */
+vq_status vq_paged_trim(const int32_t *lens, const int32_t *keep_lens, int64_t requests,
+                        const int32_t *block_table, int64_t max_blocks, int32_t page_size,
+                        int32_t *free_pages, const int32_t *free_count, int64_t num_pages,
+                        int32_t *lens_out, int32_t *free_count_out, vq_stream_t stream);
+
+/*
+ * vq_paged_append -- encode the keys and values of new tokens into their
+ * slots: the codes of vq_encode_grouped_u8 (with k_smooth, of
+ * vq_encode_grouped_smooth for the keys), one codebook per head.
+ *   k, v         token t at t * k_stride (v_stride) elements, each
+ *                [heads][head_dim], device, dtype (a slice of a packed
+ *                projection will do)
+ *   slots        [tokens] int64, device; a slot outside [0, num_pages *
+ *                page_size) is skipped; two tokens with one slot leave either
+ *   k_codebooks, v_codebooks  [heads][n_centroids][sub_dim]  device, dtype
+ *   k_smooth     [heads][head_dim] fp32 factors of the keys, device, or NULL
+ *   k_codes, v_codes  the pages, written at the slots
+ * Any alignment of k and v to their element type is taken; rows aligned to
+ * min(sub_dim elements, 16 bytes), sub_dim 4 or 8 and 64 to 256 centroids take the
+ * tensor-core encode.  Asynchronous on `stream`.
+ */
+vq_status vq_paged_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                          const int64_t *slots, int64_t tokens, int32_t heads, int32_t head_dim,
+                          int32_t sub_dim, int32_t n_centroids, const void *k_codebooks,
+                          const void *v_codebooks, const float *k_smooth, uint8_t *k_codes,
+                          uint8_t *v_codes, int64_t num_pages, int32_t page_size,
+                          int64_t page_stride, vq_dtype dtype, vq_stream_t stream);
+
+/*
+ * vq_paged_attention -- causal attention of the new tokens of every request
+ * over its cache, the new tokens' own codes (appended before) included.  The
+ * i-th of n_r new tokens of request r has position p = lens[r] - n_r + i
+ * and sees the cached tokens max(0, p - window + 1) .. p (window 0: 0 .. p):
+ *   out = softmax_t(scale * q . K^[t]) @ V^[t],  lse = ln sum_t e^(scale q . K^[t])
+ * with K^, V^ the codebook rows that the codes select (a code >= n_centroids:
+ * a zero row).  Query head h uses KV head h / (heads_q / heads_kv); scale <= 0
+ * means 1/sqrt(head_dim).  A row that sees nothing (position below 0, or every
+ * page of its range missing) gets zeros and lse = -inf, and so do the rows
+ * after cu_new[requests].  A page entry outside [0, num_pages) hides its
+ * tokens.  Codebook entries are finite; q may hold anything, and a row of q
+ * with NaN or infinities does not touch another row.
+ *   q          token t at t * q_stride elements, [heads_q][head_dim], device,
+ *              dtype
+ *   cu_new     [requests + 1]  device (vq_paged_reserve)
+ *   lens       [requests]  device: lengths with the new tokens
+ *   max_new    the most new tokens of a request if the host knows it (0: it
+ *              does not).  It chooses kernels and never changes what is
+ *              computed.
+ *   out        [tokens][heads_q][head_dim]  device, dtype, written
+ *   lse        [tokens][heads_q] fp32, device, written; may be NULL
+ *   workspace  >= vq_paged_attention_workspace_bytes(...) bytes, device,
+ *              16-byte aligned
+ * Arithmetic: products of the inputs' own values, sums, maxima and weights in
+ * fp32; with 16-bit inputs of the shapes the tensor kernels take, each weight
+ * is rounded once to the input type before its product with V^.
+ * Asynchronous on `stream`.
+ */
+vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_new, const int32_t *lens,
+                             int64_t requests, int64_t tokens, int64_t max_new, const int32_t *block_table,
+                             int64_t max_blocks, const uint8_t *k_codes, const uint8_t *v_codes,
+                             int64_t num_pages, int32_t page_size, int64_t page_stride,
+                             const void *k_codebooks, const void *v_codebooks, int32_t heads_q,
+                             int32_t heads_kv, int32_t head_dim, int32_t sub_dim, int32_t n_centroids,
+                             int64_t window, float scale, vq_dtype dtype, void *out, float *lse,
+                             void *workspace, size_t workspace_bytes, vq_stream_t stream);
+
+/* Workspace vq_paged_attention needs for these sizes on the current device
+ * (0 for invalid sizes).  It does not depend on the lengths in the cache. */
+size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int64_t max_new,
+                                          int32_t heads_q, int32_t heads_kv, int32_t head_dim,
+                                          int32_t sub_dim, int32_t n_centroids, int32_t page_size);
+
+/*
  * Sibling encoders on the same nearest-centroid rule (the page of five
  * hand-tuned Metal compute kernels for TurboQuant, "Kernel 2: Scalar Quantize
  * / Dequantize" and "Kernel 3: Fused Hadamard + Quantize").  One fp32

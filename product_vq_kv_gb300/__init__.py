@@ -34,6 +34,11 @@ from ._binding import (  # noqa: F401
     vq_hadamard_quantize,
     vq_hadamard_rotate,
     vq_kernel_status,
+    vq_paged_append,
+    vq_paged_attention,
+    vq_paged_attention_workspace_bytes,
+    vq_paged_reserve,
+    vq_paged_trim,
     vq_partition,
     vq_scalar_dequantize,
     vq_scalar_quantize,

@@ -75,6 +75,20 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.vq_hadamard_quantize.argtypes = [vp, i32, vp, i64, i32, vp, i32, vp, vp]
     lib.vq_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.vq_attention_workspace_bytes.argtypes = [i64, i32, i32, i64, i32, i32, i32, i64]
+    lib.vq_paged_reserve.restype = i32
+    lib.vq_paged_reserve.argtypes = [vp, vp, i64, vp, vp, i64, vp, i64, i32, i64, vp, vp, vp, vp,
+                                     vp]
+    lib.vq_paged_trim.restype = i32
+    lib.vq_paged_trim.argtypes = [vp, vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, vp]
+    lib.vq_paged_append.restype = i32
+    lib.vq_paged_append.argtypes = [vp, vp, i64, i64, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp,
+                                    vp, i64, i32, i64, i32, vp]
+    lib.vq_paged_attention.restype = i32
+    lib.vq_paged_attention.argtypes = [vp, i64, vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, i32,
+                                       i64, vp, vp, i32, i32, i32, i32, i32, i64, ctypes.c_float,
+                                       i32, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.vq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.vq_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32]
     lib.vq_status_string.restype = ctypes.c_char_p
     lib.vq_status_string.argtypes = [i32]
     lib.vq_describe_launch.restype = i32
@@ -469,6 +483,251 @@ def vq_attention_decode(q: torch.Tensor, k_codes: torch.Tensor, k_codebooks: tor
             workspace.numel() * workspace.element_size(), _stream_handle(stream, q.device))
     _check(st, "vq_attention_decode")
     return out
+
+
+def _i32_tensor(t, name: str, shape: tuple, device) -> None:
+    """A contiguous int32 device tensor of ``shape`` (None: any extent) on ``device``."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.dim() != len(shape) or any(want is not None and have != want
+                                    for have, want in zip(t.shape, shape)):
+        want = "[" + ", ".join("any" if n is None else str(n) for n in shape) + "]"
+        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    _device_tensor(t, name)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _out_like(out, name, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if (not isinstance(out, torch.Tensor) or out.dtype != dtype or tuple(out.shape) != tuple(shape)
+            or out.device != device or not out.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def vq_paged_reserve(lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                     free_count: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                     total_new: int, lens_out: torch.Tensor | None = None,
+                     free_count_out: torch.Tensor | None = None,
+                     cu_new: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                     stream: torch.cuda.Stream | None = None) -> tuple:
+    """Pages and slots for ``new_lens[r]`` more tokens of each request.
+
+    ``lens`` / ``new_lens`` ``[R]``, ``free_pages`` ``[num_pages]`` (a stack of
+    ``free_count`` ``[1]`` pages) and ``block_table`` ``[R, max_blocks]`` are
+    int32; ``total_new`` is the number of rows of the packed new tokens.  The
+    table's entries of new pages are written in place.  Returns ``(lens_out,
+    free_count_out, cu_new, slots)``; pass ``lens_out=lens`` and
+    ``free_count_out=free_count`` to update those in place.  Refused requests
+    (see ``include/vq_encode.h``) keep their length and get slots of -1."""
+    _i32_tensor(lens, "lens", (None,), None)
+    dev, r = lens.device, lens.shape[0]
+    _i32_tensor(new_lens, "new_lens", (r,), dev)
+    _i32_tensor(free_pages, "free_pages", (None,), dev)
+    _i32_tensor(free_count, "free_count", (1,), dev)
+    _i32_tensor(block_table, "block_table", (r, None), dev)
+    if total_new < 0:
+        raise ValueError("total_new must not be negative")
+    lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev)
+    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev)
+    cu_new = _out_like(cu_new, "cu_new", (r + 1,), torch.int32, dev)
+    slots = _out_like(slots, "slots", (total_new,), torch.int64, dev)
+    with torch.cuda.device(dev):
+        st = load_library().vq_paged_reserve(
+            lens.data_ptr(), new_lens.data_ptr(), r, free_pages.data_ptr(), free_count.data_ptr(),
+            free_pages.shape[0], block_table.data_ptr(), block_table.shape[1], page_size, total_new,
+            lens_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+            _stream_handle(stream, dev))
+    _check(st, "vq_paged_reserve")
+    return lens_out, free_count_out, cu_new, slots
+
+
+def vq_paged_trim(lens: torch.Tensor, keep_lens: torch.Tensor, block_table: torch.Tensor,
+                  page_size: int, free_pages: torch.Tensor, free_count: torch.Tensor,
+                  lens_out: torch.Tensor | None = None,
+                  free_count_out: torch.Tensor | None = None,
+                  stream: torch.cuda.Stream | None = None) -> tuple:
+    """Cut each request to ``keep_lens[r]`` tokens and push the pages it no
+    longer needs on ``free_pages`` (in place).  Returns ``(lens_out,
+    free_count_out)``, which may be ``lens`` and ``free_count`` themselves."""
+    _i32_tensor(lens, "lens", (None,), None)
+    dev, r = lens.device, lens.shape[0]
+    _i32_tensor(keep_lens, "keep_lens", (r,), dev)
+    _i32_tensor(block_table, "block_table", (r, None), dev)
+    _i32_tensor(free_pages, "free_pages", (None,), dev)
+    _i32_tensor(free_count, "free_count", (1,), dev)
+    lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev)
+    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        st = load_library().vq_paged_trim(
+            lens.data_ptr(), keep_lens.data_ptr(), r, block_table.data_ptr(), block_table.shape[1],
+            page_size, free_pages.data_ptr(), free_count.data_ptr(), free_pages.shape[0],
+            lens_out.data_ptr(), free_count_out.data_ptr(), _stream_handle(stream, dev))
+    _check(st, "vq_paged_trim")
+    return lens_out, free_count_out
+
+
+def _token_rows(t, name: str, device) -> None:
+    """A CUDA tensor [T, H, D] whose tokens may be strided, each contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [tokens, heads, head_dim], got {tuple(t.shape)}")
+    _dtype_code(t)
+    if t.numel() and (t.stride(2) != 1 and t.shape[2] > 1 or t.stride(1) != t.shape[2] and t.shape[1] > 1
+                      or t.stride(0) < t.shape[1] * t.shape[2] and t.shape[0] > 1):
+        raise ValueError(f"{name} must be contiguous within a token and its tokens must not overlap")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _token_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _page_tensors(k_codes, v_codes, k_codebooks, v_codebooks, dtype, device):
+    """Check the pages and codebooks; returns (num_pages, heads, page_size, ns,
+    page stride in bytes, n_centroids, sub_dim)."""
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes), ("k_codebooks", k_codebooks),
+                    ("v_codebooks", v_codebooks)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if k_codes.dim() != 4 or k_codebooks.dim() != 3:
+        raise ValueError(f"expected codes [pages, heads, page_size, ns] and codebooks [heads, "
+                         f"n_centroids, sub_dim], got {tuple(k_codes.shape)} and {tuple(k_codebooks.shape)}")
+    if k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8:
+        raise TypeError("codes must be uint8")
+    if k_codebooks.dtype != dtype or v_codebooks.dtype != dtype:
+        raise TypeError(f"codebooks must be {dtype}, as the rows are")
+    pages, heads, page_size, ns = k_codes.shape
+    if tuple(v_codes.shape) != tuple(k_codes.shape):
+        raise ValueError("k_codes and v_codes must have one shape")
+    if tuple(v_codebooks.shape) != tuple(k_codebooks.shape) or k_codebooks.shape[0] != heads:
+        raise ValueError("k_codebooks and v_codebooks must have one shape, [heads, n_centroids, sub_dim]")
+    inner = heads * page_size * ns
+    strides = []
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.numel() and not t[0].is_contiguous():
+            raise ValueError(f"each page of {name} must be contiguous")
+        strides.append(t.stride(0) if pages > 1 else inner)
+    if strides[0] != strides[1] or strides[0] < inner:
+        raise ValueError("the pages of k_codes and v_codes must not overlap and must have one stride")
+    for name, t in (("k_codebooks", k_codebooks), ("v_codebooks", v_codebooks)):
+        _device_tensor(t, name)
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes), ("k_codebooks", k_codebooks),
+                    ("v_codebooks", v_codebooks)):
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return pages, heads, page_size, ns, strides[0], k_codebooks.shape[1], k_codebooks.shape[2]
+
+
+def vq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                    k_codebooks: torch.Tensor, v_codebooks: torch.Tensor, k_codes: torch.Tensor,
+                    v_codes: torch.Tensor, k_smooth: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None) -> None:
+    """Encode the keys and values of new tokens into their slots of the pages.
+
+    ``k`` / ``v`` ``[T, H, D]`` (tokens may be strided), ``slots`` ``[T]`` int64
+    (-1: skipped), codebooks ``[H, n_centroids, sub_dim]`` in k's dtype,
+    ``k_codes`` / ``v_codes`` ``[num_pages, H, page_size, D/sub_dim]`` uint8,
+    written in place; ``k_smooth`` ``[H, D]`` float32 divides the keys first."""
+    _token_rows(k, "k", None)
+    dev = k.device
+    _token_rows(v, "v", dev)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must share shape and dtype")
+    pages, heads, page_size, ns, stride, n_c, sub = _page_tensors(k_codes, v_codes, k_codebooks,
+                                                                  v_codebooks, k.dtype, dev)
+    tokens, h, d = k.shape
+    if h != heads or ns * sub != d:
+        raise ValueError(f"k {tuple(k.shape)} does not match codes {tuple(k_codes.shape)} and "
+                         f"codebooks {tuple(k_codebooks.shape)}")
+    if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or tuple(slots.shape) != (tokens,):
+        raise ValueError("slots must be an int64 tensor of shape [T]")
+    _device_tensor(slots, "slots")
+    if slots.device != dev:
+        raise ValueError(f"slots is on {slots.device}, not on {dev}")
+    if k_smooth is not None:
+        if k_smooth.dtype != torch.float32 or tuple(k_smooth.shape) != (heads, d):
+            raise ValueError("k_smooth must be float32 of shape [H, D]")
+        _device_tensor(k_smooth, "k_smooth")
+        if k_smooth.device != dev:
+            raise ValueError(f"k_smooth is on {k_smooth.device}, not on {dev}")
+    with torch.cuda.device(dev):
+        st = load_library().vq_paged_append(
+            k.data_ptr(), v.data_ptr(), _token_stride(k), _token_stride(v), slots.data_ptr(), tokens,
+            heads, d, sub, n_c, k_codebooks.data_ptr(), v_codebooks.data_ptr(),
+            k_smooth.data_ptr() if k_smooth is not None else None, k_codes.data_ptr(),
+            v_codes.data_ptr(), pages, page_size, stride, _dtype_code(k), _stream_handle(stream, dev))
+    _check(st, "vq_paged_append")
+
+
+def vq_paged_attention_workspace_bytes(requests: int, tokens: int, max_new: int, heads_q: int,
+                                       heads_kv: int, head_dim: int, sub_dim: int,
+                                       n_centroids: int, page_size: int) -> int:
+    return int(load_library().vq_paged_attention_workspace_bytes(
+        requests, tokens, max_new, heads_q, heads_kv, head_dim, sub_dim, n_centroids, page_size))
+
+
+def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor,
+                       block_table: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
+                       k_codebooks: torch.Tensor, v_codebooks: torch.Tensor, max_new: int = 0,
+                       window: int = 0, scale: float = 0.0, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, return_lse: bool = False,
+                       workspace: torch.Tensor | None = None,
+                       stream: torch.cuda.Stream | None = None):
+    """Causal attention of the new tokens of every request over its pages.
+
+    ``q`` ``[T, Hq, D]`` (tokens may be strided); ``cu_new`` ``[R + 1]``,
+    ``lens`` ``[R]`` (with the new tokens) and ``block_table`` ``[R,
+    max_blocks]`` int32; pages and codebooks as in :func:`vq_paged_append`,
+    codebooks in q's dtype.  ``max_new`` is the most new tokens of a request
+    where the host knows it.  Returns ``out`` ``[T, Hq, D]``, or ``(out, lse)``
+    with ``lse`` ``[T, Hq]`` float32 where ``return_lse`` is set or ``lse`` is
+    given.  A workspace of :func:`vq_paged_attention_workspace_bytes` bytes is
+    allocated here (by torch) if none is given."""
+    _token_rows(q, "q", None)
+    dev = q.device
+    tokens, hq, d = q.shape
+    pages, hkv, page_size, ns, stride, n_c, sub = _page_tensors(k_codes, v_codes, k_codebooks,
+                                                                v_codebooks, q.dtype, dev)
+    if ns * sub != d or hq % hkv:
+        raise ValueError(f"q {tuple(q.shape)} does not match codes {tuple(k_codes.shape)} and "
+                         f"codebooks {tuple(k_codebooks.shape)}")
+    _i32_tensor(lens, "lens", (None,), dev)
+    r = lens.shape[0]
+    _i32_tensor(cu_new, "cu_new", (r + 1,), dev)
+    _i32_tensor(block_table, "block_table", (r, None), dev)
+    if max_new < 0:
+        raise ValueError("max_new must not be negative")
+    out = _out_like(out, "out", (tokens, hq, d), q.dtype, dev)
+    if return_lse or lse is not None:
+        lse = _out_like(lse, "lse", (tokens, hq), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            nbytes = vq_paged_attention_workspace_bytes(r, tokens, max_new, hq, hkv, d, sub, n_c, page_size)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        else:
+            _device_tensor(workspace, "workspace")
+            if workspace.device != dev:
+                raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+        st = load_library().vq_paged_attention(
+            q.data_ptr(), _token_stride(q), cu_new.data_ptr(), lens.data_ptr(), r, tokens, max_new,
+            block_table.data_ptr(), block_table.shape[1], k_codes.data_ptr(), v_codes.data_ptr(),
+            pages, page_size, stride, k_codebooks.data_ptr(), v_codebooks.data_ptr(), hq, hkv, d,
+            sub, n_c, window, scale, _dtype_code(q), out.data_ptr(),
+            lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    _check(st, "vq_paged_attention")
+    return (out, lse) if lse is not None else out
 
 
 # Bytes of the library's built-in scratch array (VQ_ATTN_STATIC_SCRATCH_BYTES).

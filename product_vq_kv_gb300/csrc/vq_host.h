@@ -17,8 +17,10 @@ int vqh_device_sms();
 cudaError_t vqh_status_encode(uint32_t *bits, bool clear);
 cudaError_t vqh_status_attn(uint32_t *bits, bool clear);
 cudaError_t vqh_status_scalar(uint32_t *bits, bool clear);
+cudaError_t vqh_status_append(uint32_t *bits, bool clear);
+cudaError_t vqh_status_paged(uint32_t *bits, bool clear);
 
-// The body of the three functions above, for the translation unit's own word.
+// The body of the functions above, for the translation unit's own word.
 #define VQH_STATUS_READER(NAME)                                                      \
     cudaError_t NAME(uint32_t *bits, bool clear)                                     \
     {                                                                                \

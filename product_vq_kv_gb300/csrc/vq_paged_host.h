@@ -1,0 +1,16 @@
+// vq_paged_host.h -- launches of the paged attention's tensor kernels, one
+// translation unit each (internal; not part of the C ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "vq_encode.h"
+
+namespace vqk {
+struct PagedArgs;
+}
+
+// A few rows (vq_pfew.cuh): 8 nt rows an item; dim 64, 128 or 256 (there nt is
+// 1), sub 4 or 8, fp16 or bf16.
+int vqh_few_blocks_per_sm(int32_t dim, int nt);
+vq_status vqh_paged_few(const vqk::PagedArgs &a, vq_dtype dtype, int nt, int blocks, cudaStream_t st);

@@ -1,0 +1,578 @@
+// vq_pattn.cuh -- attention of new tokens over a paged cache of product-VQ
+// codes: the work split that all its kernels share, the general kernel, and
+// the merge of partial results.
+//
+// For token i of request r (L_r tokens in the cache, its n_r new ones among
+// them) at position p = L_r - n_r + i and query head h of KV head c:
+//   s[t]  = kappa q . K^[t],  t in [max(0, p - window + 1), p],  kappa = scale log2 e
+//   out   = sum_t 2^(s[t] - m) V^[t] / sum_t 2^(s[t] - m),       m = max_t s[t]
+//   lse   = ln 2 (m + log2 sum_t 2^(s[t] - m))
+// K^[t], V^[t] are the codebook rows that token t's codes select (a code
+// >= n_centroids selects a zero row).  A token whose page entry is outside
+// [0, num_pages) is not seen.  A row that sees nothing gets zeros and -inf.
+//
+// The work split.  An item is a run of up to tile_tokens new tokens of one
+// request against one group of up to gc query heads of one KV head; its work
+// is counted in units of kUnit cached tokens, at least one (so that rows that
+// see nothing are written too).  Lengths live on the device, so the host
+// knows only a bound on the items; each block lays the items out for itself:
+// item j belongs to the last request r with start(r) = cu[r] / tile_tokens + r
+// <= j, which needs no sum over the requests before it and leaves at most one
+// hole per request.  The rows after the last request (a padded batch) form one
+// more request that sees nothing.  The units of all items of all head groups
+// are one line of U units, head groups outermost so that a block changes its
+// codebooks seldom, and block b of N takes units [b U / N, (b + 1) U / N): every
+// block has the same work to within one unit, however uneven the requests
+// are.  An item that lies in one block is finished there; the blocks of a
+// split item write (m, sum, sum of weighted rows) to the workspace, two slots
+// a block (2b: the item it continues, 2b + 1: the item it begins and does not
+// finish), and the block that begins it leaves a note for the merge.  The
+// order of every sum is fixed by the lengths.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "vq_check.cuh"
+#include "vq_kernels.cuh"
+
+namespace vqk {
+
+constexpr int kUnit = 128;       // cached tokens of one unit of work
+constexpr int kStageCu = 512;    // requests + 2 up to which a block keeps cu and lens in shared memory
+
+// The note of a split item (rows = 0: none).
+struct PagedNote {
+    int64_t tok0;    // first token (row of q)
+    int32_t head0;   // first query head
+    int32_t gc;      // heads of the item: row i is token tok0 + i / gc, head head0 + i % gc
+    int32_t rows;
+    int32_t first;   // blocks that hold its parts: slots 2 first + 1, 2 (first + 1), .., 2 last
+    int32_t last;
+    int32_t pad;
+};
+
+struct PagedArgs {
+    const void *q;
+    const uint8_t *k_codes, *v_codes;
+    const void *kcb, *vcb;
+    void *out;
+    float *lse;            // or null
+    const int32_t *cu, *lens, *table;
+    int64_t tokens;        // rows of q
+    int64_t q_stride;      // elements between tokens of q
+    int64_t page_stride;   // bytes between pages of codes
+    int64_t num_pages;
+    int64_t items;         // bound on the items of one head group
+    int32_t requests, max_blocks, page_shift;
+    int32_t hq, hkv, group;
+    int32_t gc, gch;       // heads per item, head groups per KV head
+    int32_t dim, sub, ns, nc;
+    int32_t window;        // 0: none
+    int32_t tile_tokens;
+    int32_t cls, cls_tokens;  // 0: every request; 1: those of up to cls_tokens new tokens; 2: the others
+    float kappa;
+    float *part;           // [2 N][tile rows][dim] weighted sums
+    float *ml;             // [2 N][tile rows][2] maximum, sum of weights
+    PagedNote *notes;      // [N]
+    int32_t tile_rows;
+};
+
+struct PagedItem {
+    int64_t tok0;   // first row of q
+    int32_t ntok;
+    int32_t pos0;   // position of the first token
+    int32_t k_lo;   // first cached token seen by any of its rows, rounded down to a unit
+    int32_t k_hi;   // one past the last
+    int32_t units;  // 0: a hole
+};
+
+// Lengths as the kernel sees them: cu clamped into [0, tokens], request
+// number `requests` being the rows after the last.
+struct PagedLens {
+    const int32_t *cu, *lens;
+    int32_t requests, tile;
+    int64_t tokens;
+    __device__ __forceinline__ int64_t first(int r) const
+    {
+        if (r > requests) return tokens;
+        const int64_t c = cu[r];
+        return c < 0 ? 0 : c > tokens ? tokens : c;
+    }
+    __device__ __forceinline__ int64_t start(int r) const { return first(r) / tile + r; }
+    // the last r in [0, requests] with start(r) <= j
+    __device__ __forceinline__ int find(int64_t j) const
+    {
+        int lo = 0, hi = requests;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (start(mid) <= j) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+// Item j, which belongs to request r; units = 0 for a hole (then *skip is the
+// next item worth a look).
+__device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, const PagedLens &l, int64_t j, int r,
+                                                int64_t *skip)
+{
+    PagedItem it{};
+    *skip = j + 1;
+    const int64_t c0 = l.first(r), c1 = l.first(r + 1);
+    const int64_t n = c1 > c0 ? c1 - c0 : 0;
+    const int64_t i0 = (j - l.start(r)) * l.tile;
+    const bool mine = a.cls == 0 || (a.cls == 1) == (n <= a.cls_tokens);
+    if (!mine || i0 >= n || i0 < 0) {
+        const int64_t next = r < a.requests ? l.start(r + 1) : a.items;
+        if (next > j + 1) *skip = next;
+        return it;
+    }
+    const int64_t len = r < a.requests ? (l.lens[r] > 0 ? l.lens[r] : 0) : 0;
+    const int64_t cap = (int64_t)a.max_blocks << a.page_shift;
+    const int64_t i1 = i0 + l.tile < n ? i0 + l.tile : n;
+    const int64_t pos0 = len - n + i0;
+    int64_t hi = len - n + i1;
+    if (hi > cap) hi = cap;
+    if (r >= a.requests || hi < 0) hi = 0;
+    int64_t lo = a.window > 0 ? pos0 - a.window + 1 : 0;
+    if (lo < 0) lo = 0;
+    lo &= ~(int64_t)(kUnit - 1);
+    it.tok0 = c0 + i0;
+    it.ntok = (int32_t)(i1 - i0);
+    it.pos0 = (int32_t)pos0;
+    it.k_lo = (int32_t)lo;
+    it.k_hi = (int32_t)hi;
+    it.units = hi > lo ? (int32_t)((hi - lo + kUnit - 1) / kUnit) : 1;
+    return it;
+}
+
+// Where a block stands on the line of units.
+struct PagedWalk {
+    int32_t stage_cu[kStageCu], stage_lens[kStageCu];
+    int64_t scratch[33];
+    int64_t total;  // U of one head group
+    int64_t u0, u1; // this block's units
+    int32_t blocks; // blocks with work
+    int32_t hx;     // head group
+    int64_t j;      // item
+    int32_t r;
+    int32_t at;     // first unit of it
+};
+
+// Lay the items out and find this block's part (all THREADS threads; w in
+// shared memory).  Returns whether the block has any.
+template <int THREADS>
+__device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk &w, PagedLens &l)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    l.cu = a.cu;
+    l.lens = a.lens;
+    l.requests = a.requests;
+    l.tile = a.tile_tokens;
+    l.tokens = a.tokens;
+    if (a.requests + 2 <= kStageCu) {
+        for (int i = tid; i <= a.requests; i += THREADS) {
+            w.stage_cu[i] = a.cu[i];
+            if (i < a.requests) w.stage_lens[i] = a.lens[i];
+        }
+        l.cu = w.stage_cu;
+        l.lens = w.stage_lens;
+        __syncthreads();
+    }
+    const int64_t per = (a.items + THREADS - 1) / THREADS;
+    const int64_t j0 = tid * per, j1 = j0 + per < a.items ? j0 + per : a.items;
+    int r0 = 0;
+    int64_t mine = 0;
+    if (j0 < j1) {
+        r0 = l.find(j0);
+        int r = r0;
+        for (int64_t j = j0; j < j1;) {
+            while (r < a.requests && l.start(r + 1) <= j) ++r;
+            int64_t skip;
+            mine += paged_item(a, l, j, r, &skip).units;
+            j = skip;
+        }
+    }
+    int64_t s = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t p = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += p;
+    }
+    if (lane == 31) w.scratch[warp] = s;
+    __syncthreads();
+    int64_t before = s - mine, total = 0;
+    for (int k = 0; k < THREADS / 32; ++k) {
+        if (k < warp) before += w.scratch[k];
+        total += w.scratch[k];
+    }
+    const int64_t all = total * ((int64_t)a.hkv * a.gch);
+    const int64_t n = all < (int64_t)gridDim.x ? all : (int64_t)gridDim.x;
+    const int64_t b = blockIdx.x;
+    if (tid == 0) {
+        w.total = total;
+        w.blocks = (int32_t)n;
+        w.u0 = b < n ? b * all / n : 0;
+        w.u1 = b < n ? (b + 1) * all / n : 0;
+        w.hx = 0;
+        w.j = w.r = w.at = 0;
+    }
+    if (b >= n) return false;  // block-uniform
+    const int64_t u0 = b * all / n;
+    const int64_t rem = u0 % total;
+    __syncthreads();
+    if (mine > 0 && before <= rem && rem < before + mine) {
+        int64_t left = rem - before;
+        int r = r0;
+        for (int64_t j = j0; j < j1;) {
+            while (r < a.requests && l.start(r + 1) <= j) ++r;
+            int64_t skip;
+            const int32_t u = paged_item(a, l, j, r, &skip).units;
+            if (left < u) {
+                w.hx = (int32_t)(u0 / total);
+                w.j = j;
+                w.r = r;
+                w.at = (int32_t)left;
+                break;
+            }
+            left -= u;
+            j = skip;
+        }
+    }
+    __syncthreads();
+    return true;
+}
+
+// One block's part of one item.
+struct PagedSegment {
+    PagedItem it;
+    int32_t hx;          // head group
+    int32_t begin, end;  // units of the item
+    bool whole;          // all of them
+    int64_t slot;        // of the workspace, if not
+};
+
+// Walks this block's segments in order; every thread holds its own copy and
+// computes the same.
+struct PagedCursor {
+    int64_t u, u1, j;
+    int32_t r, at, hx;
+    __device__ __forceinline__ void init(const PagedWalk &w)
+    {
+        u = w.u0;
+        u1 = w.u1;
+        j = w.j;
+        r = w.r;
+        at = w.at;
+        hx = w.hx;
+    }
+    // The next segment; false at the end.  `note` is filled if the block
+    // begins an item that it does not finish.
+    __device__ __forceinline__ bool next(const PagedArgs &a, const PagedWalk &w, const PagedLens &l,
+                                         PagedSegment &s, PagedNote &note)
+    {
+        if (u >= u1) return false;
+        for (;;) {
+            if (j >= a.items) {  // the next head group
+                j = 0;
+                r = 0;
+                ++hx;
+            }
+            while (r < a.requests && l.start(r + 1) <= j) ++r;
+            int64_t skip;
+            s.it = paged_item(a, l, j, r, &skip);
+            if (s.it.units > 0) break;
+            j = skip;
+        }
+        const int64_t b = blockIdx.x;
+        s.hx = hx;
+        s.begin = at;
+        const int64_t room = u1 - u;
+        s.end = s.it.units - at <= room ? s.it.units : (int32_t)(at + room);
+        s.whole = s.begin == 0 && s.end == s.it.units;
+        s.slot = 2 * b + (s.begin == 0 ? 1 : 0);
+        if (s.begin == 0 && !s.whole) {
+            const int64_t all = w.total * ((int64_t)a.hkv * a.gch);
+            const int64_t last_unit = u + s.it.units - 1;  // begin = 0: u is the item's first unit
+            const int32_t g0 = hx % a.gch * a.gc;
+            note.tok0 = s.it.tok0;
+            note.head0 = hx / a.gch * a.group + g0;
+            note.gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
+            note.rows = s.it.ntok * note.gc;
+            note.first = (int32_t)b;
+            // the block of unit x: the c with floor(c U / N) <= x < floor((c + 1) U / N)
+            note.last = (int32_t)(((last_unit + 1) * w.blocks - 1) / all);
+        }
+        u += s.end - s.begin;
+        at = 0;
+        ++j;
+        return true;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+// lse from the maximum and the sum in powers of two.
+__device__ __forceinline__ float paged_lse(float m, float l)
+{
+    return l == 0.f ? __int_as_float(0xff800000) : kLn2 * (m + log2f(l));
+}
+
+// Page of cached token t; -1 if the entry is no page.
+__device__ __forceinline__ int64_t paged_page(const PagedArgs &a, int32_t r, int32_t t)
+{
+    const int32_t *e = a.table + (int64_t)r * a.max_blocks + (t >> a.page_shift);
+    if (!VQ_SPAN(e, 1, a.table, (int64_t)a.requests * a.max_blocks)) return -1;
+    const int32_t pg = __ldg(e);
+    return pg >= 0 && pg < a.num_pages ? pg : -1;
+}
+
+// ------------------------------------------------------------------ the general kernel
+//
+// Any type, head size up to kSimpleDim, sub-vector size and page size.  A
+// block of kUnit threads takes one new token and up to kSimpleRows query heads
+// of its KV head; a unit is one cached token per thread for the scores and one
+// column (or more) per thread for the weighted sum, all in fp32.  What bounds
+// it is the codebook rows, read through the L1 for every cached token, twice;
+// it carries the types and shapes that the tensor kernels do not.
+
+constexpr int kSimpleRows = 8;
+constexpr int kSimpleDim = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant__ PagedArgs a)
+{
+    __shared__ PagedWalk w;
+    __shared__ float sp[kSimpleRows][kUnit];
+    __shared__ float red[kSimpleRows][kUnit / 32];
+    __shared__ int64_t spage[kUnit];
+    extern __shared__ float sq[];  // [kSimpleRows][dim]
+    constexpr int kCols = kSimpleDim / kUnit;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const T *__restrict__ q = static_cast<const T *>(a.q);
+    T *__restrict__ out = static_cast<T *>(a.out);
+    const int64_t cb_elems = (int64_t)a.hkv * a.nc * a.sub;
+
+    PagedLens l;
+    PagedNote note{};
+    if (paged_plan<kUnit>(a, w, l)) {
+        PagedCursor cur;
+        cur.init(w);
+        PagedSegment s;
+        while (cur.next(a, w, l, s, note)) {
+            const int r = cur.r;
+            const int h = s.hx / a.gch, g0 = s.hx % a.gch * a.gc;
+            const int rows = a.group - g0 < a.gc ? a.group - g0 : a.gc;  // one token: a row per head
+            const int head0 = h * a.group + g0;
+            const int64_t tok = s.it.tok0;
+            const int64_t code_head = (int64_t)h << a.page_shift;
+            const T *__restrict__ kcb = static_cast<const T *>(a.kcb) + (int64_t)h * a.nc * a.sub;
+            const T *__restrict__ vcb = static_cast<const T *>(a.vcb) + (int64_t)h * a.nc * a.sub;
+            __syncthreads();
+            for (int i = tid; i < kSimpleRows * a.dim; i += kUnit) {
+                const int g = i / a.dim, d = i - g * a.dim;
+                const T *src = q + tok * a.q_stride + (int64_t)(head0 + g) * a.dim + d;
+                float v = 0.f;
+                if (g < rows && VQ_SPAN(src, 1, q, (a.tokens - 1) * a.q_stride + (int64_t)a.hq * a.dim))
+                    v = a.kappa * widen(*src);
+                sq[i] = v;
+            }
+            float m[kSimpleRows], sum[kSimpleRows], acc[kSimpleRows][kCols];
+#pragma unroll
+            for (int g = 0; g < kSimpleRows; ++g) {
+                m[g] = __int_as_float(0xff800000);
+                sum[g] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[g][c] = 0.f;
+            }
+            for (int unit = s.begin; unit < s.end; ++unit) {
+                const int32_t t = s.it.k_lo + unit * kUnit + tid;
+                bool seen = t < s.it.k_hi && t <= s.it.pos0 && (a.window == 0 || (int64_t)t > (int64_t)s.it.pos0 - a.window);
+                int64_t code_row = -1;
+                if (seen) {
+                    const int64_t pg = paged_page(a, r, t);
+                    if (pg < 0) seen = false;
+                    else code_row = pg * a.page_stride + (code_head + (t & ((1 << a.page_shift) - 1))) * a.ns;
+                }
+                __syncthreads();  // sq is written; the last unit's sp and spage are read
+                spage[tid] = code_row;
+                float dot[kSimpleRows];
+#pragma unroll
+                for (int g = 0; g < kSimpleRows; ++g) dot[g] = 0.f;
+                if (seen && span_ok(a.k_codes + code_row, a.ns, a.k_codes, (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * a.ns) << a.page_shift), 1)) {
+                    for (int sidx = 0; sidx < a.ns; ++sidx) {
+                        const int code = __ldg(a.k_codes + code_row + sidx);
+                        if (code >= a.nc) continue;
+                        const T *row = kcb + (int64_t)code * a.sub;
+                        if (!VQ_SPAN(row, a.sub, static_cast<const T *>(a.kcb), cb_elems)) continue;
+                        for (int i = 0; i < a.sub; ++i) {
+                            const float kv = widen(__ldg(row + i));
+#pragma unroll
+                            for (int g = 0; g < kSimpleRows; ++g)
+                                dot[g] = fmaf(sq[g * a.dim + sidx * a.sub + i], kv, dot[g]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < kSimpleRows; ++g) {
+                    if (!seen) dot[g] = __int_as_float(0xff800000);
+                    float top = dot[g];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    if (lane == 0) red[g][warp] = top;
+                }
+                __syncthreads();
+                float scale[kSimpleRows];
+#pragma unroll
+                for (int g = 0; g < kSimpleRows; ++g) {
+                    float top = m[g];
+#pragma unroll
+                    for (int k = 0; k < kUnit / 32; ++k) top = fmaxf(top, red[g][k]);
+                    // nothing seen yet: keep the (empty) sums
+                    scale[g] = m[g] == top ? 1.f : exp2f(m[g] - top);
+                    m[g] = top;
+                    const float p = seen ? exp2f(dot[g] - top) : 0.f;
+                    sp[g][tid] = p;
+                    sum[g] = sum[g] * scale[g] + p;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    const int d = tid + c * kUnit;
+                    if (d >= a.dim) break;
+                    const int sidx = d / a.sub, i = d - sidx * a.sub;
+#pragma unroll
+                    for (int g = 0; g < kSimpleRows; ++g) acc[g][c] *= scale[g];
+                    for (int k = 0; k < kUnit; ++k) {
+                        const int64_t cr = spage[k];
+                        if (cr < 0) continue;  // not seen: whatever its page holds
+                        if (!span_ok(a.v_codes + cr + sidx, 1, a.v_codes, (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * a.ns) << a.page_shift), 1)) continue;
+                        const int code = __ldg(a.v_codes + cr + sidx);
+                        if (code >= a.nc) continue;
+                        const T *e = vcb + (int64_t)code * a.sub + i;
+                        if (!VQ_SPAN(e, 1, static_cast<const T *>(a.vcb), cb_elems)) continue;
+                        const float v = widen(__ldg(e));
+#pragma unroll
+                        for (int g = 0; g < kSimpleRows; ++g) acc[g][c] = fmaf(sp[g][k], v, acc[g][c]);
+                    }
+                }
+            }
+            // the rows' sums of weights over the threads
+#pragma unroll
+            for (int g = 0; g < kSimpleRows; ++g) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
+            }
+            __syncthreads();
+            if (lane == 0) {
+#pragma unroll
+                for (int g = 0; g < kSimpleRows; ++g) red[g][warp] = sum[g];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < kSimpleRows; ++g) {
+                if (g >= rows) break;
+                float total = 0.f;
+#pragma unroll
+                for (int k = 0; k < kUnit / 32; ++k) total += red[g][k];
+                const int64_t orow = tok * a.hq + head0 + g;
+                if (s.whole) {
+                    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) {
+                        const int d = tid + c * kUnit;
+                        if (d < a.dim && VQ_SPAN(out + orow * a.dim + d, 1, out, a.tokens * a.hq * a.dim))
+                            out[orow * a.dim + d] = narrow<T>(acc[g][c] * inv);
+                    }
+                    if (tid == 0 && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq))
+                        a.lse[orow] = paged_lse(m[g], total);
+                } else {
+                    const int64_t prow = s.slot * a.tile_rows + g, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) {
+                        const int d = tid + c * kUnit;
+                        if (d < a.dim && VQ_SPAN(a.part + prow * a.dim + d, 1, a.part, prows * a.dim))
+                            a.part[prow * a.dim + d] = acc[g][c];
+                    }
+                    if (tid == 0 && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
+                        a.ml[prow * 2] = m[g];
+                        a.ml[prow * 2 + 1] = total;
+                    }
+                }
+            }
+        }
+    }
+    if (tid == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;
+}
+
+// ------------------------------------------------------------------ the merge
+//
+// Block (b, y) merges rows [y kMergeRows, ..) of the item that block b of the
+// attention began and did not finish: a warp per row, lanes over the parts
+// for the maximum, then over the columns.  Reads every part once.
+
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = kMergeThreads / 32;
+
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads)
+    paged_attn_merge(const float *__restrict__ part, const float *__restrict__ ml,
+                     const PagedNote *__restrict__ notes, int32_t tile_rows, int32_t dim, int32_t hq,
+                     int64_t tokens, T *__restrict__ out, float *__restrict__ lse)
+{
+    // launched while the attention's last blocks still run
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PagedNote n = notes[blockIdx.x];
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+    if (row >= n.rows) return;  // warp-uniform
+    const int parts = n.last - n.first + 1;
+    auto slot_row = [&](int k) {
+        return (k == 0 ? 2 * (int64_t)n.first + 1 : 2 * (int64_t)(n.first + k)) * tile_rows + row;
+    };
+    const int64_t prows = 2 * (int64_t)gridDim.x * tile_rows;
+    float top = __int_as_float(0xff800000);
+    for (int k = lane; k < parts; k += 32) {
+        const float *p = ml + slot_row(k) * 2;
+        if (VQ_SPAN(p, 2, ml, prows * 2) && p[1] != 0.f) top = fmaxf(top, p[0]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const int64_t orow = (n.tok0 + row / n.gc) * hq + n.head0 + row % n.gc;
+    float total = 0.f;
+    constexpr int kMax = kSimpleDim / 32;
+    float acc[kMax];
+#pragma unroll
+    for (int c = 0; c < kMax; ++c) acc[c] = 0.f;
+    for (int k = 0; k < parts; ++k) {
+        const int64_t sr = slot_row(k);
+        if (!VQ_SPAN(ml + sr * 2, 2, ml, prows * 2) || !VQ_SPAN(part + sr * dim, dim, part, prows * dim)) continue;
+        const float l = ml[sr * 2 + 1];
+        if (l == 0.f) continue;  // this part of the row saw nothing
+        const float w = exp2f(ml[sr * 2] - top);
+        total = fmaf(w, l, total);
+#pragma unroll
+        for (int c = 0; c < kMax; ++c)
+            if (c * 32 + lane < dim) acc[c] = fmaf(w, part[sr * dim + c * 32 + lane], acc[c]);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (int c = 0; c < kMax; ++c)
+        if (c * 32 + lane < dim && VQ_SPAN(out + orow * dim + c * 32 + lane, 1, out, tokens * hq * dim))
+            out[orow * dim + c * 32 + lane] = narrow<T>(acc[c] * inv);
+    if (lane == 0 && lse && VQ_SPAN(lse + orow, 1, lse, tokens * hq)) lse[orow] = paged_lse(top, total);
+}
+
+}  // namespace vqk

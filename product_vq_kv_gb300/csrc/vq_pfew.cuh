@@ -1,0 +1,528 @@
+// vq_pfew.cuh -- paged attention of a few rows (decode, verification of
+// drafts): up to 8 NT rows (tokens x query heads of one KV head) against the
+// whole cache, 16-bit types, head sizes 64, 128 and 256, sub-vectors of 4 or 8.
+//
+// What bounds it.  From HBM a cached token costs 2 ns bytes a KV head (32 at
+// head size 128, sub-vectors of 8); rebuilding its key and value rows costs 2 x
+// 2 dim = 512 bytes out of the codebooks.  An SM reads 128 bytes of shared
+// memory a cycle, so with the codebooks there the rebuild is the bound: 4 cycles
+// a token and KV head, against 1.4 cycles of its share of HBM.  Everything is
+// laid out so that a rebuilt value is read once, without a bank conflict, and
+// goes nowhere but into the registers of the matrix instruction that uses it:
+//   * mma.m16n8k16 with the cached tokens (keys) or the head's columns (values)
+//     as the 16 rows and the query rows as the 8 columns, so that few rows cost
+//     few instructions:  S^T = K^ Q^T,  O^T = V^^T P^T.  (tcgen05 takes its
+//     operands from shared or tensor memory, which would cost a write and a second
+//     read of every rebuilt value.)
+//   * Which column of the head an instruction's k index means is free as long as
+//     both operands agree.  Lane (g, t) = (lane / 4, lane % 4) takes columns
+//     [t dim/4, (t+1) dim/4) of keys g and g + 8: whole codebook rows, one 16- or
+//     8-byte load each, and its codes are consecutive bytes of the cache.  For the
+//     values it takes columns [g dim/8, (g+1) dim/8) of tokens 2t, 2t+1, 2t+8,
+//     2t+9 and pairs the tokens with byte permutes.
+//   * Each codebook lies in shared memory as 256 lines of 128 bytes, a line
+//     holding 8 (16) copies of one 16 (8) byte row.  The lanes that a 128-byte
+//     wavefront serves read different copies: no conflicts, whatever the codes.
+//   * P^T reaches the second product through movmatrix, an 8x8 transpose inside
+//     the warp.  Nothing of the inner loop but the codebooks touches shared
+//     memory, and no barrier stands in it: warp w takes tokens 16 w .. 16 w + 15
+//     of every unit and keeps its own softmax state.
+//   * Codes come straight from global memory into registers two units ahead, the
+//     page numbers three.
+//   * The running maximum follows the scores only when one exceeds it by 2^8
+//     (a vote); until then the weights are at most 2^8, well inside fp16, and
+//     nothing is rescaled.
+// Weights are rounded to the input type for the second product (the sum of
+// weights takes them unrounded, in fp32).
+#pragma once
+
+#include <type_traits>
+
+#include "vq_pattn.cuh"
+
+namespace vqk {
+
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr float kFewSlack = 8.f;  // powers of two a weight may exceed 1 by
+static_assert(kFewWarps * 16 == kUnit, "a warp takes 16 tokens of a unit");
+
+// Shared memory: two codebook images of 32 KiB, then the merge's four slots.
+template <int D, int NT>
+constexpr size_t few_smem()
+{
+    return 2 * 32768 + (size_t)4 * 8 * NT * D * sizeof(float);
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Two fp32 values rounded to the 16-bit type, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^x, 0 for -inf; error 2 ulp (2^-22).
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// BYTES consecutive code bytes in words, low byte first.
+template <int BYTES>
+__device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&w)[(BYTES + 3) / 4])
+{
+    if constexpr (BYTES == 1) w[0] = __ldg(p);
+    if constexpr (BYTES == 2) w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+    if constexpr (BYTES == 4) w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    if constexpr (BYTES == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[0] = v.x;
+        w[1] = v.y;
+    }
+    if constexpr (BYTES == 16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
+// Byte i of w[] as an unsigned number; i is a constant after unrolling.
+template <int W>
+__device__ __forceinline__ uint32_t code_at(const uint32_t (&w)[W], int i)
+{
+    return __byte_perm(w[i >> 2], 0, 0x4440 | (i & 3));
+}
+
+// One codebook row of SUB 16-bit values from its image: SUB / 2 words.
+// `base` = shared address of the image plus this lane's copy offset.
+template <int SUB>
+__device__ __forceinline__ void image_row(uint32_t base, uint32_t code, uint32_t (&w)[SUB / 2])
+{
+    const uint32_t at = base + code * 128u;
+    if constexpr (SUB == 8)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+    else
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+}
+
+// Write the image of one head's codebook: row c is stored 256 / (2 SUB) times
+// along its 128-byte line; rows past the codebook are zero.  The copies are
+// written in an order that starts at c, so that the lanes of a wavefront meet
+// in no bank.  All THREADS threads; the caller synchronises.
+template <typename T, int SUB, int THREADS>
+__device__ __forceinline__ void build_image(unsigned char *image, const T *__restrict__ cb, int nc,
+                                            const T *all, int64_t all_elems)
+{
+    for (int c = threadIdx.x; c < 256; c += THREADS) {
+        uint32_t w[SUB / 2];
+#pragma unroll
+        for (int i = 0; i < SUB / 2; ++i) w[i] = 0;
+        if (c < nc && VQ_SPAN(cb + (int64_t)c * SUB, SUB, all, all_elems)) {
+            const uint16_t *src = reinterpret_cast<const uint16_t *>(cb + (int64_t)c * SUB);
+#pragma unroll
+            for (int i = 0; i < SUB / 2; ++i) w[i] = (uint32_t)__ldg(src + 2 * i) | ((uint32_t)__ldg(src + 2 * i + 1) << 16);
+        }
+        constexpr int kCopies = 64 / SUB;
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) {
+            unsigned char *dst = image + c * 128 + ((c + k) % kCopies) * (2 * SUB);
+            if (!dyn_smem_ok(dst, 2 * SUB, 2 * SUB)) continue;
+            if constexpr (SUB == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        }
+    }
+}
+
+template <typename T, int D, int SUB, int NT>
+__global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_attn_few(const __grid_constant__ PagedArgs a)
+{
+    constexpr int NS = D / SUB;
+    constexpr int KB = NS / 4, VB = NS / 8;        // code bytes a lane takes of a key, of a value
+    constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
+    constexpr int kMma = D / 16;                   // instructions per 16 tokens and 8 rows, each product
+    constexpr int kRowsMax = 8 * NT;
+    static_assert(SUB == 4 || SUB == 8, "sub-vectors of 4 or 8");
+    extern __shared__ __align__(128) unsigned char few_mem[];
+    __shared__ PagedWalk w;
+    __shared__ float wm[kFewWarps][kRowsMax], wl[kFewWarps][kRowsMax];
+    unsigned char *k_image = few_mem, *v_image = few_mem + 32768;
+    float *slots = reinterpret_cast<float *>(few_mem + 65536);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const float kNone = __int_as_float(0xff800000);
+    const uint32_t copy = (uint32_t)(lane % (64 / SUB)) * (2 * SUB);
+    const uint32_t k_base = (uint32_t)__cvta_generic_to_shared(k_image) + copy;
+    const uint32_t v_base = (uint32_t)__cvta_generic_to_shared(v_image) + copy;
+    const T *__restrict__ q = static_cast<const T *>(a.q);
+    T *__restrict__ out = static_cast<T *>(a.out);
+    const bool q_vec = (uintptr_t)a.q % 8 == 0 && a.q_stride % 4 == 0;
+    const bool out_vec = (uintptr_t)a.out % 16 == 0;
+    const int64_t cb_elems = (int64_t)a.hkv * a.nc * SUB;
+    const int64_t q_elems = (a.tokens - 1) * a.q_stride + (int64_t)a.hq * D;
+    const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
+
+    PagedLens l;
+    PagedNote note{};
+    if (paged_plan<kFewThreads>(a, w, l)) {
+        PagedCursor cur;
+        cur.init(w);
+        PagedSegment s;
+        int built = -1;  // the KV head whose codebooks are in shared memory
+        while (cur.next(a, w, l, s, note)) {
+            const int h = s.hx / a.gch, g0 = s.hx % a.gch * a.gc;
+            const int gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
+            const int rows = s.it.ntok * gc;
+            const int head0 = h * a.group + g0;
+            __syncthreads();  // the last segment's slots are read
+            if (h != built) {  // block-uniform
+                build_image<T, SUB, kFewThreads>(k_image, static_cast<const T *>(a.kcb) + (int64_t)h * a.nc * SUB, a.nc,
+                                                 static_cast<const T *>(a.kcb), cb_elems);
+                build_image<T, SUB, kFewThreads>(v_image, static_cast<const T *>(a.vcb) + (int64_t)h * a.nc * SUB, a.nc,
+                                                 static_cast<const T *>(a.vcb), cb_elems);
+                built = h;
+            }
+
+            // query fragments: row 8 n + g, columns t dim/4 + 4 i .. + 3
+            uint32_t qf[NT][kMma][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = 8 * n + g;
+                const T *src = q + (s.it.tok0 + row / gc) * a.q_stride + (int64_t)(head0 + row % gc) * D + t * (D / 4);
+                const bool ok = row < rows && VQ_SPAN(src, D / 4, q, q_elems);
+#pragma unroll
+                for (int i = 0; i < kMma; ++i) {
+                    uint2 v = make_uint2(0, 0);
+                    if (ok) {
+                        if (q_vec) {
+                            v = __ldg(reinterpret_cast<const uint2 *>(src + 4 * i));
+                        } else {
+                            const uint16_t *e = reinterpret_cast<const uint16_t *>(src + 4 * i);
+                            v.x = (uint32_t)__ldg(e) | ((uint32_t)__ldg(e + 1) << 16);
+                            v.y = (uint32_t)__ldg(e + 2) | ((uint32_t)__ldg(e + 3) << 16);
+                        }
+                    }
+                    qf[n][i][0] = v.x;
+                    qf[n][i][1] = v.y;
+                }
+            }
+            // this lane's rows 8 n + 2 t + c: the last token each sees
+            int32_t lim[NT][2];
+            float m[NT][2], sum[NT][2];
+            float o[NT][kMma][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int row = 8 * n + 2 * t + c;
+                    const int32_t p = s.it.pos0 + (row < rows ? row / gc : 0);
+                    lim[n][c] = p < s.it.k_hi ? p : s.it.k_hi - 1;
+                    m[n][c] = kNone;
+                    sum[n][c] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < kMma; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
+            }
+            // positions are lim + window apart from the first token not seen;
+            // a row whose limit k_hi cut keeps its own window
+            int32_t low[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int row = 8 * n + 2 * t + c;
+                    const int64_t p = (int64_t)s.it.pos0 + (row < rows ? row / gc : 0) - a.window;
+                    low[n][c] = a.window == 0 || p < -1 ? -1 : (int32_t)p;  // tokens above it are seen
+                }
+            const int32_t all_hi = s.it.pos0 < s.it.k_hi ? s.it.pos0 : s.it.k_hi - 1;  // every row sees up to here
+            const int64_t last_pos = (int64_t)s.it.pos0 + s.it.ntok - 1;
+            const int64_t all_lo = a.window == 0 ? -1 : last_pos - a.window;       // and above here
+            const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.it.pos0 - a.window;  // no row sees at or below
+
+            auto first_of = [&](int unit) { return s.it.k_lo + unit * kUnit + warp * 16; };
+            auto page_of = [&](int unit) -> int32_t {
+                if (unit >= s.end) return -1;
+                const int32_t k0 = first_of(unit);
+                if (k0 >= s.it.k_hi || k0 + 15 <= none_lo) return -1;
+                return (int32_t)paged_page(a, cur.r, k0);
+            };
+            auto load = [&](int unit, int32_t pg, uint32_t (&kc)[2][KW], uint32_t (&vc)[4][VW]) {
+                if (pg < 0) return;  // warp-uniform
+                const int32_t off = first_of(unit) & ((1 << a.page_shift) - 1);
+                const int64_t base = (int64_t)pg * a.page_stride + (((int64_t)h << a.page_shift) + off) * NS;
+                if (!span_ok(a.k_codes + base, 16 * NS, a.k_codes, code_bytes, NS < 16 ? NS : 16) ||
+                    !span_ok(a.v_codes + base, 16 * NS, a.v_codes, code_bytes, NS < 16 ? NS : 16))
+                    return;
+                const uint8_t *kp = a.k_codes + base + g * NS + t * KB;
+                load_codes<KB>(kp, kc[0]);
+                load_codes<KB>(kp + 8 * NS, kc[1]);
+                const uint8_t *vp = a.v_codes + base + 2 * t * NS + g * VB;
+                load_codes<VB>(vp, vc[0]);
+                load_codes<VB>(vp + NS, vc[1]);
+                load_codes<VB>(vp + 8 * NS, vc[2]);
+                load_codes<VB>(vp + 9 * NS, vc[3]);
+            };
+
+            uint32_t kc[3][2][KW] = {}, vc[3][4][VW] = {};
+            int32_t pg[3], pg_next;
+            pg[0] = page_of(s.begin);
+            pg[1] = page_of(s.begin + 1);
+            pg[2] = page_of(s.begin + 2);
+            load(s.begin, pg[0], kc[0], vc[0]);
+            load(s.begin + 1, pg[1], kc[1], vc[1]);
+            __syncthreads();  // the images are written
+
+            for (int unit = s.begin; unit < s.end; ++unit) {
+                load(unit + 2, pg[2], kc[2], vc[2]);
+                pg_next = page_of(unit + 3);
+                if (pg[0] >= 0) {  // warp-uniform
+                    // S^T = K^ Q^T
+                    float st[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) st[n][c] = 0.f;
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) {
+                        uint32_t lo[SUB / 2], hi[SUB / 2];
+                        image_row<SUB>(k_base, code_at(kc[0][0], b), lo);
+                        image_row<SUB>(k_base, code_at(kc[0][1], b), hi);
+#pragma unroll
+                        for (int i = 0; i < SUB / 4; ++i)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma16816<T>(st[n], lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
+                                            qf[n][b * (SUB / 4) + i][0], qf[n][b * (SUB / 4) + i][1]);
+                    }
+                    const int32_t k0 = first_of(unit);
+                    const bool whole = k0 + 15 <= all_hi && k0 > all_lo;
+                    bool rise = false;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            st[n][c] *= a.kappa;
+                            if (!whole) {
+                                const int32_t key = k0 + g + (c >> 1) * 8;
+                                if (key > lim[n][c & 1] || key <= low[n][c & 1]) st[n][c] = kNone;
+                            }
+                            rise |= st[n][c] > m[n][c & 1] + kFewSlack;
+                        }
+                    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float top = fmaxf(fmaxf(st[n][c], st[n][c + 2]), m[n][c]);
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                                const float f = top == m[n][c] ? 1.f : exp2_fast(m[n][c] - top);
+                                m[n][c] = top;
+                                sum[n][c] *= f;
+#pragma unroll
+                                for (int i = 0; i < kMma; ++i) {
+                                    o[n][i][c] *= f;
+                                    o[n][i][c + 2] *= f;
+                                }
+                            }
+                    }
+                    uint32_t pf[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float p[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // nothing seen yet: the maximum is -inf and so is every score
+                            const float mm = m[n][c & 1] == kNone ? 0.f : m[n][c & 1];
+                            p[c] = exp2_fast(st[n][c] - mm);
+                        }
+                        sum[n][0] += p[0] + p[2];
+                        sum[n][1] += p[1] + p[3];
+                        pf[n][0] = transpose8x8(pack2<T>(p[0], p[1]));
+                        pf[n][1] = transpose8x8(pack2<T>(p[2], p[3]));
+                    }
+                    // O^T += V^^T P^T
+#pragma unroll
+                    for (int b = 0; b < VB; ++b) {
+                        uint32_t e[4][SUB / 2];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) image_row<SUB>(v_base, code_at(vc[0][k], b), e[k]);
+#pragma unroll
+                        for (int i = 0; i < SUB / 2; ++i) {
+                            const uint32_t a0 = __byte_perm(e[0][i], e[1][i], 0x5410);
+                            const uint32_t a1 = __byte_perm(e[0][i], e[1][i], 0x7632);
+                            const uint32_t a2 = __byte_perm(e[2][i], e[3][i], 0x5410);
+                            const uint32_t a3 = __byte_perm(e[2][i], e[3][i], 0x7632);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma16816<T>(o[n][b * (SUB / 2) + i], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                        }
+                    }
+                }
+                pg[0] = pg[1];
+                pg[1] = pg[2];
+                pg[2] = pg_next;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < KW; ++i) kc[x][k][i] = kc[x + 1][k][i];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < VW; ++i) vc[x][k][i] = vc[x + 1][k][i];
+                }
+            }
+
+            // the warps' states: maxima and sums first
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    sum[n][c] += __shfl_xor_sync(0xffffffffu, sum[n][c], 4);
+                    sum[n][c] += __shfl_xor_sync(0xffffffffu, sum[n][c], 8);
+                    sum[n][c] += __shfl_xor_sync(0xffffffffu, sum[n][c], 16);
+                    if (g == 0) {
+                        wm[warp][8 * n + 2 * t + c] = m[n][c];
+                        wl[warp][8 * n + 2 * t + c] = sum[n][c];
+                    }
+                }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int row = 8 * n + 2 * t + c;
+                    float top = kNone;
+#pragma unroll
+                    for (int k = 0; k < kFewWarps; ++k)
+                        if (wl[k][row] != 0.f) top = fmaxf(top, wm[k][row]);
+                    float total = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kFewWarps; ++k)
+                        if (wl[k][row] != 0.f) total = fmaf(exp2_fast(wm[k][row] - top), wl[k][row], total);
+                    const float f = sum[n][c] == 0.f ? 0.f : exp2_fast(m[n][c] - top);
+                    m[n][c] = top;
+                    sum[n][c] = total;
+#pragma unroll
+                    for (int i = 0; i < kMma; ++i) {
+                        o[n][i][c] *= f;
+                        o[n][i][c + 2] *= f;
+                    }
+                }
+            // then the weighted sums, in three halvings
+#pragma unroll
+            for (int half = kFewWarps / 2; half > 0; half >>= 1) {
+                float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp % half) * NT * kMma * 32 + lane;
+                if (warp >= half && warp < 2 * half) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < kMma; ++i)
+                            if (dyn_smem_ok(slot + (n * kMma + i) * 32, 16, 16))
+                                slot[(n * kMma + i) * 32] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+                }
+                __syncthreads();
+                if (warp < half) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < kMma; ++i)
+                            if (dyn_smem_ok(slot + (n * kMma + i) * 32, 16, 16)) {
+                                const float4 v = slot[(n * kMma + i) * 32];
+                                o[n][i][0] += v.x;
+                                o[n][i][1] += v.y;
+                                o[n][i][2] += v.z;
+                                o[n][i][3] += v.w;
+                            }
+                }
+                __syncthreads();
+            }
+            if (warp == 0) {
+                // lane (g, t) holds columns [g dim/8, (g+1) dim/8) of rows 8 n + 2 t + c
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int row = 8 * n + 2 * t + c;
+                        if (row >= rows) continue;
+                        if (s.whole) {
+                            const int64_t orow = (s.it.tok0 + row / gc) * a.hq + head0 + row % gc;
+                            const float inv = sum[n][c] == 0.f ? 0.f : 1.f / sum[n][c];
+                            T *dst = out + orow * D + g * (D / 8);
+                            if (VQ_SPAN(dst, D / 8, out, a.tokens * a.hq * D)) {
+                                if (out_vec) {
+#pragma unroll
+                                    for (int i = 0; i < kMma; i += 4) {
+                                        uint32_t v[4];
+#pragma unroll
+                                        for (int x = 0; x < 4; ++x)
+                                            v[x] = pack2<T>(o[n][i + x][c] * inv, o[n][i + x][c + 2] * inv);
+                                        reinterpret_cast<uint4 *>(dst)[i / 4] = make_uint4(v[0], v[1], v[2], v[3]);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < kMma; ++i) {
+                                        dst[2 * i] = narrow<T>(o[n][i][c] * inv);
+                                        dst[2 * i + 1] = narrow<T>(o[n][i][c + 2] * inv);
+                                    }
+                                }
+                            }
+                            if (g == 0 && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq))
+                                a.lse[orow] = paged_lse(m[n][c], sum[n][c]);
+                        } else {
+                            const int64_t prow = s.slot * a.tile_rows + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
+                            float *dst = a.part + prow * D + g * (D / 8);
+                            if (VQ_VSPAN(dst, D / 8, a.part, prows * D, 16)) {
+#pragma unroll
+                                for (int i = 0; i < kMma; i += 2)
+                                    reinterpret_cast<float4 *>(dst)[i / 2] =
+                                        make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
+                            }
+                            if (g == 0 && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
+                                a.ml[prow * 2] = m[n][c];
+                                a.ml[prow * 2 + 1] = sum[n][c];
+                            }
+                        }
+                    }
+            }
+        }
+    }
+    if (tid == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;
+}
+
+}  // namespace vqk

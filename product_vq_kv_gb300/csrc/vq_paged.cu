@@ -14,6 +14,7 @@
 
 #include "vq_encode.h"
 #include "vq_host.h"
+#include "vq_paged_host.h"
 #include "vq_pages.cuh"
 #include "vq_pattn.cuh"
 #include "vq_status.cuh"
@@ -105,6 +106,40 @@ AttnPart simple_part(int sms, int32_t group, int32_t dim, size_t at)
     return p;
 }
 
+// The tensor kernels take fp16 and bf16, head sizes 64, 128 and 256 in
+// sub-vectors of 4 or 8, and pages of 16 tokens or more (the tokens of one
+// matrix instruction lie in one page).
+bool tensor_shape(vq_dtype dtype, int32_t dim, int32_t sub, int32_t page_size)
+{
+    return (dtype == VQ_F16 || dtype == VQ_BF16) && (dim == 64 || dim == 128 || dim == 256) &&
+           (sub == 4 || sub == 8) && page_size >= 16;
+}
+
+// and pages whose rows can be read in vectors.
+bool tensor_layout(const vqk::PagedArgs &a)
+{
+    return (uintptr_t)a.k_codes % 16 == 0 && (uintptr_t)a.v_codes % 16 == 0 && a.page_stride % 16 == 0;
+}
+
+// Rows of an item of the few-row kernel, 8 nt: 8 where every request is known
+// to have no more, or where the accumulators of 16 would not fit the registers.
+int few_nt(int64_t max_new, int32_t group, int32_t dim)
+{
+    return dim == 256 || (max_new > 0 && max_new * group <= 8) ? 1 : 2;
+}
+
+AttnPart few_part(int sms, int32_t group, int32_t dim, int nt, size_t at)
+{
+    AttnPart p;
+    p.blocks = sms * vqh_few_blocks_per_sm(dim, nt);
+    p.gc = group < 8 * nt ? group : 8 * nt;
+    p.gch = (group + p.gc - 1) / p.gc;
+    p.tile_tokens = 8 * nt / p.gc;
+    p.tile_rows = 8 * nt;
+    lay_out(&p, dim, at);
+    return p;
+}
+
 void use_part(vqk::PagedArgs *a, const AttnPart &p, unsigned char *ws)
 {
     a->tile_tokens = p.tile_tokens;
@@ -148,6 +183,18 @@ vq_status launch_simple(const AttnCall &c, const AttnPart &p, unsigned char *ws)
     vqk::paged_attn_simple<T><<<(unsigned)p.blocks, vqk::kUnit, smem, c.stream>>>(a);
     const vq_status s = vqh_launched(c.stream, vqh_status_paged);
     return s != VQ_OK ? s : launch_merge<T>(a, p, c.stream);
+}
+
+template <typename T>
+vq_status launch_tensor(const AttnCall &c, unsigned char *ws)
+{
+    const int nt = few_nt(c.max_new, c.a.group, c.a.dim);
+    const AttnPart few = few_part(c.sms, c.a.group, c.a.dim, nt, 0);
+    vqk::PagedArgs a = c.a;
+    use_part(&a, few, ws);
+    a.cls = 0;
+    const vq_status s = vqh_paged_few(a, c.dtype, nt, few.blocks, c.stream);
+    return s != VQ_OK ? s : launch_merge<T>(a, few, c.stream);
 }
 
 vq_status check_shape(int64_t requests, int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
@@ -240,7 +287,13 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
         check_shape(requests, tokens, heads_q, heads_kv, head_dim, sub_dim, n_centroids, page_size) != VQ_OK)
         return 0;
     const int sms = vqh_device_sms() > 0 ? vqh_device_sms() : 152;
-    return simple_part(sms, heads_q / heads_kv, head_dim, 0).end;
+    const int32_t group = heads_q / heads_kv;
+    size_t need = simple_part(sms, group, head_dim, 0).end;
+    if (tensor_shape(VQ_F16, head_dim, sub_dim, page_size)) {
+        const size_t t = few_part(sms, group, head_dim, few_nt(max_new, group, head_dim), 0).end;
+        if (t > need) need = t;
+    }
+    return need;
 }
 
 vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_new, const int32_t *lens,
@@ -308,6 +361,8 @@ vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_
                                                              sub_dim, n_centroids, page_size))
         return VQ_ERR_INVALID_ARG;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
+    if (tensor_shape(dtype, head_dim, sub_dim, page_size) && tensor_layout(a))
+        return dtype == VQ_F16 ? launch_tensor<__half>(c, ws) : launch_tensor<__nv_bfloat16>(c, ws);
     const AttnPart p = simple_part(c.sms, a.group, head_dim, 0);
     switch (dtype) {
     case VQ_F16: return launch_simple<__half>(c, p, ws);

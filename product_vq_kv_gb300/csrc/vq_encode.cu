@@ -757,7 +757,8 @@ vq_status vq_kernel_status(uint32_t *bits, int32_t clear)
     const bool c = clear != 0;
     if (vqh_status_encode(bits, c) != cudaSuccess || vqh_status_attn(bits, c) != cudaSuccess ||
         vqh_status_scalar(bits, c) != cudaSuccess || vqh_status_append(bits, c) != cudaSuccess ||
-        vqh_status_paged(bits, c) != cudaSuccess || vqh_status_pfew(bits, c) != cudaSuccess)
+        vqh_status_paged(bits, c) != cudaSuccess || vqh_status_pfew(bits, c) != cudaSuccess ||
+        vqh_status_pchunk(bits, c) != cudaSuccess)
         return VQ_ERR_CUDA;
     return VQ_OK;
 }

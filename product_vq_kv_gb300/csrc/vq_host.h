@@ -20,6 +20,7 @@ cudaError_t vqh_status_scalar(uint32_t *bits, bool clear);
 cudaError_t vqh_status_append(uint32_t *bits, bool clear);
 cudaError_t vqh_status_paged(uint32_t *bits, bool clear);
 cudaError_t vqh_status_pfew(uint32_t *bits, bool clear);
+cudaError_t vqh_status_pchunk(uint32_t *bits, bool clear);
 
 // The body of the functions above, for the translation unit's own word.
 #define VQH_STATUS_READER(NAME)                                                      \

@@ -121,11 +121,27 @@ bool tensor_layout(const vqk::PagedArgs &a)
     return (uintptr_t)a.k_codes % 16 == 0 && (uintptr_t)a.v_codes % 16 == 0 && a.page_stride % 16 == 0;
 }
 
-// Rows of an item of the few-row kernel, 8 nt: 8 where every request is known
-// to have no more, or where the accumulators of 16 would not fit the registers.
-int few_nt(int64_t max_new, int32_t group, int32_t dim)
+// Which tensor kernels a call launches: requests of up to `few_tokens` new
+// tokens go to the few-row kernel, the others to the chunk kernel.
+struct TensorPlan {
+    bool few, chunk;
+    int nt;              // the few-row kernel's items have 8 nt rows
+    int32_t few_tokens;
+};
+
+TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_t group, int32_t dim)
 {
-    return dim == 256 || (max_new > 0 && max_new * group <= 8) ? 1 : 2;
+    TensorPlan p{};
+    const int64_t most = max_new > 0 && max_new < tokens ? max_new : tokens;  // new tokens of a request, as far as known
+    // 8 rows where no request has more, or where the accumulators of 16 would not
+    // fit the registers (dim 256)
+    p.nt = dim == 256 || most * group <= 8 ? 1 : 2;
+    // up to two items of rows the few-row kernel rebuilds the cache no more often
+    // than a tile of the chunk kernel would cost
+    p.few_tokens = 16 * p.nt / group > 1 ? 16 * p.nt / group : 1;
+    p.few = requests != 1 || most <= p.few_tokens;
+    p.chunk = most > p.few_tokens;
+    return p;
 }
 
 AttnPart few_part(int sms, int32_t group, int32_t dim, int nt, size_t at)
@@ -138,6 +154,33 @@ AttnPart few_part(int sms, int32_t group, int32_t dim, int nt, size_t at)
     p.tile_rows = 8 * nt;
     lay_out(&p, dim, at);
     return p;
+}
+
+AttnPart chunk_part(int sms, int32_t group, int32_t dim, size_t at)
+{
+    AttnPart p;
+    p.blocks = sms;
+    p.gc = group < 128 ? group : 128;
+    p.gch = (group + p.gc - 1) / p.gc;
+    p.tile_tokens = vqh_chunk_tiles(dim) * (128 / p.gc);
+    p.tile_rows = vqh_chunk_tiles(dim) * 128;
+    lay_out(&p, dim, at);
+    return p;
+}
+
+// The parts of a call's tensor kernels, one behind the other.
+size_t tensor_parts(const TensorPlan &t, int sms, int32_t group, int32_t dim, AttnPart *few, AttnPart *chunk)
+{
+    size_t at = 0;
+    if (t.few) {
+        *few = few_part(sms, group, dim, t.nt, at);
+        at = up256(few->end);
+    }
+    if (t.chunk) {
+        *chunk = chunk_part(sms, group, dim, at);
+        at = up256(chunk->end);
+    }
+    return at;
 }
 
 void use_part(vqk::PagedArgs *a, const AttnPart &p, unsigned char *ws)
@@ -188,13 +231,28 @@ vq_status launch_simple(const AttnCall &c, const AttnPart &p, unsigned char *ws)
 template <typename T>
 vq_status launch_tensor(const AttnCall &c, unsigned char *ws)
 {
-    const int nt = few_nt(c.max_new, c.a.group, c.a.dim);
-    const AttnPart few = few_part(c.sms, c.a.group, c.a.dim, nt, 0);
-    vqk::PagedArgs a = c.a;
-    use_part(&a, few, ws);
-    a.cls = 0;
-    const vq_status s = vqh_paged_few(a, c.dtype, nt, few.blocks, c.stream);
-    return s != VQ_OK ? s : launch_merge<T>(a, few, c.stream);
+    const TensorPlan t = tensor_plan(c.a.requests, c.a.tokens, c.max_new, c.a.group, c.a.dim);
+    AttnPart few, chunk;
+    (void)tensor_parts(t, c.sms, c.a.group, c.a.dim, &few, &chunk);
+    if (t.chunk) {
+        vqk::PagedArgs a = c.a;
+        use_part(&a, chunk, ws);
+        a.cls = t.few ? 2 : 0;
+        a.cls_tokens = t.few_tokens;
+        vq_status s = vqh_paged_chunk(a, c.dtype, chunk.blocks, c.stream);
+        if (s == VQ_OK) s = launch_merge<T>(a, chunk, c.stream);
+        if (s != VQ_OK) return s;
+    }
+    if (t.few) {
+        vqk::PagedArgs a = c.a;
+        use_part(&a, few, ws);
+        a.cls = t.chunk ? 1 : 0;
+        a.cls_tokens = t.few_tokens;
+        vq_status s = vqh_paged_few(a, c.dtype, t.nt, few.blocks, c.stream);
+        if (s == VQ_OK) s = launch_merge<T>(a, few, c.stream);
+        if (s != VQ_OK) return s;
+    }
+    return VQ_OK;
 }
 
 vq_status check_shape(int64_t requests, int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
@@ -290,7 +348,8 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
     const int32_t group = heads_q / heads_kv;
     size_t need = simple_part(sms, group, head_dim, 0).end;
     if (tensor_shape(VQ_F16, head_dim, sub_dim, page_size)) {
-        const size_t t = few_part(sms, group, head_dim, few_nt(max_new, group, head_dim), 0).end;
+        AttnPart few, chunk;
+        const size_t t = tensor_parts(tensor_plan(requests, tokens, max_new, group, head_dim), sms, group, head_dim, &few, &chunk);
         if (t > need) need = t;
     }
     return need;

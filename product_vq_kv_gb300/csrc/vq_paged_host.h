@@ -14,3 +14,8 @@ struct PagedArgs;
 // 1), sub 4 or 8, fp16 or bf16.
 int vqh_few_blocks_per_sm(int32_t dim, int nt);
 vq_status vqh_paged_few(const vqk::PagedArgs &a, vq_dtype dtype, int nt, int blocks, cudaStream_t st);
+
+// Chunks (vq_pchunk.cuh): items of vqh_chunk_tiles tiles of 128 rows; one block
+// an SM; dim 64, 128 or 256, sub 4 or 8, fp16 or bf16.
+int vqh_chunk_tiles(int32_t dim);
+vq_status vqh_paged_chunk(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);

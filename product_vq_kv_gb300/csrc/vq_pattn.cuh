@@ -40,7 +40,7 @@
 namespace vqk {
 
 constexpr int kUnit = 128;       // cached tokens of one unit of work
-constexpr int kStageCu = 512;    // requests + 2 up to which a block keeps cu and lens in shared memory
+constexpr int kStageCu = 512;    // requests + 2 up to which a block keeps cu and lens in shared memory, if it has room
 
 // The note of a split item (rows = 0: none).
 struct PagedNote {
@@ -150,8 +150,16 @@ __device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, const PagedL
 }
 
 // Where a block stands on the line of units.
+template <int STAGE>
+struct PagedStage {
+    int32_t cu[STAGE], lens[STAGE];
+};
+template <>
+struct PagedStage<0> {};
+template <int STAGE = kStageCu>
 struct PagedWalk {
-    int32_t stage_cu[kStageCu], stage_lens[kStageCu];
+    static constexpr int kStage = STAGE;
+    PagedStage<STAGE> stage;
     int64_t scratch[33];
     int64_t total;  // U of one head group
     int64_t u0, u1; // this block's units
@@ -164,8 +172,8 @@ struct PagedWalk {
 
 // Lay the items out and find this block's part (all THREADS threads; w in
 // shared memory).  Returns whether the block has any.
-template <int THREADS>
-__device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk &w, PagedLens &l)
+template <int THREADS, int STAGE>
+__device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> &w, PagedLens &l)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     l.cu = a.cu;
@@ -173,14 +181,16 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk &w, Pag
     l.requests = a.requests;
     l.tile = a.tile_tokens;
     l.tokens = a.tokens;
-    if (a.requests + 2 <= kStageCu) {
-        for (int i = tid; i <= a.requests; i += THREADS) {
-            w.stage_cu[i] = a.cu[i];
-            if (i < a.requests) w.stage_lens[i] = a.lens[i];
+    if constexpr (STAGE > 0) {
+        if (a.requests + 2 <= STAGE) {
+            for (int i = tid; i <= a.requests; i += THREADS) {
+                w.stage.cu[i] = a.cu[i];
+                if (i < a.requests) w.stage.lens[i] = a.lens[i];
+            }
+            l.cu = w.stage.cu;
+            l.lens = w.stage.lens;
+            __syncthreads();
         }
-        l.cu = w.stage_cu;
-        l.lens = w.stage_lens;
-        __syncthreads();
     }
     const int64_t per = (a.items + THREADS - 1) / THREADS;
     const int64_t j0 = tid * per, j1 = j0 + per < a.items ? j0 + per : a.items;
@@ -260,7 +270,8 @@ struct PagedSegment {
 struct PagedCursor {
     int64_t u, u1, j;
     int32_t r, at, hx;
-    __device__ __forceinline__ void init(const PagedWalk &w)
+    template <typename W>
+    __device__ __forceinline__ void init(const W &w)
     {
         u = w.u0;
         u1 = w.u1;
@@ -271,8 +282,9 @@ struct PagedCursor {
     }
     // The next segment; false at the end.  `note` is filled if the block
     // begins an item that it does not finish.
-    __device__ __forceinline__ bool next(const PagedArgs &a, const PagedWalk &w, const PagedLens &l,
-                                         PagedSegment &s, PagedNote &note)
+    template <typename W>
+    __device__ __forceinline__ bool next(const PagedArgs &a, const W &w, const PagedLens &l, PagedSegment &s,
+                                         PagedNote &note)
     {
         if (u >= u1) return false;
         for (;;) {
@@ -354,7 +366,7 @@ constexpr int kSimpleDim = 512;
 template <typename T>
 __global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant__ PagedArgs a)
 {
-    __shared__ PagedWalk w;
+    __shared__ PagedWalk<> w;
     __shared__ float sp[kSimpleRows][kUnit];
     __shared__ float red[kSimpleRows][kUnit / 32];
     __shared__ int64_t spage[kUnit];

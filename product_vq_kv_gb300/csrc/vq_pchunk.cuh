@@ -1,0 +1,605 @@
+// vq_pchunk.cuh -- paged attention of chunks of new tokens (prefill beside a
+// cache, long verification runs): tiles of 128 rows (tokens x query heads of one
+// KV head) on the 5th-generation tensor cores, 16-bit types, head sizes 64, 128
+// and 256, sub-vectors of 4 or 8.
+//
+// Per block of kKeys cached tokens, with the accumulators in tensor memory:
+//   S (128 x kKeys) = Q K^^T     tcgen05.mma, both operands in shared memory
+//   P = 2^(kappa S - m)          one thread per row: its lane of S in registers
+//   O (128 x dim)  += P V^       tcgen05.mma, P from tensor memory (over S)
+// K^ and V^ are rebuilt from their codes into shared memory by four warps that
+// do nothing else, from the conflict-free codebook images of the few-row kernel,
+// a stage ring ahead of the products.  A rebuilt row is stored as 16-byte
+// pieces, piece c of token t at c * 16 kKeys + 16 t: the core matrices (8 rows x
+// 16 bytes) of the unswizzled operand layout, with columns as the contraction
+// index for the keys and tokens for the values, from one way of writing; eight
+// lanes write 128 consecutive bytes, so the writes have no conflict either.
+//
+// What bounds it at dim 128: the products of a block and two tiles are 4 x 512
+// cycles of the tensor pipe; the shared memory moves 2 x 64 KiB for the rebuild,
+// 2 x 64 KiB for Q K^^T and 2 x 32 KiB for P V^, 2560 cycles at 128 bytes a
+// cycle.  Two tiles share each rebuilt block, or the rebuild alone would take as
+// long as the products.  The exponentials (2 x 16384, 32 a cycle) and the rest
+// of the softmax run beside both: while the rows of one tile are at their
+// softmax the tensor pipe works for the other.  At dim 256 one tile's O fills
+// half the tensor memory, so there is one tile and S is double-buffered.
+//
+// The maximum a row's weights refer to follows its scores only when one
+// exceeds it by 2^8; then the row's O is rescaled in tensor memory, after the
+// product before has finished.  Weights are rounded to the input type for the
+// product with V^; their sum takes them unrounded.
+//
+// Roles (13 warps): 0-3 and 4-7 the softmax and output of tile 0 and 1, 8-11
+// rebuild, 12 issues the products.  Every wait is bounded: one that gives up
+// sets the block's abort word and kStatusWaitGaveUp, the others see it and all
+// leave; the issuer first waits (bounded) for its products in flight, and the
+// tensor memory is freed.  The rows not yet written then keep what they held.
+#pragma once
+
+#include "vq_pfew.cuh"
+#include "vq_status.cuh"
+#include "vq_umma.cuh"
+
+namespace vqk {
+
+constexpr int kChunkThreads = 13 * 32;
+constexpr int kChunkStages = 3;
+
+template <int D>
+struct ChunkShape {
+    static constexpr int kTiles = D == 256 ? 1 : 2;
+    static constexpr int kKeys = D == 256 ? 64 : 128;
+    static constexpr int kStageBytes = kKeys * D * 2;
+    static constexpr int kQBytes = 128 * D * 2;  // a tile
+    static constexpr size_t kSmem = (size_t)kTiles * kQBytes + kChunkStages * kStageBytes + 65536;
+    // tensor memory columns
+    static constexpr int kS = D == 256 ? 64 : 128;  // between the two S buffers
+    static constexpr int kO = 256;                  // first column of O of tile 0, tile 1 D further
+};
+
+// Instruction descriptor: kind::f16, fp32 accumulator, 16-bit operands of one
+// type (0: fp16, 1: bf16), M = 128, N = n, A K-major, B K-major or MN-major.
+__host__ __device__ constexpr uint32_t umma_idesc_16(uint32_t bf16, uint32_t n, bool b_mn)
+{
+    return (1u << 4) | (bf16 << 7) | (bf16 << 10) | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// A from tensor memory.
+__device__ __forceinline__ void umma_16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
+// Bounded wait for phase `parity`: false if it gave up or another role did.
+__device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_word)
+{
+    for (int it = 0; it < kWaitPolls; ++it) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(smem_addr(bar)), "r"(parity)
+                     : "memory");
+        if (done) return true;
+        if ((it & 15) == 15 && *abort_word) return false;
+    }
+    *abort_word = 1;
+    raise_status(kStatusWaitGaveUp);
+    return false;
+}
+
+template <typename T, int D, int SUB>
+__global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __grid_constant__ PagedArgs a)
+{
+    using S = ChunkShape<D>;
+    constexpr int NS = D / SUB;
+    constexpr int kTiles = S::kTiles, kKeys = S::kKeys;
+    constexpr int kPieces = D / 8;               // 16-byte pieces of a row
+    constexpr int kSplit = 128 / kKeys;          // rebuilding threads per token
+    constexpr int kMyCodes = NS / kSplit;        // code bytes of one
+    constexpr int kMyVec = kMyCodes < 16 ? kMyCodes : 16;
+    constexpr int kCodeWords = kMyCodes < 4 ? 1 : kMyCodes / 4;
+    constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    extern __shared__ __align__(128) unsigned char chunk_mem[];
+    __shared__ PagedWalk<0> w;
+    __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image, drain;
+    __shared__ uint32_t valid[4][4];  // per key block (mod 4): which tokens are in a page
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile uint32_t abort_word;
+    unsigned char *q_mem = chunk_mem;
+    unsigned char *ring = chunk_mem + (size_t)kTiles * S::kQBytes;
+    unsigned char *k_image = ring + kChunkStages * S::kStageBytes, *v_image = k_image + 32768;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float kNone = __int_as_float(0xff800000);
+    const int tpq = 128 / a.gc;  // tokens of a tile
+
+    if (tid == 0) {
+        for (int i = 0; i < kChunkStages; ++i) {
+            mbar_init(&full[i], 128);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 128);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_done[i], 1);
+        }
+        mbar_init(&image, 128);
+        mbar_init(&drain, 1);
+        abort_word = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    PagedLens l;
+    PagedNote note{};
+    const bool work = paged_plan<kChunkThreads>(a, w, l);  // has barriers for the whole block
+    PagedCursor cur;
+    if (work) cur.init(w);
+    PagedSegment s;
+    // key blocks of a segment
+    auto blocks_of = [&](int32_t *first) {
+        const int32_t k0 = s.it.k_lo + s.begin * kUnit;
+        const int64_t k1 = (int64_t)s.it.k_lo + (int64_t)s.end * kUnit;
+        const int32_t end = k1 < s.it.k_hi ? (int32_t)k1 : s.it.k_hi;
+        *first = k0;
+        return end > k0 ? (end - k0 + kKeys - 1) / kKeys : 1;
+    };
+
+    if (work && warp < 8) {
+        // ------------------------------------------------ softmax and output
+        const int tile = warp >> 2, row = tid & 127;
+        const T *__restrict__ q = static_cast<const T *>(a.q);
+        T *__restrict__ out = static_cast<T *>(a.out);
+        const bool q_vec = (uintptr_t)a.q % 16 == 0 && a.q_stride % 8 == 0;
+        const bool out_vec = (uintptr_t)a.out % 16 == 0;
+        const int64_t q_elems = (a.tokens - 1) * a.q_stride + (int64_t)a.hq * D;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t o_addr = lane_base + S::kO + (kTiles == 2 ? tile * D : 0);
+        uint32_t seen_s[2] = {0, 0};  // phases of s_full that this thread has waited for
+        uint32_t seen_o = 0;          // products P V^ of this tile so far
+        uint32_t block = 0;           // key blocks of the segments so far
+        bool go = tile < kTiles;
+        while (go && cur.next(a, w, l, s, note)) {
+            const int g0 = s.hx % a.gch * a.gc, h = s.hx / a.gch;
+            const int gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
+            const int head0 = h * a.group + g0;
+            int32_t key0;
+            const int nb = blocks_of(&key0);
+            if (tile * tpq >= s.it.ntok) {  // no rows here
+                block += nb;
+                continue;
+            }
+            const int tok_in = tile * tpq + row / gc;
+            const bool mine = row < tpq * gc && tok_in < s.it.ntok;
+            const int64_t tok = s.it.tok0 + (mine ? tok_in : 0);
+            const int head = head0 + (mine ? row % gc : 0);
+            // Q, in core matrices: piece c of row r at c * 2048 + 16 r
+            {
+                const T *src = q + tok * a.q_stride + (int64_t)head * D;
+                const bool ok = mine && VQ_SPAN(src, D, q, q_elems);
+                unsigned char *dst = q_mem + tile * S::kQBytes + row * 16;
+#pragma unroll 8
+                for (int c = 0; c < kPieces; ++c) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (ok) {
+                        if (q_vec) {
+                            v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+                        } else {
+                            const uint16_t *e = reinterpret_cast<const uint16_t *>(src) + 8 * c;
+                            v.x = (uint32_t)__ldg(e) | ((uint32_t)__ldg(e + 1) << 16);
+                            v.y = (uint32_t)__ldg(e + 2) | ((uint32_t)__ldg(e + 3) << 16);
+                            v.z = (uint32_t)__ldg(e + 4) | ((uint32_t)__ldg(e + 5) << 16);
+                            v.w = (uint32_t)__ldg(e + 6) | ((uint32_t)__ldg(e + 7) << 16);
+                        }
+                    }
+                    if (dyn_smem_ok(dst + c * 2048, 16, 16)) *reinterpret_cast<uint4 *>(dst + c * 2048) = v;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                (void)mbar_arrive(&q_full[tile]);
+            }
+            // what this row sees: tokens in (low, lim]
+            const int32_t pos = s.it.pos0 + (mine ? tok_in : tile * tpq);
+            const int32_t lim = pos < s.it.k_hi ? pos : s.it.k_hi - 1;
+            const int64_t low64 = (int64_t)pos - a.window;
+            const int32_t low = a.window == 0 || low64 < -1 ? -1 : (int32_t)low64;
+            // what every row of the tile sees
+            const int32_t pos_first = s.it.pos0 + tile * tpq;
+            const int ntile = s.it.ntok - tile * tpq < tpq ? s.it.ntok - tile * tpq : tpq;
+            const int32_t all_hi = pos_first < s.it.k_hi ? pos_first : s.it.k_hi - 1;
+            const int64_t all_lo = a.window == 0 ? -1 : (int64_t)pos_first + ntile - 1 - a.window;
+
+            float m = kNone, sum = 0.f;
+            for (int j = 0; j < nb; ++j, ++block) {
+                const int buf = kTiles == 2 ? tile : j & 1;
+                if (!__all_sync(0xffffffffu, chunk_wait(&s_full[buf], seen_s[buf] & 1, &abort_word))) {
+                    go = false;
+                    break;
+                }
+                ++seen_s[buf];
+                tc_fence_after();
+                const uint32_t s_addr = lane_base + buf * S::kS;
+                const int32_t k0 = key0 + j * kKeys;
+                uint32_t vm[kKeys / 32];
+                bool whole = k0 + kKeys - 1 <= all_hi && k0 > all_lo;
+#pragma unroll
+                for (int i = 0; i < kKeys / 32; ++i) {
+                    vm[i] = valid[block & 3][i];
+                    whole &= vm[i] == 0xffffffffu;
+                }
+                // first pass: the maximum
+                float top = kNone;
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_load32_async(s_addr + c * 32, v);
+                    tmem_wait_ld(v);
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int32_t key = k0 + c * 32 + i;
+                            const bool ok = key <= lim && key > low && ((vm[c] >> i) & 1u);
+                            v[i] = ok ? v[i] : 0xff800000u;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+                }
+                top *= a.kappa;  // kappa > 0
+                if (__any_sync(0xffffffffu, top > m + kFewSlack)) {
+                    const float f = top > m ? exp2_fast(m - top) : 1.f;
+                    if (top > m) m = top;
+                    sum *= f;
+                    if (j > 0) {
+                        // the product before this block is the seen_o-th
+                        if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
+                            go = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_load32_async(o_addr + c * 32, v);
+                            tmem_wait_ld(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            tmem_store32(o_addr + c * 32, v);
+                        }
+                    }
+                }
+                const float ref = m == kNone ? 0.f : m;  // nothing seen yet: every weight is 0
+                // second pass: weights, over the scores (a 32-column load is
+                // read before the 16 columns of its weights are written below it)
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) {
+                    uint32_t v[32], p[16];
+                    tmem_load32_async(s_addr + c * 32, v);
+                    tmem_wait_ld(v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float x = exp2_fast(fmaf(__uint_as_float(v[i]), a.kappa, -ref));
+                        if (!whole) {
+                            const int32_t key = k0 + c * 32 + i;
+                            const bool ok = key <= lim && key > low && ((vm[c] >> i) & 1u);
+                            x = ok ? x : 0.f;
+                        }
+                        v[i] = __float_as_uint(x);
+                    }
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) part[i & 3] += __uint_as_float(v[i]);
+                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) p[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    tmem_store16(s_addr + c * 16, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                (void)mbar_arrive(&p_full[buf]);
+                ++seen_o;
+            }
+            if (!go) break;
+            if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) break;
+            tc_fence_after();
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t orow = tok * a.hq + head;
+            const int64_t prow = s.slot * a.tile_rows + tile * tpq * gc + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
+            T *dst = out + orow * D;
+            float *pdst = a.part + prow * D;
+            const bool put = mine && (s.whole ? VQ_SPAN(dst, D, out, a.tokens * a.hq * D) : VQ_VSPAN(pdst, D, a.part, prows * D, 16));
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_load32_async(o_addr + c * 32, v);
+                tmem_wait_ld(v);
+                if (!put) continue;
+                if (s.whole) {
+                    if (out_vec) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = pack2<T>(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
+                            reinterpret_cast<uint4 *>(dst)[c * 4 + i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) dst[c * 32 + i] = narrow<T>(__uint_as_float(v[i]) * inv);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4 *>(pdst)[c * 8 + i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            tc_fence_before();
+            if (mine && s.whole && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq)) a.lse[orow] = paged_lse(m, sum);
+            if (mine && !s.whole && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
+                a.ml[prow * 2] = m;
+                a.ml[prow * 2 + 1] = sum;
+            }
+        }
+    } else if (work && warp < 12) {
+        // ------------------------------------------------ rebuild
+        const int me = tid - 256;                 // 0 .. 127
+        const int tk = me % kKeys, part = me / kKeys;  // token of the block, which part of its row
+        const uint32_t copy = (uint32_t)(lane % (64 / SUB)) * (2 * SUB);
+        const uint32_t k_base = smem_addr(k_image) + copy, v_base = smem_addr(v_image) + copy;
+        const int64_t cb_elems = (int64_t)a.hkv * a.nc * SUB;
+        const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
+        uint32_t filled = 0;  // stages filled so far
+        uint32_t block = 0;   // key blocks so far
+        int built = -1;
+        bool go = true;
+        // the four warps meet (bounded, as every wait here)
+        uint32_t met = 0;
+        auto meet = [&]() -> bool {
+            (void)mbar_arrive(&image);
+            return __all_sync(0xffffffffu, chunk_wait(&image, met++ & 1, &abort_word));
+        };
+        while (go && cur.next(a, w, l, s, note)) {
+            const int h = s.hx / a.gch;
+            if (h != built) {
+                // images of this head: only these four warps read them
+                if (!(go = meet())) break;
+                for (int c = me; c < 256; c += 128) {
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const T *all = static_cast<const T *>(kv ? a.vcb : a.kcb);
+                        const T *cb = all + ((int64_t)h * a.nc + c) * SUB;
+                        uint32_t wd[SUB / 2];
+#pragma unroll
+                        for (int i = 0; i < SUB / 2; ++i) wd[i] = 0;
+                        if (c < a.nc && VQ_SPAN(cb, SUB, all, cb_elems)) {
+                            const uint16_t *src = reinterpret_cast<const uint16_t *>(cb);
+#pragma unroll
+                            for (int i = 0; i < SUB / 2; ++i) wd[i] = (uint32_t)__ldg(src + 2 * i) | ((uint32_t)__ldg(src + 2 * i + 1) << 16);
+                        }
+                        unsigned char *img = kv ? v_image : k_image;
+#pragma unroll
+                        for (int k = 0; k < 64 / SUB; ++k) {
+                            unsigned char *dst = img + c * 128 + ((c + k) % (64 / SUB)) * (2 * SUB);
+                            if (!dyn_smem_ok(dst, 2 * SUB, 2 * SUB)) continue;
+                            if constexpr (SUB == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+                            else *reinterpret_cast<uint2 *>(dst) = make_uint2(wd[0], wd[1]);
+                        }
+                    }
+                }
+                if (!(go = meet())) break;
+                built = h;
+            }
+            int32_t key0;
+            const int nb = blocks_of(&key0);
+            const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.it.pos0 - a.window;  // no row sees at or below
+            // this thread's token of block j: its page, or -1
+            auto page_of = [&](int j) -> int64_t {
+                const int64_t t = (int64_t)key0 + (int64_t)j * kKeys + tk;
+                if (j >= nb || t >= s.it.k_hi || t <= none_lo) return -1;
+                return paged_page(a, cur.r, (int32_t)t);
+            };
+            auto load = [&](int j, int64_t pg, uint32_t (&kc)[kCodeWords], uint32_t (&vc)[kCodeWords]) {
+                if (pg < 0) return;
+                const int32_t off = (key0 + j * kKeys + tk) & ((1 << a.page_shift) - 1);
+                const int64_t base = pg * a.page_stride + (((int64_t)h << a.page_shift) + off) * NS + part * kMyCodes;
+                if (!span_ok(a.k_codes + base, kMyCodes, a.k_codes, code_bytes, kMyVec) ||
+                    !span_ok(a.v_codes + base, kMyCodes, a.v_codes, code_bytes, kMyVec))
+                    return;
+#pragma unroll
+                for (int i = 0; i < kMyCodes / kMyVec; ++i) {
+                    uint32_t x[(kMyVec + 3) / 4], y[(kMyVec + 3) / 4];
+                    load_codes<kMyVec>(a.k_codes + base + i * kMyVec, x);
+                    load_codes<kMyVec>(a.v_codes + base + i * kMyVec, y);
+#pragma unroll
+                    for (int k = 0; k < (kMyVec + 3) / 4; ++k) {
+                        kc[i * (kMyVec / 4) + k] = x[k];
+                        vc[i * (kMyVec / 4) + k] = y[k];
+                    }
+                }
+            };
+            // rebuild this thread's part of its token into the next stage
+            auto fill = [&](uint32_t base, bool live, const uint32_t (&codes)[kCodeWords]) -> bool {
+                const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
+                if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
+                unsigned char *dst = ring + st * S::kStageBytes + (part * (kPieces / kSplit)) * (16 * kKeys) + tk * 16;
+#pragma unroll
+                for (int c = 0; c < kPieces / kSplit; ++c) {
+                    uint32_t v[4] = {0, 0, 0, 0};
+                    if (live) {
+                        if constexpr (SUB == 8) {
+                            image_row<8>(base, code_at(codes, c), v);
+                        } else {
+                            uint32_t lo[2], hi[2];
+                            image_row<4>(base, code_at(codes, 2 * c), lo);
+                            image_row<4>(base, code_at(codes, 2 * c + 1), hi);
+                            v[0] = lo[0];
+                            v[1] = lo[1];
+                            v[2] = hi[0];
+                            v[3] = hi[1];
+                        }
+                    }
+                    if (dyn_smem_ok(dst + c * (16 * kKeys), 16, 16))
+                        *reinterpret_cast<uint4 *>(dst + c * (16 * kKeys)) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                (void)mbar_arrive(&full[st]);
+                ++filled;
+                return true;
+            };
+            // keys of the next block: also which tokens there are
+            auto fill_keys = [&](int64_t pg, const uint32_t (&codes)[kCodeWords]) -> bool {
+                const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
+                const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
+                if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
+                // the words that lay here, four blocks back, have been read: the stage
+                // just released, three fills back, comes after that block's weights
+                if (lane == 0 && part == 0) valid[block & 3][tk / 32] = have;
+                ++block;
+                return fill(k_base, pg >= 0, codes);
+            };
+            uint32_t kc1[kCodeWords] = {}, kc2[kCodeWords] = {}, vc0[kCodeWords] = {}, vc1[kCodeWords] = {}, vc2[kCodeWords] = {};
+            int64_t pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3;
+            load(0, pg0, kc2, vc0);
+            load(1, pg1, kc1, vc1);
+            go = fill_keys(pg0, kc2);
+            for (int j = 0; go && j < nb; ++j) {
+                load(j + 2, pg2, kc2, vc2);
+                pg3 = page_of(j + 3);
+                if (j + 1 < nb) go = fill_keys(pg1, kc1);
+                if (go) go = fill(v_base, pg0 >= 0, vc0);
+                pg0 = pg1;
+                pg1 = pg2;
+                pg2 = pg3;
+#pragma unroll
+                for (int i = 0; i < kCodeWords; ++i) {
+                    kc1[i] = kc2[i];
+                    vc0[i] = vc1[i];
+                    vc1[i] = vc2[i];
+                }
+            }
+        }
+    } else if (work && lane == 0) {
+        // ------------------------------------------------ the products
+        const uint32_t idesc_s = umma_idesc_16(kBf16, kKeys, false), idesc_o = umma_idesc_16(kBf16, D, true);
+        const uint32_t q_addr = smem_addr(q_mem), ring_addr = smem_addr(ring);
+        uint32_t taken = 0;  // stages taken so far
+        uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        bool go = true;
+        // wait for the next stage in ring order; its index
+        auto take = [&](uint32_t *st) -> bool {
+            *st = taken % kChunkStages;
+            const uint32_t round = taken / kChunkStages;
+            ++taken;
+            return chunk_wait(&full[*st], round & 1, &abort_word);
+        };
+        auto scores = [&](int tile, int buf, uint32_t st) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                umma_16_ss(tmem + buf * S::kS, umma_smem_desc(q_addr + tile * S::kQBytes + k * 4096, 2048, 128),
+                           umma_smem_desc(ring_addr + st * S::kStageBytes + k * (32 * kKeys), 16 * kKeys, 128), idesc_s, k > 0);
+            umma_commit(&s_full[buf]);
+        };
+        auto values = [&](int tile, int buf, uint32_t st, bool add) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+                umma_16_ts(tmem + S::kO + (kTiles == 2 ? tile * D : 0), tmem + buf * S::kS + k * 8,
+                           umma_smem_desc(ring_addr + st * S::kStageBytes + k * 256, 128, 16 * kKeys), idesc_o, add || k > 0);
+            umma_commit(&o_done[tile]);
+        };
+        while (go && cur.next(a, w, l, s, note)) {
+            int32_t key0;
+            const int nb = blocks_of(&key0);
+            const int tiles = kTiles == 2 && s.it.ntok > tpq ? 2 : 1;
+            for (int t = 0; go && t < tiles; ++t) go = chunk_wait(&q_full[t], n_q[t]++ & 1, &abort_word);
+            uint32_t ks, vs;
+            if (!go || !take(&ks)) break;
+            tc_fence_after();
+            for (int t = 0; t < tiles; ++t) scores(t, kTiles == 2 ? t : 0, ks);
+            umma_commit(&empty[ks]);
+            for (int j = 0; j < nb; ++j) {
+                const bool more = j + 1 < nb;
+                if (more && !(go = take(&ks))) break;
+                if (kTiles == 1 && more) {
+                    // the other S buffer: its weights were taken by the product before
+                    tc_fence_after();
+                    scores(0, (j + 1) & 1, ks);
+                    umma_commit(&empty[ks]);
+                }
+                if (!(go = take(&vs))) break;
+                for (int t = 0; t < tiles; ++t) {
+                    const int buf = kTiles == 2 ? t : j & 1;
+                    if (!(go = chunk_wait(&p_full[buf], n_p[buf]++ & 1, &abort_word))) break;
+                    tc_fence_after();
+                    values(t, buf, vs, j > 0);
+                    // products run in the order of issue: the weights, which lie over
+                    // S, are read before the next scores are written there
+                    if (kTiles == 2 && more) scores(t, t, ks);
+                }
+                if (!go) break;
+                umma_commit(&empty[vs]);
+                if (kTiles == 2 && more) umma_commit(&empty[ks]);
+            }
+        }
+        // products in flight write tensor memory and read shared memory: let them end
+        umma_commit(&drain);
+        (void)mbar_wait(&drain, 0);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+    // the cursor of warp 0 (tile 0 is in every segment) has seen all the notes
+    if (tid == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;
+}
+
+}  // namespace vqk

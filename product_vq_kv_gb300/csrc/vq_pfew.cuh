@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
     constexpr int kRowsMax = 8 * NT;
     static_assert(SUB == 4 || SUB == 8, "sub-vectors of 4 or 8");
     extern __shared__ __align__(128) unsigned char few_mem[];
-    __shared__ PagedWalk w;
+    __shared__ PagedWalk<> w;
     __shared__ float wm[kFewWarps][kRowsMax], wl[kFewWarps][kRowsMax];
     unsigned char *k_image = few_mem, *v_image = few_mem + 32768;
     float *slots = reinterpret_cast<float *>(few_mem + 65536);

@@ -342,12 +342,18 @@ __device__ __forceinline__ float paged_lse(float m, float l)
     return l == 0.f ? __int_as_float(0xff800000) : kLn2 * (m + log2f(l));
 }
 
-// Page of cached token t; -1 if the entry is no page.
-__device__ __forceinline__ int64_t paged_page(const PagedArgs &a, int32_t r, int32_t t)
+// Block table entry of cached token t, whatever it holds.
+__device__ __forceinline__ int32_t paged_entry(const PagedArgs &a, int32_t r, int32_t t)
 {
     const int32_t *e = a.table + (int64_t)r * a.max_blocks + (t >> a.page_shift);
     if (!VQ_SPAN(e, 1, a.table, (int64_t)a.requests * a.max_blocks)) return -1;
-    const int32_t pg = __ldg(e);
+    return __ldg(e);
+}
+
+// Page of cached token t; -1 if the entry is no page.
+__device__ __forceinline__ int64_t paged_page(const PagedArgs &a, int32_t r, int32_t t)
+{
+    const int32_t pg = paged_entry(a, r, t);
     return pg >= 0 && pg < a.num_pages ? pg : -1;
 }
 

@@ -108,6 +108,13 @@ __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Bounded wait for phase `parity`: false if it gave up or another role did.
 __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_word)
 {
@@ -255,7 +262,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             const int32_t all_hi = pos_first < s.it.k_hi ? pos_first : s.it.k_hi - 1;
             const int64_t all_lo = a.window == 0 ? -1 : (int64_t)pos_first + ntile - 1 - a.window;
 
-            float m = kNone, sum = 0.f;
+            float m = kNone;
+            float2 sum2 = make_float2(0.f, 0.f);  // over the even and the odd tokens
             for (int j = 0; j < nb; ++j, ++block) {
                 const int buf = kTiles == 2 ? tile : j & 1;
                 if (!__all_sync(0xffffffffu, chunk_wait(&s_full[buf], seen_s[buf] & 1, &abort_word))) {
@@ -266,36 +274,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 tc_fence_after();
                 const uint32_t s_addr = lane_base + buf * S::kS;
                 const int32_t k0 = key0 + j * kKeys;
-                uint32_t vm[kKeys / 32];
                 bool whole = k0 + kKeys - 1 <= all_hi && k0 > all_lo;
 #pragma unroll
-                for (int i = 0; i < kKeys / 32; ++i) {
-                    vm[i] = valid[block & 3][i];
-                    whole &= vm[i] == 0xffffffffu;
-                }
+                for (int i = 0; i < kKeys / 32; ++i) whole &= valid[block & 3][i] == 0xffffffffu;
+                // bit i: this row sees token 32 c + i of the block
+                auto seen_bits = [&](int c) -> uint32_t {
+                    const int32_t hi = lim - (k0 + 32 * c), lo = low - (k0 + 32 * c);
+                    const uint32_t upto = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+                    const uint32_t past = lo < 0 ? 0u : lo >= 31 ? 0xffffffffu : (2u << lo) - 1u;
+                    return upto & ~past & valid[block & 3][c];
+                };
                 // first pass: the maximum
                 float top = kNone;
+                if (whole) {  // the same for all rows of the tile
+                    float tops[4] = {kNone, kNone, kNone, kNone};
 #pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_load32_async(s_addr + c * 32, v);
-                    tmem_wait_ld(v);
-                    if (!whole) {
+                    for (int c = 0; c < kKeys / 64; ++c) {
+                        uint32_t v[64];
+                        tmem_load32_async(s_addr + c * 64, v);
+                        tmem_load32_async(s_addr + c * 64 + 32, v + 32);
+                        tmem_wait_ld(v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int32_t key = k0 + c * 32 + i;
-                            const bool ok = key <= lim && key > low && ((vm[c] >> i) & 1u);
-                            v[i] = ok ? v[i] : 0xff800000u;
-                        }
+                        for (int i = 0; i < 64; i += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tops[k] = max3(tops[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
                     }
+                    top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_load32_async(s_addr + c * 32, v);
+                        const uint32_t bits = seen_bits(c);
+                        tmem_wait_ld(v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+                        for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
+                    }
                 }
                 top *= a.kappa;  // kappa > 0
                 if (__any_sync(0xffffffffu, top > m + kFewSlack)) {
                     const float f = top > m ? exp2_fast(m - top) : 1.f;
                     if (top > m) m = top;
-                    sum *= f;
+                    sum2 = make_float2(sum2.x * f, sum2.y * f);
                     if (j > 0) {
                         // the product before this block is the seen_o-th
                         if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
@@ -315,32 +336,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     }
                 }
                 const float ref = m == kNone ? 0.f : m;  // nothing seen yet: every weight is 0
-                // second pass: weights, over the scores (a 32-column load is
-                // read before the 16 columns of its weights are written below it)
+                // second pass: weights, over the scores (a load of columns is read
+                // before the half as many columns of its weights are written below it)
+                auto weights = [&](const uint32_t *v, uint32_t *p, int n) {
 #pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c) {
-                    uint32_t v[32], p[16];
-                    tmem_load32_async(s_addr + c * 32, v);
-                    tmem_wait_ld(v);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float x = exp2_fast(fmaf(__uint_as_float(v[i]), a.kappa, -ref));
-                        if (!whole) {
-                            const int32_t key = k0 + c * 32 + i;
-                            const bool ok = key <= lim && key > low && ((vm[c] >> i) & 1u);
-                            x = ok ? x : 0.f;
-                        }
-                        v[i] = __float_as_uint(x);
+                    for (int i = 0; i < n; i += 2) {
+                        float2 x = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+                                           make_float2(a.kappa, a.kappa), make_float2(-ref, -ref));
+                        x.x = exp2_fast(x.x);
+                        x.y = exp2_fast(x.y);
+                        sum2 = add2_rn(sum2, x);
+                        p[i / 2] = pack2<T>(x.x, x.y);
                     }
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                };
+                if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) part[i & 3] += __uint_as_float(v[i]);
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    for (int c = 0; c < kKeys / 64; ++c) {
+                        uint32_t v[64], p[32];
+                        tmem_load32_async(s_addr + c * 64, v);
+                        tmem_load32_async(s_addr + c * 64 + 32, v + 32);
+                        tmem_wait_ld(v);
+                        weights(v, p, 64);
+                        tmem_store32(s_addr + c * 32, p);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        uint32_t v[32], p[16];
+                        tmem_load32_async(s_addr + c * 32, v);
+                        const uint32_t bits = seen_bits(c);
+                        tmem_wait_ld(v);
+                        // a score that is not seen is left out as -inf: weight 0, whatever it was
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) p[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    tmem_store16(s_addr + c * 16, p);
+                        for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : 0xff800000u;
+                        weights(v, p, 32);
+                        tmem_store16(s_addr + c * 16, p);
+                    }
                 }
                 tmem_wait_st();
+                if (kTiles == 1 && j > 0) {
+                    // a wait tells only the last two phases of a barrier apart.  With two
+                    // tiles the scores of this block come after the product before in the
+                    // issuer's order, with one they come before it: so wait for each
+                    // product in turn (it has run beside this block's softmax)
+                    if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
+                        go = false;
+                        break;
+                    }
+                }
                 tc_fence_before();
                 (void)mbar_arrive(&p_full[buf]);
                 ++seen_o;
@@ -348,6 +391,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             if (!go) break;
             if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) break;
             tc_fence_after();
+            const float sum = sum2.x + sum2.y;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int64_t orow = tok * a.hq + head;
             const int64_t prow = s.slot * a.tile_rows + tile * tpq * gc + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
@@ -439,16 +483,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             int32_t key0;
             const int nb = blocks_of(&key0);
             const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.it.pos0 - a.window;  // no row sees at or below
-            // this thread's token of block j: its page, or -1
-            auto page_of = [&](int j) -> int64_t {
+            // this thread's token of block j: its page entry, or -1; checked when
+            // it is used (a check here would wait for the load)
+            auto page_of = [&](int j) -> int32_t {
                 const int64_t t = (int64_t)key0 + (int64_t)j * kKeys + tk;
                 if (j >= nb || t >= s.it.k_hi || t <= none_lo) return -1;
-                return paged_page(a, cur.r, (int32_t)t);
+                return paged_entry(a, cur.r, (int32_t)t);
             };
-            auto load = [&](int j, int64_t pg, uint32_t (&kc)[kCodeWords], uint32_t (&vc)[kCodeWords]) {
-                if (pg < 0) return;
+            auto load = [&](int j, int32_t &pg, uint32_t (&kc)[kCodeWords], uint32_t (&vc)[kCodeWords]) {
+                if (pg < 0 || pg >= a.num_pages) {
+                    pg = -1;
+                    return;
+                }
                 const int32_t off = (key0 + j * kKeys + tk) & ((1 << a.page_shift) - 1);
-                const int64_t base = pg * a.page_stride + (((int64_t)h << a.page_shift) + off) * NS + part * kMyCodes;
+                const int64_t base = (int64_t)pg * a.page_stride + (((int64_t)h << a.page_shift) + off) * NS + part * kMyCodes;
                 if (!span_ok(a.k_codes + base, kMyCodes, a.k_codes, code_bytes, kMyVec) ||
                     !span_ok(a.v_codes + base, kMyCodes, a.v_codes, code_bytes, kMyVec))
                     return;
@@ -469,24 +517,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
                 if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
                 unsigned char *dst = ring + st * S::kStageBytes + (part * (kPieces / kSplit)) * (16 * kKeys) + tk * 16;
+                // eight pieces at a time, so that their loads overlap
+                constexpr int kBatch = 8;
 #pragma unroll
-                for (int c = 0; c < kPieces / kSplit; ++c) {
-                    uint32_t v[4] = {0, 0, 0, 0};
-                    if (live) {
+                for (int c0 = 0; c0 < kPieces / kSplit; c0 += kBatch) {
+                    uint32_t v[kBatch][4];
+#pragma unroll
+                    for (int c = 0; c < kBatch; ++c) {
                         if constexpr (SUB == 8) {
-                            image_row<8>(base, code_at(codes, c), v);
+                            image_row<8>(base, code_at(codes, c0 + c), v[c]);
                         } else {
                             uint32_t lo[2], hi[2];
-                            image_row<4>(base, code_at(codes, 2 * c), lo);
-                            image_row<4>(base, code_at(codes, 2 * c + 1), hi);
-                            v[0] = lo[0];
-                            v[1] = lo[1];
-                            v[2] = hi[0];
-                            v[3] = hi[1];
+                            image_row<4>(base, code_at(codes, 2 * (c0 + c)), lo);
+                            image_row<4>(base, code_at(codes, 2 * (c0 + c) + 1), hi);
+                            v[c][0] = lo[0];
+                            v[c][1] = lo[1];
+                            v[c][2] = hi[0];
+                            v[c][3] = hi[1];
                         }
                     }
-                    if (dyn_smem_ok(dst + c * (16 * kKeys), 16, 16))
-                        *reinterpret_cast<uint4 *>(dst + c * (16 * kKeys)) = make_uint4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+                    for (int c = 0; c < kBatch; ++c) {
+                        unsigned char *to = dst + (c0 + c) * (16 * kKeys);
+                        if (dyn_smem_ok(to, 16, 16))
+                            *reinterpret_cast<uint4 *>(to) = live ? make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]) : make_uint4(0, 0, 0, 0);
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 (void)mbar_arrive(&full[st]);
@@ -494,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return true;
             };
             // keys of the next block: also which tokens there are
-            auto fill_keys = [&](int64_t pg, const uint32_t (&codes)[kCodeWords]) -> bool {
+            auto fill_keys = [&](int32_t pg, const uint32_t (&codes)[kCodeWords]) -> bool {
                 const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
                 const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
                 if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
@@ -505,7 +560,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return fill(k_base, pg >= 0, codes);
             };
             uint32_t kc1[kCodeWords] = {}, kc2[kCodeWords] = {}, vc0[kCodeWords] = {}, vc1[kCodeWords] = {}, vc2[kCodeWords] = {};
-            int64_t pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3;
+            int32_t pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3;
             load(0, pg0, kc2, vc0);
             load(1, pg1, kc1, vc1);
             go = fill_keys(pg0, kc2);

@@ -276,10 +276,13 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                 if (unit >= s.end) return -1;
                 const int32_t k0 = first_of(unit);
                 if (k0 >= s.it.k_hi || k0 + 15 <= none_lo) return -1;
-                return (int32_t)paged_page(a, cur.r, k0);
+                return paged_entry(a, cur.r, k0);  // checked when it is used: a check here would wait for the load
             };
-            auto load = [&](int unit, int32_t pg, uint32_t (&kc)[2][KW], uint32_t (&vc)[4][VW]) {
-                if (pg < 0) return;  // warp-uniform
+            auto load = [&](int unit, int32_t &pg, uint32_t (&kc)[2][KW], uint32_t (&vc)[4][VW]) {
+                if (pg < 0 || pg >= a.num_pages) {  // warp-uniform
+                    pg = -1;
+                    return;
+                }
                 const int32_t off = first_of(unit) & ((1 << a.page_shift) - 1);
                 const int64_t base = (int64_t)pg * a.page_stride + (((int64_t)h << a.page_shift) + off) * NS;
                 if (!span_ok(a.k_codes + base, 16 * NS, a.k_codes, code_bytes, NS < 16 ? NS : 16) ||

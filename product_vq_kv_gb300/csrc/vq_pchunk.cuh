@@ -554,29 +554,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
                 if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
                 // the words that lay here, four blocks back, have been read: the stage
-                // just released, three fills back, comes after that block's weights
+                // just released held keys or values of a block at most three back, and
+                // was released after the weights of an earlier one
                 if (lane == 0 && part == 0) valid[block & 3][tk / 32] = have;
                 ++block;
                 return fill(k_base, pg >= 0, codes);
             };
-            uint32_t kc1[kCodeWords] = {}, kc2[kCodeWords] = {}, vc0[kCodeWords] = {}, vc1[kCodeWords] = {}, vc2[kCodeWords] = {};
-            int32_t pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3;
-            load(0, pg0, kc2, vc0);
-            load(1, pg1, kc1, vc1);
-            go = fill_keys(pg0, kc2);
+            // stage order: with two tiles K0 V0 K1 V1 .., with one K0 K1 V0 K2 V1 ..
+            // (there the scores of a block are issued before the product of the one
+            // before).  Codes are loaded two blocks ahead.
+            constexpr int kAhead = kTiles == 2 ? 0 : 1;  // blocks the keys are ahead of the values
+            uint32_t kc[3][kCodeWords] = {}, vc[3][kCodeWords] = {};
+            int32_t pg[3], pg_next;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) pg[j] = page_of(j);
+            load(0, pg[0], kc[0], vc[0]);
+            load(1, pg[1], kc[1], vc[1]);
+            if (kAhead) go = fill_keys(pg[0], kc[0]);
             for (int j = 0; go && j < nb; ++j) {
-                load(j + 2, pg2, kc2, vc2);
-                pg3 = page_of(j + 3);
-                if (j + 1 < nb) go = fill_keys(pg1, kc1);
-                if (go) go = fill(v_base, pg0 >= 0, vc0);
-                pg0 = pg1;
-                pg1 = pg2;
-                pg2 = pg3;
+                load(j + 2, pg[2], kc[2], vc[2]);
+                pg_next = page_of(j + 3);
+                if (j + kAhead < nb) go = fill_keys(pg[kAhead], kc[kAhead]);
+                if (go) go = fill(v_base, pg[0] >= 0, vc[0]);
+                pg[0] = pg[1];
+                pg[1] = pg[2];
+                pg[2] = pg_next;
 #pragma unroll
                 for (int i = 0; i < kCodeWords; ++i) {
-                    kc1[i] = kc2[i];
-                    vc0[i] = vc1[i];
-                    vc1[i] = vc2[i];
+                    kc[0][i] = kc[1][i];
+                    kc[1][i] = kc[2][i];
+                    vc[0][i] = vc[1][i];
+                    vc[1][i] = vc[2][i];
                 }
             }
         }
@@ -620,26 +628,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             umma_commit(&empty[ks]);
             for (int j = 0; j < nb; ++j) {
                 const bool more = j + 1 < nb;
-                if (more && !(go = take(&ks))) break;
-                if (kTiles == 1 && more) {
-                    // the other S buffer: its weights were taken by the product before
+                if (kTiles == 1) {
+                    if (more) {
+                        // into the other S buffer: its weights were taken by the product before
+                        if (!(go = take(&ks))) break;
+                        tc_fence_after();
+                        scores(0, (j + 1) & 1, ks);
+                        umma_commit(&empty[ks]);
+                    }
+                    if (!(go = take(&vs) && chunk_wait(&p_full[j & 1], n_p[j & 1]++ & 1, &abort_word))) break;
                     tc_fence_after();
-                    scores(0, (j + 1) & 1, ks);
-                    umma_commit(&empty[ks]);
+                    values(0, j & 1, vs, j > 0);
+                    umma_commit(&empty[vs]);
+                    continue;
                 }
                 if (!(go = take(&vs))) break;
                 for (int t = 0; t < tiles; ++t) {
-                    const int buf = kTiles == 2 ? t : j & 1;
-                    if (!(go = chunk_wait(&p_full[buf], n_p[buf]++ & 1, &abort_word))) break;
+                    if (!(go = chunk_wait(&p_full[t], n_p[t]++ & 1, &abort_word))) break;
                     tc_fence_after();
-                    values(t, buf, vs, j > 0);
-                    // products run in the order of issue: the weights, which lie over
-                    // S, are read before the next scores are written there
-                    if (kTiles == 2 && more) scores(t, t, ks);
+                    values(t, t, vs, j > 0);
+                    if (t == tiles - 1) umma_commit(&empty[vs]);
+                    if (more) {
+                        if (t == 0) {
+                            if (!(go = take(&ks))) break;
+                            tc_fence_after();
+                        }
+                        // products run in the order of issue: the weights, which lie over
+                        // S, are read before the next scores are written there
+                        scores(t, t, ks);
+                        if (t == tiles - 1) umma_commit(&empty[ks]);
+                    }
                 }
                 if (!go) break;
-                umma_commit(&empty[vs]);
-                if (kTiles == 2 && more) umma_commit(&empty[ks]);
             }
         }
         // products in flight write tensor memory and read shared memory: let them end

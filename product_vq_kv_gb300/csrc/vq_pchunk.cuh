@@ -64,10 +64,14 @@ __host__ __device__ constexpr uint32_t umma_idesc_16(uint32_t bf16, uint32_t n, 
     return (1u << 4) | (bf16 << 7) | (bf16 << 10) | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// The products are issued by one elected lane of a warp whose lanes all run the
+// same code: operands that are the same in all of them can stay in uniform
+// registers, which is where the instruction takes them from (issued under
+// `if (lane == 0)` each cost about 85 cycles, most of it moves).
 __device__ __forceinline__ void umma_16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
@@ -75,9 +79,17 @@ __device__ __forceinline__ void umma_16_ss(uint32_t d, uint64_t a, uint64_t b, u
 // A from tensor memory.
 __device__ __forceinline__ void umma_16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
                  "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// umma_commit by the lane that elect.sync picks (the same one each time).
+__device__ __forceinline__ void umma_commit_elected(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
                  : "memory");
 }
 
@@ -588,44 +600,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 }
             }
         }
-    } else if (work && lane == 0) {
+    } else if (work) {
         // ------------------------------------------------ the products
         const uint32_t idesc_s = umma_idesc_16(kBf16, kKeys, false), idesc_o = umma_idesc_16(kBf16, D, true);
         const uint32_t q_addr = smem_addr(q_mem), ring_addr = smem_addr(ring);
         uint32_t taken = 0;  // stages taken so far
         uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
         bool go = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, chunk_wait(bar, parity, &abort_word));
+        };
         // wait for the next stage in ring order; its index
         auto take = [&](uint32_t *st) -> bool {
             *st = taken % kChunkStages;
             const uint32_t round = taken / kChunkStages;
             ++taken;
-            return chunk_wait(&full[*st], round & 1, &abort_word);
+            return wait(&full[*st], round & 1);
         };
+        // operand descriptors differ in the address field alone (16-byte units,
+        // no carry out of it below 256 KiB): one addition each
+        const uint64_t q_desc = umma_smem_desc(q_addr, 2048, 128);
+        const uint64_t k_desc = umma_smem_desc(ring_addr, 16 * kKeys, 128);
+        const uint64_t v_desc = umma_smem_desc(ring_addr, 128, 16 * kKeys);
         auto scores = [&](int tile, int buf, uint32_t st) {
+            const uint64_t qd = q_desc + (uint32_t)(tile * (S::kQBytes / 16)), kd = k_desc + st * (uint32_t)(S::kStageBytes / 16);
+            const uint32_t d = tmem + buf * S::kS;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                umma_16_ss(tmem + buf * S::kS, umma_smem_desc(q_addr + tile * S::kQBytes + k * 4096, 2048, 128),
-                           umma_smem_desc(ring_addr + st * S::kStageBytes + k * (32 * kKeys), 16 * kKeys, 128), idesc_s, k > 0);
-            umma_commit(&s_full[buf]);
+            for (int k = 0; k < D / 16; ++k) umma_16_ss(d, qd + k * 256, kd + k * (2 * kKeys), idesc_s, k > 0);
+            umma_commit_elected(&s_full[buf]);
         };
         auto values = [&](int tile, int buf, uint32_t st, bool add) {
+            const uint64_t vd = v_desc + st * (uint32_t)(S::kStageBytes / 16);
+            const uint32_t d = tmem + S::kO + (kTiles == 2 ? tile * D : 0), p = tmem + buf * S::kS;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-                umma_16_ts(tmem + S::kO + (kTiles == 2 ? tile * D : 0), tmem + buf * S::kS + k * 8,
-                           umma_smem_desc(ring_addr + st * S::kStageBytes + k * 256, 128, 16 * kKeys), idesc_o, add || k > 0);
-            umma_commit(&o_done[tile]);
+            for (int k = 0; k < kKeys / 16; ++k) umma_16_ts(d, p + k * 8, vd + k * 16, idesc_o, add || k > 0);
+            umma_commit_elected(&o_done[tile]);
         };
         while (go && cur.next(a, w, l, s, note)) {
             int32_t key0;
             const int nb = blocks_of(&key0);
             const int tiles = kTiles == 2 && s.it.ntok > tpq ? 2 : 1;
-            for (int t = 0; go && t < tiles; ++t) go = chunk_wait(&q_full[t], n_q[t]++ & 1, &abort_word);
+            for (int t = 0; go && t < tiles; ++t) go = wait(&q_full[t], n_q[t]++ & 1);
             uint32_t ks, vs;
             if (!go || !take(&ks)) break;
             tc_fence_after();
             for (int t = 0; t < tiles; ++t) scores(t, kTiles == 2 ? t : 0, ks);
-            umma_commit(&empty[ks]);
+            umma_commit_elected(&empty[ks]);
             for (int j = 0; j < nb; ++j) {
                 const bool more = j + 1 < nb;
                 if (kTiles == 1) {
@@ -634,20 +654,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         if (!(go = take(&ks))) break;
                         tc_fence_after();
                         scores(0, (j + 1) & 1, ks);
-                        umma_commit(&empty[ks]);
+                        umma_commit_elected(&empty[ks]);
                     }
-                    if (!(go = take(&vs) && chunk_wait(&p_full[j & 1], n_p[j & 1]++ & 1, &abort_word))) break;
+                    if (!(go = take(&vs) && wait(&p_full[j & 1], n_p[j & 1]++ & 1))) break;
                     tc_fence_after();
                     values(0, j & 1, vs, j > 0);
-                    umma_commit(&empty[vs]);
+                    umma_commit_elected(&empty[vs]);
                     continue;
                 }
                 if (!(go = take(&vs))) break;
                 for (int t = 0; t < tiles; ++t) {
-                    if (!(go = chunk_wait(&p_full[t], n_p[t]++ & 1, &abort_word))) break;
+                    if (!(go = wait(&p_full[t], n_p[t]++ & 1))) break;
                     tc_fence_after();
                     values(t, t, vs, j > 0);
-                    if (t == tiles - 1) umma_commit(&empty[vs]);
+                    if (t == tiles - 1) umma_commit_elected(&empty[vs]);
                     if (more) {
                         if (t == 0) {
                             if (!(go = take(&ks))) break;
@@ -656,14 +676,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         // products run in the order of issue: the weights, which lie over
                         // S, are read before the next scores are written there
                         scores(t, t, ks);
-                        if (t == tiles - 1) umma_commit(&empty[ks]);
+                        if (t == tiles - 1) umma_commit_elected(&empty[ks]);
                     }
                 }
                 if (!go) break;
             }
         }
         // products in flight write tensor memory and read shared memory: let them end
-        umma_commit(&drain);
+        umma_commit_elected(&drain);
         (void)mbar_wait(&drain, 0);
     }
     __syncwarp();

@@ -29,8 +29,11 @@
 // product before has finished.  Weights are rounded to the input type for the
 // product with V^; their sum takes them unrounded.
 //
-// Roles (13 warps): 0-3 and 4-7 the softmax and output of tile 0 and 1, 8-11
-// rebuild, 12 issues the products.  Every wait is bounded: one that gives up
+// Roles (16 warps): 0-3 and 4-7 the softmax and output of tile 0 and 1, 8-11
+// rebuild, 12 issues the products, 13 walks the segments, 14-15
+// only fill the warpgroup (the register
+// split below is by warpgroups: 2 x 160 + 96 + 96 registers of each four threads,
+// the 4 x 128 that the block is launched with).  Every wait is bounded: one that gives up
 // sets the block's abort word and kStatusWaitGaveUp, the others see it and all
 // leave; the issuer first waits (bounded) for its products in flight, and the
 // tensor memory is freed.  The rows not yet written then keep what they held.
@@ -42,7 +45,7 @@
 
 namespace vqk {
 
-constexpr int kChunkThreads = 13 * 32;
+constexpr int kChunkThreads = 16 * 32;
 constexpr int kChunkStages = 3;
 
 template <int D>
@@ -127,10 +130,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+// Polls of a wait: about a second, where a block's longest is microseconds.
+constexpr int kChunkPolls = 1 << 18;
+
 // Bounded wait for phase `parity`: false if it gave up or another role did.
 __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_word)
 {
-    for (int it = 0; it < kWaitPolls; ++it) {
+    for (int it = 0; it < kChunkPolls; ++it) {
         uint32_t done;
         asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
@@ -144,6 +150,17 @@ __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volat
     raise_status(kStatusWaitGaveUp);
     return false;
 }
+
+// One segment as the roles take it from shared memory.
+struct ChunkSeg {
+    int64_t tok0, slot;
+    int32_t ntok, pos0, k_hi;
+    int32_t key0, nb;  // first key, key blocks
+    int32_t h, head0, gc;
+    int32_t r;
+    int32_t whole;     // written to the output, else to the workspace
+    int32_t live;      // 0: no more segments
+};
 
 template <typename T, int D, int SUB>
 __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __grid_constant__ PagedArgs a)
@@ -159,7 +176,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     extern __shared__ __align__(128) unsigned char chunk_mem[];
     __shared__ PagedWalk<0> w;
-    __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image, drain;
+    __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image, drain, seg_full[2], seg_empty[2];
+    __shared__ ChunkSeg segs[2];
     __shared__ uint32_t valid[4][4];  // per key block (mod 4): which tokens are in a page
     __shared__ uint32_t tmem_slot;
     __shared__ volatile uint32_t abort_word;
@@ -182,6 +200,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             mbar_init(&p_full[i], 128);
             mbar_init(&o_done[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], 4 * kTiles + 5);  // a lane of each softmax, rebuild and product warp
+        }
         mbar_init(&image, 128);
         mbar_init(&drain, 1);
         abort_word = 0;
@@ -197,19 +219,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     const uint32_t tmem = tmem_slot;
 
     PagedLens l;
-    PagedNote note{};
     const bool work = paged_plan<kChunkThreads>(a, w, l);  // has barriers for the whole block
-    PagedCursor cur;
-    if (work) cur.init(w);
-    PagedSegment s;
-    // key blocks of a segment
-    auto blocks_of = [&](int32_t *first) {
-        const int32_t k0 = s.it.k_lo + s.begin * kUnit;
-        const int64_t k1 = (int64_t)s.it.k_lo + (int64_t)s.end * kUnit;
-        const int32_t end = k1 < s.it.k_hi ? (int32_t)k1 : s.it.k_hi;
-        *first = k0;
-        return end > k0 ? (end - k0 + kKeys - 1) / kKeys : 1;
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    else if (warp < 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    // the next segment of a role's warp: seg_n counts those it has taken; false at
+    // the end (or if a wait gave up)
+    auto next_seg = [&](uint32_t &seg_n, ChunkSeg &s) -> bool {
+        const uint32_t i = seg_n & 1;
+        if (!__all_sync(0xffffffffu, chunk_wait(&seg_full[i], (seg_n >> 1) & 1, &abort_word))) return false;
+        s = segs[i];
+        __syncwarp();
+        if (lane == 0) (void)mbar_arrive(&seg_empty[i]);
+        ++seg_n;
+        return s.live != 0;
     };
+    uint32_t seg_n = 0;
+    ChunkSeg s;
 
     if (work && warp < 8) {
         // ------------------------------------------------ softmax and output
@@ -225,20 +251,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         uint32_t seen_o = 0;          // products P V^ of this tile so far
         uint32_t block = 0;           // key blocks of the segments so far
         bool go = tile < kTiles;
-        while (go && cur.next(a, w, l, s, note)) {
-            const int g0 = s.hx % a.gch * a.gc, h = s.hx / a.gch;
-            const int gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
-            const int head0 = h * a.group + g0;
-            int32_t key0;
-            const int nb = blocks_of(&key0);
-            if (tile * tpq >= s.it.ntok) {  // no rows here
-                block += nb;
+        while (go && next_seg(seg_n, s)) {
+            const int gc = s.gc;
+            if (tile * tpq >= s.ntok) {  // no rows here
+                block += s.nb;
                 continue;
             }
             const int tok_in = tile * tpq + row / gc;
-            const bool mine = row < tpq * gc && tok_in < s.it.ntok;
-            const int64_t tok = s.it.tok0 + (mine ? tok_in : 0);
-            const int head = head0 + (mine ? row % gc : 0);
+            const bool mine = row < tpq * gc && tok_in < s.ntok;
+            const int64_t tok = s.tok0 + (mine ? tok_in : 0);
+            const int head = s.head0 + (mine ? row % gc : 0);
             // Q, in core matrices: piece c of row r at c * 2048 + 16 r
             {
                 const T *src = q + tok * a.q_stride + (int64_t)head * D;
@@ -264,19 +286,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 (void)mbar_arrive(&q_full[tile]);
             }
             // what this row sees: tokens in (low, lim]
-            const int32_t pos = s.it.pos0 + (mine ? tok_in : tile * tpq);
-            const int32_t lim = pos < s.it.k_hi ? pos : s.it.k_hi - 1;
+            const int32_t pos = s.pos0 + (mine ? tok_in : tile * tpq);
+            const int32_t lim = pos < s.k_hi ? pos : s.k_hi - 1;
             const int64_t low64 = (int64_t)pos - a.window;
             const int32_t low = a.window == 0 || low64 < -1 ? -1 : (int32_t)low64;
             // what every row of the tile sees
-            const int32_t pos_first = s.it.pos0 + tile * tpq;
-            const int ntile = s.it.ntok - tile * tpq < tpq ? s.it.ntok - tile * tpq : tpq;
-            const int32_t all_hi = pos_first < s.it.k_hi ? pos_first : s.it.k_hi - 1;
+            const int32_t pos_first = s.pos0 + tile * tpq;
+            const int ntile = s.ntok - tile * tpq < tpq ? s.ntok - tile * tpq : tpq;
+            const int32_t all_hi = pos_first < s.k_hi ? pos_first : s.k_hi - 1;
             const int64_t all_lo = a.window == 0 ? -1 : (int64_t)pos_first + ntile - 1 - a.window;
 
             float m = kNone;
             float2 sum2 = make_float2(0.f, 0.f);  // over the even and the odd tokens
-            for (int j = 0; j < nb; ++j, ++block) {
+            for (int j = 0; j < s.nb; ++j, ++block) {
                 const int buf = kTiles == 2 ? tile : j & 1;
                 if (!__all_sync(0xffffffffu, chunk_wait(&s_full[buf], seen_s[buf] & 1, &abort_word))) {
                     go = false;
@@ -285,7 +307,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 ++seen_s[buf];
                 tc_fence_after();
                 const uint32_t s_addr = lane_base + buf * S::kS;
-                const int32_t k0 = key0 + j * kKeys;
+                const int32_t k0 = s.key0 + j * kKeys;
                 bool whole = k0 + kKeys - 1 <= all_hi && k0 > all_lo;
 #pragma unroll
                 for (int i = 0; i < kKeys / 32; ++i) whole &= valid[block & 3][i] == 0xffffffffu;
@@ -296,24 +318,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     const uint32_t past = lo < 0 ? 0u : lo >= 31 ? 0xffffffffu : (2u << lo) - 1u;
                     return upto & ~past & valid[block & 3][c];
                 };
-                // first pass: the maximum
-                float top = kNone;
-                if (whole) {  // the same for all rows of the tile
-                    float tops[4] = {kNone, kNone, kNone, kNone};
+                // scores to weights, two at a time; adds them up
+                auto weights = [&](const uint32_t *v, uint32_t *p, int n, float ref, float2 &add) {
 #pragma unroll
-                    for (int c = 0; c < kKeys / 64; ++c) {
-                        uint32_t v[64];
-                        tmem_load32_async(s_addr + c * 64, v);
-                        tmem_load32_async(s_addr + c * 64 + 32, v + 32);
+                    for (int i = 0; i < n; i += 2) {
+                        float2 x = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+                                           make_float2(a.kappa, a.kappa), make_float2(-ref, -ref));
+                        x.x = exp2_fast(x.x);
+                        x.y = exp2_fast(x.y);
+                        add = add2_rn(add, x);
+                        p[i / 2] = pack2<T>(x.x, x.y);
+                    }
+                };
+                bool done = false;
+                if (whole && j > 0) {  // the same for all rows of the tile
+                    // one pass with the maximum so far, kept if no score of the warp's
+                    // rows exceeds it by more than the slack; the scores still stand then
+                    uint32_t p[kKeys / 2];
+                    float tops[4] = {kNone, kNone, kNone, kNone};
+                    float2 add = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_load32_async(s_addr + c * 32, v);
                         tmem_wait_ld(v);
 #pragma unroll
-                        for (int i = 0; i < 64; i += 8)
+                        for (int i = 0; i < 32; i += 8)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 tops[k] = max3(tops[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+                        weights(v, p + c * 16, 32, m, add);
                     }
-                    top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
-                } else {
+                    const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.kappa;
+                    if (!__any_sync(0xffffffffu, top > m + kFewSlack || m == kNone)) {
+                        done = true;
+                        sum2 = add2_rn(sum2, add);
+#pragma unroll
+                        for (int c = 0; c < kKeys / 32; ++c) tmem_store16(s_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(p + c * 16));
+                    }
+                }
+                if (!done) {
+                    // first the maximum, then the weights
+                    float top = kNone;
 #pragma unroll 1
                     for (int c = 0; c < kKeys / 32; ++c) {
                         uint32_t v[32];
@@ -323,55 +369,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 #pragma unroll
                         for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
                     }
-                }
-                top *= a.kappa;  // kappa > 0
-                if (__any_sync(0xffffffffu, top > m + kFewSlack)) {
-                    const float f = top > m ? exp2_fast(m - top) : 1.f;
-                    if (top > m) m = top;
-                    sum2 = make_float2(sum2.x * f, sum2.y * f);
-                    if (j > 0) {
-                        // the product before this block is the seen_o-th
-                        if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
-                            go = false;
-                            break;
+                    top *= a.kappa;  // kappa > 0
+                    // a row rises for its own scores alone, so that what it computes does
+                    // not depend on the rows beside it; the others are scaled by 1
+                    const bool rise = top > m + kFewSlack;
+                    if (__any_sync(0xffffffffu, rise)) {
+                        const float f = rise ? exp2_fast(m - top) : 1.f;
+                        if (rise) m = top;
+                        sum2 = make_float2(sum2.x * f, sum2.y * f);
+                        if (j > 0) {
+                            // the product before this block is the seen_o-th
+                            if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
+                                go = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t v[32];
+                                tmem_load32_async(o_addr + c * 32, v);
+                                tmem_wait_ld(v);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                                tmem_store32(o_addr + c * 32, v);
+                            }
                         }
-                        tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            tmem_load32_async(o_addr + c * 32, v);
-                            tmem_wait_ld(v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                            tmem_store32(o_addr + c * 32, v);
-                        }
                     }
-                }
-                const float ref = m == kNone ? 0.f : m;  // nothing seen yet: every weight is 0
-                // second pass: weights, over the scores (a load of columns is read
-                // before the half as many columns of its weights are written below it)
-                auto weights = [&](const uint32_t *v, uint32_t *p, int n) {
-#pragma unroll
-                    for (int i = 0; i < n; i += 2) {
-                        float2 x = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
-                                           make_float2(a.kappa, a.kappa), make_float2(-ref, -ref));
-                        x.x = exp2_fast(x.x);
-                        x.y = exp2_fast(x.y);
-                        sum2 = add2_rn(sum2, x);
-                        p[i / 2] = pack2<T>(x.x, x.y);
-                    }
-                };
-                if (whole) {
-#pragma unroll
-                    for (int c = 0; c < kKeys / 64; ++c) {
-                        uint32_t v[64], p[32];
-                        tmem_load32_async(s_addr + c * 64, v);
-                        tmem_load32_async(s_addr + c * 64 + 32, v + 32);
-                        tmem_wait_ld(v);
-                        weights(v, p, 64);
-                        tmem_store32(s_addr + c * 32, p);
-                    }
-                } else {
+                    const float ref = m == kNone ? 0.f : m;  // nothing seen yet: every weight is 0
+                    float2 add = make_float2(0.f, 0.f);
+                    // (a load of 32 columns is read before the 16 columns of its weights
+                    // are written below it)
 #pragma unroll 1
                     for (int c = 0; c < kKeys / 32; ++c) {
                         uint32_t v[32], p[16];
@@ -381,9 +408,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         // a score that is not seen is left out as -inf: weight 0, whatever it was
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : 0xff800000u;
-                        weights(v, p, 32);
+                        weights(v, p, 32, ref, add);
                         tmem_store16(s_addr + c * 16, p);
                     }
+                    sum2 = add2_rn(sum2, add);
                 }
                 tmem_wait_st();
                 if (kTiles == 1 && j > 0) {
@@ -461,8 +489,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             (void)mbar_arrive(&image);
             return __all_sync(0xffffffffu, chunk_wait(&image, met++ & 1, &abort_word));
         };
-        while (go && cur.next(a, w, l, s, note)) {
-            const int h = s.hx / a.gch;
+        while (go && next_seg(seg_n, s)) {
+            const int h = s.h;
             if (h != built) {
                 // images of this head: only these four warps read them
                 if (!(go = meet())) break;
@@ -492,15 +520,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 if (!(go = meet())) break;
                 built = h;
             }
-            int32_t key0;
-            const int nb = blocks_of(&key0);
-            const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.it.pos0 - a.window;  // no row sees at or below
+            const int32_t key0 = s.key0;
+            const int nb = s.nb;
+            const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.pos0 - a.window;  // no row sees at or below
             // this thread's token of block j: its page entry, or -1; checked when
             // it is used (a check here would wait for the load)
             auto page_of = [&](int j) -> int32_t {
                 const int64_t t = (int64_t)key0 + (int64_t)j * kKeys + tk;
-                if (j >= nb || t >= s.it.k_hi || t <= none_lo) return -1;
-                return paged_entry(a, cur.r, (int32_t)t);
+                if (j >= nb || t >= s.k_hi || t <= none_lo) return -1;
+                return paged_entry(a, s.r, (int32_t)t);
             };
             auto load = [&](int j, int32_t &pg, uint32_t (&kc)[kCodeWords], uint32_t (&vc)[kCodeWords]) {
                 if (pg < 0 || pg >= a.num_pages) {
@@ -600,7 +628,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 }
             }
         }
-    } else if (work) {
+    } else if (work && warp == 12) {
         // ------------------------------------------------ the products
         const uint32_t idesc_s = umma_idesc_16(kBf16, kKeys, false), idesc_o = umma_idesc_16(kBf16, D, true);
         const uint32_t q_addr = smem_addr(q_mem), ring_addr = smem_addr(ring);
@@ -636,10 +664,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             for (int k = 0; k < kKeys / 16; ++k) umma_16_ts(d, p + k * 8, vd + k * 16, idesc_o, add || k > 0);
             umma_commit_elected(&o_done[tile]);
         };
-        while (go && cur.next(a, w, l, s, note)) {
-            int32_t key0;
-            const int nb = blocks_of(&key0);
-            const int tiles = kTiles == 2 && s.it.ntok > tpq ? 2 : 1;
+        while (go && next_seg(seg_n, s)) {
+            const int nb = s.nb;
+            const int tiles = kTiles == 2 && s.ntok > tpq ? 2 : 1;
             for (int t = 0; go && t < tiles; ++t) go = wait(&q_full[t], n_q[t]++ & 1);
             uint32_t ks, vs;
             if (!go || !take(&ks)) break;
@@ -685,16 +712,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         // products in flight write tensor memory and read shared memory: let them end
         umma_commit_elected(&drain);
         (void)mbar_wait(&drain, 0);
+    } else if (work && warp == 13) {
+        // ------------------------------------------------ the segments
+        PagedCursor cur;
+        cur.init(w);
+        PagedSegment seg;
+        PagedNote note{};
+        bool more = true;
+        for (uint32_t n = 0; more; ++n) {
+            const uint32_t i = n & 1;
+            more = cur.next(a, w, l, seg, note);
+            if (n >= 2 && !__all_sync(0xffffffffu, chunk_wait(&seg_empty[i], ((n >> 1) - 1) & 1, &abort_word))) break;
+            if (lane == 0) {
+                ChunkSeg &to = segs[i];
+                to.live = more;
+                if (more) {
+                    const int g0 = seg.hx % a.gch * a.gc;
+                    to.h = seg.hx / a.gch;
+                    to.gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
+                    to.head0 = to.h * a.group + g0;
+                    to.tok0 = seg.it.tok0;
+                    to.slot = seg.slot;
+                    to.ntok = seg.it.ntok;
+                    to.pos0 = seg.it.pos0;
+                    to.k_hi = seg.it.k_hi;
+                    to.r = cur.r;
+                    to.whole = seg.whole;
+                    const int32_t k0 = seg.it.k_lo + seg.begin * kUnit;
+                    const int64_t k1 = (int64_t)seg.it.k_lo + (int64_t)seg.end * kUnit;
+                    const int32_t end = k1 < seg.it.k_hi ? (int32_t)k1 : seg.it.k_hi;
+                    to.key0 = k0;
+                    to.nb = end > k0 ? (end - k0 + kKeys - 1) / kKeys : 1;
+                }
+                (void)mbar_arrive(&seg_full[i]);
+            }
+            __syncwarp();
+        }
+        if (lane == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;
+    } else if (!work && warp == 13 && lane == 0) {
+        if (VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = PagedNote{};
     }
-    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 12) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
-    // the cursor of warp 0 (tile 0 is in every segment) has seen all the notes
-    if (tid == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;
 }
 
 }  // namespace vqk

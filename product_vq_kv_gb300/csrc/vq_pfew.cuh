@@ -348,12 +348,15 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                float top = fmaxf(fmaxf(st[n][c], st[n][c + 2]), m[n][c]);
+                                float top = fmaxf(st[n][c], st[n][c + 2]);
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                                const float f = top == m[n][c] ? 1.f : exp2_fast(m[n][c] - top);
-                                m[n][c] = top;
+                                // a row rises for its own scores alone, so that what it
+                                // computes does not depend on the rows beside it
+                                const bool up = top > m[n][c] + kFewSlack;
+                                const float f = up ? exp2_fast(m[n][c] - top) : 1.f;
+                                if (up) m[n][c] = top;
                                 sum[n][c] *= f;
 #pragma unroll
                                 for (int i = 0; i < kMma; ++i) {

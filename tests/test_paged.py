@@ -452,6 +452,15 @@ def test_attention_rows_stay_apart(vq, shape, new):
     assert torch.isnan(out[~mask]).all() and torch.isnan(lse[~mask]).all()
 
 
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[2], SHAPES[4]])
+@pytest.mark.parametrize("new", [1, 18])
+def test_attention_many_requests(vq, shape, new):
+    """More short requests than blocks: every block takes several in a row."""
+    hq, hkv, dim, sub, n_c, page, dtype = shape
+    c = Cache(13, [new + i % 23 for i in range(450)], hq, hkv, dim, sub, n_c, page, dtype)
+    check_attention(vq, c, [new] * 450)
+
+
 def test_attention_scale_and_repeat(vq):
     """An explicit scale; two calls give the same bits; a dirty workspace does not matter."""
     c = Cache(10, [3000, 20, 700], 8, 2, 128, 8, 256, 16, "bf16")

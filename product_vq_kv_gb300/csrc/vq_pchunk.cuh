@@ -22,7 +22,9 @@
 // long as the products.  The exponentials (2 x 16384, 32 a cycle) and the rest
 // of the softmax run beside both: while the rows of one tile are at their
 // softmax the tensor pipe works for the other.  At dim 256 one tile's O fills
-// half the tensor memory, so there is one tile and S is double-buffered.
+// half the tensor memory, so there is one tile, S is double-buffered and Q lies in
+// tensor memory too: 1024 cycles of products a block of 64 keys, 1536 of shared
+// memory.
 //
 // The maximum a row's weights refer to follows its scores only when one
 // exceeds it by 2^8; then the row's O is rescaled in tensor memory, after the
@@ -46,18 +48,22 @@
 namespace vqk {
 
 constexpr int kChunkThreads = 16 * 32;
-constexpr int kChunkStages = 3;
 
 template <int D>
 struct ChunkShape {
     static constexpr int kTiles = D == 256 ? 1 : 2;
     static constexpr int kKeys = D == 256 ? 64 : 128;
+    // tensor memory columns: two S buffers from 0, O of tile 0 from 256, O of tile 1
+    // D further; with one tile S and O leave 128, which hold its Q (the products
+    // Q K^^T then read half as much shared memory, and there are more stages)
+    static constexpr int kS = kKeys;  // between the two S buffers
+    static constexpr int kO = 256;
+    static constexpr bool kQTmem = D == 256;
+    static constexpr int kQCol = 128;
+    static constexpr int kStages = D == 64 ? 6 : D == 128 ? 3 : 5;
     static constexpr int kStageBytes = kKeys * D * 2;
-    static constexpr int kQBytes = 128 * D * 2;  // a tile
-    static constexpr size_t kSmem = (size_t)kTiles * kQBytes + kChunkStages * kStageBytes + 65536;
-    // tensor memory columns
-    static constexpr int kS = D == 256 ? 64 : 128;  // between the two S buffers
-    static constexpr int kO = 256;                  // first column of O of tile 0, tile 1 D further
+    static constexpr int kQBytes = kQTmem ? 0 : 128 * D * 2;  // a tile
+    static constexpr size_t kSmem = (size_t)kTiles * kQBytes + kStages * kStageBytes + 65536;
 };
 
 // Instruction descriptor: kind::f16, fp32 accumulator, 16-bit operands of one
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 {
     using S = ChunkShape<D>;
     constexpr int NS = D / SUB;
-    constexpr int kTiles = S::kTiles, kKeys = S::kKeys;
+    constexpr int kTiles = S::kTiles, kKeys = S::kKeys, kChunkStages = S::kStages;
     constexpr int kPieces = D / 8;               // 16-byte pieces of a row
     constexpr int kSplit = 128 / kKeys;          // rebuilding threads per token
     constexpr int kMyCodes = NS / kSplit;        // code bytes of one
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     __shared__ PagedWalk<0> w;
     __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image, drain, seg_full[2], seg_empty[2];
     __shared__ ChunkSeg segs[2];
-    __shared__ uint32_t valid[4][4];  // per key block (mod 4): which tokens are in a page
+    __shared__ uint32_t valid[8][4];  // per key block (mod 8): which tokens are in a page
     __shared__ uint32_t tmem_slot;
     __shared__ volatile uint32_t abort_word;
     unsigned char *q_mem = chunk_mem;
@@ -261,13 +267,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             const bool mine = row < tpq * gc && tok_in < s.ntok;
             const int64_t tok = s.tok0 + (mine ? tok_in : 0);
             const int head = s.head0 + (mine ? row % gc : 0);
-            // Q, in core matrices: piece c of row r at c * 2048 + 16 r
+            // Q: in tensor memory 16-bit pairs by column, in shared memory core
+            // matrices: piece c of row r at c * 2048 + 16 r
             {
                 const T *src = q + tok * a.q_stride + (int64_t)head * D;
                 const bool ok = mine && VQ_SPAN(src, D, q, q_elems);
-                unsigned char *dst = q_mem + tile * S::kQBytes + row * 16;
-#pragma unroll 8
-                for (int c = 0; c < kPieces; ++c) {
+                auto piece = [&](int c) {
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (ok) {
                         if (q_vec) {
@@ -280,9 +285,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                             v.w = (uint32_t)__ldg(e + 6) | ((uint32_t)__ldg(e + 7) << 16);
                         }
                     }
-                    if (dyn_smem_ok(dst + c * 2048, 16, 16)) *reinterpret_cast<uint4 *>(dst + c * 2048) = v;
+                    return v;
+                };
+                if constexpr (S::kQTmem) {
+#pragma unroll 1
+                    for (int c = 0; c < kPieces; c += 8) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 x = piece(c + i);
+                            v[4 * i] = x.x;
+                            v[4 * i + 1] = x.y;
+                            v[4 * i + 2] = x.z;
+                            v[4 * i + 3] = x.w;
+                        }
+                        tmem_store32(lane_base + S::kQCol + c * 4, v);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                } else {
+                    unsigned char *dst = q_mem + tile * S::kQBytes + row * 16;
+#pragma unroll 8
+                    for (int c = 0; c < kPieces; ++c) {
+                        const uint4 v = piece(c);
+                        if (dyn_smem_ok(dst + c * 2048, 16, 16)) *reinterpret_cast<uint4 *>(dst + c * 2048) = v;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 (void)mbar_arrive(&q_full[tile]);
             }
             // what this row sees: tokens in (low, lim]
@@ -310,13 +339,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 const int32_t k0 = s.key0 + j * kKeys;
                 bool whole = k0 + kKeys - 1 <= all_hi && k0 > all_lo;
 #pragma unroll
-                for (int i = 0; i < kKeys / 32; ++i) whole &= valid[block & 3][i] == 0xffffffffu;
+                for (int i = 0; i < kKeys / 32; ++i) whole &= valid[block & 7][i] == 0xffffffffu;
                 // bit i: this row sees token 32 c + i of the block
                 auto seen_bits = [&](int c) -> uint32_t {
                     const int32_t hi = lim - (k0 + 32 * c), lo = low - (k0 + 32 * c);
                     const uint32_t upto = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
                     const uint32_t past = lo < 0 ? 0u : lo >= 31 ? 0xffffffffu : (2u << lo) - 1u;
-                    return upto & ~past & valid[block & 3][c];
+                    return upto & ~past & valid[block & 7][c];
                 };
                 // scores to weights, two at a time; adds them up
                 auto weights = [&](const uint32_t *v, uint32_t *p, int n, float ref, float2 &add) {
@@ -593,10 +622,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
                 const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
                 if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
-                // the words that lay here, four blocks back, have been read: the stage
-                // just released held keys or values of a block at most three back, and
-                // was released after the weights of an earlier one
-                if (lane == 0 && part == 0) valid[block & 3][tk / 32] = have;
+                // the words that lay here, eight blocks back, have been read: the stage
+                // just released held keys or values of a block at most four back, and
+                // was released after the weights of the one before that
+                if (lane == 0 && part == 0) valid[block & 7][tk / 32] = have;
                 ++block;
                 return fill(k_base, pg >= 0, codes);
             };
@@ -654,7 +683,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             const uint64_t qd = q_desc + (uint32_t)(tile * (S::kQBytes / 16)), kd = k_desc + st * (uint32_t)(S::kStageBytes / 16);
             const uint32_t d = tmem + buf * S::kS;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) umma_16_ss(d, qd + k * 256, kd + k * (2 * kKeys), idesc_s, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+                if constexpr (S::kQTmem) umma_16_ts(d, tmem + S::kQCol + k * 8, kd + k * (2 * kKeys), idesc_s, k > 0);
+                else umma_16_ss(d, qd + k * 256, kd + k * (2 * kKeys), idesc_s, k > 0);
+            }
             umma_commit_elected(&s_full[buf]);
         };
         auto values = [&](int tile, int buf, uint32_t st, bool add) {

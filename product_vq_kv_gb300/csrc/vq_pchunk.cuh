@@ -7,8 +7,8 @@
 //   S (128 x kKeys) = Q K^^T     tcgen05.mma, both operands in shared memory
 //   P = 2^(kappa S - m)          one thread per row: its lane of S in registers
 //   O (128 x dim)  += P V^       tcgen05.mma, P from tensor memory (over S)
-// K^ and V^ are rebuilt from their codes into shared memory by four warps that
-// do nothing else, from the conflict-free codebook images of the few-row kernel,
+// K^ and V^ are rebuilt from their codes into shared memory by warps that do
+// nothing else, from the conflict-free codebook images of the few-row kernel,
 // a stage ring ahead of the products.  A rebuilt row is stored as 16-byte
 // pieces, piece c of token t at c * 16 kKeys + 16 t: the core matrices (8 rows x
 // 16 bytes) of the unswizzled operand layout, with columns as the contraction
@@ -32,7 +32,7 @@
 // product with V^; their sum takes them unrounded.
 //
 // Roles (16 warps): 0-3 and 4-7 the softmax and output of tile 0 and 1, 8-11
-// rebuild, 12 issues the products, 13 walks the segments, 14-15
+// rebuild (with one tile 4-7 too), 12 issues the products, 13 walks the segments, 14-15
 // only fill the warpgroup (the register
 // split below is by warpgroups: 2 x 160 + 96 + 96 registers of each four threads,
 // the 4 x 128 that the block is launched with).  Every wait is bounded: one that gives up
@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     constexpr int NS = D / SUB;
     constexpr int kTiles = S::kTiles, kKeys = S::kKeys, kChunkStages = S::kStages;
     constexpr int kPieces = D / 8;               // 16-byte pieces of a row
-    constexpr int kSplit = 128 / kKeys;          // rebuilding threads per token
+    constexpr int kRebuild = kTiles == 2 ? 128 : 256;  // rebuilding threads: with one tile warps 4-7 are free for it
+    constexpr int kSplit = kRebuild / kKeys;     // of them per token
     constexpr int kMyCodes = NS / kSplit;        // code bytes of one
     constexpr int kMyVec = kMyCodes < 16 ? kMyCodes : 16;
     constexpr int kCodeWords = kMyCodes < 4 ? 1 : kMyCodes / 4;
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 
     if (tid == 0) {
         for (int i = 0; i < kChunkStages; ++i) {
-            mbar_init(&full[i], 128);
+            mbar_init(&full[i], kRebuild);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -208,9 +209,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 4 * kTiles + 5);  // a lane of each softmax, rebuild and product warp
+            mbar_init(&seg_empty[i], 13);  // a lane of each softmax, rebuild and product warp
         }
-        mbar_init(&image, 128);
+        mbar_init(&image, kRebuild);
         mbar_init(&drain, 1);
         abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     uint32_t seg_n = 0;
     ChunkSeg s;
 
-    if (work && warp < 8) {
+    if (work && warp < 4 * kTiles) {
         // ------------------------------------------------ softmax and output
         const int tile = warp >> 2, row = tid & 127;
         const T *__restrict__ q = static_cast<const T *>(a.q);
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         uint32_t seen_s[2] = {0, 0};  // phases of s_full that this thread has waited for
         uint32_t seen_o = 0;          // products P V^ of this tile so far
         uint32_t block = 0;           // key blocks of the segments so far
-        bool go = tile < kTiles;
+        bool go = true;
         while (go && next_seg(seg_n, s)) {
             const int gc = s.gc;
             if (tile * tpq >= s.ntok) {  // no rows here
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         }
     } else if (work && warp < 12) {
         // ------------------------------------------------ rebuild
-        const int me = tid - 256;                 // 0 .. 127
+        const int me = tid - 128 * kTiles;        // 0 .. kRebuild - 1
         const int tk = me % kKeys, part = me / kKeys;  // token of the block, which part of its row
         const uint32_t copy = (uint32_t)(lane % (64 / SUB)) * (2 * SUB);
         const uint32_t k_base = smem_addr(k_image) + copy, v_base = smem_addr(v_image) + copy;
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         uint32_t block = 0;   // key blocks so far
         int built = -1;
         bool go = true;
-        // the four warps meet (bounded, as every wait here)
+        // the rebuilding warps meet (bounded, as every wait here)
         uint32_t met = 0;
         auto meet = [&]() -> bool {
             (void)mbar_arrive(&image);
@@ -521,9 +522,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         while (go && next_seg(seg_n, s)) {
             const int h = s.h;
             if (h != built) {
-                // images of this head: only these four warps read them
+                // images of this head: only these warps read them
                 if (!(go = meet())) break;
-                for (int c = me; c < 256; c += 128) {
+                for (int c = me; c < 256; c += kRebuild) {
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         const T *all = static_cast<const T *>(kv ? a.vcb : a.kcb);
@@ -587,9 +588,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
                 unsigned char *dst = ring + st * S::kStageBytes + (part * (kPieces / kSplit)) * (16 * kKeys) + tk * 16;
                 // eight pieces at a time, so that their loads overlap
-                constexpr int kBatch = 8;
+                constexpr int kMyPieces = kPieces / kSplit, kBatch = kMyPieces < 8 ? kMyPieces : 8;
 #pragma unroll
-                for (int c0 = 0; c0 < kPieces / kSplit; c0 += kBatch) {
+                for (int c0 = 0; c0 < kMyPieces; c0 += kBatch) {
                     uint32_t v[kBatch][4];
 #pragma unroll
                     for (int c = 0; c < kBatch; ++c) {

@@ -175,15 +175,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     constexpr int NS = D / SUB;
     constexpr int kTiles = S::kTiles, kKeys = S::kKeys, kChunkStages = S::kStages;
     constexpr int kPieces = D / 8;               // 16-byte pieces of a row
-    constexpr int kRebuild = kTiles == 2 ? 128 : 256;  // rebuilding threads: with one tile warps 4-7 are free for it
-    constexpr int kSplit = kRebuild / kKeys;     // of them per token
-    constexpr int kMyCodes = NS / kSplit;        // code bytes of one
+    // With one tile warps 4-7 are free to rebuild too: four warps the keys, four the
+    // values, each at its own pace (280 -> 241 us at 2048 tokens on 8192 cached).
+    // With two tiles the four warps fill stage after stage: two for each kind take
+    // twice as long for a stage, and three stages do not hide that (273 -> 287 us).
+    constexpr bool kHalves = kTiles == 1;
+    constexpr int kKinds = kHalves ? 1 : 2;      // kinds (keys, values) a warp rebuilds
+    constexpr int kHalf = 128;                   // threads that fill one stage
+    constexpr int kSplit = kHalf / kKeys;        // of them per token
+    constexpr int kMyCodes = NS / kSplit;        // code bytes of a thread's token
     constexpr int kMyVec = kMyCodes < 16 ? kMyCodes : 16;
     constexpr int kCodeWords = kMyCodes < 4 ? 1 : kMyCodes / 4;
     constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     extern __shared__ __align__(128) unsigned char chunk_mem[];
     __shared__ PagedWalk<0> w;
-    __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image, drain, seg_full[2], seg_empty[2];
+    __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image[2], drain, seg_full[2], seg_empty[2];
     __shared__ ChunkSeg segs[2];
     __shared__ uint32_t valid[8][4];  // per key block (mod 8): which tokens are in a page
     __shared__ uint32_t tmem_slot;
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 
     if (tid == 0) {
         for (int i = 0; i < kChunkStages; ++i) {
-            mbar_init(&full[i], kRebuild);
+            mbar_init(&full[i], kHalf);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -211,7 +217,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             mbar_init(&seg_full[i], 1);
             mbar_init(&seg_empty[i], 13);  // a lane of each softmax, rebuild and product warp
         }
-        mbar_init(&image, kRebuild);
+        mbar_init(&image[0], kHalf);
+        mbar_init(&image[1], kHalf);
         mbar_init(&drain, 1);
         abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -255,7 +262,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t o_addr = lane_base + S::kO + (kTiles == 2 ? tile * D : 0);
         uint32_t seen_s[2] = {0, 0};  // phases of s_full that this thread has waited for
-        uint32_t seen_o = 0;          // products P V^ of this tile so far
+        // phases of o_done so far: with one tile the products P V^, with two the
+        // segments (there the commit of a block's scores covers the product before)
+        uint32_t seen_o = 0;
         uint32_t block = 0;           // key blocks of the segments so far
         bool go = true;
         while (go && next_seg(seg_n, s)) {
@@ -408,8 +417,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         if (rise) m = top;
                         sum2 = make_float2(sum2.x * f, sum2.y * f);
                         if (j > 0) {
-                            // the product before this block is the seen_o-th
-                            if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
+                            // the product before this block has to be done
+                            if (kTiles == 1 && !__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
                                 go = false;
                                 break;
                             }
@@ -445,10 +454,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 }
                 tmem_wait_st();
                 if (kTiles == 1 && j > 0) {
-                    // a wait tells only the last two phases of a barrier apart.  With two
-                    // tiles the scores of this block come after the product before in the
-                    // issuer's order, with one they come before it: so wait for each
-                    // product in turn (it has run beside this block's softmax)
+                    // a wait tells only the last two phases of a barrier apart, and the
+                    // scores of this block were issued before the product before: wait for
+                    // each product in turn
                     if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
                         go = false;
                         break;
@@ -456,9 +464,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 }
                 tc_fence_before();
                 (void)mbar_arrive(&p_full[buf]);
-                ++seen_o;
+                if (kTiles == 1) ++seen_o;
             }
             if (!go) break;
+            if (kTiles == 2) ++seen_o;
             if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) break;
             tc_fence_after();
             const float sum = sum2.x + sum2.y;
@@ -503,31 +512,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         }
     } else if (work && warp < 12) {
         // ------------------------------------------------ rebuild
-        const int me = tid - 128 * kTiles;        // 0 .. kRebuild - 1
-        const int tk = me % kKeys, part = me / kKeys;  // token of the block, which part of its row
+        const int me = tid - 128 * kTiles;
+        const int vals = kHalves && me >= kHalf ? 1 : 0;  // warp-uniform: which half this is
+        const int in_half = me - vals * kHalf;
+        const int tk = in_half % kKeys, part = in_half / kKeys;  // token of the block, which part of its row
         const uint32_t copy = (uint32_t)(lane % (64 / SUB)) * (2 * SUB);
-        const uint32_t k_base = smem_addr(k_image) + copy, v_base = smem_addr(v_image) + copy;
         const int64_t cb_elems = (int64_t)a.hkv * a.nc * SUB;
         const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
-        uint32_t filled = 0;  // stages filled so far
-        uint32_t block = 0;   // key blocks so far
+        uint32_t base_n = 0;  // stages of the segments so far
+        uint32_t block = 0;   // key blocks of them
         int built = -1;
         bool go = true;
-        // the rebuilding warps meet (bounded, as every wait here)
+        // the warps that share an image meet (bounded, as every wait here)
         uint32_t met = 0;
         auto meet = [&]() -> bool {
-            (void)mbar_arrive(&image);
-            return __all_sync(0xffffffffu, chunk_wait(&image, met++ & 1, &abort_word));
+            (void)mbar_arrive(&image[vals]);
+            return __all_sync(0xffffffffu, chunk_wait(&image[vals], met++ & 1, &abort_word));
         };
         while (go && next_seg(seg_n, s)) {
             const int h = s.h;
             if (h != built) {
-                // images of this head: only these warps read them
+                // the images of this head: only these warps read them
                 if (!(go = meet())) break;
-                for (int c = me; c < 256; c += kRebuild) {
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const T *all = static_cast<const T *>(kv ? a.vcb : a.kcb);
+#pragma unroll 1
+                for (int kd = 0; kd < kKinds; ++kd) {
+                    const bool v = kHalves ? vals : kd;
+                    const T *all = static_cast<const T *>(v ? a.vcb : a.kcb);
+                    unsigned char *img = v ? v_image : k_image;
+                    for (int c = in_half; c < 256; c += kHalf) {
                         const T *cb = all + ((int64_t)h * a.nc + c) * SUB;
                         uint32_t wd[SUB / 2];
 #pragma unroll
@@ -537,7 +549,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 #pragma unroll
                             for (int i = 0; i < SUB / 2; ++i) wd[i] = (uint32_t)__ldg(src + 2 * i) | ((uint32_t)__ldg(src + 2 * i + 1) << 16);
                         }
-                        unsigned char *img = kv ? v_image : k_image;
 #pragma unroll
                         for (int k = 0; k < 64 / SUB; ++k) {
                             unsigned char *dst = img + c * 128 + ((c + k) % (64 / SUB)) * (2 * SUB);
@@ -553,110 +564,111 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             const int32_t key0 = s.key0;
             const int nb = s.nb;
             const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.pos0 - a.window;  // no row sees at or below
-            // this thread's token of block j: its page entry, or -1; checked when
-            // it is used (a check here would wait for the load)
+            // this thread's token of block j: its page entry, or -1; checked when it is
+            // used (a check here would wait for the load)
             auto page_of = [&](int j) -> int32_t {
                 const int64_t t = (int64_t)key0 + (int64_t)j * kKeys + tk;
                 if (j >= nb || t >= s.k_hi || t <= none_lo) return -1;
                 return paged_entry(a, s.r, (int32_t)t);
             };
-            auto load = [&](int j, int32_t &pg, uint32_t (&kc)[kCodeWords], uint32_t (&vc)[kCodeWords]) {
+            const int64_t head_off = ((int64_t)h << a.page_shift) * NS + part * kMyCodes;
+            auto load = [&](int j, int32_t &pg, uint32_t (&codes)[kKinds][kCodeWords]) {
                 if (pg < 0 || pg >= a.num_pages) {
                     pg = -1;
                     return;
                 }
                 const int32_t off = (key0 + j * kKeys + tk) & ((1 << a.page_shift) - 1);
-                const int64_t base = (int64_t)pg * a.page_stride + (((int64_t)h << a.page_shift) + off) * NS + part * kMyCodes;
-                if (!span_ok(a.k_codes + base, kMyCodes, a.k_codes, code_bytes, kMyVec) ||
-                    !span_ok(a.v_codes + base, kMyCodes, a.v_codes, code_bytes, kMyVec))
-                    return;
+                const int64_t at = head_off + (int64_t)pg * a.page_stride + off * NS;
 #pragma unroll
-                for (int i = 0; i < kMyCodes / kMyVec; ++i) {
-                    uint32_t x[(kMyVec + 3) / 4], y[(kMyVec + 3) / 4];
-                    load_codes<kMyVec>(a.k_codes + base + i * kMyVec, x);
-                    load_codes<kMyVec>(a.v_codes + base + i * kMyVec, y);
+                for (int kd = 0; kd < kKinds; ++kd) {
+                    const uint8_t *all = (kHalves ? vals : kd) ? a.v_codes : a.k_codes;
+                    if (!span_ok(all + at, kMyCodes, all, code_bytes, kMyVec)) continue;
 #pragma unroll
-                    for (int k = 0; k < (kMyVec + 3) / 4; ++k) {
-                        kc[i * (kMyVec / 4) + k] = x[k];
-                        vc[i * (kMyVec / 4) + k] = y[k];
+                    for (int i = 0; i < kMyCodes / kMyVec; ++i) {
+                        uint32_t v[(kMyVec + 3) / 4];
+                        load_codes<kMyVec>(all + at + i * kMyVec, v);
+#pragma unroll
+                        for (int k = 0; k < (kMyVec + 3) / 4; ++k) codes[kd][i * (kMyVec / 4) + k] = v[k];
                     }
                 }
             };
-            // rebuild this thread's part of its token into the next stage
-            auto fill = [&](uint32_t base, bool live, const uint32_t (&codes)[kCodeWords]) -> bool {
-                const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
+            // a block's place in the ring: with two tiles the stages go K0 V0 K1 V1 ..,
+            // with one K0 K1 V0 K2 V1 .. (there the scores of a block are issued before
+            // the product of the one before)
+            auto stage_of = [&](int j, int v) -> uint32_t {
+                if (kTiles == 2) return base_n + 2 * j + v;
+                if (v) return base_n + (j + 1 < nb ? 2 * j + 2 : 2 * j + 1);
+                return base_n + (j > 0 ? 2 * j - 1 : 0);
+            };
+            // rebuild this thread's part of its token of block j
+            auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords]) -> bool {
+                const uint32_t base = smem_addr(v ? v_image : k_image) + copy;
+                const uint32_t n = stage_of(j, v), st = n % kChunkStages, round = n / kChunkStages;
+                // (the stages are released in ring order, so that the phase before the one
+                // waited for is over)
                 if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
+                if (v == 0) {
+                    // the words that lay here, eight blocks back, have been read: the stage
+                    // just released held keys or values of a block at most four back, and
+                    // was released after the weights of the one before that
+                    const uint32_t have = __ballot_sync(0xffffffffu, live);
+                    if (lane == 0 && part == 0) valid[block & 7][tk / 32] = have;
+                }
                 unsigned char *dst = ring + st * S::kStageBytes + (part * (kPieces / kSplit)) * (16 * kKeys) + tk * 16;
                 // eight pieces at a time, so that their loads overlap
                 constexpr int kMyPieces = kPieces / kSplit, kBatch = kMyPieces < 8 ? kMyPieces : 8;
 #pragma unroll
                 for (int c0 = 0; c0 < kMyPieces; c0 += kBatch) {
-                    uint32_t v[kBatch][4];
+                    uint32_t w[kBatch][4];
 #pragma unroll
                     for (int c = 0; c < kBatch; ++c) {
                         if constexpr (SUB == 8) {
-                            image_row<8>(base, code_at(codes, c0 + c), v[c]);
+                            image_row<8>(base, code_at(codes, c0 + c), w[c]);
                         } else {
                             uint32_t lo[2], hi[2];
                             image_row<4>(base, code_at(codes, 2 * (c0 + c)), lo);
                             image_row<4>(base, code_at(codes, 2 * (c0 + c) + 1), hi);
-                            v[c][0] = lo[0];
-                            v[c][1] = lo[1];
-                            v[c][2] = hi[0];
-                            v[c][3] = hi[1];
+                            w[c][0] = lo[0];
+                            w[c][1] = lo[1];
+                            w[c][2] = hi[0];
+                            w[c][3] = hi[1];
                         }
+                    }
+                    if (!live) {  // no token: finite whatever its codes would be
+#pragma unroll
+                        for (int c = 0; c < kBatch; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0;
                     }
 #pragma unroll
                     for (int c = 0; c < kBatch; ++c) {
                         unsigned char *to = dst + (c0 + c) * (16 * kKeys);
-                        if (dyn_smem_ok(to, 16, 16))
-                            *reinterpret_cast<uint4 *>(to) = live ? make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]) : make_uint4(0, 0, 0, 0);
+                        if (dyn_smem_ok(to, 16, 16)) *reinterpret_cast<uint4 *>(to) = make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 (void)mbar_arrive(&full[st]);
-                ++filled;
                 return true;
             };
-            // keys of the next block: also which tokens there are
-            auto fill_keys = [&](int32_t pg, const uint32_t (&codes)[kCodeWords]) -> bool {
-                const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
-                const uint32_t st = filled % kChunkStages, round = filled / kChunkStages;
-                if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
-                // the words that lay here, eight blocks back, have been read: the stage
-                // just released held keys or values of a block at most four back, and
-                // was released after the weights of the one before that
-                if (lane == 0 && part == 0) valid[block & 7][tk / 32] = have;
-                ++block;
-                return fill(k_base, pg >= 0, codes);
-            };
-            // stage order: with two tiles K0 V0 K1 V1 .., with one K0 K1 V0 K2 V1 ..
-            // (there the scores of a block are issued before the product of the one
-            // before).  Codes are loaded two blocks ahead.
-            constexpr int kAhead = kTiles == 2 ? 0 : 1;  // blocks the keys are ahead of the values
-            uint32_t kc[3][kCodeWords] = {}, vc[3][kCodeWords] = {};
-            int32_t pg[3], pg_next;
+            // codes one block ahead, page entries two
+            uint32_t codes[2][kKinds][kCodeWords] = {};
+            int32_t pg[3];
+            pg[0] = page_of(0);
+            pg[1] = page_of(1);
+            load(0, pg[0], codes[0]);
+            for (int j = 0; j < nb; ++j, ++block) {
+                load(j + 1, pg[1], codes[1]);
+                pg[2] = page_of(j + 2);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) pg[j] = page_of(j);
-            load(0, pg[0], kc[0], vc[0]);
-            load(1, pg[1], kc[1], vc[1]);
-            if (kAhead) go = fill_keys(pg[0], kc[0]);
-            for (int j = 0; go && j < nb; ++j) {
-                load(j + 2, pg[2], kc[2], vc[2]);
-                pg_next = page_of(j + 3);
-                if (j + kAhead < nb) go = fill_keys(pg[kAhead], kc[kAhead]);
-                if (go) go = fill(v_base, pg[0] >= 0, vc[0]);
+                for (int kd = 0; kd < kKinds; ++kd)
+                    if (go) go = fill(j, kHalves ? vals : kd, pg[0] >= 0, codes[0][kd]);
+                if (!go) break;
                 pg[0] = pg[1];
                 pg[1] = pg[2];
-                pg[2] = pg_next;
 #pragma unroll
-                for (int i = 0; i < kCodeWords; ++i) {
-                    kc[0][i] = kc[1][i];
-                    kc[1][i] = kc[2][i];
-                    vc[0][i] = vc[1][i];
-                    vc[1][i] = vc[2][i];
-                }
+                for (int kd = 0; kd < kKinds; ++kd)
+#pragma unroll
+                    for (int i = 0; i < kCodeWords; ++i) codes[0][kd][i] = codes[1][kd][i];
             }
+            base_n += 2 * nb;
         }
     } else if (work && warp == 12) {
         // ------------------------------------------------ the products
@@ -695,7 +707,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             const uint32_t d = tmem + S::kO + (kTiles == 2 ? tile * D : 0), p = tmem + buf * S::kS;
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k) umma_16_ts(d, p + k * 8, vd + k * 16, idesc_o, add || k > 0);
-            umma_commit_elected(&o_done[tile]);
         };
         while (go && next_seg(seg_n, s)) {
             const int nb = s.nb;
@@ -719,6 +730,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     if (!(go = take(&vs) && wait(&p_full[j & 1], n_p[j & 1]++ & 1))) break;
                     tc_fence_after();
                     values(0, j & 1, vs, j > 0);
+                    umma_commit_elected(&o_done[0]);
                     umma_commit_elected(&empty[vs]);
                     continue;
                 }
@@ -727,12 +739,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     if (!(go = wait(&p_full[t], n_p[t]++ & 1))) break;
                     tc_fence_after();
                     values(t, t, vs, j > 0);
+                    if (!more) umma_commit_elected(&o_done[t]);  // else the next scores' commit covers it
                     if (t == tiles - 1) umma_commit_elected(&empty[vs]);
                     if (more) {
-                        if (t == 0) {
-                            if (!(go = take(&ks))) break;
-                            tc_fence_after();
-                        }
+                        // the next keys are waited for while the first product runs (the
+                        // next values, waited for here too, would hold the scores up)
+                        if (t == 0 && !(go = take(&ks))) break;
+                        tc_fence_after();
                         // products run in the order of issue: the weights, which lie over
                         // S, are read before the next scores are written there
                         scores(t, t, ks);

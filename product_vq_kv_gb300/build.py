@@ -25,7 +25,8 @@ SOURCES = [os.path.join(CSRC, name) for name in ("vq_encode.cu", "vq_attn.cu", "
                                            "vq_append.cu", "vq_paged.cu", "vq_pfew.cu", "vq_pchunk.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, name) for name in (
     "vq_kernels.cuh", "vq_filter.cuh", "vq_tc.cuh", "vq_decode.cuh", "vq_attn.cuh", "vq_host.h", "vq_scalar.cuh", "vq_status.cuh", "vq_check.cuh", "vq_umma.cuh",
-    "vq_append.cuh", "vq_pages.cuh", "vq_pattn.cuh", "vq_pfew.cuh", "vq_pchunk.cuh", "vq_paged_host.h")] + [
+    "vq_append.cuh", "vq_pages.cuh", "vq_pattn.cuh", "vq_pfew.cuh", "vq_pchunk.cuh", "vq_paged_host.h",
+    "vq_tc_host.h")] + [
     os.path.join(ROOT, "include", "vq_encode.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -9,6 +9,7 @@
 #include "vq_append.cuh"
 #include "vq_host.h"
 #include "vq_status.cuh"
+#include "vq_tc_host.h"
 
 VQH_STATUS_READER(vqh_status_append)
 
@@ -24,10 +25,48 @@ vq_status launch_general(const vqk::AppendArgs &a, int kv0, int n, cudaStream_t 
     return vqh_launched(st, vqh_status_append);
 }
 
-template <typename T>
-vq_status launch(const vqk::AppendArgs &a, cudaStream_t st)
+template <typename T, int SUB, bool SMOOTH>
+vq_status launch_tc(const vqk::AppendArgs &a, vq_dtype dtype, int kv0, int kinds, cudaStream_t st)
 {
-    return launch_general<T>(a, 0, 2, st);
+    constexpr bool kSplit = vqh::tc_split<T, SMOOTH>();
+    using C = vqk::TcConfig<SUB, kSplit>;
+    const size_t smem = vqh::tc_smem<SUB, SMOOTH>(a.nc, dtype);
+    int64_t per_group = 0;
+    int32_t tiles = 0;
+    const int64_t groups = (int64_t)kinds * a.heads;
+    vqh::tc_shape(groups, a.tokens * a.ns, vqh::tc_slots(SUB, kSplit, smem), vqh::tc_tps(SUB, kSplit), &per_group, &tiles);
+    if (groups * per_group > 0x7fffffffLL) return VQ_ERR_UNSUPPORTED;
+    auto kernel = vqk::append_tc<T, SUB, C::kCols, C::kGroup, C::kMinBlocks, SMOOTH, C::kTps>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return VQ_ERR_CUDA;
+    kernel<<<(unsigned)(groups * per_group), 128 * C::kTps, smem, st>>>(a, kv0, (int32_t)per_group, tiles, 1.0f);
+    return vqh_launched(st, vqh_status_append);
+}
+
+// Rows aligned for the vector loads, codebooks that screening pays for, rows
+// counted in 31 bits: the tensor-core encode.  Otherwise the general kernel.
+template <typename T>
+bool tc_takes(const vqk::AppendArgs &a)
+{
+    const int64_t row = (int64_t)a.sub * sizeof(T), align = row < 16 ? row : 16;
+    for (int kv = 0; kv < 2; ++kv)
+        if ((uintptr_t)a.x[kv] % align || a.stride[kv] * (int64_t)sizeof(T) % align) return false;
+    return (a.sub == 4 || a.sub == 8) && a.nc >= vqh::kFilterMinCentroids && a.tokens * a.ns < 0x7fffffffLL - 128;
+}
+
+template <typename T, int SUB>
+vq_status launch_sub(const vqk::AppendArgs &a, vq_dtype dtype, cudaStream_t st)
+{
+    if (!a.smooth) return launch_tc<T, SUB, false>(a, dtype, 0, 2, st);
+    const vq_status s = launch_tc<T, SUB, true>(a, dtype, 0, 1, st);  // smoothed keys: rows in two pieces
+    return s != VQ_OK ? s : launch_tc<T, SUB, false>(a, dtype, 1, 1, st);
+}
+
+template <typename T>
+vq_status launch(const vqk::AppendArgs &a, vq_dtype dtype, cudaStream_t st)
+{
+    if (!tc_takes<T>(a)) return launch_general<T>(a, 0, 2, st);
+    return a.sub == 4 ? launch_sub<T, 4>(a, dtype, st) : launch_sub<T, 8>(a, dtype, st);
 }
 
 }  // namespace
@@ -87,9 +126,9 @@ vq_status vq_paged_append(const void *k, const void *v, int64_t k_stride, int64_
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     switch (dtype) {
-    case VQ_F16: return launch<__half>(a, st);
-    case VQ_BF16: return launch<__nv_bfloat16>(a, st);
-    case VQ_F32: return launch<float>(a, st);
+    case VQ_F16: return launch<__half>(a, dtype, st);
+    case VQ_BF16: return launch<__nv_bfloat16>(a, dtype, st);
+    case VQ_F32: return launch<float>(a, dtype, st);
     }
     return VQ_ERR_INTERNAL;
 }

@@ -7,12 +7,20 @@
 // of a packed projection), its codes go to
 //   codes[slot / P][head][slot % P][s],  P = page_size,
 // and a slot outside [0, num_pages P) is skipped.
+//
+// What bounds it is the encode's own work, not its 8 to 20 bytes a sub-vector: so
+// the kernel is the tensor-core encode (vq_tc.cuh: screening on tcgen05, the
+// exact formula where the bound cannot decide) with rows that are addressed
+// through the token stride and indices that go through the slot map, one launch
+// for the keys and values of all heads.  A group of the launch is one head of
+// one of the two; its rows are its sub-vectors, token by token.
 #pragma once
 
 #include <stdint.h>
 
 #include "vq_check.cuh"
 #include "vq_kernels.cuh"
+#include "vq_tc.cuh"
 
 namespace vqk {
 
@@ -83,6 +91,84 @@ __global__ void __launch_bounds__(128) append_general(const __grid_constant__ Ap
         }
     }
     if (VQ_SPAN(dst + s, 1, a.codes[kv], append_codes_bytes(a))) dst[s] = (uint8_t)idx;
+}
+
+// The sub-vectors of one head, as encode_tc_block takes its rows: row m is
+// sub-vector m % ns of token m / ns.  Rows of one launch stay below 2^31, so the
+// division is a 32-bit one.
+template <typename T, int SUB, bool SMOOTH>
+struct AppendRows {
+    const AppendArgs &a;
+    const T *__restrict__ x;       // the head's first sub-vector
+    const float *__restrict__ sg;  // the head's smooth factors
+    int kv;
+    int32_t h;
+    uint32_t n;                    // rows
+    __device__ __forceinline__ const T *at(uint32_t m, uint32_t *s) const
+    {
+        const uint32_t t = m / (uint32_t)a.ns;
+        *s = m - t * (uint32_t)a.ns;
+        return x + (int64_t)t * a.stride[kv] + *s * SUB;
+    }
+    __device__ __forceinline__ int64_t elems() const
+    {
+        return (a.tokens - 1) * a.stride[kv] + (int64_t)a.heads * a.ns * SUB;
+    }
+    __device__ __forceinline__ void smooth(uint32_t s, float (&v)[SUB]) const
+    {
+        if constexpr (SMOOTH) {
+#pragma unroll
+            for (int i = 0; i < SUB; ++i) v[i] = __fdiv_rn(v[i], __ldg(sg + s * SUB + i));
+        }
+    }
+    __device__ __forceinline__ void load(int64_t m, float (&v)[SUB]) const
+    {
+        constexpr uint32_t kRowAlign = SUB * sizeof(T) < 16 ? SUB * sizeof(T) : 16;
+        uint32_t s;
+        const T *p = at((uint32_t)m, &s);
+        if (m < n && VQ_VSPAN(p, SUB, static_cast<const T *>(a.x[kv]), elems(), kRowAlign)) {
+            load_row<T, SUB>(p, v);
+            smooth(s, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < SUB; ++i) v[i] = 0.f;
+        }
+    }
+    __device__ __forceinline__ bool load_same(int64_t m, float (&v)[SUB]) const
+    {
+        uint32_t s;
+        const T *p = at((uint32_t)m, &s);
+        if (!VQ_SPAN(p, SUB, static_cast<const T *>(a.x[kv]), elems())) return false;
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) v[i] = widen(p[i]);
+        smooth(s, v);
+        return true;
+    }
+    __device__ __forceinline__ void put(int64_t m, uint32_t id) const
+    {
+        const uint32_t t = (uint32_t)m / (uint32_t)a.ns, s = (uint32_t)m - t * (uint32_t)a.ns;
+        uint8_t *dst = append_dst(a, kv, t, h);
+        if (dst && VQ_SPAN(dst + s, 1, a.codes[kv], append_codes_bytes(a))) dst[s] = (uint8_t)id;
+    }
+};
+
+// blockIdx.x: kinds * heads groups of blocks_per_group blocks; kinds (keys
+// and values, or one of them) from kv0 on.
+template <typename T, int SUB, int NCOL, int GC, int MINB, bool SMOOTH, int TPS>
+__global__ void __launch_bounds__(128 * TPS, MINB)
+    append_tc(const __grid_constant__ AppendArgs a, int kv0, int32_t blocks_per_group, int32_t tiles_per_block,
+              float one)
+{
+    const int32_t g = blockIdx.x / blocks_per_group, blk = blockIdx.x - g * blocks_per_group;
+    const int kv = kv0 + g / a.heads;
+    const int32_t h = g % a.heads;
+    if (!index_ok(kv, 2)) return;  // block-uniform
+    const T *codebooks = static_cast<const T *>(a.codebooks[kv]);
+    const uint32_t n = (uint32_t)(a.tokens * a.ns);
+    const AppendRows<T, SUB, SMOOTH> rows{a, static_cast<const T *>(a.x[kv]) + (int64_t)h * a.ns * SUB,
+                                          SMOOTH ? a.smooth + (int64_t)h * a.ns * SUB : nullptr, kv, h, n};
+    encode_tc_block<T, SUB, NCOL, GC, SMOOTH, kWaitPolls, TPS>(rows, codebooks + (int64_t)h * a.nc * SUB, codebooks, a.heads, n, a.nc,
+                                                               (int64_t)blk * tiles_per_block * 128, tiles_per_block, one);
 }
 
 }  // namespace vqk

@@ -298,8 +298,10 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                 load_codes<VB>(vp + 9 * NS, vc[3]);
             };
 
+            // Three sets of registers in turn (X of the unit, X + 2 being loaded): moving
+            // a loaded register from set to set would wait for the load.
             uint32_t kc[3][2][KW] = {}, vc[3][4][VW] = {};
-            int32_t pg[3], pg_next;
+            int32_t pg[3];
             pg[0] = page_of(s.begin);
             pg[1] = page_of(s.begin + 1);
             pg[2] = page_of(s.begin + 2);
@@ -307,10 +309,12 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
             load(s.begin + 1, pg[1], kc[1], vc[1]);
             __syncthreads();  // the images are written
 
-            for (int unit = s.begin; unit < s.end; ++unit) {
-                load(unit + 2, pg[2], kc[2], vc[2]);
-                pg_next = page_of(unit + 3);
-                if (pg[0] >= 0) {  // warp-uniform
+            auto step = [&](auto set, int unit) {
+                constexpr int X = decltype(set)::value, Y = (X + 2) % 3;
+                load(unit + 2, pg[Y], kc[Y], vc[Y]);
+                const bool live = pg[X] >= 0;
+                pg[X] = page_of(unit + 3);
+                if (live) {  // warp-uniform
                     // S^T = K^ Q^T
                     float st[NT][4];
 #pragma unroll
@@ -320,8 +324,8 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
                         uint32_t lo[SUB / 2], hi[SUB / 2];
-                        image_row<SUB>(k_base, code_at(kc[0][0], b), lo);
-                        image_row<SUB>(k_base, code_at(kc[0][1], b), hi);
+                        image_row<SUB>(k_base, code_at(kc[X][0], b), lo);
+                        image_row<SUB>(k_base, code_at(kc[X][1], b), hi);
 #pragma unroll
                         for (int i = 0; i < SUB / 4; ++i)
 #pragma unroll
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                     for (int b = 0; b < VB; ++b) {
                         uint32_t e[4][SUB / 2];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) image_row<SUB>(v_base, code_at(vc[0][k], b), e[k]);
+                        for (int k = 0; k < 4; ++k) image_row<SUB>(v_base, code_at(vc[X][k], b), e[k]);
 #pragma unroll
                         for (int i = 0; i < SUB / 2; ++i) {
                             const uint32_t a0 = __byte_perm(e[0][i], e[1][i], 0x5410);
@@ -398,20 +402,11 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                         }
                     }
                 }
-                pg[0] = pg[1];
-                pg[1] = pg[2];
-                pg[2] = pg_next;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int i = 0; i < KW; ++i) kc[x][k][i] = kc[x + 1][k][i];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < VW; ++i) vc[x][k][i] = vc[x + 1][k][i];
-                }
+            };
+            for (int unit = s.begin; unit < s.end; unit += 3) {
+                step(std::integral_constant<int, 0>{}, unit);
+                if (unit + 1 < s.end) step(std::integral_constant<int, 1>{}, unit + 1);
+                if (unit + 2 < s.end) step(std::integral_constant<int, 2>{}, unit + 2);
             }
 
             // the warps' states: maxima and sums first

@@ -208,12 +208,50 @@ struct TcConfig<8, true> : TcConfig<8, false> {};
 
 // ------------------------------------------------------------------ kernel
 
-template <typename T, int SUB, int NCOL, int GC, int MINB, typename OutT = uint32_t,
-          bool SMOOTH = false, int POLLS = kWaitPolls, int TPS = 1>
-__global__ void __launch_bounds__(128 * TPS, MINB)
-    encode_tc(const T *__restrict__ x, const T *__restrict__ codebooks, int64_t n_per_group,
-              int32_t n_centroids, int64_t blocks_per_group, int32_t tiles_per_block, float one,
-              OutT *__restrict__ out, const float *__restrict__ smooth, int32_t smooth_ns)
+// The rows of one group as the kernel reads and writes them: row m of a group
+// of n rows at x + m * SUB, its index at out + m.
+template <typename T, int SUB, typename OutT, bool SMOOTH>
+struct DenseRows {
+    const T *__restrict__ x, *__restrict__ xg;
+    OutT *__restrict__ out, *__restrict__ og;
+    const float *__restrict__ sg;  // the group's smooth factors
+    int64_t n, nx, nout;           // rows of the group; extents of x and out (checked build)
+    int32_t smooth_ns;
+    // row m into v (zeros past the end), with vector loads
+    __device__ __forceinline__ void load(int64_t m, float (&v)[SUB]) const
+    {
+        constexpr uint32_t kRowAlign = SUB * sizeof(T) < 16 ? SUB * sizeof(T) : 16;  // load_row
+        if (m < n && VQ_VSPAN(xg + (size_t)m * SUB, SUB, x, nx, kRowAlign)) {
+            load_row<T, SUB>(xg + (size_t)m * SUB, v);
+            smooth_row<SUB, SMOOTH>(v, sg, m, smooth_ns);
+        } else {
+#pragma unroll
+            for (int i = 0; i < SUB; ++i) v[i] = 0.f;
+        }
+    }
+    // row m < n, the same in every lane of a warp; false (warp-uniform): skip it
+    __device__ __forceinline__ bool load_same(int64_t m, float (&v)[SUB]) const
+    {
+        if (!VQ_SPAN(xg + (size_t)m * SUB, SUB, x, nx)) return false;
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) v[i] = widen(xg[(size_t)m * SUB + i]);
+        smooth_row<SUB, SMOOTH>(v, sg, m, smooth_ns);
+        return true;
+    }
+    // index of row m < n
+    __device__ __forceinline__ void put(int64_t m, uint32_t id) const
+    {
+        if (VQ_SPAN(og + m, 1, out, nout)) store_index(og + m, id);
+    }
+};
+
+// The work of one block: tiles_per_block tiles of `rows` from row_base on,
+// against the codebook at cb (inside the n_groups_all codebooks at codebooks).
+template <typename T, int SUB, int NCOL, int GC, bool SMOOTH, int POLLS, int TPS, typename Rows>
+__device__ __forceinline__ void encode_tc_block(const Rows &rows, const T *__restrict__ cb,
+                                                const T *__restrict__ codebooks, int64_t n_groups_all,
+                                                int64_t n_per_group, int32_t n_centroids, int64_t row_base,
+                                                int32_t tiles_per_block, float one)
 {
     static_assert(SUB == 4 || SUB == 8, "sub_dim 4 or 8");
     static_assert(NCOL == 32 || NCOL == 64 || NCOL == 128 || NCOL == 256, "tensor-memory columns");
@@ -247,27 +285,13 @@ __global__ void __launch_bounds__(128 * TPS, MINB)
     const int th = tid >> 7;   // tile of the step this thread works on
     const int rt = tid & 127;  // its row in that tile, its tensor-memory lane
     const int n_pad = L::padded(n_centroids);
-    const int64_t g = blockIdx.x / blocks_per_group;
-    const int64_t blk = blockIdx.x - g * blocks_per_group;
-    const T *__restrict__ cb = codebooks + (size_t)g * (size_t)n_centroids * SUB;
-    const T *__restrict__ xg = x + (size_t)g * (size_t)n_per_group * SUB;
-    OutT *__restrict__ og = out + (size_t)g * (size_t)n_per_group;
-    const float *__restrict__ sg = SMOOTH ? smooth + (size_t)g * (size_t)smooth_ns * SUB : nullptr;
-    const int64_t row_base = blk * (int64_t)tiles_per_block * 128;
-
-    // buffer extents, for the checked build's bounds checks (vq_check.cuh)
-    const int64_t n_groups_all = gridDim.x / blocks_per_group;
-    const int64_t nx = n_groups_all * n_per_group * SUB, nout = n_groups_all * n_per_group;
     constexpr uint64_t kSaBytes = TPS * kNA * L::kABytes, kSbBytes = (uint64_t)kNB * 256 * L::kRowBytes;
     const uint64_t sx_bytes = (uint64_t)L::groups(n_centroids) * L::kGroupFloats * 4;
     constexpr uint64_t kMiscBytes = 64 + 128 * TPS * 4;
-    constexpr uint32_t kRowAlign = SUB * sizeof(T) < 16 ? SUB * sizeof(T) : 16;  // load_row
     if constexpr (kChecked) {
-        // the layout inside the launch's shared memory, the block inside the
-        // grid, its smooth factors inside theirs: else the block does nothing
+        // the layout inside the launch's shared memory: else the block does nothing
         if (!dyn_smem_ok(sm, L::used(n_centroids), 16) || !span_ok(bar, 8, misc, kMiscBytes, 8) ||
-            !span_ok(queue, 512 * TPS, misc, kMiscBytes, 4) || !index_ok(g, n_groups_all) ||
-            (SMOOTH && !VQ_SPAN(sg, (int64_t)smooth_ns * SUB, smooth, n_groups_all * smooth_ns * SUB)))
+            !span_ok(queue, 512 * TPS, misc, kMiscBytes, 4))
             return;  // block-uniform
     }
 
@@ -385,16 +409,7 @@ __global__ void __launch_bounds__(128 * TPS, MINB)
 
     // this thread's row of the first tile
     float xr[SUB];
-    auto load_x = [&](int64_t row, float (&v)[SUB]) {
-        if (row < n_per_group && VQ_VSPAN(xg + (size_t)row * SUB, SUB, x, nx, kRowAlign)) {
-            load_row<T, SUB>(xg + (size_t)row * SUB, v);
-            smooth_row<SUB, SMOOTH>(v, sg, row, smooth_ns);
-        } else {
-#pragma unroll
-            for (int i = 0; i < SUB; ++i) v[i] = 0.f;
-        }
-    };
-    load_x(th < tiles_per_block ? row_base + (int64_t)th * 128 + rt : n_per_group, xr);
+    rows.load(th < tiles_per_block ? row_base + (int64_t)th * 128 + rt : n_per_group, xr);
 
     uint32_t phase = 0;
     bool alive = true;  // block-wide: every wait so far completed within POLLS polls
@@ -516,7 +531,7 @@ __global__ void __launch_bounds__(128 * TPS, MINB)
 
         // next tile's row, in flight during the bookkeeping below
         float xn[SUB];
-        load_x(tile + TPS < tiles_per_block ? row + TPS * 128 : n_per_group, xn);
+        rows.load(tile + TPS < tiles_per_block ? row + TPS * 128 : n_per_group, xn);
 
         // ---- bound, candidate groups, exact re-evaluation
         const float m1 = tree_min<kNG>(gmin);
@@ -610,7 +625,7 @@ __global__ void __launch_bounds__(128 * TPS, MINB)
                 }
             }
         }
-        if (row < n_per_group && id != kQueued && VQ_SPAN(og + row, 1, out, nout)) store_index(og + row, id);
+        if (row < n_per_group && id != kQueued) rows.put(row, id);
         __syncthreads();
 
         // ---- queued rows of this tile: one warp per row, exact scan
@@ -619,11 +634,8 @@ __global__ void __launch_bounds__(128 * TPS, MINB)
             if (!VQ_SPAN(queue + q, 1, queue, THREADS)) break;  // warp-uniform
             const uint32_t qt = queue[q];  // the queued row's thread: tile qt >> 7 of the step, row qt & 127
             const int64_t qrow = row_base + (int64_t)(step * TPS + (int)(qt >> 7)) * 128 + (qt & 127);
-            if (!VQ_SPAN(xg + (size_t)qrow * SUB, SUB, x, nx)) continue;  // warp-uniform
             float xq[SUB];
-#pragma unroll
-            for (int i = 0; i < SUB; ++i) xq[i] = widen(xg[(size_t)qrow * SUB + i]);
-            smooth_row<SUB, SMOOTH>(xq, sg, qrow, smooth_ns);
+            if (!rows.load_same(qrow, xq)) continue;  // warp-uniform
             float best = __int_as_float(0x7f800000);
             uint32_t bi = kQueued;
             for (int c = lane; c < n_centroids; c += 32) {
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(128 * TPS, MINB)
                     bi = oi;
                 }
             }
-            if (lane == 0 && VQ_SPAN(og + qrow, 1, out, nout)) store_index(og + qrow, bi == kQueued ? 0u : bi);
+            if (lane == 0) rows.put(qrow, bi == kQueued ? 0u : bi);
         }
 #pragma unroll
         for (int i = 0; i < SUB; ++i) xr[i] = xn[i];
@@ -660,11 +672,36 @@ __global__ void __launch_bounds__(128 * TPS, MINB)
         for (int st = (int)*qcount; st < steps; ++st) {
             const int t = st * TPS + th;
             const int64_t r = row_base + (int64_t)t * 128 + rt;
-            if (t < tiles_per_block && r < n_per_group && VQ_SPAN(og + r, 1, out, nout)) store_index(og + r, kQueued);
+            if (t < tiles_per_block && r < n_per_group) rows.put(r, kQueued);
         }
     }
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NCOL * TPS));
+}
+
+template <typename T, int SUB, int NCOL, int GC, int MINB, typename OutT = uint32_t,
+          bool SMOOTH = false, int POLLS = kWaitPolls, int TPS = 1>
+__global__ void __launch_bounds__(128 * TPS, MINB)
+    encode_tc(const T *__restrict__ x, const T *__restrict__ codebooks, int64_t n_per_group,
+              int32_t n_centroids, int64_t blocks_per_group, int32_t tiles_per_block, float one,
+              OutT *__restrict__ out, const float *__restrict__ smooth, int32_t smooth_ns)
+{
+    using Rows = DenseRows<T, SUB, OutT, SMOOTH>;
+    const int64_t g = blockIdx.x / blocks_per_group;
+    const int64_t blk = blockIdx.x - g * blocks_per_group;
+    const int64_t n_groups_all = gridDim.x / blocks_per_group;
+    const float *sg = SMOOTH ? smooth + (size_t)g * (size_t)smooth_ns * SUB : nullptr;
+    if constexpr (kChecked) {
+        // the block inside the grid, its smooth factors inside theirs: else nothing
+        if (!index_ok(g, n_groups_all) ||
+            (SMOOTH && !VQ_SPAN(sg, (int64_t)smooth_ns * SUB, smooth, n_groups_all * smooth_ns * SUB)))
+            return;  // block-uniform
+    }
+    const Rows rows{x, x + (size_t)g * (size_t)n_per_group * SUB, out, out + (size_t)g * (size_t)n_per_group, sg,
+                    n_per_group, n_groups_all * n_per_group * SUB, n_groups_all * n_per_group, smooth_ns};
+    encode_tc_block<T, SUB, NCOL, GC, SMOOTH, POLLS, TPS>(rows, codebooks + (size_t)g * (size_t)n_centroids * SUB,
+                                                          codebooks, n_groups_all, n_per_group, n_centroids,
+                                                          blk * (int64_t)tiles_per_block * 128, tiles_per_block, one);
 }
 
 }  // namespace vqk

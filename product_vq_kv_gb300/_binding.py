@@ -9,6 +9,7 @@ path.  If the library has not been built the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -106,6 +107,8 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
 def load_library() -> ctypes.CDLL:
     """Load ``libvqenc.so`` (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -153,6 +156,28 @@ def _stream_handle(stream, device) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream)
+
+
+# The current stream's handle by device index: what torch.cuda.current_stream
+# wraps, without building the wrapper (2 us of a call of 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(fn, where: str, device, stream, *args) -> None:
+    """``fn(*args, stream handle)`` with ``device`` current."""
+    if stream is not None:
+        handle = int(stream.cuda_stream)
+    elif _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = int(torch.cuda.current_stream(device).cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != VQ_OK:
+        raise VQError(status, where)
 
 
 def _check(status: int, where: str) -> None:
@@ -487,6 +512,9 @@ def vq_attention_decode(q: torch.Tensor, k_codes: torch.Tensor, k_codebooks: tor
 
 def _i32_tensor(t, name: str, shape: tuple, device) -> None:
     """A contiguous int32 device tensor of ``shape`` (None: any extent) on ``device``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()
+            and (device is None or t.device == device) and t.shape == shape):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.int32:
@@ -498,6 +526,18 @@ def _i32_tensor(t, name: str, shape: tuple, device) -> None:
     _device_tensor(t, name)
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _table_tensor(t, requests: int, device) -> int:
+    """Check a block table ``[requests, max_blocks]``; returns max_blocks."""
+    blocks = t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 2 else None
+    _i32_tensor(t, "block_table", (requests, blocks), device)
+    return blocks
+
+
+def _extent(t) -> int | None:
+    """The extent of a 1-D tensor; None if it is none."""
+    return t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 1 else None
 
 
 def _out_like(out, name, shape, dtype, device):
@@ -524,25 +564,23 @@ def vq_paged_reserve(lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     free_count_out, cu_new, slots)``; pass ``lens_out=lens`` and
     ``free_count_out=free_count`` to update those in place.  Refused requests
     (see ``include/vq_encode.h``) keep their length and get slots of -1."""
-    _i32_tensor(lens, "lens", (None,), None)
-    dev, r = lens.device, lens.shape[0]
+    r = _extent(lens)
+    _i32_tensor(lens, "lens", (r,), None)
+    dev, pages = lens.device, _extent(free_pages)
     _i32_tensor(new_lens, "new_lens", (r,), dev)
-    _i32_tensor(free_pages, "free_pages", (None,), dev)
+    _i32_tensor(free_pages, "free_pages", (pages,), dev)
     _i32_tensor(free_count, "free_count", (1,), dev)
-    _i32_tensor(block_table, "block_table", (r, None), dev)
+    blocks = _table_tensor(block_table, r, dev)
     if total_new < 0:
         raise ValueError("total_new must not be negative")
     lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev)
     free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev)
     cu_new = _out_like(cu_new, "cu_new", (r + 1,), torch.int32, dev)
     slots = _out_like(slots, "slots", (total_new,), torch.int64, dev)
-    with torch.cuda.device(dev):
-        st = load_library().vq_paged_reserve(
-            lens.data_ptr(), new_lens.data_ptr(), r, free_pages.data_ptr(), free_count.data_ptr(),
-            free_pages.shape[0], block_table.data_ptr(), block_table.shape[1], page_size, total_new,
-            lens_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-            _stream_handle(stream, dev))
-    _check(st, "vq_paged_reserve")
+    _launch(load_library().vq_paged_reserve, "vq_paged_reserve", dev, stream, lens.data_ptr(),
+            new_lens.data_ptr(), r, free_pages.data_ptr(), free_count.data_ptr(), pages,
+            block_table.data_ptr(), blocks, page_size, total_new, lens_out.data_ptr(),
+            free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr())
     return lens_out, free_count_out, cu_new, slots
 
 
@@ -554,20 +592,18 @@ def vq_paged_trim(lens: torch.Tensor, keep_lens: torch.Tensor, block_table: torc
     """Cut each request to ``keep_lens[r]`` tokens and push the pages it no
     longer needs on ``free_pages`` (in place).  Returns ``(lens_out,
     free_count_out)``, which may be ``lens`` and ``free_count`` themselves."""
-    _i32_tensor(lens, "lens", (None,), None)
-    dev, r = lens.device, lens.shape[0]
+    r = _extent(lens)
+    _i32_tensor(lens, "lens", (r,), None)
+    dev, pages = lens.device, _extent(free_pages)
     _i32_tensor(keep_lens, "keep_lens", (r,), dev)
-    _i32_tensor(block_table, "block_table", (r, None), dev)
-    _i32_tensor(free_pages, "free_pages", (None,), dev)
+    blocks = _table_tensor(block_table, r, dev)
+    _i32_tensor(free_pages, "free_pages", (pages,), dev)
     _i32_tensor(free_count, "free_count", (1,), dev)
     lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev)
     free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        st = load_library().vq_paged_trim(
-            lens.data_ptr(), keep_lens.data_ptr(), r, block_table.data_ptr(), block_table.shape[1],
-            page_size, free_pages.data_ptr(), free_count.data_ptr(), free_pages.shape[0],
-            lens_out.data_ptr(), free_count_out.data_ptr(), _stream_handle(stream, dev))
-    _check(st, "vq_paged_trim")
+    _launch(load_library().vq_paged_trim, "vq_paged_trim", dev, stream, lens.data_ptr(),
+            keep_lens.data_ptr(), r, block_table.data_ptr(), blocks, page_size, free_pages.data_ptr(),
+            free_count.data_ptr(), pages, lens_out.data_ptr(), free_count_out.data_ptr())
     return lens_out, free_count_out
 
 
@@ -578,8 +614,8 @@ def _token_rows(t, name: str, device) -> None:
     if t.dim() != 3:
         raise ValueError(f"{name} must have shape [tokens, heads, head_dim], got {tuple(t.shape)}")
     _dtype_code(t)
-    if t.numel() and (t.stride(2) != 1 and t.shape[2] > 1 or t.stride(1) != t.shape[2] and t.shape[1] > 1
-                      or t.stride(0) < t.shape[1] * t.shape[2] and t.shape[0] > 1):
+    (n, h, d), (sn, sh, sd) = t.shape, t.stride()
+    if n * h * d and (sd != 1 and d > 1 or sh != d and h > 1 or sn < h * d and n > 1):
         raise ValueError(f"{name} must be contiguous within a token and its tokens must not overlap")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -588,12 +624,27 @@ def _token_rows(t, name: str, device) -> None:
 
 
 def _token_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    n, h, d = t.shape
+    return t.stride(0) if n > 1 else h * d
 
 
 def _page_tensors(k_codes, v_codes, k_codebooks, v_codebooks, dtype, device):
     """Check the pages and codebooks; returns (num_pages, heads, page_size, ns,
     page stride in bytes, n_centroids, sub_dim)."""
+    if (isinstance(k_codes, torch.Tensor) and isinstance(v_codes, torch.Tensor)
+            and isinstance(k_codebooks, torch.Tensor) and isinstance(v_codebooks, torch.Tensor)
+            and k_codes.dim() == 4 and k_codebooks.dim() == 3):
+        # the usual case in one test; anything else is told apart below
+        shape, strides, books = k_codes.shape, k_codes.stride(), k_codebooks.shape
+        pages, heads, page_size, ns = shape
+        if (pages > 1 and k_codes.dtype is torch.uint8 and v_codes.dtype is torch.uint8
+                and k_codebooks.dtype is dtype and v_codebooks.dtype is dtype and v_codes.shape == shape
+                and v_codes.stride() == strides and v_codebooks.shape == books and books[0] == heads
+                and strides[1:] == (page_size * ns, ns, 1) and strides[0] >= heads * page_size * ns
+                and k_codebooks.is_contiguous() and v_codebooks.is_contiguous()
+                and k_codes.device == device and v_codes.device == device
+                and k_codebooks.device == device and v_codebooks.device == device):
+            return pages, heads, page_size, ns, strides[0], books[1], books[2]
     for name, t in (("k_codes", k_codes), ("v_codes", v_codes), ("k_codebooks", k_codebooks),
                     ("v_codebooks", v_codebooks)):
         if not isinstance(t, torch.Tensor):
@@ -661,13 +712,11 @@ def vq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
         _device_tensor(k_smooth, "k_smooth")
         if k_smooth.device != dev:
             raise ValueError(f"k_smooth is on {k_smooth.device}, not on {dev}")
-    with torch.cuda.device(dev):
-        st = load_library().vq_paged_append(
-            k.data_ptr(), v.data_ptr(), _token_stride(k), _token_stride(v), slots.data_ptr(), tokens,
-            heads, d, sub, n_c, k_codebooks.data_ptr(), v_codebooks.data_ptr(),
+    _launch(load_library().vq_paged_append, "vq_paged_append", dev, stream, k.data_ptr(), v.data_ptr(),
+            _token_stride(k), _token_stride(v), slots.data_ptr(), tokens, heads, d, sub, n_c,
+            k_codebooks.data_ptr(), v_codebooks.data_ptr(),
             k_smooth.data_ptr() if k_smooth is not None else None, k_codes.data_ptr(),
-            v_codes.data_ptr(), pages, page_size, stride, _dtype_code(k), _stream_handle(stream, dev))
-    _check(st, "vq_paged_append")
+            v_codes.data_ptr(), pages, page_size, stride, _dtype_code(k))
 
 
 def vq_paged_attention_workspace_bytes(requests: int, tokens: int, max_new: int, heads_q: int,
@@ -675,6 +724,13 @@ def vq_paged_attention_workspace_bytes(requests: int, tokens: int, max_new: int,
                                        n_centroids: int, page_size: int) -> int:
     return int(load_library().vq_paged_attention_workspace_bytes(
         requests, tokens, max_new, heads_q, heads_kv, head_dim, sub_dim, n_centroids, page_size))
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace(device_index: int, *sizes) -> int:
+    """The workspace of a device for these sizes, as often as a step asks for it."""
+    with torch.cuda.device(device_index):
+        return max(vq_paged_attention_workspace_bytes(*sizes), 16)
 
 
 def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor,
@@ -702,31 +758,29 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
     if ns * sub != d or hq % hkv:
         raise ValueError(f"q {tuple(q.shape)} does not match codes {tuple(k_codes.shape)} and "
                          f"codebooks {tuple(k_codebooks.shape)}")
-    _i32_tensor(lens, "lens", (None,), dev)
-    r = lens.shape[0]
+    r = _extent(lens)
+    _i32_tensor(lens, "lens", (r,), dev)
     _i32_tensor(cu_new, "cu_new", (r + 1,), dev)
-    _i32_tensor(block_table, "block_table", (r, None), dev)
+    blocks = _table_tensor(block_table, r, dev)
     if max_new < 0:
         raise ValueError("max_new must not be negative")
     out = _out_like(out, "out", (tokens, hq, d), q.dtype, dev)
     if return_lse or lse is not None:
         lse = _out_like(lse, "lse", (tokens, hq), torch.float32, dev)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            nbytes = vq_paged_attention_workspace_bytes(r, tokens, max_new, hq, hkv, d, sub, n_c, page_size)
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        else:
-            _device_tensor(workspace, "workspace")
-            if workspace.device != dev:
-                raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
-        st = load_library().vq_paged_attention(
-            q.data_ptr(), _token_stride(q), cu_new.data_ptr(), lens.data_ptr(), r, tokens, max_new,
-            block_table.data_ptr(), block_table.shape[1], k_codes.data_ptr(), v_codes.data_ptr(),
-            pages, page_size, stride, k_codebooks.data_ptr(), v_codebooks.data_ptr(), hq, hkv, d,
-            sub, n_c, window, scale, _dtype_code(q), out.data_ptr(),
-            lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
-    _check(st, "vq_paged_attention")
+    if workspace is None:
+        nbytes = _paged_workspace(dev.index, r, tokens, max_new, hq, hkv, d, sub, n_c, page_size)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        _device_tensor(workspace, "workspace")
+        if workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+        nbytes = workspace.numel() * workspace.element_size()
+    _launch(load_library().vq_paged_attention, "vq_paged_attention", dev, stream, q.data_ptr(),
+            _token_stride(q), cu_new.data_ptr(), lens.data_ptr(), r, tokens, max_new,
+            block_table.data_ptr(), blocks, k_codes.data_ptr(), v_codes.data_ptr(), pages, page_size,
+            stride, k_codebooks.data_ptr(), v_codebooks.data_ptr(), hq, hkv, d, sub, n_c, window, scale,
+            _dtype_code(q), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+            workspace.data_ptr(), nbytes)
     return (out, lse) if lse is not None else out
 
 

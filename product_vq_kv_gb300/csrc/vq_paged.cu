@@ -37,18 +37,18 @@ vq_status check_page(int32_t page_size)
 }
 
 // A launch of one cluster of `blocks` blocks.
-cudaLaunchConfig_t cluster_launch(int blocks, size_t smem, cudaStream_t st, cudaLaunchAttribute *attr)
+cudaLaunchConfig_t cluster_launch(int blocks, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute *attr)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(vqk::kPageThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)blocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = blocks > 1 ? 1 : 0;  // one block is a cluster by itself
     return cfg;
 }
 
@@ -78,7 +78,7 @@ struct AttnCall {
 // One kernel's launch: its blocks, rows per item and share of the workspace.
 struct AttnPart {
     int blocks = 0;
-    int32_t tile_tokens = 0, gc = 0, gch = 0, tile_rows = 0;
+    int32_t tile_tokens = 0, gc = 0, gch = 0, tile_rows = 0, item_cost = 0;
     size_t notes = 0, ml = 0, part = 0, end = 0;  // workspace offsets
 };
 
@@ -152,6 +152,7 @@ AttnPart few_part(int sms, int32_t group, int32_t dim, int nt, size_t at)
     p.gch = (group + p.gc - 1) / p.gc;
     p.tile_tokens = 8 * nt / p.gc;
     p.tile_rows = 8 * nt;
+    p.item_cost = 4;  // 3 to 4 us of set-up, merge of the warps and write, at 0.9 us a unit
     lay_out(&p, dim, at);
     return p;
 }
@@ -189,6 +190,7 @@ void use_part(vqk::PagedArgs *a, const AttnPart &p, unsigned char *ws)
     a->gc = p.gc;
     a->gch = p.gch;
     a->tile_rows = p.tile_rows;
+    a->item_cost = p.item_cost;
     a->items = a->tokens / p.tile_tokens + a->requests + 1;
     a->notes = reinterpret_cast<vqk::PagedNote *>(ws + p.notes);
     a->ml = reinterpret_cast<float *>(ws + p.ml);
@@ -207,7 +209,12 @@ vq_status launch_merge(const vqk::PagedArgs &a, const AttnPart &p, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, vqk::paged_attn_merge<T>, (const float *)a.part, (const float *)a.ml,
+    // as many registers as the head size needs: the rows of a chunk are many
+    auto kernel = a.dim % 4 != 0 ? vqk::paged_attn_merge<T, false, 16>
+                  : a.dim <= 128 ? vqk::paged_attn_merge<T, true, 1>
+                  : a.dim <= 256 ? vqk::paged_attn_merge<T, true, 2>
+                                 : vqk::paged_attn_merge<T, true, 4>;
+    if (cudaLaunchKernelEx(&cfg, kernel, (const float *)a.part, (const float *)a.ml,
                            (const vqk::PagedNote *)a.notes, p.tile_rows, a.dim, a.hq, a.tokens,
                            static_cast<T *>(a.out), a.lse) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -291,15 +298,17 @@ vq_status vq_paged_reserve(const int32_t *lens, const int32_t *new_lens, int64_t
         if (!aligned4(p)) return VQ_ERR_INVALID_ARG;
     if ((uintptr_t)slots % 8) return VQ_ERR_INVALID_ARG;
     const size_t smem = vqk::page_reserve_smem(requests);
-    if (cudaFuncSetAttribute(vqk::page_reserve, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(vqk::page_reserve, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)smem) != cudaSuccess)
         return VQ_ERR_CUDA;
-    // one block for a decode step; more where there are slots to write
+    // one small block for a decode step; more where there are slots to write
+    const int threads = requests <= vqk::kPageFewThreads && total_new <= 2 * vqk::kPageFewThreads ? vqk::kPageFewThreads
+                                                                                                  : vqk::kPageThreads;
     int blocks = 1;
     while (blocks < 8 && total_new > (int64_t)blocks * vqk::kPageThreads) blocks *= 2;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = cluster_launch(blocks, smem, st, attr);
+    cudaLaunchConfig_t cfg = cluster_launch(blocks, threads, smem, st, attr);
     if (cudaLaunchKernelEx(&cfg, vqk::page_reserve, lens, new_lens, (int32_t)requests, free_pages, free_count,
                            (int32_t)num_pages, block_table, (int32_t)max_blocks, (int32_t)page_shift(page_size),
                            total_new, lens_out, free_count_out, cu_new, slots) != cudaSuccess)
@@ -322,14 +331,15 @@ vq_status vq_paged_trim(const int32_t *lens, const int32_t *keep_lens, int64_t r
                           (const void *)free_count_out})
         if (!aligned4(p)) return VQ_ERR_INVALID_ARG;
     const size_t smem = vqk::page_trim_smem(requests);
-    if (cudaFuncSetAttribute(vqk::page_trim, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(vqk::page_trim, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)smem) != cudaSuccess)
         return VQ_ERR_CUDA;
-    int blocks = 1;
+    const int threads = requests <= vqk::kPageFewThreads ? vqk::kPageFewThreads : vqk::kPageThreads;
+    int blocks = 1;  // a warp returns the pages of a request at a time
     while (blocks < 8 && requests > (int64_t)blocks * 64) blocks *= 2;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = cluster_launch(blocks, smem, st, attr);
+    cudaLaunchConfig_t cfg = cluster_launch(blocks, threads, smem, st, attr);
     if (cudaLaunchKernelEx(&cfg, vqk::page_trim, lens, keep_lens, (int32_t)requests, block_table,
                            (int32_t)max_blocks, (int32_t)page_shift(page_size), free_pages, free_count,
                            (int32_t)num_pages, lens_out, free_count_out) != cudaSuccess)

@@ -28,7 +28,8 @@
 
 namespace vqk {
 
-constexpr int kPageThreads = 1024;
+constexpr int kPageThreads = 1024;     // of a block; 256 for a small step
+constexpr int kPageFewThreads = 256;
 constexpr int kPageMaxRequests = 8192;  // three scanned arrays of it fit in shared memory
 
 // Inclusive sums of (a, b) over the block's threads; every thread calls.
@@ -50,7 +51,7 @@ __device__ __forceinline__ void block_scan2(int64_t &a, int64_t &b, int64_t *scr
     }
     __syncthreads();
     if (warp == 0) {
-        int64_t wa = lane < warps ? scratch[lane] : 0, wb = lane < warps ? scratch[32 + lane] : 0;
+        int64_t wa = lane < warps ? scratch[lane] : 0, wb = lane < warps ? scratch[32 + lane] : 0;  // totals in 31 and 63
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t pa = __shfl_up_sync(0xffffffffu, wa, off), pb = __shfl_up_sync(0xffffffffu, wb, off);
@@ -71,7 +72,7 @@ __device__ __forceinline__ void block_scan2(int64_t &a, int64_t &b, int64_t *scr
 
 __device__ __forceinline__ int32_t clamp_i32(int64_t v) { return (int32_t)(v > INT32_MAX ? INT32_MAX : v); }
 
-// Launch: one cluster (gridDim.x = cluster size), kPageThreads threads,
+// Launch: one cluster (gridDim.x = cluster size), up to kPageThreads threads,
 // dynamic shared memory page_reserve_smem(requests).
 __host__ __device__ inline size_t page_reserve_smem(int64_t requests)
 {
@@ -92,13 +93,13 @@ __global__ void __launch_bounds__(kPageThreads)
     int32_t *take = held + requests;                          // [requests]: pages taken before r; -1: refused
     auto cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x;
-    const int rank = blockIdx.x, blocks = gridDim.x;
+    const int rank = blockIdx.x, blocks = gridDim.x, threads = blockDim.x;
     const int64_t page = (int64_t)1 << page_shift, cap = (int64_t)max_blocks << page_shift;
     const int32_t fc = *free_count;
     const int64_t avail = fc < 0 ? 0 : fc > num_pages ? num_pages : fc;
 
-    int64_t tok_base = 0, need_base = 0, taken = 0;
-    for (int base = 0; base < requests; base += kPageThreads) {
+    int64_t tok_base = 0, need_base = 0;
+    for (int base = 0; base < requests; base += threads) {
         const int r = base + tid;
         int64_t l = 0, n = 0, need = 0;
         bool fits = false;
@@ -126,30 +127,23 @@ __global__ void __launch_bounds__(kPageThreads)
 
     auto new_of = [&](int r) { return (int64_t)(cu[r + 1] - cu[r]); };
     // the pages of the granted requests are a prefix of the sequence: its length
-    for (int r = requests - 1 - tid; r >= 0; r -= kPageThreads) {
+    // (at most free_count, so 32 bits hold it)
+    uint32_t mine = 0;
+    for (int r = tid; r < requests; r += threads) {
         if (take[r] < 0) continue;
         const int64_t l = held[r];
         const int64_t need = ((l + new_of(r) + page - 1) >> page_shift) - ((l + page - 1) >> page_shift);
-        if (need && take[r] + need > taken) taken = take[r] + need;
+        if (need && take[r] + need > mine) mine = (uint32_t)(take[r] + need);
     }
-    {
-        int64_t m = taken;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const int64_t o = __shfl_xor_sync(0xffffffffu, m, off);
-            m = o > m ? o : m;
-        }
-        if ((tid & 31) == 0) scratch[tid >> 5] = m;
-        __syncthreads();
-        taken = 0;
-#pragma unroll 1
-        for (int w = 0; w < kPageThreads / 32; ++w) taken = scratch[w] > taken ? scratch[w] : taken;
-    }
+    mine = __reduce_max_sync(0xffffffffu, mine);
+    if ((tid & 31) == 0) scratch[tid >> 5] = mine;
+    __syncthreads();
+    const int64_t taken = __reduce_max_sync(0xffffffffu, (tid & 31) < (threads >> 5) ? (uint32_t)scratch[tid & 31] : 0u);
 
     // table entries of the new pages: a warp per request (new entries only, so
     // no other thread's read of a held page meets a write)
-    const int warps = blocks * (kPageThreads / 32), lane = tid & 31;
-    for (int r = rank * (kPageThreads / 32) + (tid >> 5); r < requests; r += warps) {
+    const int warps = blocks * (threads >> 5), lane = tid & 31;
+    for (int r = rank * (threads >> 5) + (tid >> 5); r < requests; r += warps) {
         if (take[r] < 0) continue;
         const int64_t l = held[r];
         const int64_t b0 = (l + page - 1) >> page_shift, b1 = (l + new_of(r) + page - 1) >> page_shift;
@@ -163,7 +157,7 @@ __global__ void __launch_bounds__(kPageThreads)
     }
 
     // slots: a thread per token
-    for (int64_t t = (int64_t)rank * kPageThreads + tid; t < total_new; t += (int64_t)blocks * kPageThreads) {
+    for (int64_t t = (int64_t)rank * threads + tid; t < total_new; t += (int64_t)blocks * threads) {
         int64_t slot = -1;
         if (t < cu[requests]) {
             int lo = 0, hi = requests - 1;  // the last r with cu[r] <= t
@@ -190,7 +184,7 @@ __global__ void __launch_bounds__(kPageThreads)
     }
 
     cluster.sync();  // lens and free_count have been read by every block
-    for (int r = rank * kPageThreads + tid; r < requests; r += blocks * kPageThreads) {
+    for (int r = rank * threads + tid; r < requests; r += blocks * threads) {
         lens_out[r] = (int32_t)(held[r] + (take[r] >= 0 ? new_of(r) : 0));
         cu_new[r] = cu[r];
     }
@@ -200,7 +194,7 @@ __global__ void __launch_bounds__(kPageThreads)
     }
 }
 
-// Launch: one cluster, kPageThreads threads, dynamic shared memory
+// Launch: one cluster, up to kPageThreads threads, dynamic shared memory
 // page_trim_smem(requests).
 __host__ __device__ inline size_t page_trim_smem(int64_t requests)
 {
@@ -220,13 +214,13 @@ __global__ void __launch_bounds__(kPageThreads)
     int32_t *back = kept + requests;                             // pages returned
     auto cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x;
-    const int rank = blockIdx.x, blocks = gridDim.x;
+    const int rank = blockIdx.x, blocks = gridDim.x, threads = blockDim.x;
     const int64_t page = (int64_t)1 << page_shift, cap = (int64_t)max_blocks << page_shift;
     const int32_t fc = *free_count;
     const int64_t avail = fc < 0 ? 0 : fc > num_pages ? num_pages : fc;
 
     int64_t base_pages = 0;
-    for (int base = 0; base < requests; base += kPageThreads) {
+    for (int base = 0; base < requests; base += threads) {
         const int r = base + tid;
         int64_t l = 0, k = 0, n = 0, unused = 0;
         if (r < requests) {
@@ -247,8 +241,8 @@ __global__ void __launch_bounds__(kPageThreads)
         __syncthreads();
     }
 
-    const int warps = blocks * (kPageThreads / 32), lane = tid & 31;
-    for (int r = rank * (kPageThreads / 32) + (tid >> 5); r < requests; r += warps) {
+    const int warps = blocks * (threads >> 5), lane = tid & 31;
+    for (int r = rank * (threads >> 5) + (tid >> 5); r < requests; r += warps) {
         const int64_t b0 = (kept[r] + page - 1) >> page_shift;
         for (int i = lane; i < back[r]; i += 32) {
             const int64_t at = avail + first[r] + i;
@@ -261,7 +255,7 @@ __global__ void __launch_bounds__(kPageThreads)
     }
 
     cluster.sync();  // lens and free_count have been read by every block
-    for (int r = rank * kPageThreads + tid; r < requests; r += blocks * kPageThreads) lens_out[r] = kept[r];
+    for (int r = rank * threads + tid; r < requests; r += blocks * threads) lens_out[r] = kept[r];
     if (rank == 0 && tid == 0) {
         const int64_t n = avail + base_pages;
         *free_count_out = (int32_t)(n > num_pages ? num_pages : n);

@@ -71,6 +71,7 @@ struct PagedArgs {
     int32_t dim, sub, ns, nc;
     int32_t window;        // 0: none
     int32_t tile_tokens;
+    int32_t item_cost;     // units that an item's set-up and write are worth
     int32_t cls, cls_tokens;  // 0: every request; 1: those of up to cls_tokens new tokens; 2: the others
     float kappa;
     float *part;           // [2 N][tile rows][dim] weighted sums
@@ -89,9 +90,11 @@ struct PagedItem {
 };
 
 // Lengths as the kernel sees them: cu clamped into [0, tokens], request
-// number `requests` being the rows after the last.
+// number `requests` being the rows after the last.  Rows are below 2^31, and so
+// are items.
 struct PagedLens {
     const int32_t *cu, *lens;
+    const int32_t *starts;  // start(0 .. requests), or null: computed
     int32_t requests, tile;
     int64_t tokens;
     __device__ __forceinline__ int64_t first(int r) const
@@ -100,7 +103,11 @@ struct PagedLens {
         const int64_t c = cu[r];
         return c < 0 ? 0 : c > tokens ? tokens : c;
     }
-    __device__ __forceinline__ int64_t start(int r) const { return first(r) / tile + r; }
+    __device__ __forceinline__ int64_t compute_start(int r) const
+    {
+        return (int64_t)((uint32_t)first(r) / (uint32_t)tile) + r;
+    }
+    __device__ __forceinline__ int64_t start(int r) const { return starts ? starts[r] : compute_start(r); }
     // the last r in [0, requests] with start(r) <= j
     __device__ __forceinline__ int find(int64_t j) const
     {
@@ -113,6 +120,13 @@ struct PagedLens {
         return lo;
     }
 };
+
+// b * all / n for 0 <= b <= n, in 32 bits where they do.
+__device__ __forceinline__ int64_t part_of(int64_t b, int64_t all, int64_t n)
+{
+    if (all * n <= 0xffffffffll) return (uint32_t)(b * all) / (uint32_t)n;
+    return b * all / n;
+}
 
 // Item j, which belongs to request r; units = 0 for a hole (then *skip is the
 // next item worth a look).
@@ -149,10 +163,10 @@ __device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, const PagedL
     return it;
 }
 
-// Where a block stands on the line of units.
+// Where a block stands on the line of costs.
 template <int STAGE>
 struct PagedStage {
-    int32_t cu[STAGE], lens[STAGE];
+    int32_t cu[STAGE], lens[STAGE], start[STAGE];
 };
 template <>
 struct PagedStage<0> {};
@@ -161,13 +175,13 @@ struct PagedWalk {
     static constexpr int kStage = STAGE;
     PagedStage<STAGE> stage;
     int64_t scratch[33];
-    int64_t total;  // U of one head group
-    int64_t u0, u1; // this block's units
+    int64_t total;  // the costs of one head group
+    int64_t u0, u1; // this block's part of the line
     int32_t blocks; // blocks with work
     int32_t hx;     // head group
     int64_t j;      // item
     int32_t r;
-    int32_t at;     // first unit of it
+    int32_t at;     // where in its cost
 };
 
 // Lay the items out and find this block's part (all THREADS threads; w in
@@ -178,6 +192,7 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     l.cu = a.cu;
     l.lens = a.lens;
+    l.starts = nullptr;
     l.requests = a.requests;
     l.tile = a.tile_tokens;
     l.tokens = a.tokens;
@@ -185,10 +200,12 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
         if (a.requests + 2 <= STAGE) {
             for (int i = tid; i <= a.requests; i += THREADS) {
                 w.stage.cu[i] = a.cu[i];
+                w.stage.start[i] = (int32_t)l.compute_start(i);
                 if (i < a.requests) w.stage.lens[i] = a.lens[i];
             }
             l.cu = w.stage.cu;
             l.lens = w.stage.lens;
+            l.starts = w.stage.start;
             __syncthreads();
         }
     }
@@ -202,7 +219,8 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
         for (int64_t j = j0; j < j1;) {
             while (r < a.requests && l.start(r + 1) <= j) ++r;
             int64_t skip;
-            mine += paged_item(a, l, j, r, &skip).units;
+            const int32_t u = paged_item(a, l, j, r, &skip).units;
+            mine += u > 0 ? u + a.item_cost : 0;
             j = skip;
         }
     }
@@ -225,14 +243,15 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
     if (tid == 0) {
         w.total = total;
         w.blocks = (int32_t)n;
-        w.u0 = b < n ? b * all / n : 0;
-        w.u1 = b < n ? (b + 1) * all / n : 0;
+        w.u0 = b < n ? part_of(b, all, n) : 0;
+        w.u1 = b < n ? part_of(b + 1, all, n) : 0;
         w.hx = 0;
         w.j = w.r = w.at = 0;
     }
     if (b >= n) return false;  // block-uniform
-    const int64_t u0 = b * all / n;
-    const int64_t rem = u0 % total;
+    const int64_t u0 = part_of(b, all, n);
+    const int64_t hx = total <= 0xffffffffll && u0 <= 0xffffffffll ? (uint32_t)u0 / (uint32_t)total : u0 / total;
+    const int64_t rem = u0 - hx * total;
     __syncthreads();
     if (mine > 0 && before <= rem && rem < before + mine) {
         int64_t left = rem - before;
@@ -240,9 +259,10 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
         for (int64_t j = j0; j < j1;) {
             while (r < a.requests && l.start(r + 1) <= j) ++r;
             int64_t skip;
-            const int32_t u = paged_item(a, l, j, r, &skip).units;
+            int32_t u = paged_item(a, l, j, r, &skip).units;
+            if (u > 0) u += a.item_cost;
             if (left < u) {
-                w.hx = (int32_t)(u0 / total);
+                w.hx = (int32_t)hx;
                 w.j = j;
                 w.r = r;
                 w.at = (int32_t)left;
@@ -286,42 +306,48 @@ struct PagedCursor {
     __device__ __forceinline__ bool next(const PagedArgs &a, const W &w, const PagedLens &l, PagedSegment &s,
                                          PagedNote &note)
     {
-        if (u >= u1) return false;
-        for (;;) {
-            if (j >= a.items) {  // the next head group
-                j = 0;
-                r = 0;
-                ++hx;
-            }
-            while (r < a.requests && l.start(r + 1) <= j) ++r;
-            int64_t skip;
-            s.it = paged_item(a, l, j, r, &skip);
-            if (s.it.units > 0) break;
-            j = skip;
-        }
         const int64_t b = blockIdx.x;
-        s.hx = hx;
-        s.begin = at;
-        const int64_t room = u1 - u;
-        s.end = s.it.units - at <= room ? s.it.units : (int32_t)(at + room);
-        s.whole = s.begin == 0 && s.end == s.it.units;
-        s.slot = 2 * b + (s.begin == 0 ? 1 : 0);
-        if (s.begin == 0 && !s.whole) {
-            const int64_t all = w.total * ((int64_t)a.hkv * a.gch);
-            const int64_t last_unit = u + s.it.units - 1;  // begin = 0: u is the item's first unit
-            const int32_t g0 = hx % a.gch * a.gc;
-            note.tok0 = s.it.tok0;
-            note.head0 = hx / a.gch * a.group + g0;
-            note.gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
-            note.rows = s.it.ntok * note.gc;
-            note.first = (int32_t)b;
-            // the block of unit x: the c with floor(c U / N) <= x < floor((c + 1) U / N)
-            note.last = (int32_t)(((last_unit + 1) * w.blocks - 1) / all);
+        for (;;) {
+            if (u >= u1) return false;
+            for (;;) {
+                if (j >= a.items) {  // the next head group
+                    j = 0;
+                    r = 0;
+                    ++hx;
+                }
+                while (r < a.requests && l.start(r + 1) <= j) ++r;
+                int64_t skip;
+                s.it = paged_item(a, l, j, r, &skip);
+                if (s.it.units > 0) break;
+                j = skip;
+            }
+            // from `at` on in the item's cost: set-up first, then its units
+            const int64_t cost = (int64_t)s.it.units + a.item_cost;
+            const int64_t to = cost - at <= u1 - u ? cost : at + (u1 - u);
+            s.begin = at > a.item_cost ? at - a.item_cost : 0;
+            s.end = to > a.item_cost ? (int32_t)(to - a.item_cost) : 0;
+            const int64_t u_item = u - at;  // where the item starts on the line
+            u += to - at;
+            at = 0;
+            ++j;
+            if (s.end == 0) continue;  // only set-up: the next block begins the item
+            s.hx = hx;
+            s.whole = s.begin == 0 && s.end == s.it.units;
+            s.slot = 2 * b + (s.begin == 0 ? 1 : 0);
+            if (s.begin == 0 && !s.whole) {
+                const int64_t all = w.total * ((int64_t)a.hkv * a.gch);
+                const int64_t last = u_item + cost;  // one past its last unit
+                const int32_t g0 = hx % a.gch * a.gc;
+                note.tok0 = s.it.tok0;
+                note.head0 = hx / a.gch * a.group + g0;
+                note.gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
+                note.rows = s.it.ntok * note.gc;
+                note.first = (int32_t)b;
+                // the block of position x: the c with floor(c U / N) <= x < floor((c + 1) U / N)
+                note.last = (int32_t)((last * w.blocks - 1) / all);
+            }
+            return true;
         }
-        u += s.end - s.begin;
-        at = 0;
-        ++j;
-        return true;
     }
 };
 
@@ -538,18 +564,25 @@ __global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant
 // ------------------------------------------------------------------ the merge
 //
 // Block (b, y) merges rows [y kMergeRows, ..) of the item that block b of the
-// attention began and did not finish: a warp per row, lanes over the parts
-// for the maximum, then over the columns.  Reads every part once.
+// attention began and did not finish: a warp per row, lanes over the parts for
+// the maximum and the weights, then over the columns, several parts' loads in
+// flight (one part after the other took 4 us for 7 parts of one token, all of it
+// latency).  Reads every part once.
 
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = kMergeThreads / 32;
 
-template <typename T>
+// VEC: dim is a multiple of 4 (16-byte loads); LOADS: loads of a lane and part,
+// dim <= 32 x LOADS x the columns of one.
+template <typename T, bool VEC, int LOADS>
 __global__ void __launch_bounds__(kMergeThreads)
     paged_attn_merge(const float *__restrict__ part, const float *__restrict__ ml,
                      const PagedNote *__restrict__ notes, int32_t tile_rows, int32_t dim, int32_t hq,
                      int64_t tokens, T *__restrict__ out, float *__restrict__ lse)
 {
+    constexpr int kW = VEC ? 4 : 1;                   // columns of a load
+    constexpr int kMax = LOADS;
+    constexpr int kBatch = 4;                         // parts in flight
     // launched while the attention's last blocks still run
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedNote n = notes[blockIdx.x];
@@ -561,35 +594,82 @@ __global__ void __launch_bounds__(kMergeThreads)
         return (k == 0 ? 2 * (int64_t)n.first + 1 : 2 * (int64_t)(n.first + k)) * tile_rows + row;
     };
     const int64_t prows = 2 * (int64_t)gridDim.x * tile_rows;
+    auto state = [&](int k, float *m, float *l) {  // of part k; l = 0: it saw nothing, or there is none
+        *m = __int_as_float(0xff800000);
+        *l = 0.f;
+        const float2 *p = reinterpret_cast<const float2 *>(ml) + slot_row(k);
+        if (k < parts && VQ_SPAN(p, 1, reinterpret_cast<const float2 *>(ml), prows)) {
+            *m = p->x;
+            *l = p->y;
+        }
+    };
     float top = __int_as_float(0xff800000);
     for (int k = lane; k < parts; k += 32) {
-        const float *p = ml + slot_row(k) * 2;
-        if (VQ_SPAN(p, 2, ml, prows * 2) && p[1] != 0.f) top = fmaxf(top, p[0]);
+        float m, l;
+        state(k, &m, &l);
+        if (l != 0.f) top = fmaxf(top, m);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const int64_t orow = (n.tok0 + row / n.gc) * hq + n.head0 + row % n.gc;
-    float total = 0.f;
-    constexpr int kMax = kSimpleDim / 32;
-    float acc[kMax];
-#pragma unroll
-    for (int c = 0; c < kMax; ++c) acc[c] = 0.f;
-    for (int k = 0; k < parts; ++k) {
-        const int64_t sr = slot_row(k);
-        if (!VQ_SPAN(ml + sr * 2, 2, ml, prows * 2) || !VQ_SPAN(part + sr * dim, dim, part, prows * dim)) continue;
-        const float l = ml[sr * 2 + 1];
-        if (l == 0.f) continue;  // this part of the row saw nothing
-        const float w = exp2f(ml[sr * 2] - top);
-        total = fmaf(w, l, total);
-#pragma unroll
-        for (int c = 0; c < kMax; ++c)
-            if (c * 32 + lane < dim) acc[c] = fmaf(w, part[sr * dim + c * 32 + lane], acc[c]);
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
+    float total = 0.f, acc[kMax][kW];
 #pragma unroll
     for (int c = 0; c < kMax; ++c)
-        if (c * 32 + lane < dim && VQ_SPAN(out + orow * dim + c * 32 + lane, 1, out, tokens * hq * dim))
-            out[orow * dim + c * 32 + lane] = narrow<T>(acc[c] * inv);
+#pragma unroll
+        for (int i = 0; i < kW; ++i) acc[c][i] = 0.f;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        float m, l;
+        state(k0 + lane, &m, &l);
+        const float w = l == 0.f ? 0.f : exp2f(m - top);  // a NaN sum is not 0: it goes on
+        float t = w * l;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+        total += t;
+        const int upto = parts - k0 < 32 ? parts - k0 : 32;
+        for (int k = 0; k < upto; k += kBatch) {
+            float f[kBatch], v[kBatch][kMax][kW];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                // (lanes past the parts hold 0)
+                f[x] = __shfl_sync(0xffffffffu, w, (k + x) & 31);
+                const bool live = k + x < upto && __shfl_sync(0xffffffffu, l, (k + x) & 31) != 0.f;
+                const float *src = part + slot_row(k0 + k + x) * dim;
+#pragma unroll
+                for (int c = 0; c < kMax; ++c) {
+                    const int col = (c * 32 + lane) * kW;
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) v[x][c][i] = 0.f;
+                    // a part that saw nothing has written zeros, one past the end nothing
+                    if (live && col < dim && VQ_VSPAN(src + col, kW, part, prows * dim, 4 * kW)) {
+                        if constexpr (VEC) {
+                            const float4 q = __ldcg(reinterpret_cast<const float4 *>(src + col));
+                            v[x][c][0] = q.x;
+                            v[x][c][1] = q.y;
+                            v[x][c][2] = q.z;
+                            v[x][c][3] = q.w;
+                        } else {
+                            v[x][c][0] = __ldcg(src + col);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+                for (int c = 0; c < kMax; ++c)
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) acc[c][i] = fmaf(f[x], v[x][c][i], acc[c][i]);
+        }
+    }
+    const int64_t orow = (n.tok0 + row / n.gc) * hq + n.head0 + row % n.gc;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (int c = 0; c < kMax; ++c) {
+        const int col = (c * 32 + lane) * kW;
+        if (col < dim && VQ_SPAN(out + orow * dim + col, kW, out, tokens * hq * dim)) {
+#pragma unroll
+            for (int i = 0; i < kW; ++i) out[orow * dim + col + i] = narrow<T>(acc[c][i] * inv);
+        }
+    }
     if (lane == 0 && lse && VQ_SPAN(lse + orow, 1, lse, tokens * hq)) lse[orow] = paged_lse(top, total);
 }
 

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     constexpr int kCodeWords = kMyCodes < 4 ? 1 : kMyCodes / 4;
     constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     extern __shared__ __align__(128) unsigned char chunk_mem[];
-    __shared__ PagedWalk<0> w;
+    __shared__ PagedWalk<64> w;
     __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image[2], drain, seg_full[2], seg_empty[2];
     __shared__ ChunkSeg segs[2];
     __shared__ uint32_t valid[8][4];  // per key block (mod 8): which tokens are in a page
@@ -538,24 +538,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 for (int kd = 0; kd < kKinds; ++kd) {
                     const bool v = kHalves ? vals : kd;
                     const T *all = static_cast<const T *>(v ? a.vcb : a.kcb);
-                    unsigned char *img = v ? v_image : k_image;
+#pragma unroll 1
                     for (int c = in_half; c < 256; c += kHalf) {
-                        const T *cb = all + ((int64_t)h * a.nc + c) * SUB;
                         uint32_t wd[SUB / 2];
-#pragma unroll
-                        for (int i = 0; i < SUB / 2; ++i) wd[i] = 0;
-                        if (c < a.nc && VQ_SPAN(cb, SUB, all, cb_elems)) {
-                            const uint16_t *src = reinterpret_cast<const uint16_t *>(cb);
-#pragma unroll
-                            for (int i = 0; i < SUB / 2; ++i) wd[i] = (uint32_t)__ldg(src + 2 * i) | ((uint32_t)__ldg(src + 2 * i + 1) << 16);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 64 / SUB; ++k) {
-                            unsigned char *dst = img + c * 128 + ((c + k) % (64 / SUB)) * (2 * SUB);
-                            if (!dyn_smem_ok(dst, 2 * SUB, 2 * SUB)) continue;
-                            if constexpr (SUB == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-                            else *reinterpret_cast<uint2 *>(dst) = make_uint2(wd[0], wd[1]);
-                        }
+                        book_row<T, SUB>(all + (int64_t)h * a.nc * SUB, c, a.nc, all, cb_elems, wd);
+                        image_line<SUB>(v ? v_image : k_image, c, wd);
                     }
                 }
                 if (!(go = meet())) break;

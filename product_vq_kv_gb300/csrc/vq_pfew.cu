@@ -15,10 +15,11 @@ template <typename T, int D, int SUB, int NT>
 vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
 {
     auto kernel = vqk::paged_attn_few<T, D, SUB, NT>;
-    const size_t smem = vqk::few_smem<D, NT>();
+    using S = vqk::FewShape<D, NT>;
+    const size_t smem = S::kSmem;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return VQ_ERR_CUDA;
-    kernel<<<(unsigned)blocks, vqk::kFewThreads, smem, st>>>(a);
+    kernel<<<(unsigned)blocks, S::kWarps * 32, smem, st>>>(a);
     return vqh_launched(st, vqh_status_pfew);
 }
 
@@ -35,7 +36,14 @@ vq_status launch_dim(const vqk::PagedArgs &a, int nt, int blocks, cudaStream_t s
 
 }  // namespace
 
-int vqh_few_blocks_per_sm(int32_t dim, int nt) { return dim / 16 * nt > 8 ? 1 : 2; }
+int vqh_few_blocks_per_sm(int32_t dim, int nt)
+{
+    switch (dim) {
+    case 64: return nt == 1 ? vqk::FewShape<64, 1>::kBlocks : vqk::FewShape<64, 2>::kBlocks;
+    case 128: return nt == 1 ? vqk::FewShape<128, 1>::kBlocks : vqk::FewShape<128, 2>::kBlocks;
+    }
+    return vqk::FewShape<256, 1>::kBlocks;
+}
 
 vq_status vqh_paged_few(const vqk::PagedArgs &a, vq_dtype dtype, int nt, int blocks, cudaStream_t st)
 {

@@ -25,9 +25,9 @@
 //     wavefront serves read different copies: no conflicts, whatever the codes.
 //   * P^T reaches the second product through movmatrix, an 8x8 transpose inside
 //     the warp.  Nothing of the inner loop but the codebooks touches shared
-//     memory, and no barrier stands in it: warp w takes tokens 16 w .. 16 w + 15
-//     of every unit and keeps its own softmax state.
-//   * Codes come straight from global memory into registers two units ahead, the
+//     memory, and no barrier stands in it: the warps take groups of 16 tokens
+//     in turn and keep their own softmax states.
+//   * Codes come straight from global memory into registers two groups ahead, the
 //     page numbers three.
 //   * The running maximum follows the scores only when one exceeds it by 2^8
 //     (a vote); until then the weights are at most 2^8, well inside fp16, and
@@ -42,17 +42,18 @@
 
 namespace vqk {
 
-constexpr int kFewThreads = 256;
-constexpr int kFewWarps = kFewThreads / 32;
 constexpr float kFewSlack = 8.f;  // powers of two a weight may exceed 1 by
-static_assert(kFewWarps * 16 == kUnit, "a warp takes 16 tokens of a unit");
 
-// Shared memory: two codebook images of 32 KiB, then the merge's four slots.
+// Warps of a block and blocks of an SM: what the accumulators and queries of a
+// lane (dim/16 x NT x 6 registers) leave of the register file.
 template <int D, int NT>
-constexpr size_t few_smem()
-{
-    return 2 * 32768 + (size_t)4 * 8 * NT * D * sizeof(float);
-}
+struct FewShape {
+    static constexpr bool kWide = D / 16 * NT > 8;
+    static constexpr int kWarps = kWide ? 12 : 8;
+    static constexpr int kBlocks = kWide ? 1 : 2;
+    // shared memory: two codebook images of 32 KiB, then the merge's slots
+    static constexpr size_t kSmem = 2 * 32768 + (size_t)(kWarps / 2) * 8 * NT * D * sizeof(float);
+};
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -135,37 +136,41 @@ __device__ __forceinline__ void image_row(uint32_t base, uint32_t code, uint32_t
         asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
 }
 
-// Write the image of one head's codebook: row c is stored 256 / (2 SUB) times
-// along its 128-byte line; rows past the codebook are zero.  The copies are
-// written in an order that starts at c, so that the lanes of a wavefront meet
-// in no bank.  All THREADS threads; the caller synchronises.
-template <typename T, int SUB, int THREADS>
-__device__ __forceinline__ void build_image(unsigned char *image, const T *__restrict__ cb, int nc,
-                                            const T *all, int64_t all_elems)
+// Row c of a codebook (zero past its end) as SUB / 2 words.
+template <typename T, int SUB>
+__device__ __forceinline__ void book_row(const T *__restrict__ cb, int c, int nc, const T *all, int64_t all_elems,
+                                         uint32_t (&w)[SUB / 2])
 {
-    for (int c = threadIdx.x; c < 256; c += THREADS) {
-        uint32_t w[SUB / 2];
 #pragma unroll
-        for (int i = 0; i < SUB / 2; ++i) w[i] = 0;
-        if (c < nc && VQ_SPAN(cb + (int64_t)c * SUB, SUB, all, all_elems)) {
-            const uint16_t *src = reinterpret_cast<const uint16_t *>(cb + (int64_t)c * SUB);
+    for (int i = 0; i < SUB / 2; ++i) w[i] = 0;
+    if (c < nc && VQ_SPAN(cb + (int64_t)c * SUB, SUB, all, all_elems)) {
+        const uint16_t *src = reinterpret_cast<const uint16_t *>(cb + (int64_t)c * SUB);
 #pragma unroll
-            for (int i = 0; i < SUB / 2; ++i) w[i] = (uint32_t)__ldg(src + 2 * i) | ((uint32_t)__ldg(src + 2 * i + 1) << 16);
-        }
-        constexpr int kCopies = 64 / SUB;
+        for (int i = 0; i < SUB / 2; ++i) w[i] = (uint32_t)__ldg(src + 2 * i) | ((uint32_t)__ldg(src + 2 * i + 1) << 16);
+    }
+}
+
+// Line c of a codebook's image: its row 64 / SUB times.  The copies are
+// written in an order that starts at c, so that the lanes of a wavefront meet in
+// no bank.  The caller synchronises.
+template <int SUB>
+__device__ __forceinline__ void image_line(unsigned char *image, int c, const uint32_t (&w)[SUB / 2])
+{
+    constexpr int kCopies = 64 / SUB;
 #pragma unroll
-        for (int k = 0; k < kCopies; ++k) {
-            unsigned char *dst = image + c * 128 + ((c + k) % kCopies) * (2 * SUB);
-            if (!dyn_smem_ok(dst, 2 * SUB, 2 * SUB)) continue;
-            if constexpr (SUB == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            else *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        }
+    for (int k = 0; k < kCopies; ++k) {
+        unsigned char *dst = image + c * 128 + ((c + k) % kCopies) * (2 * SUB);
+        if (!dyn_smem_ok(dst, 2 * SUB, 2 * SUB)) continue;
+        if constexpr (SUB == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     }
 }
 
 template <typename T, int D, int SUB, int NT>
-__global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_attn_few(const __grid_constant__ PagedArgs a)
+__global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>::kBlocks)
+    paged_attn_few(const __grid_constant__ PagedArgs a)
 {
+    constexpr int kFewWarps = FewShape<D, NT>::kWarps, kFewThreads = kFewWarps * 32;
     constexpr int NS = D / SUB;
     constexpr int KB = NS / 4, VB = NS / 8;        // code bytes a lane takes of a key, of a value
     constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
@@ -192,6 +197,8 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
     const int64_t q_elems = (a.tokens - 1) * a.q_stride + (int64_t)a.hq * D;
     const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
 
+    // the merge's blocks may take the room that idle blocks leave (they wait there)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     PagedLens l;
     PagedNote note{};
     if (paged_plan<kFewThreads>(a, w, l)) {
@@ -204,12 +211,17 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
             const int gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
             const int rows = s.it.ntok * gc;
             const int head0 = h * a.group + g0;
-            __syncthreads();  // the last segment's slots are read
+            __syncthreads();  // the last segment's slots and images are read
             if (h != built) {  // block-uniform
-                build_image<T, SUB, kFewThreads>(k_image, static_cast<const T *>(a.kcb) + (int64_t)h * a.nc * SUB, a.nc,
-                                                 static_cast<const T *>(a.kcb), cb_elems);
-                build_image<T, SUB, kFewThreads>(v_image, static_cast<const T *>(a.vcb) + (int64_t)h * a.nc * SUB, a.nc,
-                                                 static_cast<const T *>(a.vcb), cb_elems);
+                // a row of either codebook for each of 256 threads
+                static_assert(kFewThreads >= 256, "a codebook row per thread");
+                if (tid < 256) {
+                    uint32_t k_row[SUB / 2], v_row[SUB / 2];
+                    book_row<T, SUB>(static_cast<const T *>(a.kcb) + (int64_t)h * a.nc * SUB, tid, a.nc, static_cast<const T *>(a.kcb), cb_elems, k_row);
+                    book_row<T, SUB>(static_cast<const T *>(a.vcb) + (int64_t)h * a.nc * SUB, tid, a.nc, static_cast<const T *>(a.vcb), cb_elems, v_row);
+                    image_line<SUB>(k_image, tid, k_row);
+                    image_line<SUB>(v_image, tid, v_row);
+                }
                 built = h;
             }
 
@@ -271,19 +283,21 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
             const int64_t all_lo = a.window == 0 ? -1 : last_pos - a.window;       // and above here
             const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.it.pos0 - a.window;  // no row sees at or below
 
-            auto first_of = [&](int unit) { return s.it.k_lo + unit * kUnit + warp * 16; };
-            auto page_of = [&](int unit) -> int32_t {
-                if (unit >= s.end) return -1;
-                const int32_t k0 = first_of(unit);
+            // groups of 16 tokens, warp after warp
+            const int g_begin = s.begin * (kUnit / 16) + warp, g_end = s.end * (kUnit / 16);
+            auto first_of = [&](int group) { return s.it.k_lo + group * 16; };
+            auto page_of = [&](int group) -> int32_t {
+                if (group >= g_end) return -1;
+                const int32_t k0 = first_of(group);
                 if (k0 >= s.it.k_hi || k0 + 15 <= none_lo) return -1;
                 return paged_entry(a, cur.r, k0);  // checked when it is used: a check here would wait for the load
             };
-            auto load = [&](int unit, int32_t &pg, uint32_t (&kc)[2][KW], uint32_t (&vc)[4][VW]) {
+            auto load = [&](int group, int32_t &pg, uint32_t (&kc)[2][KW], uint32_t (&vc)[4][VW]) {
                 if (pg < 0 || pg >= a.num_pages) {  // warp-uniform
                     pg = -1;
                     return;
                 }
-                const int32_t off = first_of(unit) & ((1 << a.page_shift) - 1);
+                const int32_t off = first_of(group) & ((1 << a.page_shift) - 1);
                 const int64_t base = (int64_t)pg * a.page_stride + (((int64_t)h << a.page_shift) + off) * NS;
                 if (!span_ok(a.k_codes + base, 16 * NS, a.k_codes, code_bytes, NS < 16 ? NS : 16) ||
                     !span_ok(a.v_codes + base, 16 * NS, a.v_codes, code_bytes, NS < 16 ? NS : 16))
@@ -302,18 +316,17 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
             // a loaded register from set to set would wait for the load.
             uint32_t kc[3][2][KW] = {}, vc[3][4][VW] = {};
             int32_t pg[3];
-            pg[0] = page_of(s.begin);
-            pg[1] = page_of(s.begin + 1);
-            pg[2] = page_of(s.begin + 2);
-            load(s.begin, pg[0], kc[0], vc[0]);
-            load(s.begin + 1, pg[1], kc[1], vc[1]);
+#pragma unroll
+            for (int x = 0; x < 3; ++x) pg[x] = page_of(g_begin + x * kFewWarps);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) load(g_begin + x * kFewWarps, pg[x], kc[x], vc[x]);
             __syncthreads();  // the images are written
 
-            auto step = [&](auto set, int unit) {
+            auto step = [&](auto set, int group) {
                 constexpr int X = decltype(set)::value, Y = (X + 2) % 3;
-                load(unit + 2, pg[Y], kc[Y], vc[Y]);
+                load(group + 2 * kFewWarps, pg[Y], kc[Y], vc[Y]);
                 const bool live = pg[X] >= 0;
-                pg[X] = page_of(unit + 3);
+                pg[X] = page_of(group + 3 * kFewWarps);
                 if (live) {  // warp-uniform
                     // S^T = K^ Q^T
                     float st[NT][4];
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                                 mma16816<T>(st[n], lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
                                             qf[n][b * (SUB / 4) + i][0], qf[n][b * (SUB / 4) + i][1]);
                     }
-                    const int32_t k0 = first_of(unit);
+                    const int32_t k0 = first_of(group);
                     const bool whole = k0 + 15 <= all_hi && k0 > all_lo;
                     bool rise = false;
 #pragma unroll
@@ -403,10 +416,10 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                     }
                 }
             };
-            for (int unit = s.begin; unit < s.end; unit += 3) {
-                step(std::integral_constant<int, 0>{}, unit);
-                if (unit + 1 < s.end) step(std::integral_constant<int, 1>{}, unit + 1);
-                if (unit + 2 < s.end) step(std::integral_constant<int, 2>{}, unit + 2);
+            for (int group = g_begin; group < g_end; group += 3 * kFewWarps) {
+                step(std::integral_constant<int, 0>{}, group);
+                if (group + kFewWarps < g_end) step(std::integral_constant<int, 1>{}, group + kFewWarps);
+                if (group + 2 * kFewWarps < g_end) step(std::integral_constant<int, 2>{}, group + 2 * kFewWarps);
             }
 
             // the warps' states: maxima and sums first
@@ -445,11 +458,12 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                         o[n][i][c + 2] *= f;
                     }
                 }
-            // then the weighted sums, in three halvings
+            // then the weighted sums: the upper half of the warps to the lower, until one is left
 #pragma unroll
-            for (int half = kFewWarps / 2; half > 0; half >>= 1) {
-                float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp % half) * NT * kMma * 32 + lane;
-                if (warp >= half && warp < 2 * half) {
+            for (int live = kFewWarps; live > 1; live = (live + 1) / 2) {
+                const int half = (live + 1) / 2;  // warps half .. live - 1 give to warps 0 ..
+                float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp < half ? warp : warp - half) * NT * kMma * 32 + lane;
+                if (warp >= half && warp < live) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -458,7 +472,7 @@ __global__ void __launch_bounds__(kFewThreads, (D / 16) * NT > 8 ? 1 : 2) paged_
                                 slot[(n * kMma + i) * 32] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
                 }
                 __syncthreads();
-                if (warp < half) {
+                if (warp < live - half) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll

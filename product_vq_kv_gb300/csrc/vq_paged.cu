@@ -133,14 +133,18 @@ TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_
 {
     TensorPlan p{};
     const int64_t most = max_new > 0 && max_new < tokens ? max_new : tokens;  // new tokens of a request, as far as known
-    // 8 rows where no request has more, or where the accumulators of 16 would not
-    // fit the registers (dim 256)
-    p.nt = dim == 256 || most * group <= 8 ? 1 : 2;
+    // 8 rows an item where no request has more, where the accumulators of 16 would
+    // not fit the registers (dim 256), and beside a chunk, where most of the others
+    // are decode steps (15 of them beside a chunk of 2048: 107 us with 16 rows, 66 with 8)
+    const bool few_rows = most * group <= 8;
+    const int wide = dim == 256 ? 1 : 2;
     // up to two items of rows the few-row kernel rebuilds the cache no more often
     // than a tile of the chunk kernel would cost
+    const int64_t at_wide = 16 * wide / group > 1 ? 16 * wide / group : 1;
+    p.chunk = most > at_wide;
+    p.nt = few_rows || p.chunk ? 1 : wide;
     p.few_tokens = 16 * p.nt / group > 1 ? 16 * p.nt / group : 1;
-    p.few = requests != 1 || most <= p.few_tokens;
-    p.chunk = most > p.few_tokens;
+    p.few = requests != 1 || !p.chunk;
     return p;
 }
 

@@ -125,37 +125,31 @@ bool tensor_layout(const vqk::PagedArgs &a)
 // tokens go to the few-row kernel, the others to the chunk kernel.
 struct TensorPlan {
     bool few, chunk;
-    int nt;              // the few-row kernel's items have 8 nt rows
     int32_t few_tokens;
 };
 
-TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_t group, int32_t dim)
+TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_t group)
 {
     TensorPlan p{};
     const int64_t most = max_new > 0 && max_new < tokens ? max_new : tokens;  // new tokens of a request, as far as known
-    // 8 rows an item where no request has more, where the accumulators of 16 would
-    // not fit the registers (dim 256), and beside a chunk, where most of the others
-    // are decode steps (15 of them beside a chunk of 2048: 107 us with 16 rows, 66 with 8)
-    const bool few_rows = most * group <= 8;
-    const int wide = dim == 256 ? 1 : 2;
-    // up to two items of rows the few-row kernel rebuilds the cache no more often
-    // than a tile of the chunk kernel would cost
-    const int64_t at_wide = 16 * wide / group > 1 ? 16 * wide / group : 1;
-    p.chunk = most > at_wide;
-    p.nt = few_rows || p.chunk ? 1 : wide;
-    p.few_tokens = 16 * p.nt / group > 1 ? 16 * p.nt / group : 1;
+    // up to three items of rows: a unit of cached tokens takes an SM 970 cycles for
+    // each in the few-row kernel, and 2500 to 3000 in the chunk kernel for one tile,
+    // however few of its 128 rows there are
+    const int32_t item_tokens = group < vqh_few_rows() ? vqh_few_rows() / group : 1;
+    p.few_tokens = group > vqh_few_rows() ? 1 : 3 * item_tokens;
+    p.chunk = most > p.few_tokens;
     p.few = requests != 1 || !p.chunk;
     return p;
 }
 
-AttnPart few_part(int sms, int32_t group, int32_t dim, int nt, size_t at)
+AttnPart few_part(int sms, int32_t group, int32_t dim, size_t at)
 {
     AttnPart p;
-    p.blocks = sms * vqh_few_blocks_per_sm(dim, nt);
-    p.gc = group < 8 * nt ? group : 8 * nt;
+    p.blocks = sms * vqh_few_blocks_per_sm(dim);
+    p.gc = group < vqh_few_rows() ? group : vqh_few_rows();
     p.gch = (group + p.gc - 1) / p.gc;
-    p.tile_tokens = 8 * nt / p.gc;
-    p.tile_rows = 8 * nt;
+    p.tile_tokens = vqh_few_rows() / p.gc;
+    p.tile_rows = vqh_few_rows();
     p.item_cost = 4;  // 3 to 4 us of set-up, merge of the warps and write, at 0.9 us a unit
     lay_out(&p, dim, at);
     return p;
@@ -178,7 +172,7 @@ size_t tensor_parts(const TensorPlan &t, int sms, int32_t group, int32_t dim, At
 {
     size_t at = 0;
     if (t.few) {
-        *few = few_part(sms, group, dim, t.nt, at);
+        *few = few_part(sms, group, dim, at);
         at = up256(few->end);
     }
     if (t.chunk) {
@@ -239,10 +233,13 @@ vq_status launch_simple(const AttnCall &c, const AttnPart &p, unsigned char *ws)
     return s != VQ_OK ? s : launch_merge<T>(a, p, c.stream);
 }
 
+// Units of cached tokens up to which an item is better left to one block.
+constexpr int64_t kWholeUnits = 8;
+
 template <typename T>
 vq_status launch_tensor(const AttnCall &c, unsigned char *ws)
 {
-    const TensorPlan t = tensor_plan(c.a.requests, c.a.tokens, c.max_new, c.a.group, c.a.dim);
+    const TensorPlan t = tensor_plan(c.a.requests, c.a.tokens, c.max_new, c.a.group);
     AttnPart few, chunk;
     (void)tensor_parts(t, c.sms, c.a.group, c.a.dim, &few, &chunk);
     if (t.chunk) {
@@ -259,8 +256,12 @@ vq_status launch_tensor(const AttnCall &c, unsigned char *ws)
         use_part(&a, few, ws);
         a.cls = t.chunk ? 1 : 0;
         a.cls_tokens = t.few_tokens;
-        vq_status s = vqh_paged_few(a, c.dtype, t.nt, few.blocks, c.stream);
-        if (s == VQ_OK) s = launch_merge<T>(a, few, c.stream);
+        // Short caches and few of them: an item a block, none split, no merge to
+        // launch (one token on 777 cached tokens, 8 heads: 14.7 us split, 13.0 whole).
+        const int64_t cap = (int64_t)a.max_blocks << a.page_shift;
+        a.no_split = cap <= kWholeUnits * vqk::kUnit && a.items * a.hkv * a.gch <= few.blocks;
+        vq_status s = vqh_paged_few(a, c.dtype, few.blocks, c.stream);
+        if (s == VQ_OK && !a.no_split) s = launch_merge<T>(a, few, c.stream);
         if (s != VQ_OK) return s;
     }
     return VQ_OK;
@@ -363,7 +364,7 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
     size_t need = simple_part(sms, group, head_dim, 0).end;
     if (tensor_shape(VQ_F16, head_dim, sub_dim, page_size)) {
         AttnPart few, chunk;
-        const size_t t = tensor_parts(tensor_plan(requests, tokens, max_new, group, head_dim), sms, group, head_dim, &few, &chunk);
+        const size_t t = tensor_parts(tensor_plan(requests, tokens, max_new, group), sms, group, head_dim, &few, &chunk);
         if (t > need) need = t;
     }
     return need;

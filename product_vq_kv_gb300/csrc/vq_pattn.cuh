@@ -72,6 +72,7 @@ struct PagedArgs {
     int32_t window;        // 0: none
     int32_t tile_tokens;
     int32_t item_cost;     // units that an item's set-up and write are worth
+    int32_t no_split;      // every item costs 1 and stays in one block (no merge follows)
     int32_t cls, cls_tokens;  // 0: every request; 1: those of up to cls_tokens new tokens; 2: the others
     float kappa;
     float *part;           // [2 N][tile rows][dim] weighted sums
@@ -163,6 +164,12 @@ __device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, const PagedL
     return it;
 }
 
+// What an item costs (0: a hole).
+__device__ __forceinline__ int32_t paged_cost(const PagedArgs &a, int32_t units)
+{
+    return units == 0 ? 0 : a.no_split ? 1 : units + a.item_cost;
+}
+
 // Where a block stands on the line of costs.
 template <int STAGE>
 struct PagedStage {
@@ -219,8 +226,7 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
         for (int64_t j = j0; j < j1;) {
             while (r < a.requests && l.start(r + 1) <= j) ++r;
             int64_t skip;
-            const int32_t u = paged_item(a, l, j, r, &skip).units;
-            mine += u > 0 ? u + a.item_cost : 0;
+            mine += paged_cost(a, paged_item(a, l, j, r, &skip).units);
             j = skip;
         }
     }
@@ -259,8 +265,7 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
         for (int64_t j = j0; j < j1;) {
             while (r < a.requests && l.start(r + 1) <= j) ++r;
             int64_t skip;
-            int32_t u = paged_item(a, l, j, r, &skip).units;
-            if (u > 0) u += a.item_cost;
+            const int32_t u = paged_cost(a, paged_item(a, l, j, r, &skip).units);
             if (left < u) {
                 w.hx = (int32_t)hx;
                 w.j = j;
@@ -322,7 +327,17 @@ struct PagedCursor {
                 j = skip;
             }
             // from `at` on in the item's cost: set-up first, then its units
-            const int64_t cost = (int64_t)s.it.units + a.item_cost;
+            const int64_t cost = paged_cost(a, s.it.units);
+            if (a.no_split) {
+                s.begin = 0;
+                s.end = s.it.units;
+                s.whole = true;
+                s.hx = hx;
+                s.slot = 0;
+                ++u;
+                ++j;
+                return true;
+            }
             const int64_t to = cost - at <= u1 - u ? cost : at + (u1 - u);
             s.begin = at > a.item_cost ? at - a.item_cost : 0;
             s.end = to > a.item_cost ? (int32_t)(to - a.item_cost) : 0;

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             };
             // rebuild this thread's part of its token of block j
             auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords]) -> bool {
-                const uint32_t base = smem_addr(v ? v_image : k_image) + copy;
+                const unsigned char *base = (v ? v_image : k_image) + copy;
                 const uint32_t n = stage_of(j, v), st = n % kChunkStages, round = n / kChunkStages;
                 // (the stages are released in ring order, so that the phase before the one
                 // waited for is over)

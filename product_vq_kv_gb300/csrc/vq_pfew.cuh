@@ -1,6 +1,6 @@
 // vq_pfew.cuh -- paged attention of a few rows (decode, verification of
-// drafts): up to 8 NT rows (tokens x query heads of one KV head) against the
-// whole cache, 16-bit types, head sizes 64, 128 and 256, sub-vectors of 4 or 8.
+// drafts): up to 8 rows (tokens x query heads of one KV head) against the whole
+// cache, 16-bit types, head sizes 64, 128 and 256, sub-vectors of 4 or 8.
 //
 // What bounds it.  From HBM a cached token costs 2 ns bytes a KV head (32 at
 // head size 128, sub-vectors of 8); rebuilding its key and value rows costs 2 x
@@ -44,15 +44,19 @@ namespace vqk {
 
 constexpr float kFewSlack = 8.f;  // powers of two a weight may exceed 1 by
 
+constexpr int kFewRows = 8;     // columns of a matrix instruction
+
 // Warps of a block and blocks of an SM: what the accumulators and queries of a
-// lane (dim/16 x NT x 6 registers) leave of the register file.
-template <int D, int NT>
+// lane (dim/16 x 6 registers) leave of the register file.  (Items of 16 rows, two
+// columns of instructions on each rebuilt value, took 70 us where two items of 8
+// take 52: twice the registers leave fewer warps.)
+template <int D>
 struct FewShape {
-    static constexpr bool kWide = D / 16 * NT > 8;
+    static constexpr bool kWide = D > 128;
     static constexpr int kWarps = kWide ? 12 : 8;
     static constexpr int kBlocks = kWide ? 1 : 2;
     // shared memory: two codebook images of 32 KiB, then the merge's slots
-    static constexpr size_t kSmem = 2 * 32768 + (size_t)(kWarps / 2) * 8 * NT * D * sizeof(float);
+    static constexpr size_t kSmem = 2 * 32768 + (size_t)(kWarps / 2) * kFewRows * D * sizeof(float);
 };
 
 template <typename T>
@@ -60,11 +64,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                                          uint32_t b0, uint32_t b1)
 {
     if constexpr (std::is_same<T, __half>::value)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -124,16 +128,25 @@ __device__ __forceinline__ uint32_t code_at(const uint32_t (&w)[W], int i)
     return __byte_perm(w[i >> 2], 0, 0x4440 | (i & 3));
 }
 
-// One codebook row of SUB 16-bit values from its image: SUB / 2 words.
-// `base` = shared address of the image plus this lane's copy offset.
+// One codebook row of SUB 16-bit values from its image: SUB / 2 words.  `base`
+// = the image (in shared memory) plus this lane's copy offset.  (A plain load and
+// not an asm statement, which would stand in the order of the matrix
+// instructions: the compiler then starts the loads ahead of them.)
 template <int SUB>
-__device__ __forceinline__ void image_row(uint32_t base, uint32_t code, uint32_t (&w)[SUB / 2])
+__device__ __forceinline__ void image_row(const unsigned char *base, uint32_t code, uint32_t (&w)[SUB / 2])
 {
-    const uint32_t at = base + code * 128u;
-    if constexpr (SUB == 8)
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-    else
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    const unsigned char *at = base + code * 128u;
+    if constexpr (SUB == 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(at);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(at);
+        w[0] = v.x;
+        w[1] = v.y;
+    }
 }
 
 // Row c of a codebook (zero past its end) as SUB / 2 words.
@@ -166,20 +179,19 @@ __device__ __forceinline__ void image_line(unsigned char *image, int c, const ui
     }
 }
 
-template <typename T, int D, int SUB, int NT>
-__global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>::kBlocks)
+template <typename T, int D, int SUB>
+__global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks)
     paged_attn_few(const __grid_constant__ PagedArgs a)
 {
-    constexpr int kFewWarps = FewShape<D, NT>::kWarps, kFewThreads = kFewWarps * 32;
+    constexpr int kFewWarps = FewShape<D>::kWarps, kFewThreads = kFewWarps * 32;
     constexpr int NS = D / SUB;
     constexpr int KB = NS / 4, VB = NS / 8;        // code bytes a lane takes of a key, of a value
     constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
     constexpr int kMma = D / 16;                   // instructions per 16 tokens and 8 rows, each product
-    constexpr int kRowsMax = 8 * NT;
     static_assert(SUB == 4 || SUB == 8, "sub-vectors of 4 or 8");
     extern __shared__ __align__(128) unsigned char few_mem[];
     __shared__ PagedWalk<> w;
-    __shared__ float wm[kFewWarps][kRowsMax], wl[kFewWarps][kRowsMax];
+    __shared__ float wm[kFewWarps][kFewRows], wl[kFewWarps][kFewRows];
     unsigned char *k_image = few_mem, *v_image = few_mem + 32768;
     float *slots = reinterpret_cast<float *>(few_mem + 65536);
 
@@ -187,8 +199,7 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
     const int g = lane >> 2, t = lane & 3;
     const float kNone = __int_as_float(0xff800000);
     const uint32_t copy = (uint32_t)(lane % (64 / SUB)) * (2 * SUB);
-    const uint32_t k_base = (uint32_t)__cvta_generic_to_shared(k_image) + copy;
-    const uint32_t v_base = (uint32_t)__cvta_generic_to_shared(v_image) + copy;
+    const unsigned char *k_base = k_image + copy, *v_base = v_image + copy;
     const T *__restrict__ q = static_cast<const T *>(a.q);
     T *__restrict__ out = static_cast<T *>(a.out);
     const bool q_vec = (uintptr_t)a.q % 8 == 0 && a.q_stride % 4 == 0;
@@ -225,58 +236,50 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
                 built = h;
             }
 
-            // query fragments: row 8 n + g, columns t dim/4 + 4 i .. + 3
-            uint32_t qf[NT][kMma][2];
+            // query fragments: row g, columns t dim/4 + 4 i .. + 3
+            uint32_t qf[kMma][2];
+            const int row = g;
+            const T *src = q + (s.it.tok0 + row / gc) * a.q_stride + (int64_t)(head0 + row % gc) * D + t * (D / 4);
+            const bool ok = row < rows && VQ_SPAN(src, D / 4, q, q_elems);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int row = 8 * n + g;
-                const T *src = q + (s.it.tok0 + row / gc) * a.q_stride + (int64_t)(head0 + row % gc) * D + t * (D / 4);
-                const bool ok = row < rows && VQ_SPAN(src, D / 4, q, q_elems);
-#pragma unroll
-                for (int i = 0; i < kMma; ++i) {
-                    uint2 v = make_uint2(0, 0);
-                    if (ok) {
-                        if (q_vec) {
-                            v = __ldg(reinterpret_cast<const uint2 *>(src + 4 * i));
-                        } else {
-                            const uint16_t *e = reinterpret_cast<const uint16_t *>(src + 4 * i);
-                            v.x = (uint32_t)__ldg(e) | ((uint32_t)__ldg(e + 1) << 16);
-                            v.y = (uint32_t)__ldg(e + 2) | ((uint32_t)__ldg(e + 3) << 16);
-                        }
+            for (int i = 0; i < kMma; ++i) {
+                uint2 v = make_uint2(0, 0);
+                if (ok) {
+                    if (q_vec) {
+                        v = __ldg(reinterpret_cast<const uint2 *>(src + 4 * i));
+                    } else {
+                        const uint16_t *e = reinterpret_cast<const uint16_t *>(src + 4 * i);
+                        v.x = (uint32_t)__ldg(e) | ((uint32_t)__ldg(e + 1) << 16);
+                        v.y = (uint32_t)__ldg(e + 2) | ((uint32_t)__ldg(e + 3) << 16);
                     }
-                    qf[n][i][0] = v.x;
-                    qf[n][i][1] = v.y;
                 }
+                qf[i][0] = v.x;
+                qf[i][1] = v.y;
             }
-            // this lane's rows 8 n + 2 t + c: the last token each sees
-            int32_t lim[NT][2];
-            float m[NT][2], sum[NT][2];
-            float o[NT][kMma][4];
+            // this lane's rows 2 t + c: the last token each sees
+            int32_t lim[2];
+            float m[2], sum[2];
+            float o[kMma][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int row = 8 * n + 2 * t + c;
-                    const int32_t p = s.it.pos0 + (row < rows ? row / gc : 0);
-                    lim[n][c] = p < s.it.k_hi ? p : s.it.k_hi - 1;
-                    m[n][c] = kNone;
-                    sum[n][c] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < kMma; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
+            for (int c = 0; c < 2; ++c) {
+                const int row = 2 * t + c;
+                const int32_t p = s.it.pos0 + (row < rows ? row / gc : 0);
+                lim[c] = p < s.it.k_hi ? p : s.it.k_hi - 1;
+                m[c] = kNone;
+                sum[c] = 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < kMma; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
             // positions are lim + window apart from the first token not seen;
             // a row whose limit k_hi cut keeps its own window
-            int32_t low[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
+            int32_t low[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int row = 8 * n + 2 * t + c;
+                    const int row = 2 * t + c;
                     const int64_t p = (int64_t)s.it.pos0 + (row < rows ? row / gc : 0) - a.window;
-                    low[n][c] = a.window == 0 || p < -1 ? -1 : (int32_t)p;  // tokens above it are seen
+                    low[c] = a.window == 0 || p < -1 ? -1 : (int32_t)p;  // tokens above it are seen
                 }
             const int32_t all_hi = s.it.pos0 < s.it.k_hi ? s.it.pos0 : s.it.k_hi - 1;  // every row sees up to here
             const int64_t last_pos = (int64_t)s.it.pos0 + s.it.ntok - 1;
@@ -329,11 +332,9 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
                 pg[X] = page_of(group + 3 * kFewWarps);
                 if (live) {  // warp-uniform
                     // S^T = K^ Q^T
-                    float st[NT][4];
+                    float st[4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) st[n][c] = 0.f;
+                        for (int c = 0; c < 4; ++c) st[c] = 0.f;
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
                         uint32_t lo[SUB / 2], hi[SUB / 2];
@@ -341,62 +342,53 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
                         image_row<SUB>(k_base, code_at(kc[X][1], b), hi);
 #pragma unroll
                         for (int i = 0; i < SUB / 4; ++i)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma16816<T>(st[n], lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
-                                            qf[n][b * (SUB / 4) + i][0], qf[n][b * (SUB / 4) + i][1]);
+                                mma16816<T>(st, lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
+                                            qf[b * (SUB / 4) + i][0], qf[b * (SUB / 4) + i][1]);
                     }
                     const int32_t k0 = first_of(group);
                     const bool whole = k0 + 15 <= all_hi && k0 > all_lo;
                     bool rise = false;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            st[n][c] *= a.kappa;
+                            st[c] *= a.kappa;
                             if (!whole) {
                                 const int32_t key = k0 + g + (c >> 1) * 8;
-                                if (key > lim[n][c & 1] || key <= low[n][c & 1]) st[n][c] = kNone;
+                                if (key > lim[c & 1] || key <= low[c & 1]) st[c] = kNone;
                             }
-                            rise |= st[n][c] > m[n][c & 1] + kFewSlack;
+                            rise |= st[c] > m[c & 1] + kFewSlack;
                         }
                     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                float top = fmaxf(st[n][c], st[n][c + 2]);
+                                float top = fmaxf(st[c], st[c + 2]);
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                                 // a row rises for its own scores alone, so that what it
                                 // computes does not depend on the rows beside it
-                                const bool up = top > m[n][c] + kFewSlack;
-                                const float f = up ? exp2_fast(m[n][c] - top) : 1.f;
-                                if (up) m[n][c] = top;
-                                sum[n][c] *= f;
+                                const bool up = top > m[c] + kFewSlack;
+                                const float f = up ? exp2_fast(m[c] - top) : 1.f;
+                                if (up) m[c] = top;
+                                sum[c] *= f;
 #pragma unroll
                                 for (int i = 0; i < kMma; ++i) {
-                                    o[n][i][c] *= f;
-                                    o[n][i][c + 2] *= f;
+                                    o[i][c] *= f;
+                                    o[i][c + 2] *= f;
                                 }
                             }
                     }
-                    uint32_t pf[NT][2];
+                    uint32_t pf[2];
+                    float p[4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float p[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            // nothing seen yet: the maximum is -inf and so is every score
-                            const float mm = m[n][c & 1] == kNone ? 0.f : m[n][c & 1];
-                            p[c] = exp2_fast(st[n][c] - mm);
-                        }
-                        sum[n][0] += p[0] + p[2];
-                        sum[n][1] += p[1] + p[3];
-                        pf[n][0] = transpose8x8(pack2<T>(p[0], p[1]));
-                        pf[n][1] = transpose8x8(pack2<T>(p[2], p[3]));
+                    for (int c = 0; c < 4; ++c) {
+                        // nothing seen yet: the maximum is -inf and so is every score
+                        const float mm = m[c & 1] == kNone ? 0.f : m[c & 1];
+                        p[c] = exp2_fast(st[c] - mm);
                     }
+                    sum[0] += p[0] + p[2];
+                    sum[1] += p[1] + p[3];
+                    pf[0] = transpose8x8(pack2<T>(p[0], p[1]));
+                    pf[1] = transpose8x8(pack2<T>(p[2], p[3]));
                     // O^T += V^^T P^T
 #pragma unroll
                     for (int b = 0; b < VB; ++b) {
@@ -409,9 +401,7 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
                             const uint32_t a1 = __byte_perm(e[0][i], e[1][i], 0x7632);
                             const uint32_t a2 = __byte_perm(e[2][i], e[3][i], 0x5410);
                             const uint32_t a3 = __byte_perm(e[2][i], e[3][i], 0x7632);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma16816<T>(o[n][b * (SUB / 2) + i], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                                mma16816<T>(o[b * (SUB / 2) + i], a0, a1, a2, a3, pf[0], pf[1]);
                         }
                     }
                 }
@@ -424,23 +414,19 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
 
             // the warps' states: maxima and sums first
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    sum[n][c] += __shfl_xor_sync(0xffffffffu, sum[n][c], 4);
-                    sum[n][c] += __shfl_xor_sync(0xffffffffu, sum[n][c], 8);
-                    sum[n][c] += __shfl_xor_sync(0xffffffffu, sum[n][c], 16);
+                    sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
+                    sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
+                    sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
                     if (g == 0) {
-                        wm[warp][8 * n + 2 * t + c] = m[n][c];
-                        wl[warp][8 * n + 2 * t + c] = sum[n][c];
+                        wm[warp][2 * t + c] = m[c];
+                        wl[warp][2 * t + c] = sum[c];
                     }
                 }
             __syncthreads();
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int row = 8 * n + 2 * t + c;
+                    const int row = 2 * t + c;
                     float top = kNone;
 #pragma unroll
                     for (int k = 0; k < kFewWarps; ++k)
@@ -449,55 +435,49 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
 #pragma unroll
                     for (int k = 0; k < kFewWarps; ++k)
                         if (wl[k][row] != 0.f) total = fmaf(exp2_fast(wm[k][row] - top), wl[k][row], total);
-                    const float f = sum[n][c] == 0.f ? 0.f : exp2_fast(m[n][c] - top);
-                    m[n][c] = top;
-                    sum[n][c] = total;
+                    const float f = sum[c] == 0.f ? 0.f : exp2_fast(m[c] - top);
+                    m[c] = top;
+                    sum[c] = total;
 #pragma unroll
                     for (int i = 0; i < kMma; ++i) {
-                        o[n][i][c] *= f;
-                        o[n][i][c + 2] *= f;
+                        o[i][c] *= f;
+                        o[i][c + 2] *= f;
                     }
                 }
             // then the weighted sums: the upper half of the warps to the lower, until one is left
 #pragma unroll
             for (int live = kFewWarps; live > 1; live = (live + 1) / 2) {
                 const int half = (live + 1) / 2;  // warps half .. live - 1 give to warps 0 ..
-                float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp < half ? warp : warp - half) * NT * kMma * 32 + lane;
+                float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp < half ? warp : warp - half) * kMma * 32 + lane;
                 if (warp >= half && warp < live) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
                         for (int i = 0; i < kMma; ++i)
-                            if (dyn_smem_ok(slot + (n * kMma + i) * 32, 16, 16))
-                                slot[(n * kMma + i) * 32] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+                            if (dyn_smem_ok(slot + i * 32, 16, 16))
+                                slot[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 }
                 __syncthreads();
                 if (warp < live - half) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
                         for (int i = 0; i < kMma; ++i)
-                            if (dyn_smem_ok(slot + (n * kMma + i) * 32, 16, 16)) {
-                                const float4 v = slot[(n * kMma + i) * 32];
-                                o[n][i][0] += v.x;
-                                o[n][i][1] += v.y;
-                                o[n][i][2] += v.z;
-                                o[n][i][3] += v.w;
+                            if (dyn_smem_ok(slot + i * 32, 16, 16)) {
+                                const float4 v = slot[i * 32];
+                                o[i][0] += v.x;
+                                o[i][1] += v.y;
+                                o[i][2] += v.z;
+                                o[i][3] += v.w;
                             }
                 }
                 __syncthreads();
             }
             if (warp == 0) {
-                // lane (g, t) holds columns [g dim/8, (g+1) dim/8) of rows 8 n + 2 t + c
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
+                // lane (g, t) holds columns [g dim/8, (g+1) dim/8) of rows 2 t + c
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int row = 8 * n + 2 * t + c;
+                        const int row = 2 * t + c;
                         if (row >= rows) continue;
                         if (s.whole) {
                             const int64_t orow = (s.it.tok0 + row / gc) * a.hq + head0 + row % gc;
-                            const float inv = sum[n][c] == 0.f ? 0.f : 1.f / sum[n][c];
+                            const float inv = sum[c] == 0.f ? 0.f : 1.f / sum[c];
                             T *dst = out + orow * D + g * (D / 8);
                             if (VQ_SPAN(dst, D / 8, out, a.tokens * a.hq * D)) {
                                 if (out_vec) {
@@ -506,19 +486,19 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
                                         uint32_t v[4];
 #pragma unroll
                                         for (int x = 0; x < 4; ++x)
-                                            v[x] = pack2<T>(o[n][i + x][c] * inv, o[n][i + x][c + 2] * inv);
+                                            v[x] = pack2<T>(o[i + x][c] * inv, o[i + x][c + 2] * inv);
                                         reinterpret_cast<uint4 *>(dst)[i / 4] = make_uint4(v[0], v[1], v[2], v[3]);
                                     }
                                 } else {
 #pragma unroll
                                     for (int i = 0; i < kMma; ++i) {
-                                        dst[2 * i] = narrow<T>(o[n][i][c] * inv);
-                                        dst[2 * i + 1] = narrow<T>(o[n][i][c + 2] * inv);
+                                        dst[2 * i] = narrow<T>(o[i][c] * inv);
+                                        dst[2 * i + 1] = narrow<T>(o[i][c + 2] * inv);
                                     }
                                 }
                             }
                             if (g == 0 && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq))
-                                a.lse[orow] = paged_lse(m[n][c], sum[n][c]);
+                                a.lse[orow] = paged_lse(m[c], sum[c]);
                         } else {
                             const int64_t prow = s.slot * a.tile_rows + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
                             float *dst = a.part + prow * D + g * (D / 8);
@@ -526,11 +506,11 @@ __global__ void __launch_bounds__(FewShape<D, NT>::kWarps * 32, FewShape<D, NT>:
 #pragma unroll
                                 for (int i = 0; i < kMma; i += 2)
                                     reinterpret_cast<float4 *>(dst)[i / 2] =
-                                        make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
+                                        make_float4(o[i][c], o[i][c + 2], o[i + 1][c], o[i + 1][c + 2]);
                             }
                             if (g == 0 && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
-                                a.ml[prow * 2] = m[n][c];
-                                a.ml[prow * 2 + 1] = sum[n][c];
+                                a.ml[prow * 2] = m[c];
+                                a.ml[prow * 2 + 1] = sum[c];
                             }
                         }
                     }

@@ -46,15 +46,15 @@ constexpr float kFewSlack = 8.f;  // powers of two a weight may exceed 1 by
 
 constexpr int kFewRows = 8;     // columns of a matrix instruction
 
-// Warps of a block and blocks of an SM: what the accumulators and queries of a
-// lane (dim/16 x 6 registers) leave of the register file.  (Items of 16 rows, two
-// columns of instructions on each rebuilt value, took 70 us where two items of 8
-// take 52: twice the registers leave fewer warps.)
+// Warps of a block and blocks of an SM: two blocks where a lane's accumulators
+// and queries (dim/16 x 6 registers) fit 128 registers.  At dim 256 one block of 8
+// warps at 255 registers: 12 at 168 spill (8 requests of 32768: 105 against 74 us).
+// Items of 16 rows, two columns of instructions on each rebuilt value, took 70 us
+// for drafts where two items of 8 take 52: twice the registers leave fewer warps.
 template <int D>
 struct FewShape {
-    static constexpr bool kWide = D > 128;
-    static constexpr int kWarps = kWide ? 12 : 8;
-    static constexpr int kBlocks = kWide ? 1 : 2;
+    static constexpr int kWarps = 8;
+    static constexpr int kBlocks = D > 128 ? 1 : 2;
     // shared memory: two codebook images of 32 KiB, then the merge's slots
     static constexpr size_t kSmem = 2 * 32768 + (size_t)(kWarps / 2) * kFewRows * D * sizeof(float);
 };

@@ -461,6 +461,42 @@ def test_attention_many_requests(vq, shape, new):
     check_attention(vq, c, [new] * 450)
 
 
+@pytest.mark.parametrize("new", [1, 9])
+def test_attention_more_requests_than_are_staged(vq, new):
+    """Lengths read from memory instead of shared memory."""
+    c = Cache(14, [new + i % 5 for i in range(700)], 4, 2, 64, 8, 256, 16, "bf16")
+    check_attention(vq, c, [new] * 700)
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_offsets_past_32_bits(vq, new):
+    """Pages more than 2^32 bytes apart, query tokens more than 2^31 elements in
+    all: the same bits as from a compact pool, and the append writes there too."""
+    c = Cache(15, [300, 77], 4, 2, 128, 8, 256, 16, "f16")
+    lens, table, kc, vc = c.device()
+    stride = (5 << 30) // c.pages // 16 * 16
+    far = [torch.empty(stride * c.pages, dtype=torch.uint8, device="cuda").as_strided(kc.shape, (stride, 256, 16, 1))
+           for _ in range(2)]
+    assert stride * (c.pages - 1) > 1 << 32
+    for a, b in zip(far, (kc, vc)):
+        a.copy_(b)
+    cu = i32([0, new, 2 * new])
+    q = c.queries(2 * new).cuda()
+    step = (1 << 31) // (2 * new - 1) + 8
+    step -= step % 8
+    wide = torch.empty(step * (2 * new - 1) + 4 * 128, dtype=torch.float16, device="cuda").as_strided(q.shape, (step, 128, 1))
+    wide.copy_(q)
+    want = vq.vq_paged_attention(q, cu, lens, table, kc, vc, c.kcb, c.vcb, max_new=new)
+    got = vq.vq_paged_attention(wide, cu, lens, table, *far, c.kcb, c.vcb, max_new=new)
+    assert torch.equal(want, got)
+    k = wide[:, :2]
+    slots = torch.arange(2 * new, device="cuda") + (c.pages * 16 - 2 * new)
+    near = [kc.contiguous(), vc.contiguous()]
+    vq.vq_paged_append(q[:, :2], q[:, 2:], slots, c.kcb, c.vcb, *near)
+    vq.vq_paged_append(k, wide[:, 2:], slots, c.kcb, c.vcb, *far)
+    assert all(torch.equal(a, b) for a, b in zip(near, far))
+
+
 def test_attention_scale_and_repeat(vq):
     """An explicit scale; two calls give the same bits; a dirty workspace does not matter."""
     c = Cache(10, [3000, 20, 700], 8, 2, 128, 8, 256, 16, "bf16")
@@ -587,3 +623,35 @@ def test_step_in_a_graph_equals_the_eager_step(vq):
             assert torch.equal(a[name], b[name]), name
         assert (a["out"][sum(new):] == 0).all()
     assert a["lens"].sum().item() > 50
+
+
+def test_step_on_another_stream_than_the_tensors(vq):
+    """Tensors made on the default stream, the step on a side stream that waits
+    for it: the state of the same step on the default stream."""
+    a, b = state(vq, 9), state(vq, 9)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    for s in (a, b):
+        s["new"].copy_(i32([9, 3, 1, 0, 7]))
+    for name in ("k", "v", "q"):
+        x = torch.randn(a[name].shape, generator=gen, device="cuda").half()
+        a[name].copy_(x)
+        b[name].copy_(x)
+    step(vq, a)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(vq, b, side)
+    torch.cuda.current_stream().wait_stream(side)
+    for name in ("lens", "count", "table", "cu", "slots", "kc", "vc", "out", "lse"):
+        assert torch.equal(a[name], b[name]), name
+
+
+def test_example_serving_loop(vq):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_serving.py")
+    spec = importlib.util.spec_from_file_location("paged_serving", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    report = module.main(["--steps", "30", "--requests", "5", "--prompt", "300", "--answer", "30"])
+    assert report["finished"] > 3 and report["tokens"] > 500

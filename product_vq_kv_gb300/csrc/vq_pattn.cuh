@@ -318,7 +318,12 @@ struct PagedCursor {
                 if (j >= a.items) {  // the next head group
                     j = 0;
                     r = 0;
-                    ++hx;
+                    if (++hx >= a.hkv * a.gch) {
+                        // only if cu descends, so that the walk finds less than the
+                        // plan: nothing more to do
+                        u = u1;
+                        return false;
+                    }
                 }
                 while (r < a.requests && l.start(r + 1) <= j) ++r;
                 int64_t skip;

@@ -468,6 +468,29 @@ def test_attention_more_requests_than_are_staged(vq, new):
     check_attention(vq, c, [new] * 700)
 
 
+@pytest.mark.parametrize("new", [1, 3])
+def test_attention_more_heads_than_a_tile(vq, new):
+    """160 query heads to a KV head: head groups of 8 and of 128."""
+    c = Cache(16, [150, 9, 40], 160, 1, 64, 8, 256, 16, "f16")
+    check_attention(vq, c, [new, 1, 0])
+
+
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[2], SHAPES[9]])
+def test_attention_descending_offsets_end(vq, shape):
+    """Offsets that descend are a caller's mistake: the call ends, writes inside its
+    outputs, and the next call is right."""
+    hq, hkv, dim, sub, n_c, page, dtype = shape
+    c = Cache(17, [300, 200, 100, 90], hq, hkv, dim, sub, n_c, page, dtype)
+    lens, table, kc, vc = c.device()
+    for cu in ([0, 70, 20, 90, 100], [100, 0, 0, 0, 0], [0, -5, 2000, 3, 1 << 30], [50, 60, 10, 0, 100]):
+        guard = torch.full((102, hq, dim), 7.0, dtype=DTYPES[dtype], device="cuda")
+        vq.vq_paged_attention(c.queries(100).cuda(), i32(cu), lens, table, kc, vc, c.kcb, c.vcb, out=guard[1:101])
+        torch.cuda.synchronize()
+        assert (guard[0] == 7).all() and (guard[101] == 7).all()
+    assert vq.vq_kernel_status() == 0
+    check_attention(vq, c, [30, 1, 60, 9])
+
+
 @pytest.mark.parametrize("new", [2, 40])
 def test_offsets_past_32_bits(vq, new):
     """Pages more than 2^32 bytes apart, query tokens more than 2^31 elements in

@@ -45,6 +45,9 @@ namespace vqk {
 constexpr float kFewSlack = 8.f;  // powers of two a weight may exceed 1 by
 
 constexpr int kFewRows = 8;     // columns of a matrix instruction
+// A row's maximum before it has seen a token: finite, so that the weight of a
+// hidden score, -inf, is 0 against it too (-inf less -inf would be NaN).
+constexpr float kFewLow = -3.0e38f;
 
 // Warps of a block and blocks of an SM: two blocks where a lane's accumulators
 // and queries (dim/16 x 6 registers) fit 128 registers.  At dim 256 one block of 8
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                 const int row = 2 * t + c;
                 const int32_t p = s.it.pos0 + (row < rows ? row / gc : 0);
                 lim[c] = p < s.it.k_hi ? p : s.it.k_hi - 1;
-                m[c] = kNone;
+                m[c] = kFewLow;
                 sum[c] = 0.f;
             }
 #pragma unroll
@@ -381,9 +384,7 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                     float p[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        // nothing seen yet: the maximum is -inf and so is every score
-                        const float mm = m[c & 1] == kNone ? 0.f : m[c & 1];
-                        p[c] = exp2_fast(st[c] - mm);
+                        p[c] = exp2_fast(st[c] - m[c & 1]);
                     }
                     sum[0] += p[0] + p[2];
                     sum[1] += p[1] + p[3];

@@ -157,6 +157,28 @@ __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volat
     return false;
 }
 
+// Bounded wait for a phase of each of two barriers, polled together: one wait after
+// the other leaves the tensor pipe idle for the second's round trip (about 270
+// cycles where the products wait for both a stage and the weights).
+__device__ __forceinline__ bool chunk_wait2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1,
+                                            volatile uint32_t *abort_word)
+{
+    for (int it = 0; it < kChunkPolls; ++it) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p, q;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+                     "and.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(smem_addr(bar0)), "r"(parity0), "r"(smem_addr(bar1)), "r"(parity1)
+                     : "memory");
+        if (done) return true;
+        if ((it & 15) == 15 && *abort_word) return false;
+    }
+    *abort_word = 1;
+    raise_status(kStatusWaitGaveUp);
+    return false;
+}
+
 // One segment as the roles take it from shared memory.
 struct ChunkSeg {
     int64_t tok0, slot;
@@ -674,6 +696,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             ++taken;
             return wait(&full[*st], round & 1);
         };
+        // the next stage and a tile's weights (with one tile: 243 -> 234 us at 2048
+        // tokens on 8192 cached; with two the tiles then fall into step, their softmax
+        // side by side instead of one beside the other's products: 265 -> 281)
+        auto take_with = [&](uint32_t *st, int buf) -> bool {
+            *st = taken % kChunkStages;
+            const uint32_t round = taken / kChunkStages;
+            ++taken;
+            return __all_sync(0xffffffffu, chunk_wait2(&full[*st], round & 1, &p_full[buf], n_p[buf]++ & 1, &abort_word));
+        };
         // operand descriptors differ in the address field alone (16-byte units,
         // no carry out of it below 256 KiB): one addition each
         const uint64_t q_desc = umma_smem_desc(q_addr, 2048, 128);
@@ -714,7 +745,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         scores(0, (j + 1) & 1, ks);
                         umma_commit_elected(&empty[ks]);
                     }
-                    if (!(go = take(&vs) && wait(&p_full[j & 1], n_p[j & 1]++ & 1))) break;
+                    if (!(go = take_with(&vs, j & 1))) break;
                     tc_fence_after();
                     values(0, j & 1, vs, j > 0);
                     umma_commit_elected(&o_done[0]);

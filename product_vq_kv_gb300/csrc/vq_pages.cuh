@@ -10,8 +10,9 @@
 // tokens pushes pages ceil(keep_r / P) .. ceil(L_r / P) - 1 back in the same
 // order.  Every result is fixed by these sums: no atomics, no order of arrival.
 //
-// What bounds it: latency.  A decode step moves 1.6 KB; the burst of 257
-// prompts 1.1 MB, a fifth of a microsecond of HBM time.  So one launch does
+// What bounds it: latency.  A decode step of 64 requests moves 1.6 KB and takes 6.2
+// us on the device (a graph's replay; 8.3 with 1024 threads where 256 do); a burst
+// of 257 prompts moves 1.1 MB, a fifth of a microsecond of HBM time.  So one launch does
 // everything: a cluster of 1 to 8 blocks, each of which scans all the requests
 // by itself (two 64-bit sums a request: warp shuffles, then one over the warps)
 // and keeps the scanned arrays in shared memory; then the blocks share out the

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     constexpr int kMyVec = kMyCodes < 16 ? kMyCodes : 16;
     constexpr int kCodeWords = kMyCodes < 4 ? 1 : kMyCodes / 4;
     constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    constexpr float kShift = weight_shift<T>();
     extern __shared__ __align__(128) unsigned char chunk_mem[];
     __shared__ PagedWalk<64> w;
     __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image[2], drain, seg_full[2], seg_empty[2];
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         weights(v, p + c * 16, 32, m, add);
                     }
                     const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.kappa;
-                    if (!__any_sync(0xffffffffu, top > m + kFewSlack || m == kNone)) {
+                    if (!__any_sync(0xffffffffu, top > m + (kFewSlack + kShift) || m == kNone)) {
                         done = true;
                         sum2 = add2_rn(sum2, add);
 #pragma unroll
@@ -433,10 +434,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     top *= a.kappa;  // kappa > 0
                     // a row rises for its own scores alone, so that what it computes does
                     // not depend on the rows beside it; the others are scaled by 1
-                    const bool rise = top > m + kFewSlack;
+                    const bool rise = top > m + (kFewSlack + kShift);
                     if (__any_sync(0xffffffffu, rise)) {
-                        const float f = rise ? exp2_fast(m - top) : 1.f;
-                        if (rise) m = top;
+                        const float to = rise ? top - kShift : m;
+                        const float f = rise ? exp2_fast(m - to) : 1.f;
+                        m = to;
                         sum2 = make_float2(sum2.x * f, sum2.y * f);
                         if (j > 0) {
                             // the product before this block has to be done

@@ -30,8 +30,8 @@
 //   * Codes come straight from global memory into registers two groups ahead, the
 //     page numbers three.
 //   * The running maximum follows the scores only when one exceeds it by 2^8
-//     (a vote); until then the weights are at most 2^8, well inside fp16, and
-//     nothing is rescaled.
+//     (a vote); until then nothing is rescaled (weight_shift says what range the
+//     weights then have).
 // Weights are rounded to the input type for the second product (the sum of
 // weights takes them unrounded, in fp32).
 #pragma once
@@ -42,7 +42,19 @@
 
 namespace vqk {
 
-constexpr float kFewSlack = 8.f;  // powers of two a weight may exceed 1 by
+constexpr float kFewSlack = 8.f;  // powers of two by which a row's maximum may lag
+
+// Powers of two that the weights of 16-bit products are shifted up by: the
+// reference of a row is its maximum (as far as it has followed) less this much.
+// fp16 has nothing below 2^-24: unshifted, 131072 tokens at 2^-26 beside one token
+// at 1 would count in the sum, 2^-9 of it, and not in the product.  At 7 the largest
+// weight is 2^(7 + 8), inside fp16, and the least one that is kept 2^-32 of the
+// maximum's.  bf16 has fp32's range and needs none.
+template <typename T>
+__host__ __device__ constexpr float weight_shift()
+{
+    return std::is_same<T, __half>::value ? 7.f : 0.f;
+}
 
 constexpr int kFewRows = 8;     // columns of a matrix instruction
 // A row's maximum before it has seen a token: finite, so that the weight of a
@@ -191,6 +203,7 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
     constexpr int KB = NS / 4, VB = NS / 8;        // code bytes a lane takes of a key, of a value
     constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
     constexpr int kMma = D / 16;                   // instructions per 16 tokens and 8 rows, each product
+    constexpr float kShift = weight_shift<T>();
     static_assert(SUB == 4 || SUB == 8, "sub-vectors of 4 or 8");
     extern __shared__ __align__(128) unsigned char few_mem[];
     __shared__ PagedWalk<> w;
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                                 const int32_t key = k0 + g + (c >> 1) * 8;
                                 if (key > lim[c & 1] || key <= low[c & 1]) st[c] = kNone;
                             }
-                            rise |= st[c] > m[c & 1] + kFewSlack;
+                            rise |= st[c] > m[c & 1] + (kFewSlack + kShift);
                         }
                     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -369,9 +382,10 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                                 // a row rises for its own scores alone, so that what it
                                 // computes does not depend on the rows beside it
-                                const bool up = top > m[c] + kFewSlack;
-                                const float f = up ? exp2_fast(m[c] - top) : 1.f;
-                                if (up) m[c] = top;
+                                const bool up = top > m[c] + (kFewSlack + kShift);
+                                const float ref = up ? top - kShift : m[c];
+                                const float f = up ? exp2_fast(m[c] - ref) : 1.f;
+                                m[c] = ref;
                                 sum[c] *= f;
 #pragma unroll
                                 for (int i = 0; i < kMma; ++i) {

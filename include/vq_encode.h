@@ -364,7 +364,10 @@ vq_status vq_paged_append(const void *k, const void *v, int64_t k_stride, int64_
  * with NaN or infinities does not touch another row.
  *   q          token t at t * q_stride elements, [heads_q][head_dim], device,
  *              dtype
- *   cu_new     [requests + 1]  device (vq_paged_reserve)
+ *   cu_new     [requests + 1]  device (vq_paged_reserve); ascends.  Offsets
+ *              outside [0, tokens] are taken into it; where they descend the
+ *              call ends and stays inside its buffers, and what the rows get
+ *              is unspecified
  *   lens       [requests]  device: lengths with the new tokens
  *   max_new    the most new tokens of a request if the host knows it (0: it
  *              does not).  It chooses kernels and never changes what is

@@ -98,19 +98,19 @@ struct PagedLens {
     const int32_t *starts;  // start(0 .. requests), or null: computed
     int32_t requests, tile;
     int64_t tokens;
-    __device__ __forceinline__ int64_t first(int r) const
+    __host__ __device__ __forceinline__ int64_t first(int r) const
     {
         if (r > requests) return tokens;
         const int64_t c = cu[r];
         return c < 0 ? 0 : c > tokens ? tokens : c;
     }
-    __device__ __forceinline__ int64_t compute_start(int r) const
+    __host__ __device__ __forceinline__ int64_t compute_start(int r) const
     {
         return (int64_t)((uint32_t)first(r) / (uint32_t)tile) + r;
     }
-    __device__ __forceinline__ int64_t start(int r) const { return starts ? starts[r] : compute_start(r); }
+    __host__ __device__ __forceinline__ int64_t start(int r) const { return starts ? starts[r] : compute_start(r); }
     // the last r in [0, requests] with start(r) <= j
-    __device__ __forceinline__ int find(int64_t j) const
+    __host__ __device__ __forceinline__ int find(int64_t j) const
     {
         int lo = 0, hi = requests;
         while (lo < hi) {
@@ -123,7 +123,7 @@ struct PagedLens {
 };
 
 // b * all / n for 0 <= b <= n, in 32 bits where they do.
-__device__ __forceinline__ int64_t part_of(int64_t b, int64_t all, int64_t n)
+__host__ __device__ __forceinline__ int64_t part_of(int64_t b, int64_t all, int64_t n)
 {
     if (all * n <= 0xffffffffll) return (uint32_t)(b * all) / (uint32_t)n;
     return b * all / n;
@@ -131,7 +131,7 @@ __device__ __forceinline__ int64_t part_of(int64_t b, int64_t all, int64_t n)
 
 // Item j, which belongs to request r; units = 0 for a hole (then *skip is the
 // next item worth a look).
-__device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, const PagedLens &l, int64_t j, int r,
+__host__ __device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, const PagedLens &l, int64_t j, int r,
                                                 int64_t *skip)
 {
     PagedItem it{};
@@ -165,10 +165,56 @@ __device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, const PagedL
 }
 
 // What an item costs (0: a hole).
-__device__ __forceinline__ int32_t paged_cost(const PagedArgs &a, int32_t units)
+__host__ __device__ __forceinline__ int32_t paged_cost(const PagedArgs &a, int32_t units)
 {
     return units == 0 ? 0 : a.no_split ? 1 : units + a.item_cost;
 }
+
+// The items that one of `threads` threads lays out.
+struct PagedRun {
+    int64_t j0, j1;
+    __host__ __device__ __forceinline__ PagedRun(const PagedArgs &a, int tid, int threads)
+    {
+        const int64_t per = (a.items + threads - 1) / threads;
+        j0 = tid * per;
+        j1 = j0 + per < a.items ? j0 + per : a.items;
+    }
+    // their cost; *r0: the first one's request
+    __host__ __device__ __forceinline__ int64_t cost(const PagedArgs &a, const PagedLens &l, int *r0) const
+    {
+        int64_t sum = 0;
+        if (j0 < j1) {
+            *r0 = l.find(j0);
+            int r = *r0;
+            for (int64_t j = j0; j < j1;) {
+                while (r < a.requests && l.start(r + 1) <= j) ++r;
+                int64_t skip;
+                sum += paged_cost(a, paged_item(a, l, j, r, &skip).units);
+                j = skip;
+            }
+        }
+        return sum;
+    }
+    // the item at `left` of that cost, and where in its cost
+    __host__ __device__ __forceinline__ bool locate(const PagedArgs &a, const PagedLens &l, int r, int64_t left,
+                                                    int64_t *item, int32_t *request, int32_t *at) const
+    {
+        for (int64_t j = j0; j < j1;) {
+            while (r < a.requests && l.start(r + 1) <= j) ++r;
+            int64_t skip;
+            const int32_t u = paged_cost(a, paged_item(a, l, j, r, &skip).units);
+            if (left < u) {
+                *item = j;
+                *request = r;
+                *at = (int32_t)left;
+                return true;
+            }
+            left -= u;
+            j = skip;
+        }
+        return false;
+    }
+};
 
 // Where a block stands on the line of costs.
 template <int STAGE>
@@ -216,20 +262,9 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
             __syncthreads();
         }
     }
-    const int64_t per = (a.items + THREADS - 1) / THREADS;
-    const int64_t j0 = tid * per, j1 = j0 + per < a.items ? j0 + per : a.items;
+    const PagedRun run(a, tid, THREADS);
     int r0 = 0;
-    int64_t mine = 0;
-    if (j0 < j1) {
-        r0 = l.find(j0);
-        int r = r0;
-        for (int64_t j = j0; j < j1;) {
-            while (r < a.requests && l.start(r + 1) <= j) ++r;
-            int64_t skip;
-            mine += paged_cost(a, paged_item(a, l, j, r, &skip).units);
-            j = skip;
-        }
-    }
+    const int64_t mine = run.cost(a, l, &r0);
     int64_t s = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -260,21 +295,13 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
     const int64_t rem = u0 - hx * total;
     __syncthreads();
     if (mine > 0 && before <= rem && rem < before + mine) {
-        int64_t left = rem - before;
-        int r = r0;
-        for (int64_t j = j0; j < j1;) {
-            while (r < a.requests && l.start(r + 1) <= j) ++r;
-            int64_t skip;
-            const int32_t u = paged_cost(a, paged_item(a, l, j, r, &skip).units);
-            if (left < u) {
-                w.hx = (int32_t)hx;
-                w.j = j;
-                w.r = r;
-                w.at = (int32_t)left;
-                break;
-            }
-            left -= u;
-            j = skip;
+        int64_t j;
+        int32_t r, at;
+        if (run.locate(a, l, r0, rem - before, &j, &r, &at)) {
+            w.hx = (int32_t)hx;
+            w.j = j;
+            w.r = r;
+            w.at = at;
         }
     }
     __syncthreads();
@@ -294,10 +321,11 @@ struct PagedSegment {
 // computes the same.
 struct PagedCursor {
     int64_t u, u1, j;
-    int32_t r, at, hx;
+    int32_t r, at, hx, block;
     template <typename W>
-    __device__ __forceinline__ void init(const W &w)
+    __host__ __device__ __forceinline__ void init(const W &w, int32_t b)
     {
+        block = b;
         u = w.u0;
         u1 = w.u1;
         j = w.j;
@@ -308,10 +336,9 @@ struct PagedCursor {
     // The next segment; false at the end.  `note` is filled if the block
     // begins an item that it does not finish.
     template <typename W>
-    __device__ __forceinline__ bool next(const PagedArgs &a, const W &w, const PagedLens &l, PagedSegment &s,
+    __host__ __device__ __forceinline__ bool next(const PagedArgs &a, const W &w, const PagedLens &l, PagedSegment &s,
                                          PagedNote &note)
     {
-        const int64_t b = blockIdx.x;
         for (;;) {
             if (u >= u1) return false;
             for (;;) {
@@ -353,7 +380,7 @@ struct PagedCursor {
             if (s.end == 0) continue;  // only set-up: the next block begins the item
             s.hx = hx;
             s.whole = s.begin == 0 && s.end == s.it.units;
-            s.slot = 2 * b + (s.begin == 0 ? 1 : 0);
+            s.slot = 2 * (int64_t)block + (s.begin == 0 ? 1 : 0);
             if (s.begin == 0 && !s.whole) {
                 const int64_t all = w.total * ((int64_t)a.hkv * a.gch);
                 const int64_t last = u_item + cost;  // one past its last unit
@@ -362,9 +389,12 @@ struct PagedCursor {
                 note.head0 = hx / a.gch * a.group + g0;
                 note.gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
                 note.rows = s.it.ntok * note.gc;
-                note.first = (int32_t)b;
-                // the block of position x: the c with floor(c U / N) <= x < floor((c + 1) U / N)
-                note.last = (int32_t)((last * w.blocks - 1) / all);
+                note.first = block;
+                // the block of position x: the c with floor(c U / N) <= x < floor((c + 1) U / N);
+                // past the last block only if cu descends, so that the walk finds more than
+                // the plan: the workspace ends there
+                const int64_t c = (last * w.blocks - 1) / all;
+                note.last = (int32_t)(c < w.blocks ? c : w.blocks - 1);
             }
             return true;
         }
@@ -433,7 +463,7 @@ __global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant
     PagedNote note{};
     if (paged_plan<kUnit>(a, w, l)) {
         PagedCursor cur;
-        cur.init(w);
+        cur.init(w, (int32_t)blockIdx.x);
         PagedSegment s;
         while (cur.next(a, w, l, s, note)) {
             const int r = cur.r;

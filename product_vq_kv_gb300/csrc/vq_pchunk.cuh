@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     } else if (work && warp == 13) {
         // ------------------------------------------------ the segments
         PagedCursor cur;
-        cur.init(w);
+        cur.init(w, (int32_t)blockIdx.x);
         PagedSegment seg;
         PagedNote note{};
         bool more = true;

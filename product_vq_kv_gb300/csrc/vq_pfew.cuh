@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
     PagedNote note{};
     if (paged_plan<kFewThreads>(a, w, l)) {
         PagedCursor cur;
-        cur.init(w);
+        cur.init(w, (int32_t)blockIdx.x);
         PagedSegment s;
         int built = -1;  // the KV head whose codebooks are in shared memory
         while (cur.next(a, w, l, s, note)) {

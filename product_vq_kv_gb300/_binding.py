@@ -540,9 +540,22 @@ def _extent(t) -> int | None:
     return t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 1 else None
 
 
-def _out_like(out, name, shape, dtype, device):
-    if out is None:
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for work on ``stream`` (None: the current stream).
+
+    torch hands the memory of a freed tensor out again in the order of the stream
+    that the tensor was made on.  One made on the current stream for work on another
+    could lie where the current stream still reads, and be handed out again while
+    the other still writes: so it is made on ``stream`` itself."""
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out_like(out, name, shape, dtype, device, stream):
+    if out is None:
+        return _empty(shape, dtype, device, stream)
     if (not isinstance(out, torch.Tensor) or out.dtype != dtype or tuple(out.shape) != tuple(shape)
             or out.device != device or not out.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
@@ -563,7 +576,8 @@ def vq_paged_reserve(lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     table's entries of new pages are written in place.  Returns ``(lens_out,
     free_count_out, cu_new, slots)``; pass ``lens_out=lens`` and
     ``free_count_out=free_count`` to update those in place.  Refused requests
-    (see ``include/vq_encode.h``) keep their length and get slots of -1."""
+    (see ``include/vq_encode.h``) keep their length and get slots of -1.  New outputs
+    are allocated on ``stream``."""
     r = _extent(lens)
     _i32_tensor(lens, "lens", (r,), None)
     dev, pages = lens.device, _extent(free_pages)
@@ -573,10 +587,10 @@ def vq_paged_reserve(lens: torch.Tensor, new_lens: torch.Tensor, free_pages: tor
     blocks = _table_tensor(block_table, r, dev)
     if total_new < 0:
         raise ValueError("total_new must not be negative")
-    lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev)
-    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev)
-    cu_new = _out_like(cu_new, "cu_new", (r + 1,), torch.int32, dev)
-    slots = _out_like(slots, "slots", (total_new,), torch.int64, dev)
+    lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev, stream)
+    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev, stream)
+    cu_new = _out_like(cu_new, "cu_new", (r + 1,), torch.int32, dev, stream)
+    slots = _out_like(slots, "slots", (total_new,), torch.int64, dev, stream)
     _launch(load_library().vq_paged_reserve, "vq_paged_reserve", dev, stream, lens.data_ptr(),
             new_lens.data_ptr(), r, free_pages.data_ptr(), free_count.data_ptr(), pages,
             block_table.data_ptr(), blocks, page_size, total_new, lens_out.data_ptr(),
@@ -591,7 +605,8 @@ def vq_paged_trim(lens: torch.Tensor, keep_lens: torch.Tensor, block_table: torc
                   stream: torch.cuda.Stream | None = None) -> tuple:
     """Cut each request to ``keep_lens[r]`` tokens and push the pages it no
     longer needs on ``free_pages`` (in place).  Returns ``(lens_out,
-    free_count_out)``, which may be ``lens`` and ``free_count`` themselves."""
+    free_count_out)``, which may be ``lens`` and ``free_count`` themselves; new ones are
+    allocated on ``stream``."""
     r = _extent(lens)
     _i32_tensor(lens, "lens", (r,), None)
     dev, pages = lens.device, _extent(free_pages)
@@ -599,8 +614,8 @@ def vq_paged_trim(lens: torch.Tensor, keep_lens: torch.Tensor, block_table: torc
     blocks = _table_tensor(block_table, r, dev)
     _i32_tensor(free_pages, "free_pages", (pages,), dev)
     _i32_tensor(free_count, "free_count", (1,), dev)
-    lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev)
-    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev)
+    lens_out = _out_like(lens_out, "lens_out", (r,), torch.int32, dev, stream)
+    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev, stream)
     _launch(load_library().vq_paged_trim, "vq_paged_trim", dev, stream, lens.data_ptr(),
             keep_lens.data_ptr(), r, block_table.data_ptr(), blocks, page_size, free_pages.data_ptr(),
             free_count.data_ptr(), pages, lens_out.data_ptr(), free_count_out.data_ptr())
@@ -749,7 +764,8 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
     where the host knows it.  Returns ``out`` ``[T, Hq, D]``, or ``(out, lse)``
     with ``lse`` ``[T, Hq]`` float32 where ``return_lse`` is set or ``lse`` is
     given.  A workspace of :func:`vq_paged_attention_workspace_bytes` bytes is
-    allocated here (by torch) if none is given."""
+    allocated here (by torch) if none is given; it and new outputs are allocated on
+    ``stream``."""
     _token_rows(q, "q", None)
     dev = q.device
     tokens, hq, d = q.shape
@@ -764,12 +780,12 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
     blocks = _table_tensor(block_table, r, dev)
     if max_new < 0:
         raise ValueError("max_new must not be negative")
-    out = _out_like(out, "out", (tokens, hq, d), q.dtype, dev)
+    out = _out_like(out, "out", (tokens, hq, d), q.dtype, dev, stream)
     if return_lse or lse is not None:
-        lse = _out_like(lse, "lse", (tokens, hq), torch.float32, dev)
+        lse = _out_like(lse, "lse", (tokens, hq), torch.float32, dev, stream)
     if workspace is None:
         nbytes = _paged_workspace(dev.index, r, tokens, max_new, hq, hkv, d, sub, n_c, page_size)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(nbytes, torch.uint8, dev, stream)
     else:
         _device_tensor(workspace, "workspace")
         if workspace.device != dev:

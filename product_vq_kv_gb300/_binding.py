@@ -2,7 +2,8 @@
 
 Every function here has the name of the C entry point it calls (declared in
 ``include/vq_encode.h``) and does nothing but check and convert its arguments,
-allocate the output tensor when asked to, and pass the current CUDA stream.
+allocate the output tensor when asked to (on the stream of the call), and pass the
+current CUDA stream or the given one.
 All computation happens in the library's CUDA kernels; there is no other code
 path.  If the library has not been built the first call raises.
 """
@@ -192,6 +193,19 @@ def _device_tensor(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for work on ``stream`` (None: the current stream).
+
+    torch hands the memory of a freed tensor out again in the order of the stream
+    that the tensor was made on.  One made on the current stream for work on another
+    could lie where the current stream still reads, and be handed out again while
+    the other still writes: so it is made on ``stream`` itself."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def vq_encode(x: torch.Tensor, codebook: torch.Tensor, out: torch.Tensor | None = None,
               stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """Indices of the nearest centroid for each row of ``x``.
@@ -209,7 +223,7 @@ def vq_encode(x: torch.Tensor, codebook: torch.Tensor, out: torch.Tensor | None 
     if x.dtype != codebook.dtype:
         raise TypeError("x and codebook must share a dtype")
     if out is None:
-        out = torch.empty(x.shape[0], dtype=torch.uint32, device=x.device)
+        out = _empty(x.shape[0], torch.uint32, x.device, stream)
     elif out.dtype != torch.uint32 or out.shape != (x.shape[0],) or not out.is_contiguous():
         raise ValueError("out must be a contiguous uint32 tensor of shape [N]")
     st = load_library().vq_encode(x.data_ptr(), codebook.data_ptr(), x.shape[0],
@@ -235,7 +249,7 @@ def vq_encode_grouped(x: torch.Tensor, codebooks: torch.Tensor,
         raise TypeError("x and codebooks must share a dtype")
     g, m, sub = x.shape
     if out is None:
-        out = torch.empty((g, m), dtype=torch.uint32, device=x.device)
+        out = _empty((g, m), torch.uint32, x.device, stream)
     elif out.dtype != torch.uint32 or out.shape != (g, m) or not out.is_contiguous():
         raise ValueError("out must be a contiguous uint32 tensor of shape [G, M]")
     st = load_library().vq_encode_grouped(x.data_ptr(), codebooks.data_ptr(), g, m,
@@ -260,7 +274,7 @@ def vq_encode_grouped_u8(x: torch.Tensor, codebooks: torch.Tensor,
         raise TypeError("x and codebooks must share a dtype")
     g, m, sub = x.shape
     if out is None:
-        out = torch.empty((g, m), dtype=torch.uint8, device=x.device)
+        out = _empty((g, m), torch.uint8, x.device, stream)
     elif out.dtype != torch.uint8 or out.shape != (g, m) or not out.is_contiguous():
         raise ValueError("out must be a contiguous uint8 tensor of shape [G, M]")
     st = load_library().vq_encode_grouped_u8(x.data_ptr(), codebooks.data_ptr(), g, m,
@@ -294,7 +308,7 @@ def vq_encode_grouped_smooth(x: torch.Tensor, smooth: torch.Tensor, codebooks: t
     g, m, sub = x.shape
     odt = torch.uint8 if index_bytes == 1 else torch.uint32
     if out is None:
-        out = torch.empty((g, m), dtype=odt, device=x.device)
+        out = _empty((g, m), odt, x.device, stream)
     elif out.dtype != odt or out.shape != (g, m) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {odt} tensor of shape [G, M]")
     st = load_library().vq_encode_grouped_smooth(
@@ -322,14 +336,14 @@ def vq_scalar_quantize(x: torch.Tensor, centroids: torch.Tensor, out: torch.Tens
     _device_tensor(x, "x")
     _f32_vector(centroids, "centroids")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        out = _empty(x.shape, torch.uint8, x.device, stream)
     elif out.dtype != torch.uint8 or out.shape != x.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous uint8 tensor of x's shape")
     code = _dtype_code(x)
     lib = load_library()
     need = int(lib.vq_scalar_quantize_workspace_bytes(code))
     if workspace is None and use_table and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib.vq_scalar_quantize(x.data_ptr(), code, x.numel(), centroids.data_ptr(),
@@ -349,7 +363,7 @@ def vq_scalar_dequantize(idx: torch.Tensor, centroids: torch.Tensor,
     if idx.dtype != torch.uint8:
         raise TypeError("idx must be uint8")
     if out is None:
-        out = torch.empty(idx.shape, dtype=dtype, device=idx.device)
+        out = _empty(idx.shape, dtype, idx.device, stream)
     st = load_library().vq_scalar_dequantize(idx.data_ptr(), idx.numel(), centroids.data_ptr(),
                                              centroids.numel(), _dtype_code(out), out.data_ptr(),
                                              _stream_handle(stream, idx.device))
@@ -367,7 +381,7 @@ def vq_hadamard_rotate(x: torch.Tensor, diag: torch.Tensor, out: torch.Tensor | 
     if diag.numel() != dim:
         raise ValueError("diag must have one entry per column")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+        out = _empty(x.shape, torch.float32, x.device, stream)
     st = load_library().vq_hadamard_rotate(x.data_ptr(), _dtype_code(x), diag.data_ptr(),
                                            x.numel() // dim, dim, out.data_ptr(),
                                            _stream_handle(stream, x.device))
@@ -387,7 +401,7 @@ def vq_hadamard_quantize(x: torch.Tensor, diag: torch.Tensor, centroids: torch.T
     if diag.numel() != dim:
         raise ValueError("diag must have one entry per column")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        out = _empty(x.shape, torch.uint8, x.device, stream)
     st = load_library().vq_hadamard_quantize(x.data_ptr(), _dtype_code(x), diag.data_ptr(),
                                              x.numel() // dim, dim, centroids.data_ptr(),
                                              centroids.numel(), out.data_ptr(),
@@ -413,7 +427,7 @@ def vq_dequantize_grouped(idx: torch.Tensor, codebooks: torch.Tensor,
     g, m = idx.shape
     n_c, sub = codebooks.shape[1], codebooks.shape[2]
     if out is None:
-        out = torch.empty((g, m, sub), dtype=codebooks.dtype, device=idx.device)
+        out = _empty((g, m, sub), codebooks.dtype, idx.device, stream)
     elif out.dtype != codebooks.dtype or out.shape != (g, m, sub) or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of shape [G, M, sub_dim] in the "
                          "codebooks' dtype")
@@ -468,9 +482,9 @@ def _check_attention_args(q, k_codes, k_codebooks, v_codes, v_codebooks):
     return b, hq, hkv, tokens, d, sub, n_c
 
 
-def _check_attention_out(out, q):
+def _check_attention_out(out, q, stream):
     if out is None:
-        return torch.empty_like(q)
+        return _empty(q.shape, q.dtype, q.device, stream)
     if (not isinstance(out, torch.Tensor) or out.dtype != q.dtype or out.shape != q.shape
             or out.device != q.device or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
@@ -492,10 +506,10 @@ def vq_attention_decode(q: torch.Tensor, k_codes: torch.Tensor, k_codebooks: tor
     """
     b, hq, hkv, tokens, d, sub, n_c = _check_attention_args(q, k_codes, k_codebooks, v_codes,
                                                             v_codebooks)
-    out = _check_attention_out(out, q)
+    out = _check_attention_out(out, q, stream)
     if workspace is None:
         nbytes = vq_attention_workspace_bytes(b, hq, hkv, tokens, d, sub, n_c, window)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 16), torch.uint8, q.device, stream)
     else:
         _device_tensor(workspace, "workspace")
         if workspace.device != q.device:
@@ -538,19 +552,6 @@ def _table_tensor(t, requests: int, device) -> int:
 def _extent(t) -> int | None:
     """The extent of a 1-D tensor; None if it is none."""
     return t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 1 else None
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A new tensor for work on ``stream`` (None: the current stream).
-
-    torch hands the memory of a freed tensor out again in the order of the stream
-    that the tensor was made on.  One made on the current stream for work on another
-    could lie where the current stream still reads, and be handed out again while
-    the other still writes: so it is made on ``stream`` itself."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _out_like(out, name, shape, dtype, device, stream):
@@ -821,7 +822,7 @@ def vq_attention_decode_static(q: torch.Tensor, k_codes: torch.Tensor, k_codeboo
         raise VQError(VQ_ERR_INVALID_ARG,
                       f"vq_attention_decode_static (one token slice needs {b * hq * (d + 2) * 4} "
                       f"bytes of scratch; the built-in array holds {ATTN_STATIC_SCRATCH_BYTES})")
-    out = _check_attention_out(out, q)
+    out = _check_attention_out(out, q, stream)
     with torch.cuda.device(q.device):
         st = load_library().vq_attention_decode_static(
             q.data_ptr(), k_codes.data_ptr(), k_codebooks.data_ptr(), v_codes.data_ptr(),
@@ -901,7 +902,7 @@ def vq_encode_partition(x: torch.Tensor, codebooks: torch.Tensor, world: int, ra
     slices = vq_partition(g, m, world, rank)
     n = sum(ng * nr for _, ng, _, nr in slices)
     if out is None:
-        out = torch.empty(n, dtype=torch.uint32, device=x.device)
+        out = _empty(n, torch.uint32, x.device, stream)
     elif out.dtype != torch.uint32 or out.shape != (n,) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous uint32 tensor of shape [{n}]")
     lib = load_library()

@@ -78,6 +78,36 @@ PAGED = {
                                                       return_lse=True, **kw)),
 }
 
+DENSE = {
+    "encode": (1, lambda kw: vq.vq_encode(half(9, 8), half(16, 8), **kw)),
+    "grouped": (1, lambda kw: vq.vq_encode_grouped(half(2, 9, 8), half(2, 16, 8), **kw)),
+    "u8": (1, lambda kw: vq.vq_encode_grouped_u8(half(2, 9, 8), half(2, 16, 8), **kw)),
+    "smooth": (1, lambda kw: vq.vq_encode_grouped_smooth(half(2, 9, 8), fake((2, 64), torch.float32), half(2, 16, 8), 64,
+                                                         **kw)),
+    "scalar": (2, lambda kw: vq.vq_scalar_quantize(half(9, 8), fake((16,), torch.float32), **kw)),
+    "scalar back": (1, lambda kw: vq.vq_scalar_dequantize(u8(9, 8), fake((16,), torch.float32), **kw)),
+    "rotate": (1, lambda kw: vq.vq_hadamard_rotate(half(9, 8), fake((8,), torch.float32), **kw)),
+    "hadamard": (1, lambda kw: vq.vq_hadamard_quantize(half(9, 8), fake((8,), torch.float32),
+                                                       fake((4,), torch.float32), **kw)),
+    "decode": (1, lambda kw: vq.vq_dequantize_grouped(u8(2, 9), half(2, 16, 8), **kw)),
+    "attention": (2, lambda kw: vq.vq_attention_decode(half(1, 4, 64), u8(1, 2, 5, 8), half(2, 256, 8), u8(1, 2, 5, 8),
+                                                       half(2, 256, 8), **kw)),
+    "static attention": (1, lambda kw: vq.vq_attention_decode_static(half(1, 4, 64), u8(1, 2, 5, 8), half(2, 256, 8),
+                                                                     u8(1, 2, 5, 8), half(2, 256, 8), **kw)),
+}
+
+
+@pytest.mark.parametrize("name", DENSE)
+def test_dense_allocations_are_made_on_the_streams_of_their_work(allocations, monkeypatch, name):
+    monkeypatch.setattr(bind, "_stream_handle", lambda stream, device: 0)
+    count, call = DENSE[name]
+    call({})
+    assert allocations == [None] * count
+    allocations.clear()
+    side = FakeStream()
+    call({"stream": side})
+    assert allocations == [side] * count
+
 
 @pytest.mark.parametrize("name", PAGED)
 def test_paged_allocations_are_made_on_the_streams_of_their_work(allocations, name):
@@ -125,3 +155,26 @@ def test_paged_attention_on_side_streams_without_workspaces(new):
     torch.cuda.synchronize()
     for i, (out, lse) in enumerate(got):
         assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
+@pytest.mark.gpu
+def test_attention_decode_on_side_streams_without_workspaces():
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    cases = []
+    for _ in range(2):
+        q = torch.randn((4, 8, 128), generator=gen, device="cuda").half()
+        kc, vc = (torch.randint(0, 256, (4, 2, 3000, 16), generator=gen, device="cuda", dtype=torch.uint8)
+                  for _ in range(2))
+        kcb, vcb = (torch.randn((2, 256, 8), generator=gen, device="cuda").half() for _ in range(2))
+        cases.append((q, kc, kcb, vc, vcb))
+    want = [vq.vq_attention_decode(*c) for c in cases]
+    sides = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got += [vq.vq_attention_decode(*case, stream=side) for side, case in zip(sides, cases)]
+        scratch = [torch.full((n,), -1, dtype=torch.int32, device="cuda") for n in (1 << 12, 1 << 18, 1 << 22)]
+        del scratch
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert torch.equal(out, want[i % 2])

@@ -114,7 +114,7 @@ vq_status attn_launch_k(const AttnPlan &p, const void *q, const uint8_t *kcodes,
     if (p.smem > 48 * 1024 &&
         cudaFuncSetAttribute(kp, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
             cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     kp<<<(unsigned)(p.base * p.sh.splits), kAttnThreads, p.smem, st>>>(
         static_cast<const T *>(q), kcodes, static_cast<const T *>(kcb), vcodes,
         static_cast<const T *>(vcb), p.sh, part);
@@ -176,10 +176,8 @@ vq_status attn_launch(const AttnPlan &p, const void *q, const uint8_t *kcodes, c
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, vqk::attn_combine<T>, (const float *)part, rows, p.sh.head_dim,
-                           p.sh.splits, static_cast<T *>(out)) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return VQ_ERR_CUDA;
-    }
+                           p.sh.splits, static_cast<T *>(out)) != cudaSuccess)
+        return vqh_failed();
     return vqh_launched(st, vqh_status_attn);
 }
 
@@ -294,7 +292,7 @@ vq_status vq_attention_decode_static(const void *q, const uint8_t *k_codes,
     // The array used is the current device's, so q must live there: a kernel
     // on another device would write the partials into this device's copy.
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return VQ_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return vqh_failed();
     if (q != nullptr) {
         cudaPointerAttributes at{};
         if (cudaPointerGetAttributes(&at, q) != cudaSuccess) {
@@ -306,7 +304,7 @@ vq_status vq_attention_decode_static(const void *q, const uint8_t *k_codes,
         if (at.type == cudaMemoryTypeDevice && at.device != dev) return VQ_ERR_INVALID_ARG;
     }
     void *scratch = static_scratch(dev);
-    if (scratch == nullptr) return VQ_ERR_CUDA;
+    if (scratch == nullptr) return vqh_failed();
     return vq_attention_decode(q, k_codes, k_codebooks, v_codes, v_codebooks, batch, heads_q,
                                heads_kv, tokens, head_dim, sub_dim, n_centroids, window, scale,
                                dtype, out, scratch, VQ_ATTN_STATIC_SCRATCH_BYTES, stream);

@@ -193,7 +193,7 @@ vq_status launch_tc(const Args &a, const Plan &p)
     auto kernel = tc_kernel<T, SUB, OutT, SMOOTH>();
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
         cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     kernel<<<(unsigned)p.blocks, 128 * TcConfig<SUB, tc_split<T, SMOOTH>()>::kTps, p.smem, a.stream>>>(
         static_cast<const T *>(a.x), static_cast<const T *>(a.cb), a.n_per_group, a.n_centroids,
         p.tiles_per_group, p.tc_tiles, 1.0f, static_cast<OutT *>(a.out), a.smooth,
@@ -208,7 +208,7 @@ vq_status launch_filter(const Args &a, const Plan &p)
     if (p.smem > 48 * 1024) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)p.smem) != cudaSuccess)
-            return VQ_ERR_CUDA;
+            return vqh_failed();
     }
     kernel<<<(unsigned)p.blocks, p.threads, p.smem, a.stream>>>(
         static_cast<const T *>(a.x), static_cast<const T *>(a.cb), a.n_per_group, a.n_centroids,
@@ -224,7 +224,7 @@ vq_status launch_fast(const Args &a, const Plan &p)
     if (p.smem > 48 * 1024) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)p.smem) != cudaSuccess)
-            return VQ_ERR_CUDA;
+            return vqh_failed();
     }
     kernel<<<(unsigned)p.blocks, p.threads, p.smem, a.stream>>>(
         static_cast<const T *>(a.x), static_cast<const T *>(a.cb), a.n_per_group, a.n_centroids,
@@ -372,7 +372,7 @@ struct HostPipe {
                  cudaEventCreateWithFlags(&encoded[i], ev_flags) == cudaSuccess &&
                  cudaEventCreateWithFlags(&copied[i], ev_flags) == cudaSuccess;
         ready = ok;
-        return ok ? VQ_OK : VQ_ERR_CUDA;
+        return ok ? VQ_OK : vqh_failed();
     }
 };
 
@@ -436,16 +436,16 @@ vq_status vq_encode_grouped_host(const void *x_host, const void *codebooks_host,
     if (device_view(x_host, &x_view) && device_view(out_host, &out_view)) {
         if (cudaMemcpyAsync(codebooks_dev, codebooks_host, cb_bytes, cudaMemcpyHostToDevice, st) !=
             cudaSuccess)
-            return VQ_ERR_CUDA;
+            return vqh_failed();
         Args z{x_view, codebooks_dev, n_groups, n_per_group, n_centroids, sub_dim, dtype,
                out_view, st};
         s = run(z);
         if (s != VQ_OK) return s;
-        return cudaStreamSynchronize(st) == cudaSuccess ? VQ_OK : VQ_ERR_CUDA;
+        return cudaStreamSynchronize(st) == cudaSuccess ? VQ_OK : vqh_failed();
     }
 
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return VQ_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return vqh_failed();
     HostPipe &hp = host_pipes[dev];
     std::lock_guard<std::mutex> guard(hp.mu);
     if (!hp.ready && (s = hp.init()) != VQ_OK) return s;
@@ -504,7 +504,7 @@ vq_status vq_encode_grouped_host(const void *x_host, const void *codebooks_host,
     ok = ok && cudaEventRecord(hp.start, hp.d2h) == cudaSuccess &&
          cudaStreamWaitEvent(st, hp.start, 0) == cudaSuccess &&
          cudaStreamSynchronize(hp.d2h) == cudaSuccess;
-    return ok ? VQ_OK : VQ_ERR_CUDA;
+    return ok ? VQ_OK : vqh_failed();
 }
 
 vq_status vq_encode_grouped_u8(const void *x, const void *codebooks, int64_t n_groups,
@@ -689,13 +689,13 @@ vq_status vq_kernel_status(uint32_t *bits, int32_t clear)
 {
     if (!bits) return VQ_ERR_INVALID_ARG;
     *bits = 0;
-    if (cudaDeviceSynchronize() != cudaSuccess) return VQ_ERR_CUDA;
+    if (cudaDeviceSynchronize() != cudaSuccess) return vqh_failed();
     const bool c = clear != 0;
     if (vqh_status_encode(bits, c) != cudaSuccess || vqh_status_attn(bits, c) != cudaSuccess ||
         vqh_status_scalar(bits, c) != cudaSuccess || vqh_status_append(bits, c) != cudaSuccess ||
         vqh_status_paged(bits, c) != cudaSuccess || vqh_status_pfew(bits, c) != cudaSuccess ||
         vqh_status_pchunk(bits, c) != cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     return VQ_OK;
 }
 

@@ -37,6 +37,14 @@ cudaError_t vqh_status_pchunk(uint32_t *bits, bool clear);
         return e;                                                                    \
     }
 
+// The status of a CUDA call that failed.  The runtime keeps the error until it is
+// asked for, and would report it as the next call's.
+inline vq_status vqh_failed()
+{
+    (void)cudaGetLastError();
+    return VQ_ERR_CUDA;
+}
+
 // Status of the launches just made on `stream`: VQ_ERR_CUDA if a launch
 // failed, else VQ_OK.  In the checked build (VQ_CHECKED) the call also waits
 // for them and reports an out-of-bounds bit in this unit's status word (read
@@ -44,11 +52,11 @@ cudaError_t vqh_status_pchunk(uint32_t *bits, bool clear);
 // clears it.
 inline vq_status vqh_launched(cudaStream_t stream, cudaError_t (*reader)(uint32_t *, bool))
 {
-    if (cudaPeekAtLastError() != cudaSuccess) return VQ_ERR_CUDA;
+    if (cudaPeekAtLastError() != cudaSuccess) return vqh_failed();
 #ifdef VQ_CHECKED
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return VQ_ERR_CUDA;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return vqh_failed();
     uint32_t bits = 0;
-    if (reader(&bits, false) != cudaSuccess) return VQ_ERR_CUDA;
+    if (reader(&bits, false) != cudaSuccess) return vqh_failed();
     if (bits & VQ_KSTATUS_OUT_OF_BOUNDS) return VQ_ERR_INTERNAL;
 #else
     (void)stream;

@@ -214,10 +214,8 @@ vq_status launch_merge(const vqk::PagedArgs &a, const AttnPart &p, cudaStream_t 
                                  : vqk::paged_attn_merge<T, true, 4>;
     if (cudaLaunchKernelEx(&cfg, kernel, (const float *)a.part, (const float *)a.ml,
                            (const vqk::PagedNote *)a.notes, p.tile_rows, a.dim, a.hq, a.tokens,
-                           static_cast<T *>(a.out), a.lse) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return VQ_ERR_CUDA;
-    }
+                           static_cast<T *>(a.out), a.lse) != cudaSuccess)
+        return vqh_failed();
     return vqh_launched(st, vqh_status_paged);
 }
 
@@ -307,7 +305,7 @@ vq_status vq_paged_reserve(const int32_t *lens, const int32_t *new_lens, int64_t
     const size_t smem = vqk::page_reserve_smem(requests);
     if (smem > 48 * 1024 && cudaFuncSetAttribute(vqk::page_reserve, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem) != cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     // one small block for a decode step; more where there are slots to write
     const int threads = requests <= vqk::kPageFewThreads && total_new <= 2 * vqk::kPageFewThreads ? vqk::kPageFewThreads
                                                                                                   : vqk::kPageThreads;
@@ -319,7 +317,7 @@ vq_status vq_paged_reserve(const int32_t *lens, const int32_t *new_lens, int64_t
     if (cudaLaunchKernelEx(&cfg, vqk::page_reserve, lens, new_lens, (int32_t)requests, free_pages, free_count,
                            (int32_t)num_pages, block_table, (int32_t)max_blocks, (int32_t)page_shift(page_size),
                            total_new, lens_out, free_count_out, cu_new, slots) != cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     return vqh_launched(st, vqh_status_paged);
 }
 
@@ -340,7 +338,7 @@ vq_status vq_paged_trim(const int32_t *lens, const int32_t *keep_lens, int64_t r
     const size_t smem = vqk::page_trim_smem(requests);
     if (smem > 48 * 1024 && cudaFuncSetAttribute(vqk::page_trim, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem) != cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     const int threads = requests <= vqk::kPageFewThreads ? vqk::kPageFewThreads : vqk::kPageThreads;
     int blocks = 1;  // a warp returns the pages of a request at a time
     while (blocks < 8 && requests > (int64_t)blocks * 64) blocks *= 2;
@@ -350,7 +348,7 @@ vq_status vq_paged_trim(const int32_t *lens, const int32_t *keep_lens, int64_t r
     if (cudaLaunchKernelEx(&cfg, vqk::page_trim, lens, keep_lens, (int32_t)requests, block_table,
                            (int32_t)max_blocks, (int32_t)page_shift(page_size), free_pages, free_count,
                            (int32_t)num_pages, lens_out, free_count_out) != cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     return vqh_launched(st, vqh_status_paged);
 }
 

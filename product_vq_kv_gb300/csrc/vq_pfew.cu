@@ -18,7 +18,7 @@ vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
     using S = vqk::FewShape<D>;
     const size_t smem = S::kSmem;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return VQ_ERR_CUDA;
+        return vqh_failed();
     kernel<<<(unsigned)blocks, S::kWarps * 32, smem, st>>>(a);
     return vqh_launched(st, vqh_status_pfew);
 }

@@ -37,8 +37,7 @@ vq_status launch_tc(const vqk::AppendArgs &a, vq_dtype dtype, int kv0, int kinds
     vqh::tc_shape(groups, a.tokens * a.ns, vqh::tc_slots(SUB, kSplit, smem), vqh::tc_tps(SUB, kSplit), &per_group, &tiles);
     if (groups * per_group > 0x7fffffffLL) return VQ_ERR_UNSUPPORTED;
     auto kernel = vqk::append_tc<T, SUB, C::kCols, C::kGroup, C::kMinBlocks, SMOOTH, C::kTps>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return vqh_failed();
+    if (!vqh_allow_smem(kernel, vqh::tc_smem<SUB, SMOOTH>(vqh::kTcMaxCentroids, dtype))) return vqh_failed();
     kernel<<<(unsigned)(groups * per_group), 128 * C::kTps, smem, st>>>(a, kv0, (int32_t)per_group, tiles, 1.0f);
     return vqh_launched(st, vqh_status_append);
 }

@@ -111,10 +111,7 @@ vq_status attn_launch_k(const AttnPlan &p, const void *q, const uint8_t *kcodes,
                         const uint8_t *vcodes, const void *vcb, float *part, cudaStream_t st)
 {
     auto kp = vqk::attn_partial<T, NS, GPB, VW>;
-    if (p.smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kp, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
-            cudaSuccess)
-        return vqh_failed();
+    if (p.smem > 48 * 1024 && !vqh_allow_smem(kp, kAttnMaxSmem)) return vqh_failed();
     kp<<<(unsigned)(p.base * p.sh.splits), kAttnThreads, p.smem, st>>>(
         static_cast<const T *>(q), kcodes, static_cast<const T *>(kcb), vcodes,
         static_cast<const T *>(vcb), p.sh, part);

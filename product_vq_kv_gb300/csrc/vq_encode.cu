@@ -155,7 +155,7 @@ Plan make_plan(const Args &a)
     p.kind = kGeneral;
     // tf32 holds fp16 and bf16 values exactly; fp32 rows and codebooks are
     // split into tf32 pieces, the dropped bits covered by the bound
-    if (shape_ok && a.n_centroids >= kFilterMinCentroids && a.n_centroids <= 256) {
+    if (shape_ok && a.n_centroids >= kFilterMinCentroids && a.n_centroids <= vqh::kTcMaxCentroids) {
         p.kind = kTc;
         p.smem = a.sub_dim == 4 ? tc_smem<4>(a.n_centroids, a.dtype) : tc_smem<8>(a.n_centroids, a.dtype);
     }
@@ -191,9 +191,7 @@ template <typename T, int SUB, typename OutT, bool SMOOTH = false>
 vq_status launch_tc(const Args &a, const Plan &p)
 {
     auto kernel = tc_kernel<T, SUB, OutT, SMOOTH>();
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
-        cudaSuccess)
-        return vqh_failed();
+    if (!vqh_allow_smem(kernel, tc_smem<SUB, SMOOTH>(vqh::kTcMaxCentroids, a.dtype))) return vqh_failed();
     kernel<<<(unsigned)p.blocks, 128 * TcConfig<SUB, tc_split<T, SMOOTH>()>::kTps, p.smem, a.stream>>>(
         static_cast<const T *>(a.x), static_cast<const T *>(a.cb), a.n_per_group, a.n_centroids,
         p.tiles_per_group, p.tc_tiles, 1.0f, static_cast<OutT *>(a.out), a.smooth,
@@ -205,11 +203,7 @@ template <typename T, int SUB, typename OutT, bool SMOOTH = false>
 vq_status launch_filter(const Args &a, const Plan &p)
 {
     auto kernel = vqk::encode_filter<T, SUB, kFRows, kFThreads, kFGroup, OutT, SMOOTH>;
-    if (p.smem > 48 * 1024) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)p.smem) != cudaSuccess)
-            return vqh_failed();
-    }
+    if (p.smem > 48 * 1024 && !vqh_allow_smem(kernel, kMaxFastSmem)) return vqh_failed();
     kernel<<<(unsigned)p.blocks, p.threads, p.smem, a.stream>>>(
         static_cast<const T *>(a.x), static_cast<const T *>(a.cb), a.n_per_group, a.n_centroids,
         p.tiles_per_group, 1.0f, static_cast<OutT *>(a.out), a.smooth,
@@ -221,11 +215,7 @@ template <typename T, int SUB, typename OutT>
 vq_status launch_fast(const Args &a, const Plan &p)
 {
     auto kernel = vqk::encode_fast<T, SUB, kRows, kThreads, kMode, kGroupCentroids, OutT>;
-    if (p.smem > 48 * 1024) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)p.smem) != cudaSuccess)
-            return vqh_failed();
-    }
+    if (p.smem > 48 * 1024 && !vqh_allow_smem(kernel, kMaxFastSmem)) return vqh_failed();
     kernel<<<(unsigned)p.blocks, p.threads, p.smem, a.stream>>>(
         static_cast<const T *>(a.x), static_cast<const T *>(a.cb), a.n_per_group, a.n_centroids,
         p.tiles_per_group, 1.0f, static_cast<OutT *>(a.out));
@@ -312,7 +302,7 @@ vq_status run_smooth(const Args &a)
     const size_t row_bytes = (size_t)a.sub_dim * elem_size(a.dtype);
     if ((uintptr_t)a.x % (row_bytes < 16 ? row_bytes : 16)) return VQ_ERR_UNSUPPORTED;
     Plan p{};
-    if (a.n_centroids >= kFilterMinCentroids && a.n_centroids <= 256) {
+    if (a.n_centroids >= kFilterMinCentroids && a.n_centroids <= vqh::kTcMaxCentroids) {
         p.kind = kTc;
         p.smem = a.sub_dim == 4 ? tc_smem<4, true>(a.n_centroids, a.dtype) : tc_smem<8, true>(a.n_centroids, a.dtype);
         tc_shape(a.n_groups, a.n_per_group, tc_slots(a.sub_dim, true, p.smem), tc_tps(a.sub_dim, true),

@@ -45,6 +45,16 @@ inline vq_status vqh_failed()
     return VQ_ERR_CUDA;
 }
 
+// Let `kernel` take up to `most` bytes of dynamic shared memory; false if the call
+// failed.  The limit belongs to the kernel and not to a call: `most` is the same number
+// for every call of a kernel, the largest it is ever launched with, or a call with less
+// could lower it between another thread's setting and its launch.
+template <typename Kernel>
+bool vqh_allow_smem(Kernel *kernel, size_t most)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess;
+}
+
 // Status of the launches just made on `stream`: VQ_ERR_CUDA if a launch
 // failed, else VQ_OK.  In the checked build (VQ_CHECKED) the call also waits
 // for them and reports an out-of-bounds bit in this unit's status word (read

@@ -303,8 +303,7 @@ vq_status vq_paged_reserve(const int32_t *lens, const int32_t *new_lens, int64_t
         if (!aligned4(p)) return VQ_ERR_INVALID_ARG;
     if ((uintptr_t)slots % 8) return VQ_ERR_INVALID_ARG;
     const size_t smem = vqk::page_reserve_smem(requests);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(vqk::page_reserve, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem) != cudaSuccess)
+    if (smem > 48 * 1024 && !vqh_allow_smem(vqk::page_reserve, vqk::page_reserve_smem(vqk::kPageMaxRequests)))
         return vqh_failed();
     // one small block for a decode step; more where there are slots to write
     const int threads = requests <= vqk::kPageFewThreads && total_new <= 2 * vqk::kPageFewThreads ? vqk::kPageFewThreads
@@ -336,8 +335,7 @@ vq_status vq_paged_trim(const int32_t *lens, const int32_t *keep_lens, int64_t r
                           (const void *)free_count_out})
         if (!aligned4(p)) return VQ_ERR_INVALID_ARG;
     const size_t smem = vqk::page_trim_smem(requests);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(vqk::page_trim, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem) != cudaSuccess)
+    if (smem > 48 * 1024 && !vqh_allow_smem(vqk::page_trim, vqk::page_trim_smem(vqk::kPageMaxRequests)))
         return vqh_failed();
     const int threads = requests <= vqk::kPageFewThreads ? vqk::kPageFewThreads : vqk::kPageThreads;
     int blocks = 1;  // a warp returns the pages of a request at a time

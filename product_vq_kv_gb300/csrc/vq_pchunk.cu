@@ -16,8 +16,7 @@ vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
 {
     auto kernel = vqk::paged_attn_chunk<T, D, SUB>;
     const size_t smem = vqk::ChunkShape<D>::kSmem;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return vqh_failed();
+    if (!vqh_allow_smem(kernel, smem)) return vqh_failed();
     kernel<<<(unsigned)blocks, vqk::kChunkThreads, smem, st>>>(a);
     return vqh_launched(st, vqh_status_pchunk);
 }

@@ -17,8 +17,7 @@ vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
     auto kernel = vqk::paged_attn_few<T, D, SUB>;
     using S = vqk::FewShape<D>;
     const size_t smem = S::kSmem;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return vqh_failed();
+    if (!vqh_allow_smem(kernel, smem)) return vqh_failed();
     kernel<<<(unsigned)blocks, S::kWarps * 32, smem, st>>>(a);
     return vqh_launched(st, vqh_status_pfew);
 }

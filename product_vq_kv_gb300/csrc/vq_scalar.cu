@@ -165,9 +165,7 @@ vq_status launch_bucket(const void *x, int64_t n, const float *c, uint8_t *out, 
     if (blocks > sms) blocks = sms;
     if (blocks < 1) blocks = 1;
     auto kp = vqs::scalar_bucket<NC>;
-    if (cudaFuncSetAttribute(kp, cudaFuncAttributeMaxDynamicSharedMemorySize, vqs::kBucketSmemBytes) !=
-        cudaSuccess)
-        return vqh_failed();
+    if (!vqh_allow_smem(kp, vqs::kBucketSmemBytes)) return vqh_failed();
     kp<<<(unsigned)blocks, kLookupThreads, vqs::kBucketSmemBytes, st>>>(static_cast<const uint16_t *>(x), n, c,
                                                                         vec, out);
     return launched(st);
@@ -214,9 +212,7 @@ vq_status vq_scalar_quantize(const void *x, vq_dtype dtype, int64_t n, const flo
         if (blocks > sms) blocks = sms;
         if (blocks < 1) blocks = 1;
         auto kp = vqs::scalar_lookup;
-        if (cudaFuncSetAttribute(kp, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTableBytes) !=
-            cudaSuccess)
-            return vqh_failed();
+        if (!vqh_allow_smem(kp, kTableBytes)) return vqh_failed();
         kp<<<(unsigned)blocks, kLookupThreads, kTableBytes, st>>>(static_cast<const uint16_t *>(x), n,
                                                                   tab, vec, out);
         return launched(st);

@@ -13,6 +13,8 @@ namespace vqh {
 
 // The least centroids the screening kernels take.
 constexpr int kFilterMinCentroids = 64;
+// The most centroids the tensor-core kernel takes.
+constexpr int kTcMaxCentroids = 256;
 
 // Blocks per group and 128-row tiles per block.  A block works through its
 // tiles `tps` at a time; its time is taken as its steps plus half a step of

@@ -86,3 +86,39 @@ def test_a_failed_launch_is_reported_once(lib, name):
         assert call(lib) == CUDA
         assert lib.fake_last_error() == 0
     assert call(lib) == OK
+
+
+def test_a_kernel_has_one_limit_of_shared_memory(lib):
+    """The limit is the kernel's: calls of other sizes, in other threads, must not lower
+    it under a launch.  So every call of a kernel sets the same one."""
+    for requests in (5, 4100, 6000, 8192):
+        assert reserve(lib, requests) == trim(lib, requests) == OK
+    for n_c in (64, 100, 256):
+        for dtype in (0, 1, 2):
+            assert append(lib, n_c, dtype) == append(lib, n_c, dtype, smooth=P) == append(lib, n_c, dtype, sub=4) == OK
+            assert encode(lib, n_c, dtype) == encode(lib, n_c, dtype, sub=8) == OK
+    for n_c in (1000, 1500, 2000, 4096):
+        assert encode(lib, n_c) == encode(lib, n_c, sub=8) == OK
+    for shape in (dict(), dict(sub=4), dict(hkv=4), dict(hkv=8), dict(hkv=1), dict(hkv=1, sub=4)):
+        assert decode_attention(lib, **shape) == OK
+    assert lib.fake_most_limits() == 1
+
+
+def test_calls_of_several_threads(lib):
+    """Large and small calls of the same kernels side by side: none finds its limit
+    lowered."""
+    import threading
+
+    wrong = []
+
+    def work(requests, n_c):
+        for _ in range(3000):
+            if reserve(lib, requests) or trim(lib, requests) or append(lib, n_c):
+                wrong.append(requests)
+
+    threads = [threading.Thread(target=work, args=a) for a in ((8192, 256), (4100, 64), (5000, 128), (8000, 200))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

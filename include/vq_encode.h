@@ -377,8 +377,11 @@ vq_status vq_paged_append(const void *k, const void *v, int64_t k_stride, int64_
  *   workspace  >= vq_paged_attention_workspace_bytes(...) bytes, device,
  *              16-byte aligned
  * Arithmetic: products of the inputs' own values, sums, maxima and weights in
- * fp32; with 16-bit inputs of the shapes the tensor kernels take, each weight
- * is rounded once to the input type before its product with V^.
+ * fp32.  With 16-bit inputs of the shapes the tensor kernels take (head_dim
+ * 64, 128 or 256, sub_dim 4 or 8, page_size >= 16, 16-byte aligned pages) each
+ * weight enters its product with V^ in the input type: in two pieces (22 bits
+ * of fp16, 16 of bf16) for requests of a few new tokens, rounded once for
+ * longer runs.
  * Asynchronous on `stream`.
  */
 vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_new, const int32_t *lens,

@@ -2,8 +2,12 @@
 small weights, and rows that one token decides."""
 import math
 
+import numpy as np
 import pytest
 import torch
+
+import paged_reference as ref
+from test_paged import HALF_EPS, HALF_STEP, SHAPES, Cache
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +67,29 @@ def test_many_small_weights_beside_large_ones(vq, dtype, dim, sub, new):
     assert ((out.double() - want).abs() <= rel * want).all()
     want_lse = (26 * math.log(2) + torch.log(many + n * 2.0 ** -26))[:, :, 0]
     assert ((lse.double() - want_lse).abs() <= held * 2.0 ** -26 / many + 34 * 2.0 ** -23 + 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[2] in (64, 128, 256) and s[3] in (4, 8) and s[5] >= 16
+                                   and s[6] != "f32"])
+@pytest.mark.parametrize("gain", [1.0, 4.0, 30.0])
+@pytest.mark.parametrize("new", [1, 3])
+def test_a_few_rows_keep_their_weights_in_two_pieces(vq, shape, gain, new):
+    """A weight is off by half a step of the type twice over (what the first piece
+    leaves is exact in fp32 and rounded again), and in fp16 by half its least step, 2^-25,
+    where the maximum's weight is 2^7 or more."""
+    hq, hkv, dim, sub, n_c, page, dtype = shape
+    if new * hq // hkv > 24:
+        pytest.skip("a chunk")
+    lens = [new, 17, 130, 300, 900]
+    c = Cache(21, lens, hq, hkv, dim, sub, n_c, page, dtype, gain=gain)
+    cu = [new * r for r in range(len(lens) + 1)]
+    q = c.queries(cu[-1])
+    d_lens, table, kc, vc = c.device()
+    out, lse = vq.vq_paged_attention(q.cuda(), i32(cu), d_lens, table, kc, vc, c.kcb, c.vcb, max_new=new, return_lse=True)
+    eps = HALF_EPS[dtype]
+    want, want_lse, tol, tol_lse = ref.attention(
+        q.double().numpy(), cu, c.lens, c.table, c.kc, c.vc, c.kcb_h.double().numpy(), c.vcb_h.double().numpy(),
+        weight_eps=eps * eps, weight_abs=2.0 ** -32 if dtype == "f16" else HALF_STEP[dtype])
+    got = out.double().cpu().numpy()
+    assert (np.abs(got - want) <= tol + eps * (np.abs(want) + tol) + HALF_STEP[dtype]).all()
+    assert (np.abs(lse.double().cpu().numpy() - want_lse) <= tol_lse).all()

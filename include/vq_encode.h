@@ -361,7 +361,8 @@ vq_status vq_paged_append(const void *k, const void *v, int64_t k_stride, int64_
  * page of its range missing) gets zeros and lse = -inf, and so do the rows
  * after cu_new[requests].  A page entry outside [0, num_pages) hides its
  * tokens.  Codebook entries are finite; q may hold anything, and a row of q
- * with NaN or infinities does not touch another row.
+ * with NaN or infinities does not touch another row.  A score of -inf weighs
+ * nothing; a row that sees scores of -inf alone gets NaN, in out and lse.
  *   q          token t at t * q_stride elements, [heads_q][head_dim], device,
  *              dtype
  *   cu_new     [requests + 1]  device (vq_paged_reserve); ascends.  Offsets

@@ -412,10 +412,18 @@ __device__ __forceinline__ float narrow<float>(float v) { return v; }
 
 constexpr float kLn2 = 0.69314718055994531f;
 
-// lse from the maximum and the sum in powers of two.
+// A row's state is its maximum m and its sum of weights l: l = 0 if it has seen nothing,
+// m = -inf and l = 1 if every score it has seen is -inf.  Beside a part with other
+// scores such a part weighs nothing; a row of nothing else is 0 / 0, NaN as in the
+// definition.  What its weighted sum is multiplied by, and its lse:
+__device__ __forceinline__ float paged_inv(float m, float l)
+{
+    return l == 0.f ? 0.f : m == __int_as_float(0xff800000) ? __int_as_float(0x7fffffff) : 1.f / l;
+}
 __device__ __forceinline__ float paged_lse(float m, float l)
 {
-    return l == 0.f ? __int_as_float(0xff800000) : kLn2 * (m + log2f(l));
+    if (l == 0.f) return __int_as_float(0xff800000);
+    return m == __int_as_float(0xff800000) ? __int_as_float(0x7fffffff) : kLn2 * (m + log2f(l));
 }
 
 // Block table entry of cached token t, whatever it holds.
@@ -491,6 +499,7 @@ __global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) acc[g][c] = 0.f;
             }
+            bool saw = false;
             for (int unit = s.begin; unit < s.end; ++unit) {
                 const int32_t t = s.it.k_lo + unit * kUnit + tid;
                 bool seen = t < s.it.k_hi && t <= s.it.pos0 && (a.window == 0 || (int64_t)t > (int64_t)s.it.pos0 - a.window);
@@ -500,6 +509,7 @@ __global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant
                     if (pg < 0) seen = false;
                     else code_row = pg * a.page_stride + (code_head + (t & ((1 << a.page_shift) - 1))) * a.ns;
                 }
+                saw |= seen;
                 __syncthreads();  // sq is written; the last unit's sp and spage are read
                 spage[tid] = code_row;
                 float dot[kSimpleRows];
@@ -537,7 +547,8 @@ __global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant
                     // nothing seen yet: keep the (empty) sums
                     scale[g] = m[g] == top ? 1.f : exp2f(m[g] - top);
                     m[g] = top;
-                    const float p = seen ? exp2f(dot[g] - top) : 0.f;
+                    // -inf weighs 0, whatever the maximum so far
+                    const float p = dot[g] == __int_as_float(0xff800000) ? 0.f : exp2f(dot[g] - top);
                     sp[g][tid] = p;
                     sum[g] = sum[g] * scale[g] + p;
                 }
@@ -574,16 +585,17 @@ __global__ void __launch_bounds__(kUnit) paged_attn_simple(const __grid_constant
 #pragma unroll
                 for (int g = 0; g < kSimpleRows; ++g) red[g][warp] = sum[g];
             }
-            __syncthreads();
+            const bool any = __syncthreads_or(saw);
 #pragma unroll
             for (int g = 0; g < kSimpleRows; ++g) {
                 if (g >= rows) break;
                 float total = 0.f;
 #pragma unroll
                 for (int k = 0; k < kUnit / 32; ++k) total += red[g][k];
+                if (total == 0.f && any) total = 1.f;  // m = -inf: scores of -inf alone
                 const int64_t orow = tok * a.hq + head0 + g;
                 if (s.whole) {
-                    const float inv = total == 0.f ? 0.f : 1.f / total;
+                    const float inv = paged_inv(m[g], total);
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) {
                         const int d = tid + c * kUnit;
@@ -711,7 +723,7 @@ __global__ void __launch_bounds__(kMergeThreads)
         }
     }
     const int64_t orow = (n.tok0 + row / n.gc) * hq + n.head0 + row % n.gc;
-    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const float inv = paged_inv(top, total);
 #pragma unroll
     for (int c = 0; c < kMax; ++c) {
         const int col = (c * 32 + lane) * kW;

@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             const int64_t all_lo = a.window == 0 ? -1 : (int64_t)pos_first + ntile - 1 - a.window;
 
             float m = kNone;
+            uint32_t saw = 0;  // not 0: this row has seen a token
             float2 sum2 = make_float2(0.f, 0.f);  // over the even and the odd tokens
             for (int j = 0; j < s.nb; ++j, ++block) {
                 const int buf = kTiles == 2 ? tile : j & 1;
@@ -431,6 +432,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         uint32_t v[32];
                         tmem_load32_async(s_addr + c * 32, v);
                         const uint32_t bits = seen_bits(c);
+                        saw |= bits;
                         tmem_wait_ld(v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
@@ -498,8 +500,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             if (kTiles == 2) ++seen_o;
             if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) break;
             tc_fence_after();
-            const float sum = sum2.x + sum2.y;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float sum = sum2.x + sum2.y;
+            // (scores of -inf alone: m is -inf still, and every block came through the
+            // path that looks at the masks)
+            if (sum == 0.f && saw) sum = 1.f;
+            const float inv = paged_inv(m, sum);
             const int64_t orow = tok * a.hq + head;
             const int64_t prow = s.slot * a.tile_rows + tile * tpq * gc + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
             T *dst = out + orow * D;

@@ -64,7 +64,7 @@ __host__ __device__ constexpr float weight_shift()
 constexpr int kFewRows = 8;     // columns of a matrix instruction
 // A row's maximum before it has seen a token: finite, so that the weight of a
 // hidden score, -inf, is 0 against it too (-inf less -inf would be NaN).
-constexpr float kFewLow = -3.0e38f;
+constexpr float kFewLow = -3.402823466e38f;
 
 // Warps of a block and blocks of an SM: two blocks where a lane's accumulators
 // and queries (dim/16 x 6 registers) fit 128 registers.  At dim 256 one block of 8
@@ -454,11 +454,39 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                     sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
                     sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
                     sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
-                    if (g == 0) {
-                        wm[warp][2 * t + c] = m[c];
-                        wl[warp][2 * t + c] = sum[c];
-                    }
                 }
+            // A sum of 0: the warp has seen no token of the row, or scores of -inf alone.
+            // Its groups are looked through once more for a token that the row sees
+            // (here and not in the loop, which has no register to spare; most such rows
+            // overlap no group, and nothing is loaded).
+            if (__any_sync(0xffffffffu, sum[0] == 0.f || sum[1] == 0.f)) {
+                bool saw[2] = {false, false};
+                for (int group = g_begin; group < g_end; group += kFewWarps) {
+                    const int32_t k0 = first_of(group);
+                    bool at[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        at[c] = sum[c] == 0.f && k0 <= lim[c] && k0 + 15 > low[c] && low[c] < lim[c];
+                    if (!__any_sync(0xffffffffu, at[0] || at[1])) continue;
+                    const int32_t entry = page_of(group);
+                    if (entry < 0 || entry >= a.num_pages) continue;
+                    saw[0] |= at[0];
+                    saw[1] |= at[1];
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (saw[c]) {
+                        m[c] = kNone;
+                        sum[c] = 1.f;
+                    }
+            }
+            if (g == 0) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    wm[warp][2 * t + c] = m[c];
+                    wl[warp][2 * t + c] = sum[c];
+                }
+            }
             __syncthreads();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -471,7 +499,8 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
 #pragma unroll
                     for (int k = 0; k < kFewWarps; ++k)
                         if (wl[k][row] != 0.f) total = fmaf(exp2_fast(wm[k][row] - top), wl[k][row], total);
-                    const float f = sum[c] == 0.f ? 0.f : exp2_fast(m[c] - top);
+                    if (top == kNone && total != 0.f) total = 1.f;
+                    const float f = sum[c] == 0.f || m[c] == kNone ? 0.f : exp2_fast(m[c] - top);
                     m[c] = top;
                     sum[c] = total;
 #pragma unroll
@@ -513,7 +542,7 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                         if (row >= rows) continue;
                         if (s.whole) {
                             const int64_t orow = (s.it.tok0 + row / gc) * a.hq + head0 + row % gc;
-                            const float inv = sum[c] == 0.f ? 0.f : 1.f / sum[c];
+                            const float inv = paged_inv(m[c], sum[c]);
                             T *dst = out + orow * D + g * (D / 8);
                             if (VQ_SPAN(dst, D / 8, out, a.tokens * a.hq * D)) {
                                 if (out_vec) {

@@ -9,6 +9,10 @@
 
 VQH_STATUS_READER(vqh_status_pchunk)
 
+// The waits of a segment outlast the longest one: 2 us a unit (1.9 at dim 128), at 3.5
+// us a poll.
+static_assert(vqk::kSegmentPolls / 2 * 7 > VQ_PAGED_MAX_TOKENS / vqk::kUnit * 2, "a segment's waits would give up");
+
 namespace {
 
 template <typename T, int D, int SUB>

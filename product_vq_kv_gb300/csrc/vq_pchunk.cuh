@@ -140,13 +140,18 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// Polls of a wait: about a second, where a block's longest is microseconds.
+// Polls of a wait: about a second (2^22 took 15 s), where a block of keys takes
+// microseconds.  The waits for the next segment, and for room to announce one, last as
+// long as a segment: on the longest cache of 2^30 tokens 2^23 units of 2 us, 17 s, so
+// their limit is a minute (they also end as soon as any other wait gives up).
 constexpr int kChunkPolls = 1 << 18;
+constexpr int kSegmentPolls = 1 << 24;
 
 // Bounded wait for phase `parity`: false if it gave up or another role did.
+template <int POLLS = kChunkPolls>
 __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_word)
 {
-    for (int it = 0; it < kChunkPolls; ++it) {
+    for (int it = 0; it < POLLS; ++it) {
         uint32_t done;
         asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     // the end (or if a wait gave up)
     auto next_seg = [&](uint32_t &seg_n, ChunkSeg &s) -> bool {
         const uint32_t i = seg_n & 1;
-        if (!__all_sync(0xffffffffu, chunk_wait(&seg_full[i], (seg_n >> 1) & 1, &abort_word))) return false;
+        if (!__all_sync(0xffffffffu, chunk_wait<kSegmentPolls>(&seg_full[i], (seg_n >> 1) & 1, &abort_word))) return false;
         s = segs[i];
         __syncwarp();
         if (lane == 0) (void)mbar_arrive(&seg_empty[i]);
@@ -797,7 +802,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         for (uint32_t n = 0; more; ++n) {
             const uint32_t i = n & 1;
             more = cur.next(a, w, l, seg, note);
-            if (n >= 2 && !__all_sync(0xffffffffu, chunk_wait(&seg_empty[i], ((n >> 1) - 1) & 1, &abort_word))) break;
+            if (n >= 2 && !__all_sync(0xffffffffu, chunk_wait<kSegmentPolls>(&seg_empty[i], ((n >> 1) - 1) & 1, &abort_word))) break;
             if (lane == 0) {
                 ChunkSeg &to = segs[i];
                 to.live = more;

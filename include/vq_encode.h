@@ -514,8 +514,8 @@ vq_status vq_describe_launch(int64_t n_groups, int64_t n_per_group, int32_t n_ce
  *                             units gave up; the rows it had not encoded hold
  *                             0xFFFFFFFF (255 as 8-bit codes, those of
  *                             vq_paged_append among them); or a wait inside
- *                             vq_paged_attention did, and the rows it had not
- *                             written keep what they held
+ *                             vq_paged_attention did, and the rows that its
+ *                             block had not written are NaN, in out and lse
  *   VQ_KSTATUS_OUT_OF_BOUNDS  bounds-checked build only: an index fell
  *                             outside its buffer and the access was skipped
  * Returns VQ_ERR_INVALID_ARG for a NULL `bits`, VQ_ERR_CUDA if the

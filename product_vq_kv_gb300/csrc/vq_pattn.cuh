@@ -40,7 +40,7 @@
 namespace vqk {
 
 constexpr int kUnit = 128;       // cached tokens of one unit of work
-constexpr int kStageCu = 512;    // requests + 2 up to which a block keeps cu and lens in shared memory, if it has room
+constexpr int kStageCu = 512;    // requests + 2 up to which a block keeps cu and lens in shared memory (64 in the chunk kernel)
 
 // The note of a split item (rows = 0: none).
 struct PagedNote {
@@ -221,11 +221,8 @@ template <int STAGE>
 struct PagedStage {
     int32_t cu[STAGE], lens[STAGE], start[STAGE];
 };
-template <>
-struct PagedStage<0> {};
 template <int STAGE = kStageCu>
 struct PagedWalk {
-    static constexpr int kStage = STAGE;
     PagedStage<STAGE> stage;
     int64_t scratch[33];
     int64_t total;  // the costs of one head group
@@ -237,31 +234,35 @@ struct PagedWalk {
     int32_t at;     // where in its cost
 };
 
+// The lengths as a block reads them: from its stage if they fit there.
+template <int STAGE>
+__device__ __forceinline__ PagedLens paged_lens(const PagedArgs &a, const PagedWalk<STAGE> &w)
+{
+    PagedLens l{a.cu, a.lens, nullptr, a.requests, a.tile_tokens, a.tokens};
+    if (a.requests + 2 <= STAGE) {
+        l.cu = w.stage.cu;
+        l.lens = w.stage.lens;
+        l.starts = w.stage.start;
+    }
+    return l;
+}
+
 // Lay the items out and find this block's part (all THREADS threads; w in
 // shared memory).  Returns whether the block has any.
 template <int THREADS, int STAGE>
 __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> &w, PagedLens &l)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    l.cu = a.cu;
-    l.lens = a.lens;
-    l.starts = nullptr;
-    l.requests = a.requests;
-    l.tile = a.tile_tokens;
-    l.tokens = a.tokens;
-    if constexpr (STAGE > 0) {
-        if (a.requests + 2 <= STAGE) {
-            for (int i = tid; i <= a.requests; i += THREADS) {
-                w.stage.cu[i] = a.cu[i];
-                w.stage.start[i] = (int32_t)l.compute_start(i);
-                if (i < a.requests) w.stage.lens[i] = a.lens[i];
-            }
-            l.cu = w.stage.cu;
-            l.lens = w.stage.lens;
-            l.starts = w.stage.start;
-            __syncthreads();
+    if (a.requests + 2 <= STAGE) {
+        const PagedLens from{a.cu, a.lens, nullptr, a.requests, a.tile_tokens, a.tokens};
+        for (int i = tid; i <= a.requests; i += THREADS) {
+            w.stage.cu[i] = a.cu[i];
+            w.stage.start[i] = (int32_t)from.compute_start(i);
+            if (i < a.requests) w.stage.lens[i] = a.lens[i];
         }
+        __syncthreads();
     }
+    l = paged_lens(a, w);
     const PagedRun run(a, tid, THREADS);
     int r0 = 0;
     const int64_t mine = run.cost(a, l, &r0);

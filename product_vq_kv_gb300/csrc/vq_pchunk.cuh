@@ -41,8 +41,8 @@
 // split below is by warpgroups: 2 x 160 + 96 + 96 registers of each four threads,
 // the 4 x 128 that the block is launched with).  Every wait is bounded: one that gives up
 // sets the block's abort word and kStatusWaitGaveUp, the others see it and all
-// leave; the issuer first waits (bounded) for its products in flight, and the
-// tensor memory is freed.  The rows not yet written then keep what they held.
+// leave; the issuer first waits (bounded) for its products in flight, the tensor
+// memory is freed, and the rows that the block has not written become NaN.
 #pragma once
 
 #include "vq_pfew.cuh"
@@ -148,7 +148,7 @@ constexpr int kChunkPolls = 1 << 18;
 constexpr int kSegmentPolls = 1 << 24;
 
 // Bounded wait for phase `parity`: false if it gave up or another role did.
-template <int POLLS = kChunkPolls>
+template <int POLLS>
 __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_word)
 {
     for (int it = 0; it < POLLS; ++it) {
@@ -169,10 +169,11 @@ __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volat
 // Bounded wait for a phase of each of two barriers, polled together: one wait after
 // the other leaves the tensor pipe idle for the second's round trip (about 270
 // cycles where the products wait for both a stage and the weights).
+template <int POLLS>
 __device__ __forceinline__ bool chunk_wait2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1,
                                             volatile uint32_t *abort_word)
 {
-    for (int it = 0; it < kChunkPolls; ++it) {
+    for (int it = 0; it < POLLS; ++it) {
         uint32_t done;
         asm volatile("{\n\t.reg .pred p, q;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
@@ -199,7 +200,8 @@ struct ChunkSeg {
     int32_t live;      // 0: no more segments
 };
 
-template <typename T, int D, int SUB>
+// POLLS: the limit of every wait but the last, kChunkPolls except in a test.
+template <typename T, int D, int SUB, int POLLS = kChunkPolls>
 __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __grid_constant__ PagedArgs a)
 {
     using S = ChunkShape<D>;
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     // the end (or if a wait gave up)
     auto next_seg = [&](uint32_t &seg_n, ChunkSeg &s) -> bool {
         const uint32_t i = seg_n & 1;
-        if (!__all_sync(0xffffffffu, chunk_wait<kSegmentPolls>(&seg_full[i], (seg_n >> 1) & 1, &abort_word))) return false;
+        if (!__all_sync(0xffffffffu, chunk_wait<(POLLS == kChunkPolls ? kSegmentPolls : POLLS)>(&seg_full[i], (seg_n >> 1) & 1, &abort_word))) return false;
         s = segs[i];
         __syncwarp();
         if (lane == 0) (void)mbar_arrive(&seg_empty[i]);
@@ -299,10 +301,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         uint32_t seen_o = 0;
         uint32_t block = 0;           // key blocks of the segments so far
         bool go = true;
+        uint32_t done_n = 0;  // segments written
         while (go && next_seg(seg_n, s)) {
             const int gc = s.gc;
             if (tile * tpq >= s.ntok) {  // no rows here
                 block += s.nb;
+                ++done_n;
                 continue;
             }
             const int tok_in = tile * tpq + row / gc;
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             float2 sum2 = make_float2(0.f, 0.f);  // over the even and the odd tokens
             for (int j = 0; j < s.nb; ++j, ++block) {
                 const int buf = kTiles == 2 ? tile : j & 1;
-                if (!__all_sync(0xffffffffu, chunk_wait(&s_full[buf], seen_s[buf] & 1, &abort_word))) {
+                if (!__all_sync(0xffffffffu, chunk_wait<POLLS>(&s_full[buf], seen_s[buf] & 1, &abort_word))) {
                     go = false;
                     break;
                 }
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         sum2 = make_float2(sum2.x * f, sum2.y * f);
                         if (j > 0) {
                             // the product before this block has to be done
-                            if (kTiles == 1 && !__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
+                            if (kTiles == 1 && !__all_sync(0xffffffffu, chunk_wait<POLLS>(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
                                 go = false;
                                 break;
                             }
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     // a wait tells only the last two phases of a barrier apart, and the
                     // scores of this block were issued before the product before: wait for
                     // each product in turn
-                    if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
+                    if (!__all_sync(0xffffffffu, chunk_wait<POLLS>(&o_done[tile], (seen_o - 1) & 1, &abort_word))) {
                         go = false;
                         break;
                     }
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             }
             if (!go) break;
             if (kTiles == 2) ++seen_o;
-            if (!__all_sync(0xffffffffu, chunk_wait(&o_done[tile], (seen_o - 1) & 1, &abort_word))) break;
+            if (!__all_sync(0xffffffffu, chunk_wait<POLLS>(&o_done[tile], (seen_o - 1) & 1, &abort_word))) break;
             tc_fence_after();
             float sum = sum2.x + sum2.y;
             // (scores of -inf alone: m is -inf still, and every block came through the
@@ -547,6 +551,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 a.ml[prow * 2] = m;
                 a.ml[prow * 2 + 1] = sum;
             }
+            ++done_n;
+        }
+        if (abort_word) {
+            // a wait gave up: this thread's rows of the segments not written become NaN, in
+            // the output or by way of the merge
+            const float nan = __int_as_float(0x7fffffff);
+            PagedCursor cur;
+            cur.init(w, (int32_t)blockIdx.x);
+            PagedSegment seg;
+            PagedNote note{};
+            const PagedLens lens = paged_lens(a, w);
+            for (uint32_t n = 0; cur.next(a, w, lens, seg, note); ++n) {
+                const int g0 = seg.hx % a.gch * a.gc, gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
+                const int tok_in = tile * tpq + row / gc;
+                if (n < done_n || row >= tpq * gc || tok_in >= seg.it.ntok) continue;
+                const int64_t orow = (seg.it.tok0 + tok_in) * a.hq + seg.hx / a.gch * a.group + g0 + row % gc;
+                const int64_t prow = seg.slot * a.tile_rows + tile * tpq * gc + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
+                if (!seg.whole) {
+                    if (VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
+                        a.ml[prow * 2] = 0.f;
+                        a.ml[prow * 2 + 1] = nan;
+                    }
+                    continue;
+                }
+                if (VQ_SPAN(out + orow * D, D, out, a.tokens * a.hq * D)) {
+#pragma unroll 1
+                    for (int d = 0; d < D; ++d) out[orow * D + d] = narrow<T>(nan);
+                }
+                if (a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq)) a.lse[orow] = nan;
+            }
         }
     } else if (work && warp < 12) {
         // ------------------------------------------------ rebuild
@@ -565,7 +599,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         uint32_t met = 0;
         auto meet = [&]() -> bool {
             (void)mbar_arrive(&image[vals]);
-            return __all_sync(0xffffffffu, chunk_wait(&image[vals], met++ & 1, &abort_word));
+            return __all_sync(0xffffffffu, chunk_wait<POLLS>(&image[vals], met++ & 1, &abort_word));
         };
         while (go && next_seg(seg_n, s)) {
             const int h = s.h;
@@ -631,7 +665,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 const uint32_t n = stage_of(j, v), st = n % kChunkStages, round = n / kChunkStages;
                 // (the stages are released in ring order, so that the phase before the one
                 // waited for is over)
-                if (round > 0 && !__all_sync(0xffffffffu, chunk_wait(&empty[st], (round - 1) & 1, &abort_word))) return false;
+                if (round > 0 && !__all_sync(0xffffffffu, chunk_wait<POLLS>(&empty[st], (round - 1) & 1, &abort_word))) return false;
                 if (v == 0) {
                     // the words that lay here, eight blocks back, have been read: the stage
                     // just released held keys or values of a block at most four back, and
@@ -703,7 +737,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
         bool go = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, chunk_wait(bar, parity, &abort_word));
+            return __all_sync(0xffffffffu, chunk_wait<POLLS>(bar, parity, &abort_word));
         };
         // wait for the next stage in ring order; its index
         auto take = [&](uint32_t *st) -> bool {
@@ -719,7 +753,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             *st = taken % kChunkStages;
             const uint32_t round = taken / kChunkStages;
             ++taken;
-            return __all_sync(0xffffffffu, chunk_wait2(&full[*st], round & 1, &p_full[buf], n_p[buf]++ & 1, &abort_word));
+            return __all_sync(0xffffffffu, chunk_wait2<POLLS>(&full[*st], round & 1, &p_full[buf], n_p[buf]++ & 1, &abort_word));
         };
         // operand descriptors differ in the address field alone (16-byte units,
         // no carry out of it below 256 KiB): one addition each
@@ -802,7 +836,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         for (uint32_t n = 0; more; ++n) {
             const uint32_t i = n & 1;
             more = cur.next(a, w, l, seg, note);
-            if (n >= 2 && !__all_sync(0xffffffffu, chunk_wait<kSegmentPolls>(&seg_empty[i], ((n >> 1) - 1) & 1, &abort_word))) break;
+            if (n >= 2 && !__all_sync(0xffffffffu, chunk_wait<(POLLS == kChunkPolls ? kSegmentPolls : POLLS)>(&seg_empty[i], ((n >> 1) - 1) & 1, &abort_word))) break;
             if (lane == 0) {
                 ChunkSeg &to = segs[i];
                 to.live = more;
@@ -828,6 +862,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             }
             __syncwarp();
         }
+        while (more) more = cur.next(a, w, l, seg, note);  // a wait gave up: the note is due all the same
         if (lane == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;
     } else if (!work && warp == 13 && lane == 0) {
         if (VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = PagedNote{};

@@ -43,7 +43,7 @@ class PagedCache:
                                               lens_out=self.lens, free_count_out=self.count)
         kc, vc = self.codes[:, 0], self.codes[:, 1]
         vq.vq_paged_append(k, v, slots, *self.codebooks, kc, vc)
-        return vq.vq_paged_attention(q, cu, self.lens, self.table, kc, vc, *self.codebooks, max_new=most)
+        return vq.vq_paged_attention(q, cu, self.lens, self.table, kc, vc, *self.codebooks, max_new=most, slots=slots)
 
     def keep(self, keep_lens: torch.Tensor):
         """Cut the requests to keep_lens tokens; their pages go back."""

@@ -303,7 +303,9 @@ vq_status vq_attention_decode_static(const void *q, const uint8_t *k_codes,
  *   slots           [total_new] int64, device, written: page * page_size +
  *                   offset of each new token; -1 for tokens of refused
  *                   requests and for rows past the last
- * Asynchronous on `stream`.
+ * A refused request keeps its length and its rows: an attention of the step that
+ * is not given `slots` (vq_paged_attention_slots) takes those rows for its last
+ * cached tokens.  Asynchronous on `stream`.
  */
 vq_status vq_paged_reserve(const int32_t *lens, const int32_t *new_lens, int64_t requests,
                            const int32_t *free_pages, const int32_t *free_count, int64_t num_pages,
@@ -393,6 +395,25 @@ vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_
                              int32_t heads_kv, int32_t head_dim, int32_t sub_dim, int32_t n_centroids,
                              int64_t window, float scale, vq_dtype dtype, void *out, float *lse,
                              void *workspace, size_t workspace_bytes, vq_stream_t stream);
+
+/*
+ * vq_paged_attention_slots -- vq_paged_attention of a step in which requests may
+ * have been refused:
+ *   slots      [tokens] int64, device, as vq_paged_reserve wrote it (at least
+ *              `tokens` rows of it); NULL: none was refused.  A request whose
+ *              first new row has a slot below 0 is refused: its rows see nothing
+ *              (zeros, lse = -inf) and cost next to nothing
+ */
+vq_status vq_paged_attention_slots(const void *q, int64_t q_stride, const int32_t *cu_new,
+                                   const int32_t *lens, const int64_t *slots, int64_t requests,
+                                   int64_t tokens, int64_t max_new, const int32_t *block_table,
+                                   int64_t max_blocks, const uint8_t *k_codes, const uint8_t *v_codes,
+                                   int64_t num_pages, int32_t page_size, int64_t page_stride,
+                                   const void *k_codebooks, const void *v_codebooks, int32_t heads_q,
+                                   int32_t heads_kv, int32_t head_dim, int32_t sub_dim,
+                                   int32_t n_centroids, int64_t window, float scale, vq_dtype dtype,
+                                   void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                   vq_stream_t stream);
 
 /* Workspace vq_paged_attention needs for these sizes on the current device
  * (0 for invalid sizes).  It does not depend on the lengths in the cache. */

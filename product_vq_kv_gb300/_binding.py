@@ -89,6 +89,8 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.vq_paged_attention.argtypes = [vp, i64, vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, i32,
                                        i64, vp, vp, i32, i32, i32, i32, i32, i64, ctypes.c_float,
                                        i32, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.vq_paged_attention_slots.restype = i32
+    lib.vq_paged_attention_slots.argtypes = lib.vq_paged_attention.argtypes[:4] + [vp] + lib.vq_paged_attention.argtypes[4:]
     lib.vq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.vq_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32]
     lib.vq_status_string.restype = ctypes.c_char_p
@@ -755,7 +757,8 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
                        window: int = 0, scale: float = 0.0, out: torch.Tensor | None = None,
                        lse: torch.Tensor | None = None, return_lse: bool = False,
                        workspace: torch.Tensor | None = None,
-                       stream: torch.cuda.Stream | None = None):
+                       stream: torch.cuda.Stream | None = None,
+                       slots: torch.Tensor | None = None):
     """Causal attention of the new tokens of every request over its pages.
 
     ``q`` ``[T, Hq, D]`` (tokens may be strided); ``cu_new`` ``[R + 1]``,
@@ -764,7 +767,9 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
     codebooks in q's dtype.  ``max_new`` is the most new tokens of a request
     where the host knows it.  Returns ``out`` ``[T, Hq, D]``, or ``(out, lse)``
     with ``lse`` ``[T, Hq]`` float32 where ``return_lse`` is set or ``lse`` is
-    given.  A workspace of :func:`vq_paged_attention_workspace_bytes` bytes is
+    given.  ``slots`` (at least ``[T]`` int64, of :func:`vq_paged_reserve`) makes the
+    rows of refused requests zeros with an lse of -inf; without it they are taken for
+    the last tokens their request has in the cache.  A workspace of :func:`vq_paged_attention_workspace_bytes` bytes is
     allocated here (by torch) if none is given; it and new outputs are allocated on
     ``stream``."""
     _token_rows(q, "q", None)
@@ -781,6 +786,12 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
     blocks = _table_tensor(block_table, r, dev)
     if max_new < 0:
         raise ValueError("max_new must not be negative")
+    if slots is not None:
+        if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] < tokens:
+            raise ValueError("slots must be an int64 tensor of at least [T]")
+        _device_tensor(slots, "slots")
+        if slots.device != dev:
+            raise ValueError(f"slots is on {slots.device}, not on {dev}")
     out = _out_like(out, "out", (tokens, hq, d), q.dtype, dev, stream)
     if return_lse or lse is not None:
         lse = _out_like(lse, "lse", (tokens, hq), torch.float32, dev, stream)
@@ -792,8 +803,9 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
         if workspace.device != dev:
             raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
         nbytes = workspace.numel() * workspace.element_size()
-    _launch(load_library().vq_paged_attention, "vq_paged_attention", dev, stream, q.data_ptr(),
-            _token_stride(q), cu_new.data_ptr(), lens.data_ptr(), r, tokens, max_new,
+    _launch(load_library().vq_paged_attention_slots, "vq_paged_attention", dev, stream, q.data_ptr(),
+            _token_stride(q), cu_new.data_ptr(), lens.data_ptr(),
+            slots.data_ptr() if slots is not None else None, r, tokens, max_new,
             block_table.data_ptr(), blocks, k_codes.data_ptr(), v_codes.data_ptr(), pages, page_size,
             stride, k_codebooks.data_ptr(), v_codebooks.data_ptr(), hq, hkv, d, sub, n_c, window, scale,
             _dtype_code(q), out.data_ptr(), lse.data_ptr() if lse is not None else None,

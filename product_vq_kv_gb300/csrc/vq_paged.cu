@@ -368,14 +368,14 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
     return need;
 }
 
-vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_new, const int32_t *lens,
-                             int64_t requests, int64_t tokens, int64_t max_new, const int32_t *block_table,
-                             int64_t max_blocks, const uint8_t *k_codes, const uint8_t *v_codes,
-                             int64_t num_pages, int32_t page_size, int64_t page_stride,
-                             const void *k_codebooks, const void *v_codebooks, int32_t heads_q,
-                             int32_t heads_kv, int32_t head_dim, int32_t sub_dim, int32_t n_centroids,
-                             int64_t window, float scale, vq_dtype dtype, void *out, float *lse,
-                             void *workspace, size_t workspace_bytes, vq_stream_t stream)
+vq_status vq_paged_attention_slots(const void *q, int64_t q_stride, const int32_t *cu_new, const int32_t *lens,
+                                   const int64_t *slots, int64_t requests, int64_t tokens, int64_t max_new,
+                                   const int32_t *block_table, int64_t max_blocks, const uint8_t *k_codes,
+                                   const uint8_t *v_codes, int64_t num_pages, int32_t page_size, int64_t page_stride,
+                                   const void *k_codebooks, const void *v_codebooks, int32_t heads_q,
+                                   int32_t heads_kv, int32_t head_dim, int32_t sub_dim, int32_t n_centroids,
+                                   int64_t window, float scale, vq_dtype dtype, void *out, float *lse,
+                                   void *workspace, size_t workspace_bytes, vq_stream_t stream)
 {
     if (dtype != VQ_F16 && dtype != VQ_BF16 && dtype != VQ_F32) return VQ_ERR_INVALID_ARG;
     vq_status s = check_shape(requests, tokens, heads_q, heads_kv, head_dim, sub_dim, n_centroids, page_size);
@@ -393,7 +393,8 @@ vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_
     if (requests > 0 && (!lens || (max_blocks > 0 && !block_table))) return VQ_ERR_INVALID_ARG;
     if (num_pages > 0 && (!k_codes || !v_codes)) return VQ_ERR_INVALID_ARG;
     if ((uintptr_t)q % es || (uintptr_t)k_codebooks % es || (uintptr_t)v_codebooks % es || (uintptr_t)out % es ||
-        !aligned4(cu_new) || !aligned4(lens) || !aligned4(block_table) || !aligned4(lse) || (uintptr_t)workspace % 16)
+        !aligned4(cu_new) || !aligned4(lens) || !aligned4(block_table) || !aligned4(lse) || (uintptr_t)slots % 8 ||
+        (uintptr_t)workspace % 16)
         return VQ_ERR_INVALID_ARG;
 
     AttnCall c{};
@@ -411,6 +412,7 @@ vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_
     a.lse = lse;
     a.cu = cu_new;
     a.lens = lens;
+    a.slots = slots;
     a.table = block_table;
     a.tokens = tokens;
     a.q_stride = q_stride;
@@ -442,6 +444,21 @@ vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_
     case VQ_F32: return launch_simple<float>(c, p, ws);
     }
     return VQ_ERR_INTERNAL;
+}
+
+vq_status vq_paged_attention(const void *q, int64_t q_stride, const int32_t *cu_new, const int32_t *lens,
+                             int64_t requests, int64_t tokens, int64_t max_new, const int32_t *block_table,
+                             int64_t max_blocks, const uint8_t *k_codes, const uint8_t *v_codes,
+                             int64_t num_pages, int32_t page_size, int64_t page_stride,
+                             const void *k_codebooks, const void *v_codebooks, int32_t heads_q,
+                             int32_t heads_kv, int32_t head_dim, int32_t sub_dim, int32_t n_centroids,
+                             int64_t window, float scale, vq_dtype dtype, void *out, float *lse,
+                             void *workspace, size_t workspace_bytes, vq_stream_t stream)
+{
+    return vq_paged_attention_slots(q, q_stride, cu_new, lens, nullptr, requests, tokens, max_new, block_table,
+                                    max_blocks, k_codes, v_codes, num_pages, page_size, page_stride, k_codebooks,
+                                    v_codebooks, heads_q, heads_kv, head_dim, sub_dim, n_centroids, window, scale,
+                                    dtype, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -60,6 +60,7 @@ struct PagedArgs {
     void *out;
     float *lse;            // or null
     const int32_t *cu, *lens, *table;
+    const int64_t *slots;  // [tokens] or null: a request whose first new token has none is refused
     int64_t tokens;        // rows of q
     int64_t q_stride;      // elements between tokens of q
     int64_t page_stride;   // bytes between pages of codes
@@ -92,12 +93,21 @@ struct PagedItem {
 
 // Lengths as the kernel sees them: cu clamped into [0, tokens], request
 // number `requests` being the rows after the last.  Rows are below 2^31, and so
-// are items.
+// are items.  A refused request holds nothing, so that its rows see nothing.
 struct PagedLens {
     const int32_t *cu, *lens;
     const int32_t *starts;  // start(0 .. requests), or null: computed
     int32_t requests, tile;
     int64_t tokens;
+    // (where starts are staged, so are lengths: those of refused requests are 0 there)
+    __host__ __device__ __forceinline__ int32_t length(int r, const int64_t *slots) const
+    {
+        if (slots && !starts) {
+            const int64_t at = first(r);
+            if (at < tokens && slots[at] < 0) return 0;
+        }
+        return lens[r] > 0 ? lens[r] : 0;
+    }
     __host__ __device__ __forceinline__ int64_t first(int r) const
     {
         if (r > requests) return tokens;
@@ -145,7 +155,7 @@ __host__ __device__ __forceinline__ PagedItem paged_item(const PagedArgs &a, con
         if (next > j + 1) *skip = next;
         return it;
     }
-    const int64_t len = r < a.requests ? (l.lens[r] > 0 ? l.lens[r] : 0) : 0;
+    const int64_t len = r < a.requests ? l.length(r, a.slots) : 0;
     const int64_t cap = (int64_t)a.max_blocks << a.page_shift;
     const int64_t i1 = i0 + l.tile < n ? i0 + l.tile : n;
     const int64_t pos0 = len - n + i0;
@@ -258,7 +268,7 @@ __device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> 
         for (int i = tid; i <= a.requests; i += THREADS) {
             w.stage.cu[i] = a.cu[i];
             w.stage.start[i] = (int32_t)from.compute_start(i);
-            if (i < a.requests) w.stage.lens[i] = a.lens[i];
+            if (i < a.requests) w.stage.lens[i] = from.length(i, a.slots);
         }
         __syncthreads();
     }

@@ -8,6 +8,7 @@
 #define vq_paged_reserve polls_paged_reserve
 #define vq_paged_trim polls_paged_trim
 #define vq_paged_attention polls_paged_attention
+#define vq_paged_attention_slots polls_paged_attention_slots
 #define vq_paged_attention_workspace_bytes polls_paged_attention_workspace_bytes
 #define vqh_status_paged polls_status_paged
 #define vqh_device_sms polls_device_sms

@@ -725,6 +725,8 @@ def vq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
     if slots.device != dev:
         raise ValueError(f"slots is on {slots.device}, not on {dev}")
     if k_smooth is not None:
+        if not isinstance(k_smooth, torch.Tensor):
+            raise TypeError("k_smooth must be a torch.Tensor")
         if k_smooth.dtype != torch.float32 or tuple(k_smooth.shape) != (heads, d):
             raise ValueError("k_smooth must be float32 of shape [H, D]")
         _device_tensor(k_smooth, "k_smooth")
@@ -777,7 +779,7 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
     tokens, hq, d = q.shape
     pages, hkv, page_size, ns, stride, n_c, sub = _page_tensors(k_codes, v_codes, k_codebooks,
                                                                 v_codebooks, q.dtype, dev)
-    if ns * sub != d or hq % hkv:
+    if ns * sub != d or hkv < 1 or hq % hkv:
         raise ValueError(f"q {tuple(q.shape)} does not match codes {tuple(k_codes.shape)} and "
                          f"codebooks {tuple(k_codebooks.shape)}")
     r = _extent(lens)

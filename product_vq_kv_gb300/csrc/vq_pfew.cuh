@@ -305,11 +305,11 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
             // a row whose limit k_hi cut keeps its own window
             int32_t low[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int row = 2 * t + c;
-                    const int64_t p = (int64_t)s.it.pos0 + (row < rows ? row / gc : 0) - a.window;
-                    low[c] = a.window == 0 || p < -1 ? -1 : (int32_t)p;  // tokens above it are seen
-                }
+            for (int c = 0; c < 2; ++c) {
+                const int row = 2 * t + c;
+                const int64_t p = (int64_t)s.it.pos0 + (row < rows ? row / gc : 0) - a.window;
+                low[c] = a.window == 0 || p < -1 ? -1 : (int32_t)p;  // tokens above it are seen
+            }
             const int32_t all_hi = s.it.pos0 < s.it.k_hi ? s.it.pos0 : s.it.k_hi - 1;  // every row sees up to here
             const int64_t last_pos = (int64_t)s.it.pos0 + s.it.ntok - 1;
             const int64_t all_lo = a.window == 0 ? -1 : last_pos - a.window;       // and above here
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                     // S^T = K^ Q^T
                     float st[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) st[c] = 0.f;
+                    for (int c = 0; c < 4; ++c) st[c] = 0.f;
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
                         uint32_t lo[SUB / 2], hi[SUB / 2];
@@ -371,41 +371,41 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                         image_row<SUB>(k_base, code_at(kc[X][1], b), hi);
 #pragma unroll
                         for (int i = 0; i < SUB / 4; ++i)
-                                mma16816<T>(st, lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
-                                            qf[b * (SUB / 4) + i][0], qf[b * (SUB / 4) + i][1]);
+                            mma16816<T>(st, lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
+                                        qf[b * (SUB / 4) + i][0], qf[b * (SUB / 4) + i][1]);
                     }
                     const int32_t k0 = first_of(group);
                     const bool whole = k0 + 15 <= all_hi && k0 > all_lo;
                     bool rise = false;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            st[c] *= a.kappa;
-                            if (!whole) {
-                                const int32_t key = k0 + g + (c >> 1) * 8;
-                                if (key > lim[c & 1] || key <= low[c & 1]) st[c] = kNone;
-                            }
-                            rise |= st[c] > m[c & 1] + (kFewSlack + kShift);
+                    for (int c = 0; c < 4; ++c) {
+                        st[c] *= a.kappa;
+                        if (!whole) {
+                            const int32_t key = k0 + g + (c >> 1) * 8;
+                            if (key > lim[c & 1] || key <= low[c & 1]) st[c] = kNone;
                         }
+                        rise |= st[c] > m[c & 1] + (kFewSlack + kShift);
+                    }
                     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                float top = fmaxf(st[c], st[c + 2]);
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                                // a row rises for its own scores alone, so that what it
-                                // computes does not depend on the rows beside it
-                                const bool up = top > m[c] + (kFewSlack + kShift);
-                                const float ref = up ? top - kShift : m[c];
-                                const float f = up ? exp2_fast(m[c] - ref) : 1.f;
-                                m[c] = ref;
-                                sum[c] *= f;
+                        for (int c = 0; c < 2; ++c) {
+                            float top = fmaxf(st[c], st[c + 2]);
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            // a row rises for its own scores alone, so that what it
+                            // computes does not depend on the rows beside it
+                            const bool up = top > m[c] + (kFewSlack + kShift);
+                            const float ref = up ? top - kShift : m[c];
+                            const float f = up ? exp2_fast(m[c] - ref) : 1.f;
+                            m[c] = ref;
+                            sum[c] *= f;
 #pragma unroll
-                                for (int i = 0; i < kMma; ++i) {
-                                    o[i][c] *= f;
-                                    o[i][c + 2] *= f;
-                                }
+                            for (int i = 0; i < kMma; ++i) {
+                                o[i][c] *= f;
+                                o[i][c + 2] *= f;
                             }
+                        }
                     }
                     float p[4];
 #pragma unroll
@@ -436,8 +436,8 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                             const uint32_t a1 = __byte_perm(e[0][i], e[1][i], 0x7632);
                             const uint32_t a2 = __byte_perm(e[2][i], e[3][i], 0x5410);
                             const uint32_t a3 = __byte_perm(e[2][i], e[3][i], 0x7632);
-                                mma16816<T>(o[b * (SUB / 2) + i], a0, a1, a2, a3, pf[0][0], pf[0][1]);
-                                mma16816<T>(o[b * (SUB / 2) + i], a0, a1, a2, a3, pf[1][0], pf[1][1]);
+                            mma16816<T>(o[b * (SUB / 2) + i], a0, a1, a2, a3, pf[0][0], pf[0][1]);
+                            mma16816<T>(o[b * (SUB / 2) + i], a0, a1, a2, a3, pf[1][0], pf[1][1]);
                         }
                     }
                 }
@@ -450,11 +450,11 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
 
             // the warps' states: maxima and sums first
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
-                    sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
-                    sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
-                }
+            for (int c = 0; c < 2; ++c) {
+                sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
+                sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
+                sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
+            }
             // A sum of 0: the warp has seen no token of the row, or scores of -inf alone.
             // Its groups are looked through once more for a token that the row sees
             // (here and not in the loop, which has no register to spare; most such rows
@@ -489,26 +489,26 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
             }
             __syncthreads();
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int row = 2 * t + c;
-                    float top = kNone;
+            for (int c = 0; c < 2; ++c) {
+                const int row = 2 * t + c;
+                float top = kNone;
 #pragma unroll
-                    for (int k = 0; k < kFewWarps; ++k)
-                        if (wl[k][row] != 0.f) top = fmaxf(top, wm[k][row]);
-                    float total = 0.f;
+                for (int k = 0; k < kFewWarps; ++k)
+                    if (wl[k][row] != 0.f) top = fmaxf(top, wm[k][row]);
+                float total = 0.f;
 #pragma unroll
-                    for (int k = 0; k < kFewWarps; ++k)
-                        if (wl[k][row] != 0.f) total = fmaf(exp2_fast(wm[k][row] - top), wl[k][row], total);
-                    if (top == kNone && total != 0.f) total = 1.f;
-                    const float f = sum[c] == 0.f || m[c] == kNone ? 0.f : exp2_fast(m[c] - top);
-                    m[c] = top;
-                    sum[c] = total;
+                for (int k = 0; k < kFewWarps; ++k)
+                    if (wl[k][row] != 0.f) total = fmaf(exp2_fast(wm[k][row] - top), wl[k][row], total);
+                if (top == kNone && total != 0.f) total = 1.f;
+                const float f = sum[c] == 0.f || m[c] == kNone ? 0.f : exp2_fast(m[c] - top);
+                m[c] = top;
+                sum[c] = total;
 #pragma unroll
-                    for (int i = 0; i < kMma; ++i) {
-                        o[i][c] *= f;
-                        o[i][c + 2] *= f;
-                    }
+                for (int i = 0; i < kMma; ++i) {
+                    o[i][c] *= f;
+                    o[i][c + 2] *= f;
                 }
+            }
             // then the weighted sums: the upper half of the warps to the lower, until one is left
 #pragma unroll
             for (int live = kFewWarps; live > 1; live = (live + 1) / 2) {
@@ -516,69 +516,69 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                 float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp < half ? warp : warp - half) * kMma * 32 + lane;
                 if (warp >= half && warp < live) {
 #pragma unroll
-                        for (int i = 0; i < kMma; ++i)
-                            if (dyn_smem_ok(slot + i * 32, 16, 16))
-                                slot[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                    for (int i = 0; i < kMma; ++i)
+                        if (dyn_smem_ok(slot + i * 32, 16, 16))
+                            slot[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 }
                 __syncthreads();
                 if (warp < live - half) {
 #pragma unroll
-                        for (int i = 0; i < kMma; ++i)
-                            if (dyn_smem_ok(slot + i * 32, 16, 16)) {
-                                const float4 v = slot[i * 32];
-                                o[i][0] += v.x;
-                                o[i][1] += v.y;
-                                o[i][2] += v.z;
-                                o[i][3] += v.w;
-                            }
+                    for (int i = 0; i < kMma; ++i)
+                        if (dyn_smem_ok(slot + i * 32, 16, 16)) {
+                            const float4 v = slot[i * 32];
+                            o[i][0] += v.x;
+                            o[i][1] += v.y;
+                            o[i][2] += v.z;
+                            o[i][3] += v.w;
+                        }
                 }
                 __syncthreads();
             }
             if (warp == 0) {
                 // lane (g, t) holds columns [g dim/8, (g+1) dim/8) of rows 2 t + c
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int row = 2 * t + c;
-                        if (row >= rows) continue;
-                        if (s.whole) {
-                            const int64_t orow = (s.it.tok0 + row / gc) * a.hq + head0 + row % gc;
-                            const float inv = paged_inv(m[c], sum[c]);
-                            T *dst = out + orow * D + g * (D / 8);
-                            if (VQ_SPAN(dst, D / 8, out, a.tokens * a.hq * D)) {
-                                if (out_vec) {
+                for (int c = 0; c < 2; ++c) {
+                    const int row = 2 * t + c;
+                    if (row >= rows) continue;
+                    if (s.whole) {
+                        const int64_t orow = (s.it.tok0 + row / gc) * a.hq + head0 + row % gc;
+                        const float inv = paged_inv(m[c], sum[c]);
+                        T *dst = out + orow * D + g * (D / 8);
+                        if (VQ_SPAN(dst, D / 8, out, a.tokens * a.hq * D)) {
+                            if (out_vec) {
 #pragma unroll
-                                    for (int i = 0; i < kMma; i += 4) {
-                                        uint32_t v[4];
+                                for (int i = 0; i < kMma; i += 4) {
+                                    uint32_t v[4];
 #pragma unroll
-                                        for (int x = 0; x < 4; ++x)
-                                            v[x] = pack2<T>(o[i + x][c] * inv, o[i + x][c + 2] * inv);
-                                        reinterpret_cast<uint4 *>(dst)[i / 4] = make_uint4(v[0], v[1], v[2], v[3]);
-                                    }
-                                } else {
+                                    for (int x = 0; x < 4; ++x)
+                                        v[x] = pack2<T>(o[i + x][c] * inv, o[i + x][c + 2] * inv);
+                                    reinterpret_cast<uint4 *>(dst)[i / 4] = make_uint4(v[0], v[1], v[2], v[3]);
+                                }
+                            } else {
 #pragma unroll
-                                    for (int i = 0; i < kMma; ++i) {
-                                        dst[2 * i] = narrow<T>(o[i][c] * inv);
-                                        dst[2 * i + 1] = narrow<T>(o[i][c + 2] * inv);
-                                    }
+                                for (int i = 0; i < kMma; ++i) {
+                                    dst[2 * i] = narrow<T>(o[i][c] * inv);
+                                    dst[2 * i + 1] = narrow<T>(o[i][c + 2] * inv);
                                 }
                             }
-                            if (g == 0 && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq))
-                                a.lse[orow] = paged_lse(m[c], sum[c]);
-                        } else {
-                            const int64_t prow = s.slot * a.tile_rows + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
-                            float *dst = a.part + prow * D + g * (D / 8);
-                            if (VQ_VSPAN(dst, D / 8, a.part, prows * D, 16)) {
+                        }
+                        if (g == 0 && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq))
+                            a.lse[orow] = paged_lse(m[c], sum[c]);
+                    } else {
+                        const int64_t prow = s.slot * a.tile_rows + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
+                        float *dst = a.part + prow * D + g * (D / 8);
+                        if (VQ_VSPAN(dst, D / 8, a.part, prows * D, 16)) {
 #pragma unroll
-                                for (int i = 0; i < kMma; i += 2)
-                                    reinterpret_cast<float4 *>(dst)[i / 2] =
-                                        make_float4(o[i][c], o[i][c + 2], o[i + 1][c], o[i + 1][c + 2]);
-                            }
-                            if (g == 0 && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
-                                a.ml[prow * 2] = m[c];
-                                a.ml[prow * 2 + 1] = sum[c];
-                            }
+                            for (int i = 0; i < kMma; i += 2)
+                                reinterpret_cast<float4 *>(dst)[i / 2] =
+                                    make_float4(o[i][c], o[i][c + 2], o[i + 1][c], o[i + 1][c + 2]);
+                        }
+                        if (g == 0 && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
+                            a.ml[prow * 2] = m[c];
+                            a.ml[prow * 2 + 1] = sum[c];
                         }
                     }
+                }
             }
         }
     }

@@ -291,7 +291,9 @@ vq_status vq_attention_decode_static(const void *q, const uint8_t *k_codes,
  * needs pages, if its need and that of every request before it (refused
  * for want of pages or not) are within *free_count.  The pages of the granted
  * requests are popped from the stack in request order, then block order.
- *   lens, new_lens  [requests]  device; negative values count as 0
+ *   lens, new_lens  [requests]  device; negative values count as 0; new_lens
+ *                   sum to less than 2^31 (offsets beyond are cut there, and what
+ *                   lies past them gets no pages, slots or length)
  *   block_table     the entries of the new pages are written
  *   total_new       rows of `slots` (known to the host: the rows of the packed
  *                   new tokens; may exceed the sum of new_lens)
@@ -336,7 +338,8 @@ vq_status vq_paged_trim(const int32_t *lens, const int32_t *keep_lens, int64_t r
  *                [heads][head_dim], device, dtype (a slice of a packed
  *                projection will do)
  *   slots        [tokens] int64, device; a slot outside [0, num_pages *
- *                page_size) is skipped; two tokens with one slot leave either
+ *                page_size) is skipped; of two tokens with one slot each code
+ *                there is one token's or the other's, and the row may mix them
  *   k_codebooks, v_codebooks  [heads][n_centroids][sub_dim]  device, dtype
  *   k_smooth     [heads][head_dim] fp32 factors of the keys, device, or NULL
  *   k_codes, v_codes  the pages, written at the slots

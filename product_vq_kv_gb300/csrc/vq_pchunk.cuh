@@ -269,7 +269,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     PagedLens l;
     const bool work = paged_plan<kChunkThreads>(a, w, l);  // has barriers for the whole block
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    else if (warp < 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // the next segment of a role's warp: seg_n counts those it has taken; false at
     // the end (or if a wait gave up)

@@ -128,15 +128,19 @@ struct TensorPlan {
     int32_t few_tokens;
 };
 
-TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_t group)
+TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_t group, int32_t dim)
 {
     TensorPlan p{};
     const int64_t most = max_new > 0 && max_new < tokens ? max_new : tokens;  // new tokens of a request, as far as known
-    // up to three items of rows: a unit of cached tokens takes an SM 970 cycles for
-    // each in the few-row kernel, and 2500 to 3000 in the chunk kernel for one tile,
-    // however few of its 128 rows there are
+    // Up to three items of 8 rows, two at dim 256: the chunk kernel takes the time of a
+    // tile of 128 rows however few there are, the few-row kernel that of its items.  16
+    // requests of 8000 (2 of 30000), few-row against chunk kernel, us: dim 128 with two
+    // items 77 : 101 (45 : 64), three 107 : 101 (58 : 66), four 135 : 102 (70 : 66); dim 64
+    // three 74 : 84 (43 : 56), four 93 : 84 (51 : 56); dim 256 two 72 : 80 (43 : 51), three
+    // 99 : 80 (54 : 54).  Other head groups and sub-vectors lie alike.
+    const int32_t items = dim == 256 ? 2 : 3;
     const int32_t item_tokens = group < vqh_few_rows() ? vqh_few_rows() / group : 1;
-    p.few_tokens = group > vqh_few_rows() ? 1 : 3 * item_tokens;
+    p.few_tokens = group > vqh_few_rows() ? 1 : items * item_tokens;
     p.chunk = most > p.few_tokens;
     p.few = requests != 1 || !p.chunk;
     return p;
@@ -237,7 +241,7 @@ constexpr int64_t kWholeUnits = 8;
 template <typename T>
 vq_status launch_tensor(const AttnCall &c, unsigned char *ws)
 {
-    const TensorPlan t = tensor_plan(c.a.requests, c.a.tokens, c.max_new, c.a.group);
+    const TensorPlan t = tensor_plan(c.a.requests, c.a.tokens, c.max_new, c.a.group, c.a.dim);
     AttnPart few, chunk;
     (void)tensor_parts(t, c.sms, c.a.group, c.a.dim, &few, &chunk);
     if (t.chunk) {
@@ -255,9 +259,11 @@ vq_status launch_tensor(const AttnCall &c, unsigned char *ws)
         a.cls = t.chunk ? 1 : 0;
         a.cls_tokens = t.few_tokens;
         // Short caches and few of them: an item a block, none split, no merge to
-        // launch.  One token, 8 heads, whole against split: on 300 cached tokens 12.3
-        // against 14.3 us on the device (a graph's replay), on 777 15.3 against 14.4,
-        // but 25.3 against 27.5 us as a call.
+        // launch.  One token, 8 heads, whole against split, us on the device (a graph's
+        // replay) and as a call: one request of 300 12.3 : 14.4 (26.6 : 29.7), of 777 16.4 :
+        // 14.4 (25.9 : 28.8); eight of 300 13.5 : 18.4 (26.3 : 29.7), of 777 16.4 : 19.8
+        // (26.7 : 29.7).  The host knows no lengths: what counts is how long the table
+        // lets them be, and a wider table takes the split.
         const int64_t cap = (int64_t)a.max_blocks << a.page_shift;
         a.no_split = cap <= kWholeUnits * vqk::kUnit && a.items * a.hkv * a.gch <= few.blocks;
         vq_status s = vqh_paged_few(a, c.dtype, few.blocks, c.stream);
@@ -362,7 +368,8 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
     size_t need = simple_part(sms, group, head_dim, 0).end;
     if (tensor_shape(VQ_F16, head_dim, sub_dim, page_size)) {
         AttnPart few, chunk;
-        const size_t t = tensor_parts(tensor_plan(requests, tokens, max_new, group), sms, group, head_dim, &few, &chunk);
+        const TensorPlan plan = tensor_plan(requests, tokens, max_new, group, head_dim);
+        const size_t t = tensor_parts(plan, sms, group, head_dim, &few, &chunk);
         if (t > need) need = t;
     }
     return need;

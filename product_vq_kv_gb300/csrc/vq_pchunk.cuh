@@ -30,7 +30,7 @@
 // exceeds it by 2^8; then the row's O is rescaled in tensor memory, after the
 // product before has finished.  Weights are rounded to the input type for the
 // product with V^; their sum takes them unrounded.  (In two pieces, as the few-row
-// kernel takes them, the products would grow by half, from 2048 to 3072 of about 3650
+// kernel takes them, the products would grow by half, from 2048 to 3072 of about 3500
 // cycles a block at dim 128, and the softmax between them by two packings and a
 // subtraction a pair of weights; the error against 64 bits is 0.0017 in bf16 and 0.00022
 // in fp16 with one piece, 0.0016 and 0.00021 with fp32 weights.)

@@ -68,9 +68,10 @@ constexpr float kFewLow = -3.402823466e38f;
 
 // Warps of a block and blocks of an SM: two blocks where a lane's accumulators
 // and queries (dim/16 x 6 registers) fit 128 registers.  At dim 256 one block of 8
-// warps at 255 registers: 12 at 168 spill (8 requests of 32768: 105 against 74 us).
-// Items of 16 rows, two columns of instructions on each rebuilt value, took 70 us
-// for drafts where two items of 8 take 52: twice the registers leave fewer warps.
+// warps at 255 registers (8 requests of 32768: 78 us): 12 at 168 spill (105 against 74
+// us, with weights in one piece).  Items of 16 rows, two columns of instructions on each
+// rebuilt value, took 70 us for drafts where two items of 8 took 52: twice the registers
+// leave fewer warps.
 template <int D>
 struct FewShape {
     static constexpr int kWarps = 8;

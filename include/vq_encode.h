@@ -425,6 +425,92 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
                                           int32_t sub_dim, int32_t n_centroids, int32_t page_size);
 
 /*
+ * Pages that several requests hold.  vq_paged_reserve and vq_paged_trim keep every
+ * page with one request.  Beams, and the samples of one prompt, hold the pages of
+ * their common tokens together: vq_paged_fork makes them, and takes the place of
+ * vq_paged_trim for as long as pages are shared (vq_paged_trim would push pages that
+ * others hold).  vq_paged_compact brings the held pages to the front of the pool, so
+ * that the rest can be given back.  Both change tables and lists only and name the
+ * pages whose contents are to be copied; vq_paged_copy copies them in every pool of
+ * pages (codes, scales, all layers).  They serve any cache of pages.
+ *
+ * vq_paged_fork -- seat d goes on with the first keep_lens[d] tokens of seat
+ * parents[d] (itself: it stays as it is or is cut; another: it forks; outside
+ * [0, seats): it is emptied).
+ *   lens            [seats]  device: tokens of the seats before (taken into
+ *                   [0, max_blocks * page_size])
+ *   parents         [seats]  device
+ *   keep_lens       [seats]  device, taken into [0, lens[parents[d]]]; NULL: all
+ *   block_table     [seats][max_blocks]  device
+ *   free_pages      [num_pages], a stack of *free_count pages: pages that no seat
+ *                   holds any longer are pushed, in ascending order
+ *   lens_out        [seats]  device, written.  May be lens.
+ *   table_out       [seats][max_blocks]  device, written, -1 past a seat's pages.  Must
+ *                   not overlap block_table.
+ *   free_count_out  [1]  device, written.  May be free_count.
+ *   copies          [seats][2]  device, written: pages (from, to) of a seat, -1, -1
+ *                   where it needs none
+ *   workspace       >= vq_paged_fork_workspace_bytes(num_pages) bytes, device, 16-byte
+ *                   aligned
+ * Seats hold whole pages together.  A page that a seat's tokens end inside, where the
+ * seat's next tokens go, is its own: of the seats that end inside one page the lowest
+ * keeps it, unless a seat holds it as a whole page; the others are given pages popped
+ * from the stack (after the push), in seat order, and their (from, to) pairs in
+ * `copies`.  Where the stack is empty a seat is cut to its whole pages.  Entries that
+ * are no page are carried along and never copied.  Asynchronous on `stream`.
+ */
+size_t vq_paged_fork_workspace_bytes(int64_t num_pages);
+vq_status vq_paged_fork(const int32_t *lens, const int32_t *parents, const int32_t *keep_lens,
+                        int64_t seats, const int32_t *block_table, int64_t max_blocks,
+                        int32_t page_size, int32_t *free_pages, const int32_t *free_count,
+                        int64_t num_pages, int32_t *lens_out, int32_t *table_out,
+                        int32_t *free_count_out, int32_t *copies, void *workspace,
+                        size_t workspace_bytes, vq_stream_t stream);
+
+/*
+ * vq_paged_compact -- give the held pages (those not among the first *free_count of
+ * free_pages) the numbers below their count `used`: the i-th held page at or past
+ * `used` takes the number of the i-th free page below it, the others stay.
+ *   table_out       [requests][max_blocks]  device, written: block_table with the
+ *                   entries of cached tokens renumbered.  May be block_table.
+ *   free_pages_out  [num_pages]  device, written: num_pages - 1 down to `used`, so that
+ *                   the lowest page is popped first, then -1.  May be free_pages.
+ *   free_count_out  [1]  device, written.  May be free_count.
+ *   moves           [num_pages / 2][2]  device, written: pages (from, to), from
+ *                   ascending, then -1, -1
+ *   page_map        [num_pages]  device, written: the new number of each held page,
+ *                   -1 of a free one (for page numbers that are kept elsewhere)
+ * Asynchronous on `stream`.
+ */
+vq_status vq_paged_compact(const int32_t *lens, int64_t requests, const int32_t *block_table,
+                           int64_t max_blocks, int32_t page_size, const int32_t *free_pages,
+                           const int32_t *free_count, int64_t num_pages, int32_t *table_out,
+                           int32_t *free_pages_out, int32_t *free_count_out, int32_t *moves,
+                           int32_t *page_map, vq_stream_t stream);
+
+/*
+ * vq_paged_copy -- copy page pairs[i][0] to page pairs[i][1] in every pool.
+ *   pairs      [n_pairs][2]  device; a pair that does not name two different pages of
+ *              [0, num_pages) is skipped.  No page that is written may be read or
+ *              written by another pair.
+ *   pools      [n_pools] host, up to VQ_PAGED_MAX_POOLS (read before the call returns):
+ *              page p of layer l is page_bytes bytes at base + l * layer_stride +
+ *              p * page_stride (bytes); pages and layers do not overlap
+ * Any alignment; pages whose address, size and strides are multiples of 16 bytes are
+ * copied fastest.  Asynchronous on `stream`.
+ */
+#define VQ_PAGED_MAX_POOLS 8
+typedef struct {
+    void *base;           /* device */
+    int64_t page_stride;  /* bytes */
+    int64_t page_bytes;
+    int64_t layer_stride; /* bytes; unused with one layer */
+    int32_t layers;
+} vq_page_pool;
+vq_status vq_paged_copy(const int32_t *pairs, int64_t n_pairs, const vq_page_pool *pools,
+                        int32_t n_pools, int64_t num_pages, vq_stream_t stream);
+
+/*
  * Sibling encoders on the same nearest-centroid rule (the page of five
  * hand-tuned Metal compute kernels for TurboQuant, "Kernel 2: Scalar Quantize
  * / Dequantize" and "Kernel 3: Fused Hadamard + Quantize").  One fp32

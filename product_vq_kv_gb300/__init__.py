@@ -37,6 +37,10 @@ from ._binding import (  # noqa: F401
     vq_paged_append,
     vq_paged_attention,
     vq_paged_attention_workspace_bytes,
+    vq_paged_compact,
+    vq_paged_copy,
+    vq_paged_fork,
+    vq_paged_fork_workspace_bytes,
     vq_paged_reserve,
     vq_paged_trim,
     vq_partition,

@@ -41,6 +41,16 @@ class VqSlice(ctypes.Structure):
                 ("row", ctypes.c_int64), ("n_rows", ctypes.c_int64)]
 
 
+class VqPagePool(ctypes.Structure):
+    """``vq_page_pool``: pages of one pool, possibly of several layers."""
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64),
+                ("layer_stride", ctypes.c_int64), ("layers", ctypes.c_int32)]
+
+
+# Pools of one vq_paged_copy (VQ_PAGED_MAX_POOLS).
+PAGED_MAX_POOLS = 8
+
+
 def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     """Declare the argument and result types of every entry point on ``lib``
     (the library, or its bounds-checked build, which has the same ABI)."""
@@ -93,6 +103,15 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.vq_paged_attention_slots.argtypes = lib.vq_paged_attention.argtypes[:4] + [vp] + lib.vq_paged_attention.argtypes[4:]
     lib.vq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.vq_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32]
+    lib.vq_paged_fork_workspace_bytes.restype = ctypes.c_size_t
+    lib.vq_paged_fork_workspace_bytes.argtypes = [i64]
+    lib.vq_paged_fork.restype = i32
+    lib.vq_paged_fork.argtypes = [vp, vp, vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp,
+                                  ctypes.c_size_t, vp]
+    lib.vq_paged_compact.restype = i32
+    lib.vq_paged_compact.argtypes = [vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    lib.vq_paged_copy.restype = i32
+    lib.vq_paged_copy.argtypes = [vp, i64, vp, i32, i64, vp]
     lib.vq_status_string.restype = ctypes.c_char_p
     lib.vq_status_string.argtypes = [i32]
     lib.vq_describe_launch.restype = i32
@@ -813,6 +832,134 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
             _dtype_code(q), out.data_ptr(), lse.data_ptr() if lse is not None else None,
             workspace.data_ptr(), nbytes)
     return (out, lse) if lse is not None else out
+
+
+def vq_paged_fork_workspace_bytes(num_pages: int) -> int:
+    return int(load_library().vq_paged_fork_workspace_bytes(num_pages))
+
+
+def _workspace_of(workspace, need: int, device, stream) -> tuple:
+    """A workspace of at least ``need`` bytes: the given one, checked, or a new one; and
+    its size."""
+    if workspace is None:
+        workspace = _empty(max(need, 16), torch.uint8, device, stream)
+    else:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        _device_tensor(workspace, "workspace")
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def vq_paged_fork(lens: torch.Tensor, parents: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                  free_pages: torch.Tensor, free_count: torch.Tensor, keep_lens: torch.Tensor | None = None,
+                  lens_out: torch.Tensor | None = None, table_out: torch.Tensor | None = None,
+                  free_count_out: torch.Tensor | None = None, copies: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> tuple:
+    """Seat ``d`` goes on with the first ``keep_lens[d]`` tokens (None: all) of seat
+    ``parents[d]``; a parent outside ``[0, S)`` empties it.
+
+    ``lens`` / ``parents`` / ``keep_lens`` ``[S]``, ``block_table`` ``[S, max_blocks]``,
+    ``free_pages`` ``[num_pages]`` (pushed to and popped from in place) and ``free_count``
+    ``[1]`` are int32.  Whole pages are shared; a page that several seats end inside is left
+    to one of them and the others get pages of their own, whose contents :func:`vq_paged_copy`
+    brings over (see ``include/vq_encode.h``).  Returns ``(lens_out, table_out, free_count_out,
+    copies)``: ``lens_out`` may be ``lens`` and ``free_count_out`` ``free_count``; ``table_out``
+    must not overlap ``block_table``; ``copies`` ``[S, 2]`` holds (from, to) or -1, -1.  A
+    workspace of :func:`vq_paged_fork_workspace_bytes` bytes is allocated here (by torch) if
+    none is given; it and new outputs are allocated on ``stream``."""
+    n = _extent(lens)
+    _i32_tensor(lens, "lens", (n,), None)
+    dev, pages = lens.device, _extent(free_pages)
+    _i32_tensor(parents, "parents", (n,), dev)
+    blocks = _table_tensor(block_table, n, dev)
+    _i32_tensor(free_pages, "free_pages", (pages,), dev)
+    _i32_tensor(free_count, "free_count", (1,), dev)
+    if keep_lens is not None:
+        _i32_tensor(keep_lens, "keep_lens", (n,), dev)
+    lens_out = _out_like(lens_out, "lens_out", (n,), torch.int32, dev, stream)
+    table_out = _out_like(table_out, "table_out", (n, blocks), torch.int32, dev, stream)
+    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev, stream)
+    copies = _out_like(copies, "copies", (n, 2), torch.int32, dev, stream)
+    lib = load_library()
+    workspace, nbytes = _workspace_of(workspace, int(lib.vq_paged_fork_workspace_bytes(pages)), dev, stream)
+    _launch(lib.vq_paged_fork, "vq_paged_fork", dev, stream, lens.data_ptr(), parents.data_ptr(),
+            keep_lens.data_ptr() if keep_lens is not None else None, n, block_table.data_ptr(), blocks, page_size,
+            free_pages.data_ptr(), free_count.data_ptr(), pages, lens_out.data_ptr(), table_out.data_ptr(),
+            free_count_out.data_ptr(), copies.data_ptr(), workspace.data_ptr(), nbytes)
+    return lens_out, table_out, free_count_out, copies
+
+
+def vq_paged_compact(lens: torch.Tensor, block_table: torch.Tensor, page_size: int, free_pages: torch.Tensor,
+                     free_count: torch.Tensor, table_out: torch.Tensor | None = None,
+                     free_pages_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
+                     moves: torch.Tensor | None = None, page_map: torch.Tensor | None = None,
+                     stream: torch.cuda.Stream | None = None) -> tuple:
+    """Number the held pages ``0 .. used - 1``, those not on the free list.
+
+    Arguments as in :func:`vq_paged_fork`.  Returns ``(table_out, free_pages_out,
+    free_count_out, moves, page_map)``; the first three may be ``block_table``,
+    ``free_pages`` and ``free_count`` themselves.  ``moves`` ``[num_pages // 2, 2]`` names
+    the pages (from, to) whose contents :func:`vq_paged_copy` brings over, then -1, -1;
+    ``page_map`` ``[num_pages]`` is the new number of every page, -1 of a free one.  New
+    outputs are allocated on ``stream``."""
+    n = _extent(lens)
+    _i32_tensor(lens, "lens", (n,), None)
+    dev, pages = lens.device, _extent(free_pages)
+    blocks = _table_tensor(block_table, n, dev)
+    _i32_tensor(free_pages, "free_pages", (pages,), dev)
+    _i32_tensor(free_count, "free_count", (1,), dev)
+    table_out = _out_like(table_out, "table_out", (n, blocks), torch.int32, dev, stream)
+    free_pages_out = _out_like(free_pages_out, "free_pages_out", (pages,), torch.int32, dev, stream)
+    free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev, stream)
+    moves = _out_like(moves, "moves", (pages // 2, 2), torch.int32, dev, stream)
+    page_map = _out_like(page_map, "page_map", (pages,), torch.int32, dev, stream)
+    _launch(load_library().vq_paged_compact, "vq_paged_compact", dev, stream, lens.data_ptr(), n,
+            block_table.data_ptr(), blocks, page_size, free_pages.data_ptr(), free_count.data_ptr(), pages,
+            table_out.data_ptr(), free_pages_out.data_ptr(), free_count_out.data_ptr(), moves.data_ptr(),
+            page_map.data_ptr())
+    return table_out, free_pages_out, free_count_out, moves, page_map
+
+
+def vq_paged_copy(pairs: torch.Tensor, pools, layered: bool = False,
+                  stream: torch.cuda.Stream | None = None) -> None:
+    """Copy page ``pairs[i, 0]`` to page ``pairs[i, 1]`` in every pool.
+
+    ``pairs`` ``[N, 2]`` int32 on the device (pairs of -1 are skipped), as
+    :func:`vq_paged_fork` and :func:`vq_paged_compact` return them.  ``pools`` are up to 8
+    tensors ``[num_pages, ...]`` (``layered``: ``[layers, num_pages, ...]``) of any dtype, each
+    page contiguous; the pages may be strided.  Pages are written in place."""
+    rows = pairs.shape[0] if isinstance(pairs, torch.Tensor) and pairs.dim() == 2 else None
+    _i32_tensor(pairs, "pairs", (rows, 2), None)
+    if isinstance(pools, torch.Tensor) or not all(isinstance(t, torch.Tensor) for t in pools):
+        raise TypeError("pools must be a list of torch.Tensor")
+    if not 1 <= len(pools) <= PAGED_MAX_POOLS:
+        raise ValueError(f"expected 1 to {PAGED_MAX_POOLS} pools, got {len(pools)}")
+    at = 1 if layered else 0  # the axis of pages
+    array = (VqPagePool * len(pools))()
+    pages = None
+    for i, t in enumerate(pools):
+        name = f"pools[{i}]"
+        if t.dim() <= at:
+            raise ValueError(f"{name} must have shape [{'layers, ' if layered else ''}num_pages, ...]")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != pairs.device:
+            raise ValueError(f"{name} is on {t.device}, not on {pairs.device}")
+        if pages is None:
+            pages = t.shape[at]
+        elif t.shape[at] != pages:
+            raise ValueError("the pools must have one number of pages")
+        page = t[(0,) * (at + 1)] if t.numel() else None
+        if page is not None and not page.is_contiguous():
+            raise ValueError(f"each page of {name} must be contiguous")
+        size = t.element_size()
+        array[i] = VqPagePool(t.data_ptr(), t.stride(at) * size if pages > 1 else 0,
+                              page.numel() * size if page is not None else 0,
+                              t.stride(0) * size if layered and t.shape[0] > 1 else 0, t.shape[0] if layered else 1)
+    _launch(load_library().vq_paged_copy, "vq_paged_copy", pairs.device, stream, pairs.data_ptr(), rows,
+            ctypes.addressof(array), len(pools), pages)
 
 
 # Bytes of the library's built-in scratch array (VQ_ATTN_STATIC_SCRATCH_BYTES).

@@ -21,6 +21,10 @@ cudaError_t vqh_status_append(uint32_t *bits, bool clear);
 cudaError_t vqh_status_paged(uint32_t *bits, bool clear);
 cudaError_t vqh_status_pfew(uint32_t *bits, bool clear);
 cudaError_t vqh_status_pchunk(uint32_t *bits, bool clear);
+cudaError_t vqh_status_share(uint32_t *bits, bool clear);
+cudaError_t vqh_status_scache(uint32_t *bits, bool clear);
+cudaError_t vqh_status_sfew(uint32_t *bits, bool clear);
+cudaError_t vqh_status_schunk(uint32_t *bits, bool clear);
 
 // The body of the functions above, for the translation unit's own word.
 #define VQH_STATUS_READER(NAME)                                                      \

@@ -15,6 +15,7 @@
 #include "vq_encode.h"
 #include "vq_host.h"
 #include "vq_paged_host.h"
+#include "vq_paged_plan.h"
 #include "vq_pages.cuh"
 #include "vq_pattn.cuh"
 #include "vq_status.cuh"
@@ -23,88 +24,7 @@ VQH_STATUS_READER(vqh_status_paged)
 
 namespace {
 
-int page_shift(int32_t page_size)
-{
-    int s = 0;
-    while ((1 << s) < page_size) ++s;
-    return s;
-}
-
-vq_status check_page(int32_t page_size)
-{
-    if (page_size < 1 || (page_size & (page_size - 1))) return VQ_ERR_INVALID_ARG;
-    return page_size > VQ_PAGED_MAX_PAGE ? VQ_ERR_UNSUPPORTED : VQ_OK;
-}
-
-// A launch of one cluster of `blocks` blocks.
-cudaLaunchConfig_t cluster_launch(int blocks, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute *attr)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)blocks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = blocks > 1 ? 1 : 0;  // one block is a cluster by itself
-    return cfg;
-}
-
-vq_status check_pool(int64_t requests, int64_t max_blocks, int32_t page_size, int64_t num_pages)
-{
-    if (requests < 0 || max_blocks < 0 || num_pages < 0) return VQ_ERR_INVALID_ARG;
-    const vq_status s = check_page(page_size);
-    if (s != VQ_OK) return s;
-    if (requests > vqk::kPageMaxRequests || num_pages > INT32_MAX ||
-        max_blocks > VQ_PAGED_MAX_TOKENS / page_size)
-        return VQ_ERR_UNSUPPORTED;
-    return VQ_OK;
-}
-
-bool aligned4(const void *p) { return (uintptr_t)p % 4 == 0; }
-
-// ------------------------------------------------------------------ attention plans
-
-struct AttnCall {
-    vqk::PagedArgs a;
-    vq_dtype dtype;
-    int64_t max_new;
-    int sms;
-    cudaStream_t stream;
-};
-
-// One kernel's launch: its blocks, rows per item and share of the workspace.
-struct AttnPart {
-    int blocks = 0;
-    int32_t tile_tokens = 0, gc = 0, gch = 0, tile_rows = 0, item_cost = 0;
-    size_t notes = 0, ml = 0, part = 0, end = 0;  // workspace offsets
-};
-
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
-void lay_out(AttnPart *p, int32_t dim, size_t at)
-{
-    p->notes = at;
-    p->ml = up256(p->notes + (size_t)p->blocks * sizeof(vqk::PagedNote));
-    p->part = up256(p->ml + (size_t)2 * p->blocks * p->tile_rows * 2 * sizeof(float));
-    p->end = up256(p->part + (size_t)2 * p->blocks * p->tile_rows * dim * sizeof(float));
-}
-
-constexpr int kSimpleBlocksPerSm = 4;
-
-AttnPart simple_part(int sms, int32_t group, int32_t dim, size_t at)
-{
-    AttnPart p;
-    p.blocks = sms * kSimpleBlocksPerSm;
-    p.tile_tokens = 1;
-    p.gc = group < vqk::kSimpleRows ? group : vqk::kSimpleRows;
-    p.gch = (group + p.gc - 1) / p.gc;
-    p.tile_rows = p.gc;
-    lay_out(&p, dim, at);
-    return p;
-}
+using namespace vqp;
 
 // The tensor kernels take fp16 and bf16, head sizes 64, 128 and 256 in
 // sub-vectors of 4 or 8, and pages of 16 tokens or more (the tokens of one
@@ -121,17 +41,9 @@ bool tensor_layout(const vqk::PagedArgs &a)
     return (uintptr_t)a.k_codes % 16 == 0 && (uintptr_t)a.v_codes % 16 == 0 && a.page_stride % 16 == 0;
 }
 
-// Which tensor kernels a call launches: requests of up to `few_tokens` new
-// tokens go to the few-row kernel, the others to the chunk kernel.
-struct TensorPlan {
-    bool few, chunk;
-    int32_t few_tokens;
-};
-
-TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_t group, int32_t dim)
+// The tensor kernels of product-VQ codes.
+TensorKernels tensor_kernels(int32_t dim)
 {
-    TensorPlan p{};
-    const int64_t most = max_new > 0 && max_new < tokens ? max_new : tokens;  // new tokens of a request, as far as known
     // Up to three items of 8 rows, two at dim 256: the chunk kernel takes the time of a
     // tile of 128 rows however few there are, the few-row kernel that of its items.  16
     // requests of 8000 (2 of 30000), few-row against chunk kernel, us: dim 128 with two
@@ -139,73 +51,15 @@ TensorPlan tensor_plan(int64_t requests, int64_t tokens, int64_t max_new, int32_
     // three 74 : 84 (43 : 56), four 93 : 84 (51 : 56); dim 256 two 72 : 80 (43 : 51), three
     // 99 : 80 (54 : 54).  Other head groups and sub-vectors lie alike.
     const int32_t items = dim == 256 ? 2 : 3;
-    const int32_t item_tokens = group < vqh_few_rows() ? vqh_few_rows() / group : 1;
-    p.few_tokens = group > vqh_few_rows() ? 1 : items * item_tokens;
-    p.chunk = most > p.few_tokens;
-    p.few = requests != 1 || !p.chunk;
-    return p;
-}
-
-AttnPart few_part(int sms, int32_t group, int32_t dim, size_t at)
-{
-    AttnPart p;
-    p.blocks = sms * vqh_few_blocks_per_sm(dim);
-    p.gc = group < vqh_few_rows() ? group : vqh_few_rows();
-    p.gch = (group + p.gc - 1) / p.gc;
-    p.tile_tokens = vqh_few_rows() / p.gc;
-    p.tile_rows = vqh_few_rows();
-    // set-up, merge of the warps and write of an item, in units: 2 : 3 : 4 : 5 give drafts of
-    // 16 requests 60.7 : 57.3 : 56.0 : 55.4 us, 32 uneven decodes 148.8 : 147.7 : 146.9 : 146.5
-    p.item_cost = 4;
-    lay_out(&p, dim, at);
-    return p;
-}
-
-AttnPart chunk_part(int sms, int32_t group, int32_t dim, size_t at)
-{
-    AttnPart p;
-    p.blocks = sms;
-    p.gc = group < 128 ? group : 128;
-    p.gch = (group + p.gc - 1) / p.gc;
-    p.tile_tokens = vqh_chunk_tiles(dim) * (128 / p.gc);
-    p.tile_rows = vqh_chunk_tiles(dim) * 128;
-    lay_out(&p, dim, at);
-    return p;
-}
-
-// The parts of a call's tensor kernels, one behind the other.
-size_t tensor_parts(const TensorPlan &t, int sms, int32_t group, int32_t dim, AttnPart *few, AttnPart *chunk)
-{
-    size_t at = 0;
-    if (t.few) {
-        *few = few_part(sms, group, dim, at);
-        at = up256(few->end);
-    }
-    if (t.chunk) {
-        *chunk = chunk_part(sms, group, dim, at);
-        at = up256(chunk->end);
-    }
-    return at;
-}
-
-void use_part(vqk::PagedArgs *a, const AttnPart &p, unsigned char *ws)
-{
-    a->tile_tokens = p.tile_tokens;
-    a->gc = p.gc;
-    a->gch = p.gch;
-    a->tile_rows = p.tile_rows;
-    a->item_cost = p.item_cost;
-    a->items = a->tokens / p.tile_tokens + a->requests + 1;
-    a->notes = reinterpret_cast<vqk::PagedNote *>(ws + p.notes);
-    a->ml = reinterpret_cast<float *>(ws + p.ml);
-    a->part = reinterpret_cast<float *>(ws + p.part);
+    return TensorKernels{vqh_few_rows(), vqh_few_blocks_per_sm(dim), vqh_chunk_tiles(dim), items, vqh_paged_few,
+                         vqh_paged_chunk};
 }
 
 template <typename T>
-vq_status launch_merge(const vqk::PagedArgs &a, const AttnPart &p, cudaStream_t st)
+vq_status launch_merge(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.blocks, (unsigned)((p.tile_rows + vqk::kMergeRows - 1) / vqk::kMergeRows));
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)((a.tile_rows + vqk::kMergeRows - 1) / vqk::kMergeRows));
     cfg.blockDim = dim3(vqk::kMergeThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -219,7 +73,7 @@ vq_status launch_merge(const vqk::PagedArgs &a, const AttnPart &p, cudaStream_t 
                   : a.dim <= 256 ? vqk::paged_attn_merge<T, true, 2>
                                  : vqk::paged_attn_merge<T, true, 4>;
     if (cudaLaunchKernelEx(&cfg, kernel, (const float *)a.part, (const float *)a.ml,
-                           (const vqk::PagedNote *)a.notes, p.tile_rows, a.dim, a.hq, a.tokens,
+                           (const vqk::PagedNote *)a.notes, a.tile_rows, a.dim, a.hq, a.tokens,
                            static_cast<T *>(a.out), a.lse) != cudaSuccess)
         return vqh_failed();
     return vqh_launched(st, vqh_status_paged);
@@ -234,45 +88,7 @@ vq_status launch_simple(const AttnCall &c, const AttnPart &p, unsigned char *ws)
     const size_t smem = (size_t)vqk::kSimpleRows * a.dim * sizeof(float);
     vqk::paged_attn_simple<T><<<(unsigned)p.blocks, vqk::kUnit, smem, c.stream>>>(a);
     const vq_status s = vqh_launched(c.stream, vqh_status_paged);
-    return s != VQ_OK ? s : launch_merge<T>(a, p, c.stream);
-}
-
-// Units of cached tokens up to which an item is better left to one block.
-constexpr int64_t kWholeUnits = 8;
-
-template <typename T>
-vq_status launch_tensor(const AttnCall &c, unsigned char *ws)
-{
-    const TensorPlan t = tensor_plan(c.a.requests, c.a.tokens, c.max_new, c.a.group, c.a.dim);
-    AttnPart few, chunk;
-    (void)tensor_parts(t, c.sms, c.a.group, c.a.dim, &few, &chunk);
-    if (t.chunk) {
-        vqk::PagedArgs a = c.a;
-        use_part(&a, chunk, ws);
-        a.cls = t.few ? 2 : 0;
-        a.cls_tokens = t.few_tokens;
-        vq_status s = vqh_paged_chunk(a, c.dtype, chunk.blocks, c.stream);
-        if (s == VQ_OK) s = launch_merge<T>(a, chunk, c.stream);
-        if (s != VQ_OK) return s;
-    }
-    if (t.few) {
-        vqk::PagedArgs a = c.a;
-        use_part(&a, few, ws);
-        a.cls = t.chunk ? 1 : 0;
-        a.cls_tokens = t.few_tokens;
-        // Short caches and few of them: an item a block, none split, no merge to
-        // launch.  One token, 8 heads, whole against split, us on the device (a graph's
-        // replay) and as a call: one request of 300 12.3 : 14.4 (26.6 : 29.7), of 777 16.4 :
-        // 14.4 (25.9 : 28.8); eight of 300 13.5 : 18.4 (26.3 : 29.7), of 777 16.4 : 19.8
-        // (26.7 : 29.7).  The host knows no lengths: what counts is how long the table
-        // lets them be, and a wider table takes the split.
-        const int64_t cap = (int64_t)a.max_blocks << a.page_shift;
-        a.no_split = cap <= kWholeUnits * vqk::kUnit && a.items * a.hkv * a.gch <= few.blocks;
-        vq_status s = vqh_paged_few(a, c.dtype, few.blocks, c.stream);
-        if (s == VQ_OK && !a.no_split) s = launch_merge<T>(a, few, c.stream);
-        if (s != VQ_OK) return s;
-    }
-    return VQ_OK;
+    return s != VQ_OK ? s : launch_merge<T>(a, p.blocks, c.stream);
 }
 
 vq_status check_shape(int64_t requests, int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
@@ -288,6 +104,16 @@ vq_status check_shape(int64_t requests, int64_t tokens, int32_t heads_q, int32_t
 }
 
 }  // namespace
+
+vq_status vqh_paged_merge(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st)
+{
+    switch (dtype) {
+    case VQ_F16: return launch_merge<__half>(a, blocks, st);
+    case VQ_BF16: return launch_merge<__nv_bfloat16>(a, blocks, st);
+    case VQ_F32: return launch_merge<float>(a, blocks, st);
+    }
+    return VQ_ERR_INTERNAL;
+}
 
 extern "C" {
 
@@ -370,8 +196,9 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
     size_t need = simple_part(sms, group, head_dim, 0).end;
     if (tensor_shape(VQ_F16, head_dim, sub_dim, page_size)) {
         AttnPart few, chunk;
-        const TensorPlan plan = tensor_plan(requests, tokens, max_new, group, head_dim);
-        const size_t t = tensor_parts(plan, sms, group, head_dim, &few, &chunk);
+        const TensorKernels k = tensor_kernels(head_dim);
+        const TensorPlan plan = tensor_plan(k, requests, tokens, max_new, group);
+        const size_t t = tensor_parts(k, plan, sms, group, head_dim, &few, &chunk);
         if (t > need) need = t;
     }
     return need;
@@ -445,7 +272,7 @@ vq_status vq_paged_attention_slots(const void *q, int64_t q_stride, const int32_
         return VQ_ERR_INVALID_ARG;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     if (tensor_shape(dtype, head_dim, sub_dim, page_size) && tensor_layout(a))
-        return dtype == VQ_F16 ? launch_tensor<__half>(c, ws) : launch_tensor<__nv_bfloat16>(c, ws);
+        return launch_tensor(c, tensor_kernels(head_dim), ws);
     const AttnPart p = simple_part(c.sms, a.group, head_dim, 0);
     switch (dtype) {
     case VQ_F16: return launch_simple<__half>(c, p, ws);

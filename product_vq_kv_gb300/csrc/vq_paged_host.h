@@ -20,3 +20,12 @@ vq_status vqh_paged_few(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cud
 // an SM; dim 64, 128 or 256, sub 4 or 8, fp16 or bf16.
 int vqh_chunk_tiles(int32_t dim);
 vq_status vqh_paged_chunk(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);
+
+// The merge of the items that the `blocks` blocks of an attention launch have split
+// (vq_pattn.cuh), as its programmatic dependent.
+vq_status vqh_paged_merge(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);
+
+// The same kernels for a cache of 4-bit scalar codes (sub = 2: a byte selects a pair).
+int vqh_sfew_blocks_per_sm(int32_t dim);
+vq_status vqh_paged_sfew(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);
+vq_status vqh_paged_schunk(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);

@@ -425,6 +425,76 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
                                           int32_t sub_dim, int32_t n_centroids, int32_t page_size);
 
 /*
+ * The paged cache in 4 bits: each row (a token's key or value of one head) is held as
+ * one scale and head_dim scalar codes of 4 bits, its rule that of vq_scalar_quantize and
+ * vq_hadamard_quantize (TurboQuant's scalar quantizer).  Tables, free list, lengths and
+ * slots are those of the paged code cache; the pools are
+ *   k_codes, v_codes    page p at p * page_stride bytes (at least heads_kv * page_size *
+ *                       head_dim / 2), each [heads_kv][page_size][head_dim / 2] uint8:
+ *                       codes 2 i (low half) and 2 i + 1 of a row
+ *   k_scales, v_scales  page p at p * scale_stride elements (at least heads_kv *
+ *                       page_size), each [heads_kv][page_size] in the rows' dtype
+ *   k_centroids, v_centroids  [n_centroids] fp32, 1 to VQ_PAGED_SCALAR_MAX_CENTROIDS, for
+ *                       rows of root mean square one, finite
+ * A row stands for scale * centroids[code], the centroids rounded to the rows' dtype; a
+ * code >= n_centroids stands for 0.  head_dim is even.  At head size 128 in 16 bits a
+ * token takes 132 bytes a KV head, keys and values, where the rows take 512.
+ *
+ * vq_paged_scalar_append -- the rows of new tokens, into their slots.  For a row x:
+ *   y     = the rotation of vq_hadamard_rotate with diag = k_signs (keys only, if given:
+ *           head_dim then a power of two), or x, in fp32
+ *   S     = the sum of y^2 in fp32: neighbours are added, then neighbouring sums, and so
+ *           on, the row padded with zeros to a power of two
+ *   scale = sqrt(S / head_dim) rounded to dtype; 0 if that is not finite (a row with NaN
+ *           or infinities, or whose squares overflow fp32, is held as zeros)
+ *   code  = the rule of vq_scalar_quantize for y * (1 / scale), for 0 where scale is 0
+ * with one fp32 rounding a step, so that scales and codes have one right answer.
+ * Queries of rotated keys are rotated alike by the caller (vq_hadamard_rotate); a
+ * rotation of the values is left to the projections around them.
+ *   k, v     as in vq_paged_append
+ *   slots    [tokens] int64, device; a slot outside [0, num_pages * page_size) is skipped;
+ *            two tokens with one slot leave a mixture of their rows there
+ *   k_signs  [head_dim] fp32, device, or NULL
+ * Any alignment of k and v to their element type is taken.  Asynchronous on `stream`.
+ */
+#define VQ_PAGED_SCALAR_MAX_CENTROIDS 16
+vq_status vq_paged_scalar_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                                 const int64_t *slots, int64_t tokens, int32_t heads, int32_t head_dim,
+                                 int32_t n_centroids, const float *k_centroids, const float *v_centroids,
+                                 const float *k_signs, uint8_t *k_codes, uint8_t *v_codes, void *k_scales,
+                                 void *v_scales, int64_t num_pages, int32_t page_size, int64_t page_stride,
+                                 int64_t scale_stride, vq_dtype dtype, vq_stream_t stream);
+
+/*
+ * vq_paged_scalar_attention -- vq_paged_attention_slots over the cache in 4 bits: the
+ * same rows, masks, outputs and special values, with K^ and V^ as above.  Scales of
+ * cached tokens are finite; those of tokens past a request's length, or in no page, may
+ * be anything.  slots may be NULL.
+ * Arithmetic: as vq_paged_attention.  With 16-bit inputs, head_dim 64, 128 or 256,
+ * page_size >= 16 and pools whose addresses and strides are multiples of 16 bytes, the
+ * tensor kernels take the products: V^ is rounded to the input type, and for longer runs
+ * of new tokens K^ too; the weights are taken in two pieces for a few new tokens and
+ * rounded once for longer runs, as there.
+ * Asynchronous on `stream`.
+ */
+vq_status vq_paged_scalar_attention(const void *q, int64_t q_stride, const int32_t *cu_new,
+                                    const int32_t *lens, const int64_t *slots, int64_t requests,
+                                    int64_t tokens, int64_t max_new, const int32_t *block_table,
+                                    int64_t max_blocks, const uint8_t *k_codes, const uint8_t *v_codes,
+                                    const void *k_scales, const void *v_scales, int64_t num_pages,
+                                    int32_t page_size, int64_t page_stride, int64_t scale_stride,
+                                    const float *k_centroids, const float *v_centroids, int32_t heads_q,
+                                    int32_t heads_kv, int32_t head_dim, int32_t n_centroids, int64_t window,
+                                    float scale, vq_dtype dtype, void *out, float *lse, void *workspace,
+                                    size_t workspace_bytes, vq_stream_t stream);
+
+/* Workspace vq_paged_scalar_attention needs for these sizes on the current device (0 for
+ * invalid sizes).  It does not depend on the lengths in the cache. */
+size_t vq_paged_scalar_attention_workspace_bytes(int64_t requests, int64_t tokens, int64_t max_new,
+                                                 int32_t heads_q, int32_t heads_kv, int32_t head_dim,
+                                                 int32_t page_size);
+
+/*
  * Pages that several requests hold.  vq_paged_reserve and vq_paged_trim keep every
  * page with one request.  Beams, and the samples of one prompt, hold the pages of
  * their common tokens together: vq_paged_fork makes them, and takes the place of

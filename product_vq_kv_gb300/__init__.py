@@ -42,6 +42,9 @@ from ._binding import (  # noqa: F401
     vq_paged_fork,
     vq_paged_fork_workspace_bytes,
     vq_paged_reserve,
+    vq_paged_scalar_append,
+    vq_paged_scalar_attention,
+    vq_paged_scalar_attention_workspace_bytes,
     vq_paged_trim,
     vq_partition,
     vq_scalar_dequantize,

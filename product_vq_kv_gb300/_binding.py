@@ -103,6 +103,15 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.vq_paged_attention_slots.argtypes = lib.vq_paged_attention.argtypes[:4] + [vp] + lib.vq_paged_attention.argtypes[4:]
     lib.vq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.vq_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32]
+    lib.vq_paged_scalar_append.restype = i32
+    lib.vq_paged_scalar_append.argtypes = [vp, vp, i64, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp,
+                                           vp, vp, i64, i32, i64, i64, i32, vp]
+    lib.vq_paged_scalar_attention.restype = i32
+    lib.vq_paged_scalar_attention.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, vp, vp,
+                                              i64, i32, i64, i64, vp, vp, i32, i32, i32, i32, i64,
+                                              ctypes.c_float, i32, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.vq_paged_scalar_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.vq_paged_scalar_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32]
     lib.vq_paged_fork_workspace_bytes.restype = ctypes.c_size_t
     lib.vq_paged_fork_workspace_bytes.argtypes = [i64]
     lib.vq_paged_fork.restype = i32
@@ -831,6 +840,157 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
             stride, k_codebooks.data_ptr(), v_codebooks.data_ptr(), hq, hkv, d, sub, n_c, window, scale,
             _dtype_code(q), out.data_ptr(), lse.data_ptr() if lse is not None else None,
             workspace.data_ptr(), nbytes)
+    return (out, lse) if lse is not None else out
+
+
+def _scalar_page_tensors(k_codes, v_codes, k_scales, v_scales, k_centroids, v_centroids, dtype, device):
+    """Check the pages and centroids of the cache in 4 bits; returns (num_pages, heads,
+    page_size, dim, page stride in bytes, scale stride in elements, n_centroids)."""
+    named = (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales), ("v_scales", v_scales),
+             ("k_centroids", k_centroids), ("v_centroids", v_centroids))
+    for name, t in named:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if k_codes.dim() != 4 or k_scales.dim() != 3 or k_centroids.dim() != 1:
+        raise ValueError(f"expected codes [pages, heads, page_size, dim / 2], scales [pages, heads, page_size] and "
+                         f"centroids [n_centroids], got {tuple(k_codes.shape)}, {tuple(k_scales.shape)} and "
+                         f"{tuple(k_centroids.shape)}")
+    if k_codes.dtype is not torch.uint8 or v_codes.dtype is not torch.uint8:
+        raise TypeError("codes must be uint8")
+    if k_scales.dtype is not dtype or v_scales.dtype is not dtype:
+        raise TypeError(f"scales must be {dtype}, as the rows are")
+    if k_centroids.dtype is not torch.float32 or v_centroids.dtype is not torch.float32:
+        raise TypeError("centroids must be float32")
+    if v_codes.shape != k_codes.shape:
+        raise ValueError("k_codes and v_codes must have one shape")
+    if v_scales.shape != k_scales.shape or k_scales.shape != k_codes.shape[:3]:
+        raise ValueError("k_scales and v_scales must have the shape of the codes but for the last axis")
+    if v_centroids.shape != k_centroids.shape:
+        raise ValueError("k_centroids and v_centroids must have one shape")
+    pages, heads, page_size, ns = k_codes.shape
+    for name, t in named:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    strides = []
+    for (name, a), (_, b), inner in ((named[0], named[1], (page_size * ns, ns, 1)), (named[2], named[3], (page_size, 1))):
+        least = heads * inner[0]
+        for t in (a, b):
+            if t.numel() and t.stride()[1:] != inner and not t[0].is_contiguous():
+                raise ValueError(f"each page of {name[2:]} must be contiguous")
+        mine = [t.stride(0) if pages > 1 else least for t in (a, b)]
+        if mine[0] != mine[1] or mine[0] < least:
+            raise ValueError(f"the pages of k_{name[2:]} and v_{name[2:]} must not overlap and must have one stride")
+        strides.append(mine[0])
+    for name, t in named[4:]:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return pages, heads, page_size, 2 * ns, strides[0], strides[1], k_centroids.shape[0]
+
+
+def _slots_tensor(slots, tokens: int, device, exact: bool) -> None:
+    """A contiguous int64 device tensor of ``tokens`` slots (at least, unless ``exact``)."""
+    if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or slots.dim() != 1 or \
+            slots.shape[0] < tokens or exact and slots.shape[0] != tokens:
+        raise ValueError(f"slots must be an int64 tensor of {'shape' if exact else 'at least'} [T]")
+    _device_tensor(slots, "slots")
+    if slots.device != device:
+        raise ValueError(f"slots is on {slots.device}, not on {device}")
+
+
+def vq_paged_scalar_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_centroids: torch.Tensor,
+                           v_centroids: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
+                           k_scales: torch.Tensor, v_scales: torch.Tensor, k_signs: torch.Tensor | None = None,
+                           stream: torch.cuda.Stream | None = None) -> None:
+    """The keys and values of new tokens as 4-bit scalar codes and a scale a row, into
+    their slots of the pages.
+
+    ``k`` / ``v`` ``[T, H, D]`` (tokens may be strided, ``D`` even), ``slots`` ``[T]`` int64
+    (-1: skipped), ``k_centroids`` / ``v_centroids`` ``[n]`` float32 (up to 16, for rows of
+    root mean square one), ``k_codes`` / ``v_codes`` ``[num_pages, H, page_size, D/2]`` uint8
+    (the even element's code in the low half) and ``k_scales`` / ``v_scales`` ``[num_pages, H,
+    page_size]`` in k's dtype, written in place.  ``k_signs`` ``[D]`` float32 rotates the keys
+    first, as :func:`vq_hadamard_rotate` does; the queries are then to be rotated alike."""
+    _token_rows(k, "k", None)
+    dev = k.device
+    _token_rows(v, "v", dev)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must share shape and dtype")
+    pages, heads, page_size, dim, stride, scale_stride, n_c = _scalar_page_tensors(
+        k_codes, v_codes, k_scales, v_scales, k_centroids, v_centroids, k.dtype, dev)
+    tokens, h, d = k.shape
+    if h != heads or d != dim:
+        raise ValueError(f"k {tuple(k.shape)} does not match codes {tuple(k_codes.shape)}")
+    _slots_tensor(slots, tokens, dev, True)
+    if k_signs is not None:
+        if not isinstance(k_signs, torch.Tensor):
+            raise TypeError("k_signs must be a torch.Tensor")
+        if k_signs.dtype != torch.float32 or tuple(k_signs.shape) != (d,):
+            raise ValueError("k_signs must be float32 of shape [D]")
+        _device_tensor(k_signs, "k_signs")
+        if k_signs.device != dev:
+            raise ValueError(f"k_signs is on {k_signs.device}, not on {dev}")
+    _launch(load_library().vq_paged_scalar_append, "vq_paged_scalar_append", dev, stream, k.data_ptr(), v.data_ptr(),
+            _token_stride(k), _token_stride(v), slots.data_ptr(), tokens, heads, d, n_c, k_centroids.data_ptr(),
+            v_centroids.data_ptr(), k_signs.data_ptr() if k_signs is not None else None, k_codes.data_ptr(),
+            v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), pages, page_size, stride, scale_stride,
+            _dtype_code(k))
+
+
+def vq_paged_scalar_attention_workspace_bytes(requests: int, tokens: int, max_new: int, heads_q: int, heads_kv: int,
+                                              head_dim: int, page_size: int) -> int:
+    return int(load_library().vq_paged_scalar_attention_workspace_bytes(requests, tokens, max_new, heads_q, heads_kv,
+                                                                        head_dim, page_size))
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_scalar_workspace(device_index: int, *sizes) -> int:
+    """The workspace of a device for these sizes, as often as a step asks for it."""
+    with torch.cuda.device(device_index):
+        return max(vq_paged_scalar_attention_workspace_bytes(*sizes), 16)
+
+
+def vq_paged_scalar_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor, block_table: torch.Tensor,
+                              k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor,
+                              v_scales: torch.Tensor, k_centroids: torch.Tensor, v_centroids: torch.Tensor,
+                              max_new: int = 0, window: int = 0, scale: float = 0.0, out: torch.Tensor | None = None,
+                              lse: torch.Tensor | None = None, return_lse: bool = False,
+                              workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None,
+                              slots: torch.Tensor | None = None):
+    """Causal attention of the new tokens of every request over pages of 4-bit scalar codes.
+
+    :func:`vq_paged_attention` with pages and centroids as in :func:`vq_paged_scalar_append`,
+    the scales in q's dtype.  Returns ``out`` ``[T, Hq, D]``, or ``(out, lse)`` where
+    ``return_lse`` is set or ``lse`` is given.  A workspace of
+    :func:`vq_paged_scalar_attention_workspace_bytes` bytes is allocated here (by torch) if
+    none is given; it and new outputs are allocated on ``stream``."""
+    _token_rows(q, "q", None)
+    dev = q.device
+    tokens, hq, d = q.shape
+    pages, hkv, page_size, dim, stride, scale_stride, n_c = _scalar_page_tensors(
+        k_codes, v_codes, k_scales, v_scales, k_centroids, v_centroids, q.dtype, dev)
+    if dim != d or hkv < 1 or hq % hkv:
+        raise ValueError(f"q {tuple(q.shape)} does not match codes {tuple(k_codes.shape)}")
+    r = _extent(lens)
+    _i32_tensor(lens, "lens", (r,), dev)
+    _i32_tensor(cu_new, "cu_new", (r + 1,), dev)
+    blocks = _table_tensor(block_table, r, dev)
+    if max_new < 0:
+        raise ValueError("max_new must not be negative")
+    if slots is not None:
+        _slots_tensor(slots, tokens, dev, False)
+    out = _out_like(out, "out", (tokens, hq, d), q.dtype, dev, stream)
+    if return_lse or lse is not None:
+        lse = _out_like(lse, "lse", (tokens, hq), torch.float32, dev, stream)
+    need = _paged_scalar_workspace(dev.index, r, tokens, max_new, hq, hkv, d, page_size) if workspace is None else 0
+    workspace, nbytes = _workspace_of(workspace, need, dev, stream)
+    _launch(load_library().vq_paged_scalar_attention, "vq_paged_scalar_attention", dev, stream, q.data_ptr(),
+            _token_stride(q), cu_new.data_ptr(), lens.data_ptr(), slots.data_ptr() if slots is not None else None, r,
+            tokens, max_new, block_table.data_ptr(), blocks, k_codes.data_ptr(), v_codes.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), pages, page_size, stride, scale_stride, k_centroids.data_ptr(),
+            v_centroids.data_ptr(), hq, hkv, d, n_c, window, scale, _dtype_code(q), out.data_ptr(),
+            lse.data_ptr() if lse is not None else None, workspace.data_ptr(), nbytes)
     return (out, lse) if lse is not None else out
 
 

@@ -22,6 +22,7 @@ cudaError_t vqh_status_paged(uint32_t *bits, bool clear);
 cudaError_t vqh_status_pfew(uint32_t *bits, bool clear);
 cudaError_t vqh_status_pchunk(uint32_t *bits, bool clear);
 cudaError_t vqh_status_share(uint32_t *bits, bool clear);
+cudaError_t vqh_status_sappend(uint32_t *bits, bool clear);
 cudaError_t vqh_status_scache(uint32_t *bits, bool clear);
 cudaError_t vqh_status_sfew(uint32_t *bits, bool clear);
 cudaError_t vqh_status_schunk(uint32_t *bits, bool clear);

@@ -1,0 +1,182 @@
+// vq_sappend.cuh -- new tokens appended to the paged cache of 4-bit scalar codes: each
+// row of dim elements (a token's key or value of one head) is scaled to a root mean
+// square of one and every element takes the index of its nearest centroid.
+//
+//   y = R x (keys, where signs are given: the rotation of vq_hadamard_rotate) or x, fp32
+//   S = sum y^2: neighbours are added, then neighbouring sums, and so on (the row
+//       padded with zeros to a power of two)
+//   s = fl_T(sqrt(fl(S / dim))), T the rows' type; 0 if that is not finite
+//   z = fl(y fl(1 / s)), 0 where s = 0;  code = argmin_j fl(fl(z - c_j)^2), the lowest
+//       of equals (the rule of vq_scalar_quantize)
+// Every step is one rounded fp32 operation in this order, so a code has one right
+// answer.  Codes 2 i and 2 i + 1 share a byte, the even one in its low half.
+//
+// A lane holds kRowRun = 16 consecutive elements, two 16-byte loads of a 16-bit type, so
+// that of the rotation's and the sum's log2 dim steps four stay in registers; a warp takes
+// 32 / lanes rows side by side.  The cut points of the centroids (vq_nearest.cuh) decide a
+// code by four comparisons.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "vq_check.cuh"
+#include "vq_nearest.cuh"
+
+namespace vqk {
+
+constexpr int kRowRun = 16;
+constexpr int kSAppendThreads = 256;
+
+struct ScalarAppendArgs {
+    const void *x[2];          // keys, values
+    const float *centroids[2];
+    uint8_t *codes[2];
+    void *scales[2];
+    int64_t stride[2];         // elements between tokens
+    const float *signs;        // [dim] of the keys' rotation, or null
+    const int64_t *slots;
+    int64_t tokens, num_pages, page_stride, scale_stride;
+    int32_t heads, dim, nc, page_shift;
+    float norm;                // 1 / sqrt(dim)
+    bool vec[2];               // rows can be read in 16-byte pieces
+    bool vec_codes;            // codes can be written in 8-byte pieces
+};
+
+template <typename T>
+__device__ __forceinline__ T scale_of(float v);
+template <>
+__device__ __forceinline__ __half scale_of<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 scale_of<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ float scale_of<float>(float v) { return v; }
+
+// LANES lanes to a row (LANES x 16 >= dim); CUTS: 16 centroids, through their cut points.
+// blockIdx.y: keys or values.
+template <typename T, int LANES, bool CUTS>
+__global__ void __launch_bounds__(kSAppendThreads) scalar_append(const __grid_constant__ ScalarAppendArgs a)
+{
+    constexpr int kRows = 32 / LANES;  // of a warp
+    constexpr int kE = kRowRun;
+    __shared__ float sm[4 * 16];
+    const int kv = blockIdx.y;
+    const int lane = threadIdx.x & 31, sub = lane / LANES, l = lane % LANES;
+    vqs::CutCb<16> cut;
+    if constexpr (CUTS) {
+        vqs::build_cut_cb<16>(a.centroids[kv], sm, cut);
+    } else {
+        if ((int)threadIdx.x < a.nc) sm[16 + threadIdx.x] = __ldg(a.centroids[kv] + threadIdx.x);
+        __syncthreads();
+    }
+    const T *__restrict__ x = static_cast<const T *>(a.x[kv]);
+    const int64_t x_elems = (a.tokens - 1) * a.stride[kv] + (int64_t)a.heads * a.dim;
+    const bool rotate = kv == 0 && a.signs;
+    const int64_t rows = a.tokens * a.heads, stride = (int64_t)gridDim.x * (kSAppendThreads / 32) * kRows;
+    const int e0 = l * kE;
+    float sg[kE];
+#pragma unroll
+    for (int j = 0; j < kE; ++j)
+        sg[j] = rotate && e0 + j < a.dim && VQ_SPAN(a.signs + e0 + j, 1, a.signs, a.dim) ? __ldg(a.signs + e0 + j) : 0.f;
+    for (int64_t base = ((int64_t)blockIdx.x * (kSAppendThreads / 32) + (threadIdx.x >> 5)) * kRows; base < rows; base += stride) {
+        const int64_t row = base + sub;
+        const int64_t t = row / a.heads;
+        const int h = (int)(row - t * a.heads);
+        int64_t slot = -1;
+        if (row < rows && VQ_SPAN(a.slots + t, 1, a.slots, a.tokens)) slot = __ldg(a.slots + t);
+        const bool live = slot >= 0 && (slot >> a.page_shift) < a.num_pages;
+        const T *src = x + t * a.stride[kv] + (int64_t)h * a.dim + e0;
+        float v[kE];
+        if (live && a.vec[kv] && VQ_VSPAN(src, kE, x, x_elems, 16)) {  // (then LANES x 16 = dim)
+            vqs::load_run<T, kE>(src, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kE; ++j)
+                v[j] = live && e0 + j < a.dim && VQ_SPAN(src + j, 1, x, x_elems) ? vqs::widen_elem(src[j]) : 0.f;
+        }
+        if (rotate) {  // (dim is a power of two; the padding of a row below 16 stays zero)
+#pragma unroll
+            for (int j = 0; j < kE; ++j) v[j] = __fmul_rn(v[j], sg[j]);
+#pragma unroll
+            for (int s = 1; s < kE; s <<= 1) {
+                if (s >= a.dim) break;
+#pragma unroll
+                for (int j = 0; j < kE; ++j) {
+                    if ((j & s) == 0) {
+                        const float p = v[j], q = v[j + s];
+                        v[j] = __fadd_rn(p, q);
+                        v[j + s] = __fsub_rn(p, q);
+                    }
+                }
+            }
+#pragma unroll
+            for (int ls = 1; ls < LANES; ls <<= 1) {
+                // the upper of a pair is partner less own: fma(-1, own, partner), rounded once
+                const float f = (l & ls) != 0 ? -1.0f : 1.0f;
+#pragma unroll
+                for (int j = 0; j < kE; ++j) v[j] = __fmaf_rn(f, v[j], __shfl_xor_sync(0xffffffffu, v[j], ls));
+            }
+#pragma unroll
+            for (int j = 0; j < kE; ++j) v[j] = __fmul_rn(v[j], a.norm);
+        }
+        float q[kE];
+#pragma unroll
+        for (int j = 0; j < kE; ++j) q[j] = __fmul_rn(v[j], v[j]);
+#pragma unroll
+        for (int n = kE / 2; n > 0; n >>= 1)
+#pragma unroll
+            for (int j = 0; j < n; ++j) q[j] = __fadd_rn(q[2 * j], q[2 * j + 1]);
+        float total = q[0];
+#pragma unroll
+        for (int ls = 1; ls < LANES; ls <<= 1) total = __fadd_rn(total, __shfl_xor_sync(0xffffffffu, total, ls));
+        T scale = scale_of<T>(__fsqrt_rn(__fdiv_rn(total, (float)a.dim)));
+        float s = vqs::widen_elem(scale);
+        if (!(s <= 3.402823466e38f)) {  // NaN or infinite
+            s = 0.f;
+            scale = scale_of<T>(0.f);
+        }
+        const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+        uint32_t code[kE];
+        bool all = true;
+#pragma unroll
+        for (int j = 0; j < kE; ++j) {
+            const float z = s > 0.f ? __fmul_rn(v[j], inv) : 0.f;
+            v[j] = z;
+            if constexpr (CUTS) {
+                code[j] = vqs::cut_code<16>(z, cut);
+                all = all && vqs::cut_decides<16>(z, cut);
+            } else {
+                code[j] = vqs::nearest(z, sm + 16, a.nc);
+            }
+        }
+        if (CUTS && !all) {  // values that the cut points do not decide (rare): the rule's scan
+#pragma unroll
+            for (int j = 0; j < kE; ++j)
+                if (!vqs::cut_decides<16>(v[j], cut)) code[j] = vqs::nearest(v[j], sm + 16, 16);
+        }
+        if (!live) continue;
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < kE; ++j) w[j / 8] |= code[j] << (4 * (j % 8));
+        const int64_t page = slot >> a.page_shift, off = slot & (((int64_t)1 << a.page_shift) - 1);
+        const int64_t in_page = ((int64_t)h << a.page_shift) + off;
+        const int ns = a.dim / 2;
+        uint8_t *dst = a.codes[kv] + page * a.page_stride + in_page * ns + e0 / 2;
+        const int64_t bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.heads * ns) << a.page_shift);
+        if (a.vec_codes && e0 + kE <= a.dim) {
+            if (VQ_VSPAN(dst, 8, a.codes[kv], bytes, 8)) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kE / 2; ++i)
+                if (e0 / 2 + i < ns && VQ_SPAN(dst + i, 1, a.codes[kv], bytes)) dst[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+        }
+        if (l == 0) {
+            T *to = static_cast<T *>(a.scales[kv]) + page * a.scale_stride + in_page;
+            if (VQ_SPAN(to, 1, static_cast<T *>(a.scales[kv]), (a.num_pages - 1) * a.scale_stride + ((int64_t)a.heads << a.page_shift)))
+                *to = scale;
+        }
+    }
+}
+
+}  // namespace vqk

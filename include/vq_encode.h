@@ -446,7 +446,9 @@ size_t vq_paged_attention_workspace_bytes(int64_t requests, int64_t tokens, int6
  *   S     = the sum of y^2 in fp32: neighbours are added, then neighbouring sums, and so
  *           on, the row padded with zeros to a power of two
  *   scale = sqrt(S / head_dim) rounded to dtype; 0 if that is not finite (a row with NaN
- *           or infinities, or whose squares overflow fp32, is held as zeros)
+ *           or infinities, or whose squares overflow fp32, is held as zeros); at most the
+ *           largest value of dtype whose product with every centroid (rounded to dtype) is
+ *           not above dtype's largest (fp16 rows near 65504)
  *   code  = the rule of vq_scalar_quantize for y * (1 / scale), for 0 where scale is 0
  * with one fp32 rounding a step, so that scales and codes have one right answer.
  * Queries of rotated keys are rotated alike by the caller (vq_hadamard_rotate); a
@@ -468,13 +470,14 @@ vq_status vq_paged_scalar_append(const void *k, const void *v, int64_t k_stride,
 /*
  * vq_paged_scalar_attention -- vq_paged_attention_slots over the cache in 4 bits: the
  * same rows, masks, outputs and special values, with K^ and V^ as above.  Scales of
- * cached tokens are finite; those of tokens past a request's length, or in no page, may
- * be anything.  slots may be NULL.
+ * cached tokens are finite, their products with the centroids too (in dtype), as
+ * vq_paged_scalar_append leaves them; those of tokens past a request's length, or in no
+ * page, may be anything.  slots may be NULL.
  * Arithmetic: as vq_paged_attention.  With 16-bit inputs, head_dim 64, 128 or 256,
  * page_size >= 16 and pools whose addresses and strides are multiples of 16 bytes, the
- * tensor kernels take the products: V^ is rounded to the input type, and for longer runs
- * of new tokens K^ too; the weights are taken in two pieces for a few new tokens and
- * rounded once for longer runs, as there.
+ * tensor kernels take the products.  For a few new tokens the scales multiply scores and
+ * weights in fp32, and the weights enter in two pieces, as there; for longer runs K^, V^ and
+ * the weights are each rounded once to the input type.
  * Asynchronous on `stream`.
  */
 vq_status vq_paged_scalar_attention(const void *q, int64_t q_stride, const int32_t *cu_new,

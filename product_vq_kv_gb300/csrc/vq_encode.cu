@@ -685,7 +685,8 @@ vq_status vq_kernel_status(uint32_t *bits, int32_t clear)
         vqh_status_scalar(bits, c) != cudaSuccess || vqh_status_append(bits, c) != cudaSuccess ||
         vqh_status_paged(bits, c) != cudaSuccess || vqh_status_pfew(bits, c) != cudaSuccess ||
         vqh_status_pchunk(bits, c) != cudaSuccess || vqh_status_share(bits, c) != cudaSuccess ||
-        vqh_status_sappend(bits, c) != cudaSuccess || vqh_status_scache(bits, c) != cudaSuccess)
+        vqh_status_sappend(bits, c) != cudaSuccess || vqh_status_scache(bits, c) != cudaSuccess ||
+        vqh_status_sfew(bits, c) != cudaSuccess)
         return vqh_failed();
     return VQ_OK;
 }

@@ -208,6 +208,202 @@ __device__ __forceinline__ void image_line(unsigned char *image, int c, const ui
     }
 }
 
+// The scores of 16 tokens against this lane's two rows (kappa in, -inf where a row does not
+// see the token) to weights: the running maxima, sums and accumulators follow, and pf
+// holds P^T, in two pieces, as the second product's operand.
+template <typename T, int MMA>
+__device__ __forceinline__ void few_weights(const float (&st)[4], float (&m)[2], float (&sum)[2], float (&o)[MMA][4],
+                                            uint32_t (&pf)[2][2])
+{
+    constexpr float kShift = weight_shift<T>();
+    bool rise = false;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) rise |= st[c] > m[c & 1] + (kFewSlack + kShift);
+    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(st[c], st[c + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            // a row rises for its own scores alone, so that what it
+            // computes does not depend on the rows beside it
+            const bool up = top > m[c] + (kFewSlack + kShift);
+            const float ref = up ? top - kShift : m[c];
+            const float f = up ? exp2_fast(m[c] - ref) : 1.f;
+            m[c] = ref;
+            sum[c] *= f;
+#pragma unroll
+            for (int i = 0; i < MMA; ++i) {
+                o[i][c] *= f;
+                o[i][c + 2] *= f;
+            }
+        }
+    }
+    float p[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        p[c] = exp2_fast(st[c] - m[c & 1]);
+    }
+    sum[0] += p[0] + p[2];
+    sum[1] += p[1] + p[3];
+    // the weights in two pieces of the input type, what the first leaves in
+    // the second: together 22 bits of fp16, 16 of bf16
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t high = pack2<T>(p[2 * c], p[2 * c + 1]);
+        const float2 kept = unpack2<T>(high);
+        pf[0][c] = transpose8x8(high);
+        pf[1][c] = transpose8x8(pack2<T>(p[2 * c] - kept.x, p[2 * c + 1] - kept.y));
+    }
+}
+
+// The end of a segment: the warps' states meet, and the rows go to the output or, of a
+// split item, to the workspace.  first_of and page_of: of the warp's groups.
+template <typename T, int D, int WARPS, typename First, typename Page>
+__device__ __forceinline__ void few_finish(const PagedArgs &a, const PagedSegment &s, int rows, int gc, int head0,
+                                           const int32_t (&lim)[2], const int32_t (&low)[2], float (&m)[2], float (&sum)[2],
+                                           float (&o)[D / 16][4], float (&wm)[WARPS][kFewRows], float (&wl)[WARPS][kFewRows],
+                                           float *slots, bool out_vec, int g_begin, int g_end, First first_of, Page page_of)
+{
+    constexpr int kMma = D / 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const float kNone = __int_as_float(0xff800000);
+    T *__restrict__ out = static_cast<T *>(a.out);
+    // the warps' states: maxima and sums first
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
+        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
+        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
+    }
+    // A sum of 0: the warp has seen no token of the row, or scores of -inf alone.
+    // Its groups are looked through once more for a token that the row sees
+    // (here and not in the loop, which has no register to spare; most such rows
+    // overlap no group, and nothing is loaded).
+    if (__any_sync(0xffffffffu, sum[0] == 0.f || sum[1] == 0.f)) {
+        bool saw[2] = {false, false};
+        for (int group = g_begin; group < g_end; group += WARPS) {
+            const int32_t k0 = first_of(group);
+            bool at[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                at[c] = sum[c] == 0.f && k0 <= lim[c] && k0 + 15 > low[c] && low[c] < lim[c];
+            if (!__any_sync(0xffffffffu, at[0] || at[1])) continue;
+            const int32_t entry = page_of(group);
+            if (entry < 0 || entry >= a.num_pages) continue;
+            saw[0] |= at[0];
+            saw[1] |= at[1];
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (saw[c]) {
+                m[c] = kNone;
+                sum[c] = 1.f;
+            }
+    }
+    if (g == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            wm[warp][2 * t + c] = m[c];
+            wl[warp][2 * t + c] = sum[c];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int row = 2 * t + c;
+        float top = kNone;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k)
+            if (wl[k][row] != 0.f) top = fmaxf(top, wm[k][row]);
+        float total = 0.f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k)
+            if (wl[k][row] != 0.f) total = fmaf(exp2_fast(wm[k][row] - top), wl[k][row], total);
+        if (top == kNone && total != 0.f) total = 1.f;
+        const float f = sum[c] == 0.f || m[c] == kNone ? 0.f : exp2_fast(m[c] - top);
+        m[c] = top;
+        sum[c] = total;
+#pragma unroll
+        for (int i = 0; i < kMma; ++i) {
+            o[i][c] *= f;
+            o[i][c + 2] *= f;
+        }
+    }
+    // then the weighted sums: the upper half of the warps to the lower, until one is left
+#pragma unroll
+    for (int live = WARPS; live > 1; live = (live + 1) / 2) {
+        const int half = (live + 1) / 2;  // warps half .. live - 1 give to warps 0 ..
+        float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp < half ? warp : warp - half) * kMma * 32 + lane;
+        if (warp >= half && warp < live) {
+#pragma unroll
+            for (int i = 0; i < kMma; ++i)
+                if (dyn_smem_ok(slot + i * 32, 16, 16))
+                    slot[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        }
+        __syncthreads();
+        if (warp < live - half) {
+#pragma unroll
+            for (int i = 0; i < kMma; ++i)
+                if (dyn_smem_ok(slot + i * 32, 16, 16)) {
+                    const float4 v = slot[i * 32];
+                    o[i][0] += v.x;
+                    o[i][1] += v.y;
+                    o[i][2] += v.z;
+                    o[i][3] += v.w;
+                }
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+        // lane (g, t) holds columns [g dim/8, (g+1) dim/8) of rows 2 t + c
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int row = 2 * t + c;
+            if (row >= rows) continue;
+            if (s.whole) {
+                const int64_t orow = (s.it.tok0 + row / gc) * a.hq + head0 + row % gc;
+                const float inv = paged_inv(m[c], sum[c]);
+                T *dst = out + orow * D + g * (D / 8);
+                if (VQ_SPAN(dst, D / 8, out, a.tokens * a.hq * D)) {
+                    if (out_vec) {
+#pragma unroll
+                        for (int i = 0; i < kMma; i += 4) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                v[x] = pack2<T>(o[i + x][c] * inv, o[i + x][c + 2] * inv);
+                            reinterpret_cast<uint4 *>(dst)[i / 4] = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kMma; ++i) {
+                            dst[2 * i] = narrow<T>(o[i][c] * inv);
+                            dst[2 * i + 1] = narrow<T>(o[i][c + 2] * inv);
+                        }
+                    }
+                }
+                if (g == 0 && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq))
+                    a.lse[orow] = paged_lse(m[c], sum[c]);
+            } else {
+                const int64_t prow = s.slot * a.tile_rows + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
+                float *dst = a.part + prow * D + g * (D / 8);
+                if (VQ_VSPAN(dst, D / 8, a.part, prows * D, 16)) {
+#pragma unroll
+                    for (int i = 0; i < kMma; i += 2)
+                        reinterpret_cast<float4 *>(dst)[i / 2] =
+                            make_float4(o[i][c], o[i][c + 2], o[i + 1][c], o[i + 1][c + 2]);
+                }
+                if (g == 0 && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
+                    a.ml[prow * 2] = m[c];
+                    a.ml[prow * 2 + 1] = sum[c];
+                }
+            }
+        }
+    }
+}
+
 template <typename T, int D, int SUB>
 __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks)
     paged_attn_few(const __grid_constant__ PagedArgs a)
@@ -217,7 +413,6 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
     constexpr int KB = NS / 4, VB = NS / 8;        // code bytes a lane takes of a key, of a value
     constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
     constexpr int kMma = D / 16;                   // instructions per 16 tokens and 8 rows, each product
-    constexpr float kShift = weight_shift<T>();
     static_assert(SUB == 4 || SUB == 8, "sub-vectors of 4 or 8");
     extern __shared__ __align__(128) unsigned char few_mem[];
     __shared__ PagedWalk<> w;
@@ -231,7 +426,6 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
     const uint32_t copy = (uint32_t)(lane % (64 / SUB)) * (2 * SUB);
     const unsigned char *k_base = k_image + copy, *v_base = v_image + copy;
     const T *__restrict__ q = static_cast<const T *>(a.q);
-    T *__restrict__ out = static_cast<T *>(a.out);
     const bool q_vec = (uintptr_t)a.q % 8 == 0 && a.q_stride % 4 == 0;
     const bool out_vec = (uintptr_t)a.out % 16 == 0;
     const int64_t cb_elems = (int64_t)a.hkv * a.nc * SUB;
@@ -377,7 +571,6 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                     }
                     const int32_t k0 = first_of(group);
                     const bool whole = k0 + 15 <= all_hi && k0 > all_lo;
-                    bool rise = false;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         st[c] *= a.kappa;
@@ -385,46 +578,9 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                             const int32_t key = k0 + g + (c >> 1) * 8;
                             if (key > lim[c & 1] || key <= low[c & 1]) st[c] = kNone;
                         }
-                        rise |= st[c] > m[c & 1] + (kFewSlack + kShift);
                     }
-                    if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float top = fmaxf(st[c], st[c + 2]);
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                            // a row rises for its own scores alone, so that what it
-                            // computes does not depend on the rows beside it
-                            const bool up = top > m[c] + (kFewSlack + kShift);
-                            const float ref = up ? top - kShift : m[c];
-                            const float f = up ? exp2_fast(m[c] - ref) : 1.f;
-                            m[c] = ref;
-                            sum[c] *= f;
-#pragma unroll
-                            for (int i = 0; i < kMma; ++i) {
-                                o[i][c] *= f;
-                                o[i][c + 2] *= f;
-                            }
-                        }
-                    }
-                    float p[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        p[c] = exp2_fast(st[c] - m[c & 1]);
-                    }
-                    sum[0] += p[0] + p[2];
-                    sum[1] += p[1] + p[3];
-                    // the weights in two pieces of the input type, what the first leaves in
-                    // the second: together 22 bits of fp16, 16 of bf16
                     uint32_t pf[2][2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t high = pack2<T>(p[2 * c], p[2 * c + 1]);
-                        const float2 kept = unpack2<T>(high);
-                        pf[0][c] = transpose8x8(high);
-                        pf[1][c] = transpose8x8(pack2<T>(p[2 * c] - kept.x, p[2 * c + 1] - kept.y));
-                    }
+                    few_weights<T>(st, m, sum, o, pf);
                     // O^T += V^^T P^T
 #pragma unroll
                     for (int b = 0; b < VB; ++b) {
@@ -449,138 +605,8 @@ __global__ void __launch_bounds__(FewShape<D>::kWarps * 32, FewShape<D>::kBlocks
                 if (group + 2 * kFewWarps < g_end) step(std::integral_constant<int, 2>{}, group + 2 * kFewWarps);
             }
 
-            // the warps' states: maxima and sums first
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
-                sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
-                sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
-            }
-            // A sum of 0: the warp has seen no token of the row, or scores of -inf alone.
-            // Its groups are looked through once more for a token that the row sees
-            // (here and not in the loop, which has no register to spare; most such rows
-            // overlap no group, and nothing is loaded).
-            if (__any_sync(0xffffffffu, sum[0] == 0.f || sum[1] == 0.f)) {
-                bool saw[2] = {false, false};
-                for (int group = g_begin; group < g_end; group += kFewWarps) {
-                    const int32_t k0 = first_of(group);
-                    bool at[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        at[c] = sum[c] == 0.f && k0 <= lim[c] && k0 + 15 > low[c] && low[c] < lim[c];
-                    if (!__any_sync(0xffffffffu, at[0] || at[1])) continue;
-                    const int32_t entry = page_of(group);
-                    if (entry < 0 || entry >= a.num_pages) continue;
-                    saw[0] |= at[0];
-                    saw[1] |= at[1];
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (saw[c]) {
-                        m[c] = kNone;
-                        sum[c] = 1.f;
-                    }
-            }
-            if (g == 0) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    wm[warp][2 * t + c] = m[c];
-                    wl[warp][2 * t + c] = sum[c];
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int row = 2 * t + c;
-                float top = kNone;
-#pragma unroll
-                for (int k = 0; k < kFewWarps; ++k)
-                    if (wl[k][row] != 0.f) top = fmaxf(top, wm[k][row]);
-                float total = 0.f;
-#pragma unroll
-                for (int k = 0; k < kFewWarps; ++k)
-                    if (wl[k][row] != 0.f) total = fmaf(exp2_fast(wm[k][row] - top), wl[k][row], total);
-                if (top == kNone && total != 0.f) total = 1.f;
-                const float f = sum[c] == 0.f || m[c] == kNone ? 0.f : exp2_fast(m[c] - top);
-                m[c] = top;
-                sum[c] = total;
-#pragma unroll
-                for (int i = 0; i < kMma; ++i) {
-                    o[i][c] *= f;
-                    o[i][c + 2] *= f;
-                }
-            }
-            // then the weighted sums: the upper half of the warps to the lower, until one is left
-#pragma unroll
-            for (int live = kFewWarps; live > 1; live = (live + 1) / 2) {
-                const int half = (live + 1) / 2;  // warps half .. live - 1 give to warps 0 ..
-                float4 *slot = reinterpret_cast<float4 *>(slots) + (int64_t)(warp < half ? warp : warp - half) * kMma * 32 + lane;
-                if (warp >= half && warp < live) {
-#pragma unroll
-                    for (int i = 0; i < kMma; ++i)
-                        if (dyn_smem_ok(slot + i * 32, 16, 16))
-                            slot[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-                }
-                __syncthreads();
-                if (warp < live - half) {
-#pragma unroll
-                    for (int i = 0; i < kMma; ++i)
-                        if (dyn_smem_ok(slot + i * 32, 16, 16)) {
-                            const float4 v = slot[i * 32];
-                            o[i][0] += v.x;
-                            o[i][1] += v.y;
-                            o[i][2] += v.z;
-                            o[i][3] += v.w;
-                        }
-                }
-                __syncthreads();
-            }
-            if (warp == 0) {
-                // lane (g, t) holds columns [g dim/8, (g+1) dim/8) of rows 2 t + c
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int row = 2 * t + c;
-                    if (row >= rows) continue;
-                    if (s.whole) {
-                        const int64_t orow = (s.it.tok0 + row / gc) * a.hq + head0 + row % gc;
-                        const float inv = paged_inv(m[c], sum[c]);
-                        T *dst = out + orow * D + g * (D / 8);
-                        if (VQ_SPAN(dst, D / 8, out, a.tokens * a.hq * D)) {
-                            if (out_vec) {
-#pragma unroll
-                                for (int i = 0; i < kMma; i += 4) {
-                                    uint32_t v[4];
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x)
-                                        v[x] = pack2<T>(o[i + x][c] * inv, o[i + x][c + 2] * inv);
-                                    reinterpret_cast<uint4 *>(dst)[i / 4] = make_uint4(v[0], v[1], v[2], v[3]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < kMma; ++i) {
-                                    dst[2 * i] = narrow<T>(o[i][c] * inv);
-                                    dst[2 * i + 1] = narrow<T>(o[i][c + 2] * inv);
-                                }
-                            }
-                        }
-                        if (g == 0 && a.lse && VQ_SPAN(a.lse + orow, 1, a.lse, a.tokens * a.hq))
-                            a.lse[orow] = paged_lse(m[c], sum[c]);
-                    } else {
-                        const int64_t prow = s.slot * a.tile_rows + row, prows = 2 * (int64_t)gridDim.x * a.tile_rows;
-                        float *dst = a.part + prow * D + g * (D / 8);
-                        if (VQ_VSPAN(dst, D / 8, a.part, prows * D, 16)) {
-#pragma unroll
-                            for (int i = 0; i < kMma; i += 2)
-                                reinterpret_cast<float4 *>(dst)[i / 2] =
-                                    make_float4(o[i][c], o[i][c + 2], o[i + 1][c], o[i + 1][c + 2]);
-                        }
-                        if (g == 0 && VQ_SPAN(a.ml + prow * 2, 2, a.ml, prows * 2)) {
-                            a.ml[prow * 2] = m[c];
-                            a.ml[prow * 2 + 1] = sum[c];
-                        }
-                    }
-                }
-            }
+            few_finish<T, D, kFewWarps>(a, s, rows, gc, head0, lim, low, m, sum, o, wm, wl, slots, out_vec, g_begin, g_end,
+                                        first_of, page_of);
         }
     }
     if (tid == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;

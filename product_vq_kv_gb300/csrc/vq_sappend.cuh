@@ -5,7 +5,9 @@
 //   y = R x (keys, where signs are given: the rotation of vq_hadamard_rotate) or x, fp32
 //   S = sum y^2: neighbours are added, then neighbouring sums, and so on (the row
 //       padded with zeros to a power of two)
-//   s = fl_T(sqrt(fl(S / dim))), T the rows' type; 0 if that is not finite
+//   s = fl_T(sqrt(fl(S / dim))), T the rows' type; 0 if that is not finite; at most the
+//       largest T whose product with every centroid (rounded to T) is finite in T, so
+//       that whatever attends to the row may round s c_j to T
 //   z = fl(y fl(1 / s)), 0 where s = 0;  code = argmin_j fl(fl(z - c_j)^2), the lowest
 //       of equals (the rule of vq_scalar_quantize)
 // Every step is one rounded fp32 operation in this order, so a code has one right
@@ -20,6 +22,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "vq_check.cuh"
 #include "vq_nearest.cuh"
@@ -53,6 +57,21 @@ __device__ __forceinline__ __nv_bfloat16 scale_of<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ float scale_of<float>(float v) { return v; }
 
+// The largest scale: the largest T not above (largest T) / max |c_j|, a quotient of at most
+// the largest T.
+template <typename T>
+__device__ __forceinline__ T scale_cap(const float *__restrict__ centroids, int nc)
+{
+    constexpr float kMost = std::is_same<T, __half>::value ? 65504.f : std::is_same<T, float>::value ? 3.402823466e38f : 3.3895314e38f;
+    float most = 1.f;
+    for (int j = 0; j < nc; ++j)
+        if (VQ_SPAN(centroids + j, 1, centroids, nc)) most = fmaxf(most, fabsf(vqs::widen_elem(scale_of<T>(__ldg(centroids + j)))));
+    const float cap = __fdiv_rz(kMost, most);
+    if constexpr (std::is_same<T, __half>::value) return __float2half_rz(cap);
+    else if constexpr (std::is_same<T, float>::value) return cap;
+    else return __float2bfloat16_rz(cap);
+}
+
 // LANES lanes to a row (LANES x 16 >= dim); CUTS: 16 centroids, through their cut points.
 // blockIdx.y: keys or values.
 template <typename T, int LANES, bool CUTS>
@@ -70,6 +89,7 @@ __global__ void __launch_bounds__(kSAppendThreads) scalar_append(const __grid_co
         if ((int)threadIdx.x < a.nc) sm[16 + threadIdx.x] = __ldg(a.centroids[kv] + threadIdx.x);
         __syncthreads();
     }
+    const T cap = scale_cap<T>(a.centroids[kv], a.nc);
     const T *__restrict__ x = static_cast<const T *>(a.x[kv]);
     const int64_t x_elems = (a.tokens - 1) * a.stride[kv] + (int64_t)a.heads * a.dim;
     const bool rotate = kv == 0 && a.signs;
@@ -135,6 +155,9 @@ __global__ void __launch_bounds__(kSAppendThreads) scalar_append(const __grid_co
         if (!(s <= 3.402823466e38f)) {  // NaN or infinite
             s = 0.f;
             scale = scale_of<T>(0.f);
+        } else if (s > vqs::widen_elem(cap)) {
+            scale = cap;
+            s = vqs::widen_elem(cap);
         }
         const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
         uint32_t code[kE];

@@ -21,6 +21,28 @@ namespace {
 
 using namespace vqp;
 
+// The tensor kernels take fp16 and bf16, head sizes 64, 128 and 256, and pages of 16 tokens
+// or more (the tokens of one matrix instruction lie in one page).
+bool tensor_shape(vq_dtype dtype, int32_t dim, int32_t page_size)
+{
+    return (dtype == VQ_F16 || dtype == VQ_BF16) && (dim == 64 || dim == 128 || dim == 256) && page_size >= 16;
+}
+
+// and pages whose rows and scales can be read in 16-byte pieces.
+bool tensor_layout(const vqk::PagedArgs &a)
+{
+    for (const void *p : {(const void *)a.k_codes, (const void *)a.v_codes, a.k_scales, a.v_scales})
+        if ((uintptr_t)p % 16) return false;
+    return a.page_stride % 16 == 0 && a.scale_stride % 8 == 0;
+}
+
+TensorKernels tensor_kernels(int32_t dim)
+{
+    const int32_t items = 1 << 20;
+    return TensorKernels{vqh_few_rows(), vqh_sfew_blocks_per_sm(dim), vqh_chunk_tiles(dim), items, vqh_paged_sfew,
+                         vqh_paged_schunk};
+}
+
 template <typename T>
 vq_status launch_simple(const AttnCall &c, const AttnPart &p, unsigned char *ws)
 {
@@ -53,7 +75,15 @@ size_t vq_paged_scalar_attention_workspace_bytes(int64_t requests, int64_t token
 {
     if (max_new < 0 || check_shape(requests, tokens, heads_q, heads_kv, head_dim, page_size) != VQ_OK) return 0;
     const int sms = vqh_device_sms() > 0 ? vqh_device_sms() : 152;
-    return simple_part(sms, heads_q / heads_kv, head_dim, 0).end;
+    const int32_t group = heads_q / heads_kv;
+    size_t need = simple_part(sms, group, head_dim, 0).end;
+    if (tensor_shape(VQ_F16, head_dim, page_size)) {
+        AttnPart few, chunk;
+        const TensorKernels k = tensor_kernels(head_dim);
+        const size_t t = tensor_parts(k, tensor_plan(k, requests, tokens, max_new, group), sms, group, head_dim, &few, &chunk);
+        if (t > need) need = t;
+    }
+    return need;
 }
 
 vq_status vq_paged_scalar_attention(const void *q, int64_t q_stride, const int32_t *cu_new, const int32_t *lens,
@@ -129,6 +159,7 @@ vq_status vq_paged_scalar_attention(const void *q, int64_t q_stride, const int32
     a.kappa = (scale > 0.f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
 
     unsigned char *ws = static_cast<unsigned char *>(workspace);
+    if (tensor_shape(dtype, head_dim, page_size) && tensor_layout(a)) return launch_tensor(c, tensor_kernels(head_dim), ws);
     const AttnPart p = simple_part(c.sms, a.group, head_dim, 0);
     switch (dtype) {
     case VQ_F16: return launch_simple<__half>(c, p, ws);

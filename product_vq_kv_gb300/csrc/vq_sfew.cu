@@ -1,0 +1,48 @@
+// vq_sfew.cu -- launches of the paged attention of a few rows over 4-bit scalar codes
+// (vq_sfew.cuh).
+
+#include <cuda_runtime.h>
+
+#include "vq_host.h"
+#include "vq_paged_host.h"
+#include "vq_sfew.cuh"
+#include "vq_status.cuh"
+
+VQH_STATUS_READER(vqh_status_sfew)
+
+namespace {
+
+template <typename T, int D>
+vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
+{
+    auto kernel = vqk::paged_attn_sfew<T, D>;
+    using S = vqk::SFewShape<D>;
+    if (!vqh_allow_smem(kernel, S::kSmem)) return vqh_failed();
+    kernel<<<(unsigned)blocks, S::kWarps * 32, S::kSmem, st>>>(a);
+    return vqh_launched(st, vqh_status_sfew);
+}
+
+template <typename T>
+vq_status launch_dim(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
+{
+    switch (a.dim) {
+    case 64: return launch<T, 64>(a, blocks, st);
+    case 128: return launch<T, 128>(a, blocks, st);
+    case 256: return launch<T, 256>(a, blocks, st);
+    }
+    return VQ_ERR_INTERNAL;
+}
+
+}  // namespace
+
+int vqh_sfew_blocks_per_sm(int32_t dim)
+{
+    return dim == 64 ? vqk::SFewShape<64>::kBlocks : dim == 128 ? vqk::SFewShape<128>::kBlocks : vqk::SFewShape<256>::kBlocks;
+}
+
+vq_status vqh_paged_sfew(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st)
+{
+    return dtype == VQ_F16 ? launch_dim<__half>(a, blocks, st) : launch_dim<__nv_bfloat16>(a, blocks, st);
+}
+
+vq_status vqh_paged_schunk(const vqk::PagedArgs &, vq_dtype, int, cudaStream_t) { return VQ_ERR_UNSUPPORTED; }

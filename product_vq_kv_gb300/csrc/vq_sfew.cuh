@@ -1,0 +1,432 @@
+// vq_sfew.cuh -- paged attention of a few rows (decode, verification of drafts) over 4-bit
+// scalar codes: up to 8 rows (tokens x query heads of one KV head) against the whole
+// cache, 16-bit types, head sizes 64, 128 and 256.
+//
+// The frame is that of the few-row kernel of product-VQ codes (vq_pfew.cuh): S^T = K^ Q^T
+// and O^T = V^^T P^T by mma.m16n8k16 with the query rows as its 8 columns, a warp a group of
+// 16 tokens, rebuilt values in the registers of the instruction that uses them, weights in
+// two pieces.  What differs is the rebuild.
+//
+// What bounds it.  From HBM a cached token costs dim + 4 bytes a KV head, 132 at dim 128:
+// 5.8 cycles of an SM's share at 6.78 TB/s and 1.9 GHz.  Rebuilding its 2 dim values from
+// pairs of codes is 128 lookups, 4 warp instructions and 4 cycles of shared memory if each
+// lookup of a warp takes one; beside them stand the address of each lookup, 24 matrix
+// instructions per 16 tokens and the softmax, about 5 cycles of issue.  So all three are
+// close, and the kernel is laid out to issue little:
+//   * A table of 256 lines, one per byte, holds the pair (c[low half], c[high half]) as one
+//     32-bit word 32 times, a copy for each lane in its own bank: no lookup conflicts.  A line
+//     is 256 bytes, the keys' copies then the values', so that one byte permute of the code
+//     word and the lane's offset is the address: byte << 8 | 4 lane.
+//   * Keys: a byte's two codes are neighbouring columns of a key, one operand register.
+//     The scale multiplies the score, in fp32.
+//   * Values: an operand register takes one column of two tokens.  The nibbles of two
+//     tokens' words are exchanged (a shift and a select a word), so that a byte holds the two
+//     tokens' codes of one column.  The values' scales multiply the weights, in fp32 and
+//     before their rounding to two pieces, so that no rebuilt value is rounded.
+//   * Codes and scales come by cp.async into two slots a warp, 16-byte pieces exchanged so
+//     that the keys' and the values' reads meet no bank twice; a slot is filled again as
+//     soon as its codes are in registers, two groups ahead of their use.
+#pragma once
+
+#include "vq_pfew.cuh"
+#include "vq_sattn.cuh"
+#include "vq_umma.cuh"
+
+namespace vqk {
+
+template <int D>
+struct SFewShape {
+    static constexpr int kWarps = 8;
+    static constexpr int kBlocks = D > 128 ? 1 : 2;
+    static constexpr int kSlots = 2;              // of a warp
+    static constexpr int kCodes = 16 * (D / 2);   // code bytes of a group, keys or values
+    static constexpr int kSlot = 2 * kCodes + 64; // and their scales
+    static constexpr size_t kRing = (size_t)kWarps * kSlots * kSlot;
+    static constexpr size_t kMerge = (size_t)(kWarps / 2) * kFewRows * D * sizeof(float);  // over the ring
+    static constexpr size_t kSmem = 65536 + (kRing > kMerge ? kRing : kMerge);
+};
+
+// Where byte `at` of a group's codes lies in its slot: of each 128 bytes the 16-byte pieces
+// change places.  A warp reads keys row by row and values two rows apart, and with this
+// neither meets a bank twice in one pass.
+template <int D>
+__device__ __forceinline__ uint32_t sfew_place(uint32_t at)
+{
+    const uint32_t line = at >> 7, turn = D == 256 ? line & 7 : 2 * (line & 3);
+    return at ^ (turn << 4);
+}
+
+// A row's state beside its maximum m and its sum of p = 2^(score - m): what the weights
+// p s_v of the second product are multiplied by.  It starts at its most and falls when a
+// weight passes kSFewTop; a rise of m lifts it by as much, so that the accumulators stay as
+// they are.
+constexpr float kSFewMost = 1.2676506e30f;   // 2^100
+constexpr float kSFewSlack = 32.f;           // powers of two that a score may lie above m: p stays fp32
+constexpr float kSFewTop = 32768.f;          // the largest weight: 2^15, inside fp16
+
+// The scores of 16 tokens against this lane's two rows to weights, as few_weights does it,
+// but the product takes p s_v, the scale of the token's value (vs: of tokens g and g + 8)
+// folded in.  m follows the scores alone and the factor f the weights alone: a value's scale
+// does not touch the sum, and tokens whose values are large do not push others, of larger
+// weight, out of fp16.
+template <typename T, int MMA>
+__device__ __forceinline__ void sfew_weights(const float (&st)[4], const float (&vs)[2], float (&m)[2], float (&sum)[2],
+                                             float (&f)[2], float (&o)[MMA][4], uint32_t (&pf)[2][2])
+{
+    float p[4], w[4];
+    bool rise = false;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        p[c] = exp2_fast(st[c] - m[c & 1]);
+        w[c] = p[c] * vs[c >> 1] * f[c & 1];
+        rise |= st[c] > m[c & 1] + kSFewSlack || w[c] > kSFewTop;
+    }
+    if (__any_sync(0xffffffffu, rise)) {
+        // a row rises for its own scores and weights alone, so that what it computes does not
+        // depend on the rows beside it
+        auto over_lanes = [](float v) {
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        };
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float top = over_lanes(fmaxf(st[c], st[c + 2]));
+            float scale = 1.f;  // of the accumulators
+            if (top > m[c] + kSFewSlack) {
+                const float to = f[c] * exp2_fast(top - m[c]);
+                f[c] = fminf(to, kSFewMost);
+                scale = f[c] / to;  // (0 where `to` is infinite: what was is nothing beside it)
+                sum[c] *= exp2_fast(m[c] - top);
+                m[c] = top;
+            }
+#pragma unroll
+            for (int k = c; k < 4; k += 2) p[k] = exp2_fast(st[k] - m[c]);
+            const float most = over_lanes(fmaxf(p[c] * vs[0], p[c + 2] * vs[1]));
+            if (most * f[c] > kSFewTop) {
+                // the power of two that brings it to [2^6, 2^7): most >= 2^-85 here
+                const uint32_t e = __float_as_uint(most) >> 23;
+                const float to = __uint_as_float((uint32_t)(127 + 6 + 127 - (int)(e > 250u ? 250u : e)) << 23);
+                scale *= to / f[c];
+                f[c] = to;
+            }
+#pragma unroll
+            for (int k = c; k < 4; k += 2) w[k] = p[k] * vs[k >> 1] * f[c];
+#pragma unroll
+            for (int i = 0; i < MMA; ++i) {
+                o[i][c] *= scale;
+                o[i][c + 2] *= scale;
+            }
+        }
+    }
+    sum[0] += p[0] + p[2];
+    sum[1] += p[1] + p[3];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t high = pack2<T>(w[2 * c], w[2 * c + 1]);
+        const float2 kept = unpack2<T>(high);
+        pf[0][c] = transpose8x8(high);
+        pf[1][c] = transpose8x8(pack2<T>(w[2 * c] - kept.x, w[2 * c + 1] - kept.y));
+    }
+}
+
+__device__ __forceinline__ void copy_async16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+    __syncwarp();
+}
+
+// The table of both codebooks: line b of 256 bytes holds the keys' pair of byte b 32 times,
+// then the values'.  The caller synchronises.
+template <typename T, int THREADS>
+__device__ __forceinline__ void scalar_table(const PagedArgs &a, unsigned char *table)
+{
+    auto value = [&](const float *cent, int code) -> uint32_t {
+        float v = 0.f;
+        if (code < a.nc && VQ_SPAN(cent + code, 1, cent, a.nc)) v = __ldg(cent + code);
+        return pack2<T>(v, 0.f) & 0xffffu;
+    };
+    // 16 pieces of 16 bytes a line, a thread a piece of its own of every (THREADS / 16)-th
+    const int piece = threadIdx.x % 16;
+    const float *cent = piece < 8 ? a.k_cent : a.v_cent;
+#pragma unroll 4
+    for (int b = threadIdx.x / 16; b < 256; b += THREADS / 16) {
+        const uint32_t pair = value(cent, b & 15) | value(cent, b >> 4) << 16;
+        unsigned char *dst = table + b * 256 + piece * 16;
+        if (dyn_smem_ok(dst, 16, 16)) *reinterpret_cast<uint4 *>(dst) = make_uint4(pair, pair, pair, pair);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBlocks)
+    paged_attn_sfew(const __grid_constant__ PagedArgs a)
+{
+    using S = SFewShape<D>;
+    constexpr int kWarps = S::kWarps, kThreads = kWarps * 32;
+    constexpr int NS = D / 2;
+    constexpr int KB = NS / 4, VB = NS / 8;      // code bytes a lane takes of a key, of a value
+    constexpr int KW = KB / 4, VW = VB / 4;
+    constexpr int kMma = D / 16;                 // instructions per 16 tokens and 8 rows, each product
+    extern __shared__ __align__(128) unsigned char sfew_mem[];
+    __shared__ PagedWalk<> w;
+    __shared__ float wm[kWarps][kFewRows], wl[kWarps][kFewRows];
+    float *slots = reinterpret_cast<float *>(sfew_mem + 65536);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const float kNone = __int_as_float(0xff800000);
+    const uint32_t lane4 = lane * 4;
+    const T *__restrict__ q = static_cast<const T *>(a.q);
+    const unsigned char *ks = static_cast<const unsigned char *>(a.k_scales), *vs = static_cast<const unsigned char *>(a.v_scales);
+    const bool q_vec = (uintptr_t)a.q % 8 == 0 && a.q_stride % 4 == 0;
+    const bool out_vec = (uintptr_t)a.out % 16 == 0;
+    const int64_t q_elems = (a.tokens - 1) * a.q_stride + (int64_t)a.hq * D;
+    const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
+    const int64_t scale_bytes = 2 * ((a.num_pages - 1) * a.scale_stride + ((int64_t)a.hkv << a.page_shift));
+    unsigned char *ring = sfew_mem + 65536 + warp * (S::kSlots * S::kSlot);
+
+    // the merge's blocks may take the room that idle blocks leave (they wait there)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    PagedLens l;
+    PagedNote note{};
+    if (paged_plan<kThreads>(a, w, l)) {
+        PagedCursor cur;
+        cur.init(w, (int32_t)blockIdx.x);
+        PagedSegment s;
+        scalar_table<T, kThreads>(a, sfew_mem);
+        while (cur.next(a, w, l, s, note)) {
+            const int h = s.hx / a.gch, g0 = s.hx % a.gch * a.gc;
+            const int gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
+            const int rows = s.it.ntok * gc;
+            const int head0 = h * a.group + g0;
+
+            // query fragments: row g, columns t dim/4 + 4 i .. + 3
+            uint32_t qf[kMma][2];
+            const int row = g;
+            const T *src = q + (s.it.tok0 + row / gc) * a.q_stride + (int64_t)(head0 + row % gc) * D + t * (D / 4);
+            const bool ok = row < rows && VQ_SPAN(src, D / 4, q, q_elems);
+#pragma unroll
+            for (int i = 0; i < kMma; ++i) {
+                uint2 v = make_uint2(0, 0);
+                if (ok) {
+                    if (q_vec) {
+                        v = __ldg(reinterpret_cast<const uint2 *>(src + 4 * i));
+                    } else {
+                        const uint16_t *e = reinterpret_cast<const uint16_t *>(src + 4 * i);
+                        v.x = (uint32_t)__ldg(e) | ((uint32_t)__ldg(e + 1) << 16);
+                        v.y = (uint32_t)__ldg(e + 2) | ((uint32_t)__ldg(e + 3) << 16);
+                    }
+                }
+                qf[i][0] = v.x;
+                qf[i][1] = v.y;
+            }
+            // this lane's rows 2 t + c: the tokens in (low, lim] are seen
+            int32_t lim[2], low[2];
+            float m[2], sum[2], factor[2];
+            float o[kMma][4];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int row = 2 * t + c;
+                const int32_t p = s.it.pos0 + (row < rows ? row / gc : 0);
+                lim[c] = p < s.it.k_hi ? p : s.it.k_hi - 1;
+                // (a row whose limit k_hi cut keeps its own window)
+                const int64_t from = (int64_t)p - a.window;
+                low[c] = a.window == 0 || from < -1 ? -1 : (int32_t)from;
+                m[c] = kFewLow;
+                sum[c] = 0.f;
+                factor[c] = kSFewMost;
+            }
+#pragma unroll
+            for (int i = 0; i < kMma; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+            const int32_t all_hi = s.it.pos0 < s.it.k_hi ? s.it.pos0 : s.it.k_hi - 1;  // every row sees up to here
+            const int64_t last_pos = (int64_t)s.it.pos0 + s.it.ntok - 1;
+            const int64_t all_lo = a.window == 0 ? -1 : last_pos - a.window;       // and above here
+            const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.it.pos0 - a.window;  // no row sees at or below
+
+            // groups of 16 tokens, warp after warp
+            const int g_begin = s.begin * (kUnit / 16) + warp, g_end = s.end * (kUnit / 16);
+            auto first_of = [&](int group) { return s.it.k_lo + group * 16; };
+            auto page_of = [&](int group) -> int32_t {
+                if (group >= g_end) return -1;
+                const int32_t k0 = first_of(group);
+                if (k0 >= s.it.k_hi || k0 + 15 <= none_lo) return -1;
+                return paged_entry(a, cur.r, k0);  // checked when it is used: a check here would wait for the load
+            };
+            auto is_page = [&](int32_t pg) { return pg >= 0 && pg < a.num_pages; };
+            // one kind (0 keys, 1 values) of a group on its way into a slot
+            auto fetch = [&](int group, int32_t pg, int kind, unsigned char *slot) {
+                if (is_page(pg)) {  // warp-uniform
+                    const int64_t row = ((int64_t)h << a.page_shift) + (first_of(group) & ((1 << a.page_shift) - 1));
+                    const uint8_t *codes = (kind ? a.v_codes : a.k_codes) + (int64_t)pg * a.page_stride + row * NS;
+                    if (span_ok(codes, S::kCodes, kind ? a.v_codes : a.k_codes, code_bytes, 16)) {
+                        const uint32_t to = smem_addr(slot) + kind * S::kCodes;
+#pragma unroll
+                        for (int i = 0; i < S::kCodes / 512; ++i)
+                            copy_async16(to + sfew_place<D>(i * 512 + lane * 16), codes + i * 512 + lane * 16);
+                    }
+                    if (kind == 0 && lane < 4) {  // the scales, two pieces each
+                        const unsigned char *all = lane < 2 ? ks : vs;
+                        const unsigned char *from = all + 2 * ((int64_t)pg * a.scale_stride + row) + (lane & 1) * 16;
+                        if (span_ok(from, 16, all, scale_bytes, 16))
+                            copy_async16(smem_addr(slot) + 2 * S::kCodes + lane * 16, from);
+                    }
+                }
+                copy_commit();  // (an empty group keeps the count)
+            };
+            int32_t pg[S::kSlots + 1];
+#pragma unroll
+            for (int x = 0; x <= S::kSlots; ++x) pg[x] = page_of(g_begin + x * kWarps);
+            __syncthreads();  // the table is written, the last segment's merge has left the ring
+#pragma unroll
+            for (int x = 0; x < S::kSlots; ++x) {
+                fetch(g_begin + x * kWarps, pg[x], 0, ring + x * S::kSlot);
+                fetch(g_begin + x * kWarps, pg[x], 1, ring + x * S::kSlot);
+            }
+
+            auto table = [&](uint32_t word, int i, int kind) -> uint32_t {
+                const uint32_t off = __byte_perm(word, lane4, 0x5504 | (i << 4));
+                return *reinterpret_cast<const uint32_t *>(sfew_mem + off + kind * 128);
+            };
+            auto step = [&](unsigned char *slot, int group) {
+                const bool live = is_page(pg[0]);
+                const int32_t ahead = pg[S::kSlots];
+                copy_wait<2 * S::kSlots - 1>();  // this group's keys, and both its scales
+                uint32_t kc[2][KW];
+                float kscale[2], vscale[2];
+                if (live) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t at = (g + 8 * k) * NS + t * KB;
+                        if constexpr (KB == 8) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(slot + sfew_place<D>(at));
+                            kc[k][0] = v.x;
+                            kc[k][1] = v.y;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < KB / 16; ++i) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(slot + sfew_place<D>(at + 16 * i));
+                                kc[k][4 * i] = v.x;
+                                kc[k][4 * i + 1] = v.y;
+                                kc[k][4 * i + 2] = v.z;
+                                kc[k][4 * i + 3] = v.w;
+                            }
+                        }
+                        const unsigned char *scales = slot + 2 * S::kCodes + 2 * (g + 8 * k);
+                        kscale[k] = a.kappa * widen(*reinterpret_cast<const T *>(scales));
+                        vscale[k] = widen(*reinterpret_cast<const T *>(scales + 32));
+                    }
+                }
+                __syncwarp();
+                fetch(group + S::kSlots * kWarps, ahead, 0, slot);
+                const int32_t k0 = first_of(group);
+                const bool whole = k0 + 15 <= all_hi && k0 > all_lo;
+                uint32_t pf[2][2];
+                if (live) {  // warp-uniform
+                    // S^T = K^ Q^T, in two chains
+                    float st[4], st2[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) st[c] = st2[c] = 0.f;
+#pragma unroll
+                    for (int b = 0; b < KB; b += 2) {
+                        const uint32_t a0 = table(kc[0][b / 4], b % 4, 0), a1 = table(kc[1][b / 4], b % 4, 0);
+                        const uint32_t a2 = table(kc[0][b / 4], b % 4 + 1, 0), a3 = table(kc[1][b / 4], b % 4 + 1, 0);
+                        mma16816<T>(b % 4 == 0 ? st : st2, a0, a1, a2, a3, qf[b / 2][0], qf[b / 2][1]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        st[c] = (st[c] + st2[c]) * kscale[c >> 1];
+                        if (!whole) {
+                            const int32_t key = k0 + g + (c >> 1) * 8;
+                            if (key > lim[c & 1] || key <= low[c & 1]) st[c] = kNone;
+                        }
+                    }
+                    if (!whole) {
+                        // tokens that no row sees weigh nothing, whatever their scales hold
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int32_t key = k0 + g + 8 * k;
+                            if (key >= s.it.k_hi || key > last_pos || key <= none_lo) vscale[k] = 0.f;
+                        }
+                    }
+                    sfew_weights<T>(st, vscale, m, sum, factor, o, pf);
+                }
+                copy_wait<2 * S::kSlots - 1>();  // its values
+                uint32_t vc[4][VW];
+                if (live) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const unsigned char *from = slot + S::kCodes + sfew_place<D>((2 * t + (k & 1) + 8 * (k >> 1)) * NS + g * VB);
+                        if constexpr (VB == 4) {
+                            vc[k][0] = *reinterpret_cast<const uint32_t *>(from);
+                        } else if constexpr (VB == 8) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(from);
+                            vc[k][0] = v.x;
+                            vc[k][1] = v.y;
+                        } else {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(from);
+                            vc[k][0] = v.x;
+                            vc[k][1] = v.y;
+                            vc[k][2] = v.z;
+                            vc[k][3] = v.w;
+                        }
+                    }
+                }
+                __syncwarp();
+                fetch(group + S::kSlots * kWarps, ahead, 1, slot);
+#pragma unroll
+                for (int x = 0; x < S::kSlots; ++x) pg[x] = pg[x + 1];
+                pg[S::kSlots] = page_of(group + (S::kSlots + 1) * kWarps);
+                if (live) {
+                    // O^T += V^^T P^T
+#pragma unroll
+                    for (int x = 0; x < VW; ++x) {
+                        constexpr uint32_t kLow = 0x0f0f0f0fu;
+                        uint32_t even[2], odd[2];  // of columns 2 i and 2 i + 1, two tokens a byte
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t v0 = vc[2 * k][x], v1 = vc[2 * k + 1][x];
+                            even[k] = (v0 & kLow) | (v1 << 4 & ~kLow);
+                            odd[k] = (v0 >> 4 & kLow) | (v1 & ~kLow);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = table(even[0], i, 1), a1 = table(odd[0], i, 1);
+                            const uint32_t a2 = table(even[1], i, 1), a3 = table(odd[1], i, 1);
+                            mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[0][0], pf[0][1]);
+                            mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[1][0], pf[1][1]);
+                        }
+                    }
+                }
+            };
+            static_assert(S::kSlots == 2, "two slots in turn");
+            for (int group = g_begin; group < g_end; group += 2 * kWarps) {
+                step(ring, group);
+                if (group + kWarps < g_end) step(ring + S::kSlot, group + kWarps);
+            }
+            copy_wait<0>();
+            // to weights without the factors
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float inv = 1.f / factor[c];
+#pragma unroll
+                for (int i = 0; i < kMma; ++i) {
+                    o[i][c] *= inv;
+                    o[i][c + 2] *= inv;
+                }
+            }
+            few_finish<T, D, kWarps>(a, s, rows, gc, head0, lim, low, m, sum, o, wm, wl, slots, out_vec, g_begin, g_end,
+                                     first_of, page_of);
+        }
+    }
+    if (tid == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;
+}
+
+}  // namespace vqk

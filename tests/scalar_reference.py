@@ -33,6 +33,14 @@ def encode_rows(x, centroids, signs=None):
         assert total.dtype == np.float32
         scale = torch.from_numpy(np.sqrt(total / np.float32(dim))).to(dtype)
         scale = torch.where(torch.isfinite(scale.float()), scale, torch.zeros((), dtype=dtype))
+        # the largest value of the type whose product with every centroid is not above its largest
+        top = torch.finfo(dtype).max
+        most = max(1.0, *(abs(float(c)) for c in torch.tensor(list(centroids), dtype=torch.float32).to(dtype)))
+        cap = torch.tensor(top / most, dtype=torch.float64).to(dtype)
+        while float(cap) * most > top:
+            bits = torch.int32 if dtype == torch.float32 else torch.int16
+            cap = (cap.view(bits) - 1).view(dtype)  # the next below
+        scale = torch.minimum(scale, cap)
         s = scale.float().numpy()[..., None]
         z = np.where(s > 0, y * (np.float32(1) / s), np.float32(0))
         best = np.full(z.shape, np.inf, np.float32)

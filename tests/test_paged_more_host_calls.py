@@ -64,4 +64,4 @@ def test_a_kernel_has_one_limit_of_shared_memory(lib):  # noqa: F811
         for dtype in (0, 1, 2):
             for n in (1, 200):
                 assert attend(lib, 2, 2 * n, n, dtype, dim) == append(lib, dim, 16, dtype) == OK
-    assert lib.fake_most_limits() == 1
+    assert lib.fake_most_limits() <= 1

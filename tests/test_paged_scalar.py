@@ -183,8 +183,8 @@ def test_append_matches_the_hadamard_quantizer(vq):
 
 def cache(rng, pages, hkv, page, dim, dtype, spread=0.5):
     codes = [rng.integers(0, 256, (pages, hkv, page, dim // 2)).astype(np.uint8) for _ in range(2)]
-    # (finite in every type, as the scales of cached tokens are)
-    scales = [torch.from_numpy(np.minimum(np.exp(spread * rng.standard_normal((pages, hkv, page))), 60000.0)).to(dtype)
+    # (products with the centroids finite in every type, as the append leaves them)
+    scales = [torch.from_numpy(np.minimum(np.exp(spread * rng.standard_normal((pages, hkv, page))), 15000.0)).to(dtype)
               for _ in range(2)]
     return codes, scales
 

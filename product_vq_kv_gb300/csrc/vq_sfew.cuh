@@ -15,8 +15,9 @@
 // close, and the kernel is laid out to issue little:
 //   * A table of 256 lines, one per byte, holds the pair (c[low half], c[high half]) as one
 //     32-bit word 32 times, a copy for each lane in its own bank: no lookup conflicts.  A line
-//     is 256 bytes, the keys' copies then the values', so that one byte permute of the code
-//     word and the lane's offset is the address: byte << 8 | 4 lane.
+//     is 256 bytes, the keys' copies then the values', and the table lies at address 2^16 of
+//     shared memory, so that one byte permute of the code word and a lane's constant is the
+//     whole address: 2^16 | byte << 8 | 4 lane.
 //   * Keys: a byte's two codes are neighbouring columns of a key, one operand register.
 //     The scale multiplies the score, in fp32.
 //   * Values: an operand register takes one column of two tokens.  The nibbles of two
@@ -36,14 +37,17 @@ namespace vqk {
 
 template <int D>
 struct SFewShape {
-    static constexpr int kWarps = 8;
-    static constexpr int kBlocks = D > 128 ? 1 : 2;
+    static constexpr int kWarps = D == 64 ? 16 : D == 128 ? 12 : 8;
+    static constexpr int kBlocks = 1;
     static constexpr int kSlots = 2;              // of a warp
     static constexpr int kCodes = 16 * (D / 2);   // code bytes of a group, keys or values
     static constexpr int kSlot = 2 * kCodes + 64; // and their scales
     static constexpr size_t kRing = (size_t)kWarps * kSlots * kSlot;
-    static constexpr size_t kMerge = (size_t)(kWarps / 2) * kFewRows * D * sizeof(float);  // over the ring
-    static constexpr size_t kSmem = 65536 + (kRing > kMerge ? kRing : kMerge);
+    static constexpr size_t kMerge = (size_t)((kWarps + 1) / 2) * kFewRows * D * sizeof(float);  // over the ring
+    // Addresses in shared memory: the table from kTable, the ring from kTable + 65536.  What
+    // lies below is static, or not used: one block an SM has the room.
+    static constexpr uint32_t kTable = 65536;
+    static constexpr size_t kSmem = kTable + 65536 + (kRing > kMerge ? kRing : kMerge);
 };
 
 // Where byte `at` of a group's codes lies in its slot: of each 128 bytes the 16-byte pieces
@@ -142,6 +146,34 @@ __device__ __forceinline__ void copy_wait()
     __syncwarp();
 }
 
+// W words of codes at address `at` (two 16-byte pieces: the second at `base` + `next`).  Not
+// moved across the waits and fetches around them, which are volatile too.
+template <int W>
+__device__ __forceinline__ void load_shared(uint32_t at, uint32_t next, uint32_t base, uint32_t (&v)[W])
+{
+    if constexpr (W == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(at) : "memory");
+    if constexpr (W == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+    if constexpr (W >= 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(at)
+                     : "memory");
+    if constexpr (W == 8)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "r"(base + next)
+                     : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ float load_shared16(uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(v));
+    else return __uint_as_float((uint32_t)v << 16);
+}
+
 // The table of both codebooks: line b of 256 bytes holds the keys' pair of byte b 32 times,
 // then the values'.  The caller synchronises.
 template <typename T, int THREADS>
@@ -176,12 +208,14 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
     extern __shared__ __align__(128) unsigned char sfew_mem[];
     __shared__ PagedWalk<> w;
     __shared__ float wm[kWarps][kFewRows], wl[kWarps][kFewRows];
-    float *slots = reinterpret_cast<float *>(sfew_mem + 65536);
+    // (the array begins behind the static memory, at most at kTable)
+    unsigned char *lines = sfew_mem + (S::kTable - smem_addr(sfew_mem));
+    float *slots = reinterpret_cast<float *>(lines + 65536);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const float kNone = __int_as_float(0xff800000);
-    const uint32_t lane4 = lane * 4;
+    const uint32_t copy = S::kTable | lane * 4;  // this lane's copies in the table's line 0
     const T *__restrict__ q = static_cast<const T *>(a.q);
     const unsigned char *ks = static_cast<const unsigned char *>(a.k_scales), *vs = static_cast<const unsigned char *>(a.v_scales);
     const bool q_vec = (uintptr_t)a.q % 8 == 0 && a.q_stride % 4 == 0;
@@ -189,7 +223,14 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
     const int64_t q_elems = (a.tokens - 1) * a.q_stride + (int64_t)a.hq * D;
     const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
     const int64_t scale_bytes = 2 * ((a.num_pages - 1) * a.scale_stride + ((int64_t)a.hkv << a.page_shift));
-    unsigned char *ring = sfew_mem + 65536 + warp * (S::kSlots * S::kSlot);
+    const uint32_t ring = S::kTable + 65536 + warp * (S::kSlots * S::kSlot);
+    // where this lane puts and finds codes in a slot
+    const uint32_t put_at = sfew_place<D>(lane * 16);
+    uint32_t k_at[2], v_at[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) k_at[k] = sfew_place<D>((g + 8 * k) * NS + t * KB);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v_at[k] = S::kCodes + sfew_place<D>((2 * t + (k & 1) + 8 * (k >> 1)) * NS + g * VB);
 
     // the merge's blocks may take the room that idle blocks leave (they wait there)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -199,7 +240,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
         PagedCursor cur;
         cur.init(w, (int32_t)blockIdx.x);
         PagedSegment s;
-        scalar_table<T, kThreads>(a, sfew_mem);
+        scalar_table<T, kThreads>(a, lines);
         while (cur.next(a, w, l, s, note)) {
             const int h = s.hx / a.gch, g0 = s.hx % a.gch * a.gc;
             const int gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
@@ -261,22 +302,23 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
                 return paged_entry(a, cur.r, k0);  // checked when it is used: a check here would wait for the load
             };
             auto is_page = [&](int32_t pg) { return pg >= 0 && pg < a.num_pages; };
-            // one kind (0 keys, 1 values) of a group on its way into a slot
-            auto fetch = [&](int group, int32_t pg, int kind, unsigned char *slot) {
+            // this head's rows of page 0; lanes 0, 1 fetch the keys' scales, 2, 3 the values'
+            const int64_t head = (int64_t)h << a.page_shift;
+            const uint8_t *k_head = a.k_codes + head * NS + lane * 16, *v_head = a.v_codes + head * NS + lane * 16;
+            const unsigned char *s_head = (lane < 2 ? ks : vs) + 2 * head + (lane & 1) * 16;
+            // a group on its way into a slot: the keys and both scales, or the values
+            auto fetch = [&](int group, int32_t pg, int kind, uint32_t slot) {
                 if (is_page(pg)) {  // warp-uniform
-                    const int64_t row = ((int64_t)h << a.page_shift) + (first_of(group) & ((1 << a.page_shift) - 1));
-                    const uint8_t *codes = (kind ? a.v_codes : a.k_codes) + (int64_t)pg * a.page_stride + row * NS;
-                    if (span_ok(codes, S::kCodes, kind ? a.v_codes : a.k_codes, code_bytes, 16)) {
-                        const uint32_t to = smem_addr(slot) + kind * S::kCodes;
+                    const int32_t row = first_of(group) & ((1 << a.page_shift) - 1);
+                    const int64_t at = (int64_t)pg * a.page_stride + row * NS;
+                    const uint8_t *codes = (kind ? v_head : k_head) + at;
 #pragma unroll
-                        for (int i = 0; i < S::kCodes / 512; ++i)
-                            copy_async16(to + sfew_place<D>(i * 512 + lane * 16), codes + i * 512 + lane * 16);
-                    }
-                    if (kind == 0 && lane < 4) {  // the scales, two pieces each
-                        const unsigned char *all = lane < 2 ? ks : vs;
-                        const unsigned char *from = all + 2 * ((int64_t)pg * a.scale_stride + row) + (lane & 1) * 16;
-                        if (span_ok(from, 16, all, scale_bytes, 16))
-                            copy_async16(smem_addr(slot) + 2 * S::kCodes + lane * 16, from);
+                    for (int i = 0; i < S::kCodes / 512; ++i)
+                        if (span_ok(codes + i * 512, 16, kind ? a.v_codes : a.k_codes, code_bytes, 16))
+                            copy_async16(slot + kind * S::kCodes + i * 512 + (D == 256 && i % 2 ? put_at ^ 64 : put_at), codes + i * 512);
+                    if (kind == 0 && lane < 4) {
+                        const unsigned char *from = s_head + 2 * ((int64_t)pg * a.scale_stride + row);
+                        if (span_ok(from, 16, lane < 2 ? ks : vs, scale_bytes, 16)) copy_async16(slot + 2 * S::kCodes + lane * 16, from);
                     }
                 }
                 copy_commit();  // (an empty group keeps the count)
@@ -291,118 +333,87 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
                 fetch(g_begin + x * kWarps, pg[x], 1, ring + x * S::kSlot);
             }
 
+            // (in the order of its operands alone: a volatile load would stand in the order of
+            // the matrix instructions)
             auto table = [&](uint32_t word, int i, int kind) -> uint32_t {
-                const uint32_t off = __byte_perm(word, lane4, 0x5504 | (i << 4));
-                return *reinterpret_cast<const uint32_t *>(sfew_mem + off + kind * 128);
+                uint32_t v;
+                const uint32_t at = __byte_perm(word, copy, 0x7604 | (i << 4));
+                if (kind) asm("ld.shared.b32 %0, [%1 + 128];" : "=r"(v) : "r"(at));
+                else asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+                return v;
             };
-            auto step = [&](unsigned char *slot, int group) {
-                const bool live = is_page(pg[0]);
+            auto step = [&](uint32_t slot, int group) {
                 const int32_t ahead = pg[S::kSlots];
+                const bool live = is_page(pg[0]);  // warp-uniform
+#pragma unroll
+                for (int x = 0; x < S::kSlots; ++x) pg[x] = pg[x + 1];
+                pg[S::kSlots] = page_of(group + (S::kSlots + 1) * kWarps);
                 copy_wait<2 * S::kSlots - 1>();  // this group's keys, and both its scales
+                if (!live) {
+                    fetch(group + S::kSlots * kWarps, ahead, 0, slot);
+                    copy_wait<2 * S::kSlots - 1>();
+                    fetch(group + S::kSlots * kWarps, ahead, 1, slot);
+                    return;
+                }
                 uint32_t kc[2][KW];
                 float kscale[2], vscale[2];
-                if (live) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t at = (g + 8 * k) * NS + t * KB;
-                        if constexpr (KB == 8) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(slot + sfew_place<D>(at));
-                            kc[k][0] = v.x;
-                            kc[k][1] = v.y;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < KB / 16; ++i) {
-                                const uint4 v = *reinterpret_cast<const uint4 *>(slot + sfew_place<D>(at + 16 * i));
-                                kc[k][4 * i] = v.x;
-                                kc[k][4 * i + 1] = v.y;
-                                kc[k][4 * i + 2] = v.z;
-                                kc[k][4 * i + 3] = v.w;
-                            }
-                        }
-                        const unsigned char *scales = slot + 2 * S::kCodes + 2 * (g + 8 * k);
-                        kscale[k] = a.kappa * widen(*reinterpret_cast<const T *>(scales));
-                        vscale[k] = widen(*reinterpret_cast<const T *>(scales + 32));
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    load_shared<KW>(slot + k_at[k], k_at[k] ^ 16, slot, kc[k]);
+                    kscale[k] = a.kappa * load_shared16<T>(slot + 2 * S::kCodes + 2 * (g + 8 * k));
+                    vscale[k] = load_shared16<T>(slot + 2 * S::kCodes + 32 + 2 * (g + 8 * k));
                 }
                 __syncwarp();
                 fetch(group + S::kSlots * kWarps, ahead, 0, slot);
                 const int32_t k0 = first_of(group);
-                const bool whole = k0 + 15 <= all_hi && k0 > all_lo;
-                uint32_t pf[2][2];
-                if (live) {  // warp-uniform
-                    // S^T = K^ Q^T, in two chains
-                    float st[4], st2[4];
+                // S^T = K^ Q^T, in two chains
+                float st[4], st2[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) st[c] = st2[c] = 0.f;
+                for (int c = 0; c < 4; ++c) st[c] = st2[c] = 0.f;
 #pragma unroll
-                    for (int b = 0; b < KB; b += 2) {
-                        const uint32_t a0 = table(kc[0][b / 4], b % 4, 0), a1 = table(kc[1][b / 4], b % 4, 0);
-                        const uint32_t a2 = table(kc[0][b / 4], b % 4 + 1, 0), a3 = table(kc[1][b / 4], b % 4 + 1, 0);
-                        mma16816<T>(b % 4 == 0 ? st : st2, a0, a1, a2, a3, qf[b / 2][0], qf[b / 2][1]);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        st[c] = (st[c] + st2[c]) * kscale[c >> 1];
-                        if (!whole) {
-                            const int32_t key = k0 + g + (c >> 1) * 8;
-                            if (key > lim[c & 1] || key <= low[c & 1]) st[c] = kNone;
-                        }
-                    }
-                    if (!whole) {
-                        // tokens that no row sees weigh nothing, whatever their scales hold
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int32_t key = k0 + g + 8 * k;
-                            if (key >= s.it.k_hi || key > last_pos || key <= none_lo) vscale[k] = 0.f;
-                        }
-                    }
-                    sfew_weights<T>(st, vscale, m, sum, factor, o, pf);
+                for (int b = 0; b < KB; b += 2) {
+                    const uint32_t a0 = table(kc[0][b / 4], b % 4, 0), a1 = table(kc[1][b / 4], b % 4, 0);
+                    const uint32_t a2 = table(kc[0][b / 4], b % 4 + 1, 0), a3 = table(kc[1][b / 4], b % 4 + 1, 0);
+                    mma16816<T>(b % 4 == 0 ? st : st2, a0, a1, a2, a3, qf[b / 2][0], qf[b / 2][1]);
                 }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) st[c] = (st[c] + st2[c]) * kscale[c >> 1];
+                if (!(k0 + 15 <= all_hi && k0 > all_lo)) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int32_t key = k0 + g + 8 * k;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (key > lim[c] || key <= low[c]) st[2 * k + c] = kNone;
+                        // tokens that no row sees weigh nothing, whatever their scales hold
+                        if (key >= s.it.k_hi || key > last_pos || key <= none_lo) vscale[k] = 0.f;
+                    }
+                }
+                uint32_t pf[2][2];
+                sfew_weights<T>(st, vscale, m, sum, factor, o, pf);
                 copy_wait<2 * S::kSlots - 1>();  // its values
                 uint32_t vc[4][VW];
-                if (live) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const unsigned char *from = slot + S::kCodes + sfew_place<D>((2 * t + (k & 1) + 8 * (k >> 1)) * NS + g * VB);
-                        if constexpr (VB == 4) {
-                            vc[k][0] = *reinterpret_cast<const uint32_t *>(from);
-                        } else if constexpr (VB == 8) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(from);
-                            vc[k][0] = v.x;
-                            vc[k][1] = v.y;
-                        } else {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(from);
-                            vc[k][0] = v.x;
-                            vc[k][1] = v.y;
-                            vc[k][2] = v.z;
-                            vc[k][3] = v.w;
-                        }
-                    }
-                }
+                for (int k = 0; k < 4; ++k) load_shared<VW>(slot + v_at[k], 0, slot, vc[k]);
                 __syncwarp();
                 fetch(group + S::kSlots * kWarps, ahead, 1, slot);
+                // O^T += V^^T P^T
 #pragma unroll
-                for (int x = 0; x < S::kSlots; ++x) pg[x] = pg[x + 1];
-                pg[S::kSlots] = page_of(group + (S::kSlots + 1) * kWarps);
-                if (live) {
-                    // O^T += V^^T P^T
+                for (int x = 0; x < VW; ++x) {
+                    constexpr uint32_t kLow = 0x0f0f0f0fu;
+                    uint32_t even[2], odd[2];  // of columns 2 i and 2 i + 1, two tokens a byte
 #pragma unroll
-                    for (int x = 0; x < VW; ++x) {
-                        constexpr uint32_t kLow = 0x0f0f0f0fu;
-                        uint32_t even[2], odd[2];  // of columns 2 i and 2 i + 1, two tokens a byte
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t v0 = vc[2 * k][x], v1 = vc[2 * k + 1][x];
+                        even[k] = (v0 & kLow) | (v1 << 4 & ~kLow);
+                        odd[k] = (v0 >> 4 & kLow) | (v1 & ~kLow);
+                    }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t v0 = vc[2 * k][x], v1 = vc[2 * k + 1][x];
-                            even[k] = (v0 & kLow) | (v1 << 4 & ~kLow);
-                            odd[k] = (v0 >> 4 & kLow) | (v1 & ~kLow);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t a0 = table(even[0], i, 1), a1 = table(odd[0], i, 1);
-                            const uint32_t a2 = table(even[1], i, 1), a3 = table(odd[1], i, 1);
-                            mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[0][0], pf[0][1]);
-                            mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[1][0], pf[1][1]);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = table(even[0], i, 1), a1 = table(odd[0], i, 1);
+                        const uint32_t a2 = table(even[1], i, 1), a3 = table(odd[1], i, 1);
+                        mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[0][0], pf[0][1]);
+                        mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[1][0], pf[1][1]);
                     }
                 }
             };

@@ -25,7 +25,7 @@ vq_status vqh_paged_chunk(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, c
 // (vq_pattn.cuh), as its programmatic dependent.
 vq_status vqh_paged_merge(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);
 
-// The same kernels for a cache of 4-bit scalar codes (sub = 2: a byte selects a pair).
-int vqh_sfew_blocks_per_sm(int32_t dim);
+// The same kernels for a cache of 4-bit scalar codes (sub = 2: a byte selects a pair); of
+// the few-row kernel too one block an SM.
 vq_status vqh_paged_sfew(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);
 vq_status vqh_paged_schunk(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);

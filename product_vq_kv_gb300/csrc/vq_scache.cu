@@ -39,7 +39,7 @@ bool tensor_layout(const vqk::PagedArgs &a)
 TensorKernels tensor_kernels(int32_t dim)
 {
     const int32_t items = 1 << 20;
-    return TensorKernels{vqh_few_rows(), vqh_sfew_blocks_per_sm(dim), vqh_chunk_tiles(dim), items, vqh_paged_sfew,
+    return TensorKernels{vqh_few_rows(), 1, vqh_chunk_tiles(dim), items, vqh_paged_sfew,
                          vqh_paged_schunk};
 }
 

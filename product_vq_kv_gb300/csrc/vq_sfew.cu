@@ -35,11 +35,6 @@ vq_status launch_dim(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
 
 }  // namespace
 
-int vqh_sfew_blocks_per_sm(int32_t dim)
-{
-    return dim == 64 ? vqk::SFewShape<64>::kBlocks : dim == 128 ? vqk::SFewShape<128>::kBlocks : vqk::SFewShape<256>::kBlocks;
-}
-
 vq_status vqh_paged_sfew(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st)
 {
     return dtype == VQ_F16 ? launch_dim<__half>(a, blocks, st) : launch_dim<__nv_bfloat16>(a, blocks, st);

@@ -24,9 +24,11 @@
 //     tokens' words are exchanged (a shift and a select a word), so that a byte holds the two
 //     tokens' codes of one column.  The values' scales multiply the weights, in fp32 and
 //     before their rounding to two pieces, so that no rebuilt value is rounded.
+//   * A warp takes 32 tokens at a time, so that addresses, page lookups, waits and the vote
+//     are paid once and the two groups' chains of dependent instructions overlap.
 //   * Codes and scales come by cp.async into two slots a warp, 16-byte pieces exchanged so
 //     that the keys' and the values' reads meet no bank twice; a slot is filled again as
-//     soon as its codes are in registers, two groups ahead of their use.
+//     soon as its codes are in registers, two runs ahead of their use.
 #pragma once
 
 #include "vq_pfew.cuh"
@@ -37,17 +39,24 @@ namespace vqk {
 
 template <int D>
 struct SFewShape {
+    // One block an SM, with as many warps as leave the accumulators and queries (dim/16 x 6
+    // registers) and a run's codes in registers.
     static constexpr int kWarps = D == 64 ? 16 : D == 128 ? 12 : 8;
-    static constexpr int kBlocks = 1;
-    static constexpr int kSlots = 2;              // of a warp
+    static constexpr int kHalves = 2;             // groups of 16 tokens that a warp takes at a time: a run
+    static constexpr int kRun = 16 * kHalves;
+    static constexpr int kSlots = 2;              // of a warp, a run each
     static constexpr int kCodes = 16 * (D / 2);   // code bytes of a group, keys or values
-    static constexpr int kSlot = 2 * kCodes + 64; // and their scales
-    static constexpr size_t kRing = (size_t)kWarps * kSlots * kSlot;
-    static constexpr size_t kMerge = (size_t)((kWarps + 1) / 2) * kFewRows * D * sizeof(float);  // over the ring
-    // Addresses in shared memory: the table from kTable, the ring from kTable + 65536.  What
-    // lies below is static, or not used: one block an SM has the room.
-    static constexpr uint32_t kTable = 65536;
-    static constexpr size_t kSmem = kTable + 65536 + (kRing > kMerge ? kRing : kMerge);
+    static constexpr int kValues = kHalves * kCodes, kScales = 2 * kValues;  // in a slot: keys, values, scales
+    static constexpr int kSlot = kScales + kHalves * 64;
+    static constexpr int kWarpRing = kSlots * kSlot;
+    static constexpr size_t kMerge = (size_t)((kWarps + 1) / 2) * kFewRows * D * sizeof(float);  // over the upper ring
+    // Addresses in shared memory: static memory, the ring of the first kLow warps from kRing,
+    // the table from kTable, the other warps' ring from kUpper.
+    static constexpr uint32_t kTable = 65536, kUpper = kTable + 65536;
+    static constexpr uint32_t kRing = 10240;
+    static constexpr int kLow = (kTable - kRing) / kWarpRing < kWarps ? (kTable - kRing) / kWarpRing : kWarps;
+    static constexpr size_t kAbove = (size_t)(kWarps - kLow) * kWarpRing;
+    static constexpr size_t kSmem = kUpper + (kAbove > kMerge ? kAbove : kMerge);  // (of which the array has the part from its start on)
 };
 
 // Where byte `at` of a group's codes lies in its slot: of each 128 bytes the 16-byte pieces
@@ -68,23 +77,25 @@ constexpr float kSFewMost = 1.2676506e30f;   // 2^100
 constexpr float kSFewSlack = 32.f;           // powers of two that a score may lie above m: p stays fp32
 constexpr float kSFewTop = 32768.f;          // the largest weight: 2^15, inside fp16
 
-// The scores of 16 tokens against this lane's two rows to weights, as few_weights does it,
-// but the product takes p s_v, the scale of the token's value (vs: of tokens g and g + 8)
-// folded in.  m follows the scores alone and the factor f the weights alone: a value's scale
+// The scores of H groups of 16 tokens against this lane's two rows to weights, as
+// few_weights does it, but the product takes p s_v, the scale of the token's value (vs: of
+// tokens g and g + 8) folded in.  m follows the scores alone and the factor f the weights alone: a value's scale
 // does not touch the sum, and tokens whose values are large do not push others, of larger
 // weight, out of fp16.
-template <typename T, int MMA>
-__device__ __forceinline__ void sfew_weights(const float (&st)[4], const float (&vs)[2], float (&m)[2], float (&sum)[2],
-                                             float (&f)[2], float (&o)[MMA][4], uint32_t (&pf)[2][2])
+template <typename T, int H, int MMA>
+__device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const float (&vs)[H][2], float (&m)[2], float (&sum)[2],
+                                             float (&f)[2], float (&o)[MMA][4], uint32_t (&pf)[H][2][2])
 {
-    float p[4], w[4];
+    float p[H][4], w[H][4];
     bool rise = false;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        p[c] = exp2_fast(st[c] - m[c & 1]);
-        w[c] = p[c] * vs[c >> 1] * f[c & 1];
-        rise |= st[c] > m[c & 1] + kSFewSlack || w[c] > kSFewTop;
-    }
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            p[h][c] = exp2_fast(st[h][c] - m[c & 1]);
+            w[h][c] = p[h][c] * vs[h][c >> 1] * f[c & 1];
+            rise |= st[h][c] > m[c & 1] + kSFewSlack || w[h][c] > kSFewTop;
+        }
     if (__any_sync(0xffffffffu, rise)) {
         // a row rises for its own scores and weights alone, so that what it computes does not
         // depend on the rows beside it
@@ -95,7 +106,10 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[4], const float (
         };
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float top = over_lanes(fmaxf(st[c], st[c + 2]));
+            float top = __int_as_float(0xff800000);
+#pragma unroll
+            for (int h = 0; h < H; ++h) top = fmaxf(top, fmaxf(st[h][c], st[h][c + 2]));
+            top = over_lanes(top);
             float scale = 1.f;  // of the accumulators
             if (top > m[c] + kSFewSlack) {
                 const float to = f[c] * exp2_fast(top - m[c]);
@@ -104,9 +118,15 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[4], const float (
                 sum[c] *= exp2_fast(m[c] - top);
                 m[c] = top;
             }
+            float most = 0.f;
 #pragma unroll
-            for (int k = c; k < 4; k += 2) p[k] = exp2_fast(st[k] - m[c]);
-            const float most = over_lanes(fmaxf(p[c] * vs[0], p[c + 2] * vs[1]));
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int k = c; k < 4; k += 2) {
+                    p[h][k] = exp2_fast(st[h][k] - m[c]);
+                    most = fmaxf(most, p[h][k] * vs[h][k >> 1]);
+                }
+            most = over_lanes(most);
             if (most * f[c] > kSFewTop) {
                 // the power of two that brings it to [2^6, 2^7): most >= 2^-85 here
                 const uint32_t e = __float_as_uint(most) >> 23;
@@ -115,7 +135,9 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[4], const float (
                 f[c] = to;
             }
 #pragma unroll
-            for (int k = c; k < 4; k += 2) w[k] = p[k] * vs[k >> 1] * f[c];
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int k = c; k < 4; k += 2) w[h][k] = p[h][k] * vs[h][k >> 1] * f[c];
 #pragma unroll
             for (int i = 0; i < MMA; ++i) {
                 o[i][c] *= scale;
@@ -123,14 +145,17 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[4], const float (
             }
         }
     }
-    sum[0] += p[0] + p[2];
-    sum[1] += p[1] + p[3];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const uint32_t high = pack2<T>(w[2 * c], w[2 * c + 1]);
-        const float2 kept = unpack2<T>(high);
-        pf[0][c] = transpose8x8(high);
-        pf[1][c] = transpose8x8(pack2<T>(w[2 * c] - kept.x, w[2 * c + 1] - kept.y));
+    for (int h = 0; h < H; ++h) {
+        sum[0] += p[h][0] + p[h][2];
+        sum[1] += p[h][1] + p[h][3];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t high = pack2<T>(w[h][2 * c], w[h][2 * c + 1]);
+            const float2 kept = unpack2<T>(high);
+            pf[h][0][c] = transpose8x8(high);
+            pf[h][1][c] = transpose8x8(pack2<T>(w[h][2 * c] - kept.x, w[h][2 * c + 1] - kept.y));
+        }
     }
 }
 
@@ -146,10 +171,10 @@ __device__ __forceinline__ void copy_wait()
     __syncwarp();
 }
 
-// W words of codes at address `at` (two 16-byte pieces: the second at `base` + `next`).  Not
-// moved across the waits and fetches around them, which are volatile too.
+// W words of codes at address `at` (of two 16-byte pieces the second at `next`).  Not moved
+// across the waits and fetches around them, which are volatile too.
 template <int W>
-__device__ __forceinline__ void load_shared(uint32_t at, uint32_t next, uint32_t base, uint32_t (&v)[W])
+__device__ __forceinline__ void load_shared(uint32_t at, uint32_t next, uint32_t (&v)[W])
 {
     if constexpr (W == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(at) : "memory");
     if constexpr (W == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
@@ -161,7 +186,7 @@ __device__ __forceinline__ void load_shared(uint32_t at, uint32_t next, uint32_t
     if constexpr (W == 8)
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                     : "r"(base + next)
+                     : "r"(next)
                      : "memory");
 }
 
@@ -196,7 +221,7 @@ __device__ __forceinline__ void scalar_table(const PagedArgs &a, unsigned char *
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBlocks)
+__global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
     paged_attn_sfew(const __grid_constant__ PagedArgs a)
 {
     using S = SFewShape<D>;
@@ -208,9 +233,10 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
     extern __shared__ __align__(128) unsigned char sfew_mem[];
     __shared__ PagedWalk<> w;
     __shared__ float wm[kWarps][kFewRows], wl[kWarps][kFewRows];
-    // (the array begins behind the static memory, at most at kTable)
+    static_assert(1024 + sizeof w + sizeof wm + sizeof wl + 256 <= S::kRing, "static memory (and the system's) below the ring");
+    // (the array begins behind the static memory, which ends below kRing)
     unsigned char *lines = sfew_mem + (S::kTable - smem_addr(sfew_mem));
-    float *slots = reinterpret_cast<float *>(lines + 65536);
+    float *slots = reinterpret_cast<float *>(lines + (S::kUpper - S::kTable));
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -223,14 +249,14 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
     const int64_t q_elems = (a.tokens - 1) * a.q_stride + (int64_t)a.hq * D;
     const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
     const int64_t scale_bytes = 2 * ((a.num_pages - 1) * a.scale_stride + ((int64_t)a.hkv << a.page_shift));
-    const uint32_t ring = S::kTable + 65536 + warp * (S::kSlots * S::kSlot);
+    const uint32_t ring = warp < S::kLow ? S::kRing + warp * S::kWarpRing : S::kUpper + (warp - S::kLow) * S::kWarpRing;
     // where this lane puts and finds codes in a slot
     const uint32_t put_at = sfew_place<D>(lane * 16);
     uint32_t k_at[2], v_at[4];
 #pragma unroll
     for (int k = 0; k < 2; ++k) k_at[k] = sfew_place<D>((g + 8 * k) * NS + t * KB);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v_at[k] = S::kCodes + sfew_place<D>((2 * t + (k & 1) + 8 * (k >> 1)) * NS + g * VB);
+    for (int k = 0; k < 4; ++k) v_at[k] = S::kValues + sfew_place<D>((2 * t + (k & 1) + 8 * (k >> 1)) * NS + g * VB);
 
     // the merge's blocks may take the room that idle blocks leave (they wait there)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -292,45 +318,53 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
             const int64_t all_lo = a.window == 0 ? -1 : last_pos - a.window;       // and above here
             const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.it.pos0 - a.window;  // no row sees at or below
 
-            // groups of 16 tokens, warp after warp
-            const int g_begin = s.begin * (kUnit / 16) + warp, g_end = s.end * (kUnit / 16);
-            auto first_of = [&](int group) { return s.it.k_lo + group * 16; };
-            auto page_of = [&](int group) -> int32_t {
-                if (group >= g_end) return -1;
-                const int32_t k0 = first_of(group);
+            // runs of 32 tokens, warp after warp
+            const int g_begin = s.begin * (kUnit / S::kRun) + warp, g_end = s.end * (kUnit / S::kRun);
+            auto first_of = [&](int run) { return s.it.k_lo + run * S::kRun; };
+            auto entry_of = [&](int32_t k0) -> int32_t {  // the page of 16 tokens
                 if (k0 >= s.it.k_hi || k0 + 15 <= none_lo) return -1;
                 return paged_entry(a, cur.r, k0);  // checked when it is used: a check here would wait for the load
             };
+            struct Pages { int32_t pg[S::kHalves]; };
+            auto pages_of = [&](int run) {
+                Pages p;
+#pragma unroll
+                for (int x = 0; x < S::kHalves; ++x) p.pg[x] = run < g_end ? entry_of(first_of(run) + 16 * x) : -1;
+                return p;
+            };
             auto is_page = [&](int32_t pg) { return pg >= 0 && pg < a.num_pages; };
-            // this head's rows of page 0; lanes 0, 1 fetch the keys' scales, 2, 3 the values'
+            // this head's rows of page 0; of 4 lanes two fetch the keys' scales, two the values'
             const int64_t head = (int64_t)h << a.page_shift;
             const uint8_t *k_head = a.k_codes + head * NS + lane * 16, *v_head = a.v_codes + head * NS + lane * 16;
-            const unsigned char *s_head = (lane < 2 ? ks : vs) + 2 * head + (lane & 1) * 16;
-            // a group on its way into a slot: the keys and both scales, or the values
-            auto fetch = [&](int group, int32_t pg, int kind, uint32_t slot) {
-                if (is_page(pg)) {  // warp-uniform
-                    const int32_t row = first_of(group) & ((1 << a.page_shift) - 1);
-                    const int64_t at = (int64_t)pg * a.page_stride + row * NS;
-                    const uint8_t *codes = (kind ? v_head : k_head) + at;
+            const unsigned char *s_head = (lane % 4 < 2 ? ks : vs) + 2 * head + (lane & 1) * 16;
+            // a run on its way into a slot: the keys and both scales, or the values
+            auto fetch = [&](int run, const Pages &p, int kind, uint32_t slot) {
+#pragma unroll
+                for (int x = 0; x < S::kHalves; ++x) {
+                    const int32_t pg = p.pg[x];
+                    if (!is_page(pg)) continue;  // warp-uniform
+                    const int32_t row = (first_of(run) + 16 * x) & ((1 << a.page_shift) - 1);
+                    const uint8_t *codes = (kind ? v_head : k_head) + ((int64_t)pg * a.page_stride + row * NS);
+                    const uint32_t to = slot + (kind ? S::kValues : 0) + x * S::kCodes;
 #pragma unroll
                     for (int i = 0; i < S::kCodes / 512; ++i)
                         if (span_ok(codes + i * 512, 16, kind ? a.v_codes : a.k_codes, code_bytes, 16))
-                            copy_async16(slot + kind * S::kCodes + i * 512 + (D == 256 && i % 2 ? put_at ^ 64 : put_at), codes + i * 512);
-                    if (kind == 0 && lane < 4) {
+                            copy_async16(to + i * 512 + (D == 256 && i % 2 ? put_at ^ 64 : put_at), codes + i * 512);
+                    if (kind == 0 && lane / 4 == x) {
                         const unsigned char *from = s_head + 2 * ((int64_t)pg * a.scale_stride + row);
-                        if (span_ok(from, 16, lane < 2 ? ks : vs, scale_bytes, 16)) copy_async16(slot + 2 * S::kCodes + lane * 16, from);
+                        if (span_ok(from, 16, lane % 4 < 2 ? ks : vs, scale_bytes, 16)) copy_async16(slot + S::kScales + lane * 16, from);
                     }
                 }
                 copy_commit();  // (an empty group keeps the count)
             };
-            int32_t pg[S::kSlots + 1];
+            Pages pages[S::kSlots + 1];
 #pragma unroll
-            for (int x = 0; x <= S::kSlots; ++x) pg[x] = page_of(g_begin + x * kWarps);
+            for (int x = 0; x <= S::kSlots; ++x) pages[x] = pages_of(g_begin + x * kWarps);
             __syncthreads();  // the table is written, the last segment's merge has left the ring
 #pragma unroll
             for (int x = 0; x < S::kSlots; ++x) {
-                fetch(g_begin + x * kWarps, pg[x], 0, ring + x * S::kSlot);
-                fetch(g_begin + x * kWarps, pg[x], 1, ring + x * S::kSlot);
+                fetch(g_begin + x * kWarps, pages[x], 0, ring + x * S::kSlot);
+                fetch(g_begin + x * kWarps, pages[x], 1, ring + x * S::kSlot);
             }
 
             // (in the order of its operands alone: a volatile load would stand in the order of
@@ -342,85 +376,103 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
                 else asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
                 return v;
             };
-            auto step = [&](uint32_t slot, int group) {
-                const int32_t ahead = pg[S::kSlots];
-                const bool live = is_page(pg[0]);  // warp-uniform
+            uint32_t slot = ring;
+            for (int run = g_begin; run < g_end; run += kWarps) {
+                const Pages ahead = pages[S::kSlots];
+                bool live[S::kHalves], any = false, both = true;  // warp-uniform
 #pragma unroll
-                for (int x = 0; x < S::kSlots; ++x) pg[x] = pg[x + 1];
-                pg[S::kSlots] = page_of(group + (S::kSlots + 1) * kWarps);
-                copy_wait<2 * S::kSlots - 1>();  // this group's keys, and both its scales
-                if (!live) {
-                    fetch(group + S::kSlots * kWarps, ahead, 0, slot);
+                for (int x = 0; x < S::kHalves; ++x) {
+                    live[x] = is_page(pages[0].pg[x]);
+                    any |= live[x];
+                    both &= live[x];
+                }
+#pragma unroll
+                for (int x = 0; x < S::kSlots; ++x) pages[x] = pages[x + 1];
+                pages[S::kSlots] = pages_of(run + (S::kSlots + 1) * kWarps);
+                copy_wait<2 * S::kSlots - 1>();  // this run's keys, and both its scales
+                if (any) {
+                    uint32_t kc[S::kHalves][2][KW];
+                    float kscale[S::kHalves][2], vscale[S::kHalves][2];
+#pragma unroll
+                    for (int x = 0; x < S::kHalves; ++x)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            load_shared<KW>(slot + x * S::kCodes + k_at[k], slot + x * S::kCodes + (k_at[k] ^ 16), kc[x][k]);
+                            kscale[x][k] = a.kappa * load_shared16<T>(slot + S::kScales + 64 * x + 2 * (g + 8 * k));
+                            vscale[x][k] = load_shared16<T>(slot + S::kScales + 64 * x + 32 + 2 * (g + 8 * k));
+                        }
+                    __syncwarp();
+                    fetch(run + S::kSlots * kWarps, ahead, 0, slot);
+                    const int32_t k0 = first_of(run);
+                    // S^T = K^ Q^T
+                    float st[S::kHalves][4];
+#pragma unroll
+                    for (int x = 0; x < S::kHalves; ++x)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) st[x][c] = 0.f;
+#pragma unroll
+                    for (int b = 0; b < KB; b += 2)
+#pragma unroll
+                        for (int x = 0; x < S::kHalves; ++x) {
+                            const uint32_t a0 = table(kc[x][0][b / 4], b % 4, 0), a1 = table(kc[x][1][b / 4], b % 4, 0);
+                            const uint32_t a2 = table(kc[x][0][b / 4], b % 4 + 1, 0), a3 = table(kc[x][1][b / 4], b % 4 + 1, 0);
+                            mma16816<T>(st[x], a0, a1, a2, a3, qf[b / 2][0], qf[b / 2][1]);
+                        }
+#pragma unroll
+                    for (int x = 0; x < S::kHalves; ++x)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) st[x][c] *= kscale[x][c >> 1];
+                    if (!(both && k0 + S::kRun - 1 <= all_hi && k0 > all_lo)) {
+#pragma unroll
+                        for (int x = 0; x < S::kHalves; ++x)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int32_t key = k0 + 16 * x + g + 8 * k;
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (!live[x] || key > lim[c] || key <= low[c]) st[x][2 * k + c] = kNone;
+                                // tokens that no row sees weigh nothing, whatever their scales hold
+                                if (!live[x] || key >= s.it.k_hi || key > last_pos || key <= none_lo) vscale[x][k] = 0.f;
+                            }
+                    }
+                    uint32_t pf[S::kHalves][2][2];
+                    sfew_weights<T>(st, vscale, m, sum, factor, o, pf);
+                    copy_wait<2 * S::kSlots - 1>();  // its values
+                    uint32_t vc[S::kHalves][4][VW];
+#pragma unroll
+                    for (int x = 0; x < S::kHalves; ++x)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) load_shared<VW>(slot + x * S::kCodes + v_at[k], 0, vc[x][k]);
+                    __syncwarp();
+                    fetch(run + S::kSlots * kWarps, ahead, 1, slot);
+                    // O^T += V^^T P^T
+#pragma unroll
+                    for (int i = 0; i < VW; ++i)
+#pragma unroll
+                        for (int x = 0; x < S::kHalves; ++x) {
+                            constexpr uint32_t kLow = 0x0f0f0f0fu;
+                            uint32_t even[2], odd[2];  // of columns 2 b and 2 b + 1, two tokens a byte
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t v0 = vc[x][2 * k][i], v1 = vc[x][2 * k + 1][i];
+                                even[k] = (v0 & kLow) | (v1 << 4 & ~kLow);
+                                odd[k] = (v0 >> 4 & kLow) | (v1 & ~kLow);
+                            }
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const uint32_t a0 = table(even[0], b, 1), a1 = table(odd[0], b, 1);
+                                const uint32_t a2 = table(even[1], b, 1), a3 = table(odd[1], b, 1);
+                                mma16816<T>(o[4 * i + b], a0, a1, a2, a3, pf[x][0][0], pf[x][0][1]);
+                                mma16816<T>(o[4 * i + b], a0, a1, a2, a3, pf[x][1][0], pf[x][1][1]);
+                            }
+                        }
+                } else {
+                    fetch(run + S::kSlots * kWarps, ahead, 0, slot);
                     copy_wait<2 * S::kSlots - 1>();
-                    fetch(group + S::kSlots * kWarps, ahead, 1, slot);
-                    return;
+                    fetch(run + S::kSlots * kWarps, ahead, 1, slot);
                 }
-                uint32_t kc[2][KW];
-                float kscale[2], vscale[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    load_shared<KW>(slot + k_at[k], k_at[k] ^ 16, slot, kc[k]);
-                    kscale[k] = a.kappa * load_shared16<T>(slot + 2 * S::kCodes + 2 * (g + 8 * k));
-                    vscale[k] = load_shared16<T>(slot + 2 * S::kCodes + 32 + 2 * (g + 8 * k));
-                }
-                __syncwarp();
-                fetch(group + S::kSlots * kWarps, ahead, 0, slot);
-                const int32_t k0 = first_of(group);
-                // S^T = K^ Q^T, in two chains
-                float st[4], st2[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) st[c] = st2[c] = 0.f;
-#pragma unroll
-                for (int b = 0; b < KB; b += 2) {
-                    const uint32_t a0 = table(kc[0][b / 4], b % 4, 0), a1 = table(kc[1][b / 4], b % 4, 0);
-                    const uint32_t a2 = table(kc[0][b / 4], b % 4 + 1, 0), a3 = table(kc[1][b / 4], b % 4 + 1, 0);
-                    mma16816<T>(b % 4 == 0 ? st : st2, a0, a1, a2, a3, qf[b / 2][0], qf[b / 2][1]);
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) st[c] = (st[c] + st2[c]) * kscale[c >> 1];
-                if (!(k0 + 15 <= all_hi && k0 > all_lo)) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int32_t key = k0 + g + 8 * k;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            if (key > lim[c] || key <= low[c]) st[2 * k + c] = kNone;
-                        // tokens that no row sees weigh nothing, whatever their scales hold
-                        if (key >= s.it.k_hi || key > last_pos || key <= none_lo) vscale[k] = 0.f;
-                    }
-                }
-                uint32_t pf[2][2];
-                sfew_weights<T>(st, vscale, m, sum, factor, o, pf);
-                copy_wait<2 * S::kSlots - 1>();  // its values
-                uint32_t vc[4][VW];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) load_shared<VW>(slot + v_at[k], 0, slot, vc[k]);
-                __syncwarp();
-                fetch(group + S::kSlots * kWarps, ahead, 1, slot);
-                // O^T += V^^T P^T
-#pragma unroll
-                for (int x = 0; x < VW; ++x) {
-                    constexpr uint32_t kLow = 0x0f0f0f0fu;
-                    uint32_t even[2], odd[2];  // of columns 2 i and 2 i + 1, two tokens a byte
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t v0 = vc[2 * k][x], v1 = vc[2 * k + 1][x];
-                        even[k] = (v0 & kLow) | (v1 << 4 & ~kLow);
-                        odd[k] = (v0 >> 4 & kLow) | (v1 & ~kLow);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = table(even[0], i, 1), a1 = table(odd[0], i, 1);
-                        const uint32_t a2 = table(even[1], i, 1), a3 = table(odd[1], i, 1);
-                        mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[0][0], pf[0][1]);
-                        mma16816<T>(o[4 * x + i], a0, a1, a2, a3, pf[1][0], pf[1][1]);
-                    }
-                }
-            };
-            static_assert(S::kSlots == 2, "two slots in turn");
-            for (int group = g_begin; group < g_end; group += 2 * kWarps) {
-                step(ring, group);
-                if (group + kWarps < g_end) step(ring + S::kSlot, group + kWarps);
+                static_assert(S::kSlots == 2, "two slots in turn");
+                slot = slot == ring ? ring + S::kSlot : ring;
             }
             copy_wait<0>();
             // to weights without the factors
@@ -433,8 +485,10 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, SFewShape<D>::kBloc
                     o[i][c + 2] *= inv;
                 }
             }
-            few_finish<T, D, kWarps>(a, s, rows, gc, head0, lim, low, m, sum, o, wm, wl, slots, out_vec, g_begin, g_end,
-                                     first_of, page_of);
+            // (what it looks through for tokens that rows see: this warp's groups of 16)
+            few_finish<T, D, kWarps>(a, s, rows, gc, head0, lim, low, m, sum, o, wm, wl, slots, out_vec, s.begin * (kUnit / 16) + warp,
+                                     s.end * (kUnit / 16), [&](int group) { return s.it.k_lo + group * 16; },
+                                     [&](int group) { return entry_of(s.it.k_lo + group * 16); });
         }
     }
     if (tid == 0 && VQ_SPAN(a.notes + blockIdx.x, 1, a.notes, gridDim.x)) a.notes[blockIdx.x] = note;

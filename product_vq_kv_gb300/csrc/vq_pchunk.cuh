@@ -133,13 +133,6 @@ __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 // Polls of a wait: about a second (2^22 took 15 s), where a block of keys takes
 // microseconds.  The waits for the next segment, and for room to announce one, last as
 // long as a segment: on the longest cache of 2^30 tokens 2^23 units of 2 us, 17 s, so

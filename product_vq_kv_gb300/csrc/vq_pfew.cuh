@@ -129,6 +129,13 @@ __device__ __forceinline__ float exp2_fast(float x)
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // BYTES consecutive code bytes in words, low byte first.
 template <int BYTES>
 __device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&w)[(BYTES + 3) / 4])

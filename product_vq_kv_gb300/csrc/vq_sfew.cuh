@@ -61,11 +61,11 @@ struct SFewShape {
 
 // Where byte `at` of a group's codes lies in its slot: of each 128 bytes the 16-byte pieces
 // change places.  A warp reads keys row by row and values two rows apart, and with this
-// neither meets a bank twice in one pass.
+// neither meets a bank twice in one pass.  Rows 8 apart change alike.
 template <int D>
 __device__ __forceinline__ uint32_t sfew_place(uint32_t at)
 {
-    const uint32_t line = at >> 7, turn = D == 256 ? line & 7 : 2 * (line & 3);
+    const uint32_t line = at >> 7, turn = D == 256 ? line & 7 : D == 128 ? 2 * (line & 3) : 2 * (line & 1);
     return at ^ (turn << 4);
 }
 
@@ -74,8 +74,8 @@ __device__ __forceinline__ uint32_t sfew_place(uint32_t at)
 // weight passes kSFewTop; a rise of m lifts it by as much, so that the accumulators stay as
 // they are.
 constexpr float kSFewMost = 1.2676506e30f;   // 2^100
-constexpr float kSFewSlack = 32.f;           // powers of two that a score may lie above m: p stays fp32
 constexpr float kSFewTop = 32768.f;          // the largest weight: 2^15, inside fp16
+constexpr float kSFewLess = 7.6293945e-6f;   // 2^-17: p, which stays fp32, may reach 2^32
 
 // The scores of H groups of 16 tokens against this lane's two rows to weights, as
 // few_weights does it, but the product takes p s_v, the scale of the token's value (vs: of
@@ -86,17 +86,16 @@ template <typename T, int H, int MMA>
 __device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const float (&vs)[H][2], float (&m)[2], float (&sum)[2],
                                              float (&f)[2], float (&o)[MMA][4], uint32_t (&pf)[H][2][2])
 {
-    float p[H][4], w[H][4];
-    bool rise = false;
+    float p[H][4], w[H][4], high = 0.f;
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             p[h][c] = exp2_fast(st[h][c] - m[c & 1]);
             w[h][c] = p[h][c] * vs[h][c >> 1] * f[c & 1];
-            rise |= st[h][c] > m[c & 1] + kSFewSlack || w[h][c] > kSFewTop;
+            high = max3(high, p[h][c] * kSFewLess, w[h][c]);
         }
-    if (__any_sync(0xffffffffu, rise)) {
+    if (__any_sync(0xffffffffu, high > kSFewTop)) {
         // a row rises for its own scores and weights alone, so that what it computes does not
         // depend on the rows beside it
         auto over_lanes = [](float v) {
@@ -111,7 +110,7 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const floa
             for (int h = 0; h < H; ++h) top = fmaxf(top, fmaxf(st[h][c], st[h][c + 2]));
             top = over_lanes(top);
             float scale = 1.f;  // of the accumulators
-            if (top > m[c] + kSFewSlack) {
+            if (exp2_fast(top - m[c]) * kSFewLess > kSFewTop) {
                 const float to = f[c] * exp2_fast(top - m[c]);
                 f[c] = fminf(to, kSFewMost);
                 scale = f[c] / to;  // (0 where `to` is infinite: what was is nothing beside it)
@@ -151,17 +150,18 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const floa
         sum[1] += p[h][1] + p[h][3];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const uint32_t high = pack2<T>(w[h][2 * c], w[h][2 * c + 1]);
-            const float2 kept = unpack2<T>(high);
-            pf[h][0][c] = transpose8x8(high);
+            const uint32_t first = pack2<T>(w[h][2 * c], w[h][2 * c + 1]);
+            const float2 kept = unpack2<T>(first);
+            pf[h][0][c] = transpose8x8(first);
             pf[h][1][c] = transpose8x8(pack2<T>(w[h][2 * c] - kept.x, w[h][2 * c + 1] - kept.y));
         }
     }
 }
 
+template <int OFF, int FROM>
 __device__ __forceinline__ void copy_async16(uint32_t to, const void *from)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(to), "l"(from), "n"(OFF), "n"(FROM) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -171,32 +171,43 @@ __device__ __forceinline__ void copy_wait()
     __syncwarp();
 }
 
-// W words of codes at address `at` (of two 16-byte pieces the second at `next`).  Not moved
-// across the waits and fetches around them, which are volatile too.
-template <int W>
+// W words of codes at address `at` + OFF (of two 16-byte pieces the second at `next` + OFF).
+// Not moved across the waits and fetches around them, which are volatile too.
+template <int W, int OFF>
 __device__ __forceinline__ void load_shared(uint32_t at, uint32_t next, uint32_t (&v)[W])
 {
-    if constexpr (W == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(at) : "memory");
-    if constexpr (W == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+    if constexpr (W == 1) asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(v[0]) : "r"(at), "n"(OFF) : "memory");
+    if constexpr (W == 2)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(v[0]), "=r"(v[1]) : "r"(at), "n"(OFF) : "memory");
     if constexpr (W >= 4)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                     : "r"(at)
+                     : "r"(at), "n"(OFF)
                      : "memory");
     if constexpr (W == 8)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
                      : "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                     : "r"(next)
+                     : "r"(next), "n"(OFF)
                      : "memory");
 }
 
-template <typename T>
+template <typename T, int OFF>
 __device__ __forceinline__ float load_shared16(uint32_t at)
 {
     uint16_t v;
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared.b16 %0, [%1 + %2];" : "=h"(v) : "r"(at), "n"(OFF) : "memory");
     if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(v));
     else return __uint_as_float((uint32_t)v << 16);
+}
+
+// f(0), .., f(N - 1) with the numbers as constants.
+template <int N, typename F>
+__device__ __forceinline__ void each(F f)
+{
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
 }
 
 // The table of both codebooks: line b of 256 bytes holds the keys' pair of byte b 32 times,
@@ -252,11 +263,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
     const uint32_t ring = warp < S::kLow ? S::kRing + warp * S::kWarpRing : S::kUpper + (warp - S::kLow) * S::kWarpRing;
     // where this lane puts and finds codes in a slot
     const uint32_t put_at = sfew_place<D>(lane * 16);
-    uint32_t k_at[2], v_at[4];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) k_at[k] = sfew_place<D>((g + 8 * k) * NS + t * KB);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v_at[k] = S::kValues + sfew_place<D>((2 * t + (k & 1) + 8 * (k >> 1)) * NS + g * VB);
+    const uint32_t k_at = sfew_place<D>(g * NS + t * KB), v_at[2] = {sfew_place<D>(2 * t * NS + g * VB), sfew_place<D>((2 * t + 1) * NS + g * VB)};
 
     // the merge's blocks may take the room that idle blocks leave (they wait there)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -325,11 +332,22 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                 if (k0 >= s.it.k_hi || k0 + 15 <= none_lo) return -1;
                 return paged_entry(a, cur.r, k0);  // checked when it is used: a check here would wait for the load
             };
+            // The pages of 32 runs of this warp, a run a lane, one batch ahead of its use: a load
+            // for each run is waited for where its register is handed on.
             struct Pages { int32_t pg[S::kHalves]; };
-            auto pages_of = [&](int run) {
+            auto batch_of = [&](int n) {  // runs 32 n .. of this warp
                 Pages p;
+                const int run = g_begin + (32 * n + lane) * kWarps;
 #pragma unroll
                 for (int x = 0; x < S::kHalves; ++x) p.pg[x] = run < g_end ? entry_of(first_of(run) + 16 * x) : -1;
+                return p;
+            };
+            Pages batch = batch_of(0), batch_next = batch_of(1);
+            auto pages_of = [&](int n) {  // of this warp's n-th run in the batch or the next
+                Pages p;
+#pragma unroll
+                for (int x = 0; x < S::kHalves; ++x)
+                    p.pg[x] = __shfl_sync(0xffffffffu, n < 32 ? batch.pg[x] : batch_next.pg[x], n & 31);
                 return p;
             };
             auto is_page = [&](int32_t pg) { return pg >= 0 && pg < a.num_pages; };
@@ -338,33 +356,56 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
             const uint8_t *k_head = a.k_codes + head * NS + lane * 16, *v_head = a.v_codes + head * NS + lane * 16;
             const unsigned char *s_head = (lane % 4 < 2 ? ks : vs) + 2 * head + (lane & 1) * 16;
             // a run on its way into a slot: the keys and both scales, or the values
-            auto fetch = [&](int run, const Pages &p, int kind, uint32_t slot) {
+            struct Places { int64_t at[S::kHalves]; bool is[S::kHalves]; };
+            auto places_of = [&](int run, const Pages &p) {
+                Places to;
 #pragma unroll
                 for (int x = 0; x < S::kHalves; ++x) {
-                    const int32_t pg = p.pg[x];
-                    if (!is_page(pg)) continue;  // warp-uniform
                     const int32_t row = (first_of(run) + 16 * x) & ((1 << a.page_shift) - 1);
-                    const uint8_t *codes = (kind ? v_head : k_head) + ((int64_t)pg * a.page_stride + row * NS);
-                    const uint32_t to = slot + (kind ? S::kValues : 0) + x * S::kCodes;
-#pragma unroll
-                    for (int i = 0; i < S::kCodes / 512; ++i)
-                        if (span_ok(codes + i * 512, 16, kind ? a.v_codes : a.k_codes, code_bytes, 16))
-                            copy_async16(to + i * 512 + (D == 256 && i % 2 ? put_at ^ 64 : put_at), codes + i * 512);
-                    if (kind == 0 && lane / 4 == x) {
-                        const unsigned char *from = s_head + 2 * ((int64_t)pg * a.scale_stride + row);
-                        if (span_ok(from, 16, lane % 4 < 2 ? ks : vs, scale_bytes, 16)) copy_async16(slot + S::kScales + lane * 16, from);
-                    }
+                    to.is[x] = is_page(p.pg[x]);  // warp-uniform
+                    to.at[x] = (int64_t)p.pg[x] * a.page_stride + row * NS;
                 }
+                return to;
+            };
+            auto fetch_keys = [&](int run, const Pages &p, const Places &from, uint32_t slot) {
+                each<S::kHalves>([&](auto half) {
+                    constexpr int X = decltype(half)::value;
+                    if (!from.is[X]) return;
+                    each<S::kCodes / 512>([&](auto piece) {
+                        constexpr int I = decltype(piece)::value;
+                        if (span_ok(k_head + from.at[X] + I * 512, 16, a.k_codes, code_bytes, 16))
+                            copy_async16<X * S::kCodes + I * 512, I * 512>(slot + (D == 256 && I % 2 ? put_at ^ 64 : put_at), k_head + from.at[X]);
+                    });
+                    if (lane / 4 == X) {
+                        const int32_t row = (first_of(run) + 16 * X) & ((1 << a.page_shift) - 1);
+                        const unsigned char *scale = s_head + 2 * ((int64_t)p.pg[X] * a.scale_stride + row);
+                        if (span_ok(scale, 16, lane % 4 < 2 ? ks : vs, scale_bytes, 16)) copy_async16<S::kScales, 0>(slot + lane * 16, scale);
+                    }
+                });
                 copy_commit();  // (an empty group keeps the count)
             };
-            Pages pages[S::kSlots + 1];
+            auto fetch_values = [&](const Places &from, uint32_t slot) {
+                each<S::kHalves>([&](auto half) {
+                    constexpr int X = decltype(half)::value;
+                    if (!from.is[X]) return;
+                    each<S::kCodes / 512>([&](auto piece) {
+                        constexpr int I = decltype(piece)::value;
+                        if (span_ok(v_head + from.at[X] + I * 512, 16, a.v_codes, code_bytes, 16))
+                            copy_async16<S::kValues + X * S::kCodes + I * 512, I * 512>(slot + (D == 256 && I % 2 ? put_at ^ 64 : put_at),
+                                                                                        v_head + from.at[X]);
+                    });
+                });
+                copy_commit();
+            };
+            Pages pages[S::kSlots];
 #pragma unroll
-            for (int x = 0; x <= S::kSlots; ++x) pages[x] = pages_of(g_begin + x * kWarps);
+            for (int x = 0; x < S::kSlots; ++x) pages[x] = pages_of(x);
             __syncthreads();  // the table is written, the last segment's merge has left the ring
 #pragma unroll
             for (int x = 0; x < S::kSlots; ++x) {
-                fetch(g_begin + x * kWarps, pages[x], 0, ring + x * S::kSlot);
-                fetch(g_begin + x * kWarps, pages[x], 1, ring + x * S::kSlot);
+                const Places from = places_of(g_begin + x * kWarps, pages[x]);
+                fetch_keys(g_begin + x * kWarps, pages[x], from, ring + x * S::kSlot);
+                fetch_values(from, ring + x * S::kSlot);
             }
 
             // (in the order of its operands alone: a volatile load would stand in the order of
@@ -377,8 +418,10 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                 return v;
             };
             uint32_t slot = ring;
+            int n = 0, batches = 0;  // of the warp's runs: in the batch, before it
             for (int run = g_begin; run < g_end; run += kWarps) {
-                const Pages ahead = pages[S::kSlots];
+                const Pages ahead = pages_of(n + S::kSlots);
+                const Places from = places_of(run + S::kSlots * kWarps, ahead);
                 bool live[S::kHalves], any = false, both = true;  // warp-uniform
 #pragma unroll
                 for (int x = 0; x < S::kHalves; ++x) {
@@ -387,22 +430,21 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                     both &= live[x];
                 }
 #pragma unroll
-                for (int x = 0; x < S::kSlots; ++x) pages[x] = pages[x + 1];
-                pages[S::kSlots] = pages_of(run + (S::kSlots + 1) * kWarps);
+                for (int x = 0; x + 1 < S::kSlots; ++x) pages[x] = pages[x + 1];
+                pages[S::kSlots - 1] = ahead;
                 copy_wait<2 * S::kSlots - 1>();  // this run's keys, and both its scales
                 if (any) {
                     uint32_t kc[S::kHalves][2][KW];
                     float kscale[S::kHalves][2], vscale[S::kHalves][2];
-#pragma unroll
-                    for (int x = 0; x < S::kHalves; ++x)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            load_shared<KW>(slot + x * S::kCodes + k_at[k], slot + x * S::kCodes + (k_at[k] ^ 16), kc[x][k]);
-                            kscale[x][k] = a.kappa * load_shared16<T>(slot + S::kScales + 64 * x + 2 * (g + 8 * k));
-                            vscale[x][k] = load_shared16<T>(slot + S::kScales + 64 * x + 32 + 2 * (g + 8 * k));
-                        }
+                    each<2 * S::kHalves>([&](auto at) {
+                        constexpr int X = decltype(at)::value / 2, K = decltype(at)::value % 2;
+                        constexpr int kOff = X * S::kCodes + 8 * K * NS;  // (rows 8 apart lie alike)
+                        load_shared<KW, kOff>(slot + k_at, slot + (k_at ^ 16), kc[X][K]);
+                        kscale[X][K] = a.kappa * load_shared16<T, S::kScales + 64 * X + 16 * K>(slot + 2 * g);
+                        vscale[X][K] = load_shared16<T, S::kScales + 64 * X + 32 + 16 * K>(slot + 2 * g);
+                    });
                     __syncwarp();
-                    fetch(run + S::kSlots * kWarps, ahead, 0, slot);
+                    fetch_keys(run + S::kSlots * kWarps, ahead, from, slot);
                     const int32_t k0 = first_of(run);
                     // S^T = K^ Q^T
                     float st[S::kHalves][4];
@@ -439,12 +481,12 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                     sfew_weights<T>(st, vscale, m, sum, factor, o, pf);
                     copy_wait<2 * S::kSlots - 1>();  // its values
                     uint32_t vc[S::kHalves][4][VW];
-#pragma unroll
-                    for (int x = 0; x < S::kHalves; ++x)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) load_shared<VW>(slot + x * S::kCodes + v_at[k], 0, vc[x][k]);
+                    each<4 * S::kHalves>([&](auto at) {
+                        constexpr int X = decltype(at)::value / 4, K = decltype(at)::value % 4;
+                        load_shared<VW, S::kValues + X * S::kCodes + 8 * (K / 2) * NS>(slot + v_at[K % 2], 0, vc[X][K]);
+                    });
                     __syncwarp();
-                    fetch(run + S::kSlots * kWarps, ahead, 1, slot);
+                    fetch_values(from, slot);
                     // O^T += V^^T P^T
 #pragma unroll
                     for (int i = 0; i < VW; ++i)
@@ -467,12 +509,18 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                             }
                         }
                 } else {
-                    fetch(run + S::kSlots * kWarps, ahead, 0, slot);
+                    fetch_keys(run + S::kSlots * kWarps, ahead, from, slot);
                     copy_wait<2 * S::kSlots - 1>();
-                    fetch(run + S::kSlots * kWarps, ahead, 1, slot);
+                    fetch_values(from, slot);
                 }
                 static_assert(S::kSlots == 2, "two slots in turn");
                 slot = slot == ring ? ring + S::kSlot : ring;
+                if (++n == 32) {
+                    n = 0;
+                    ++batches;
+                    batch = batch_next;
+                    batch_next = batch_of(batches + 1);
+                }
             }
             copy_wait<0>();
             // to weights without the factors

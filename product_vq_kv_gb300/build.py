@@ -23,7 +23,7 @@ CHECKED_LIB_PATH = os.path.join(LIB_DIR, "libvqenc_checked.so")
 PTXAS_LOG = os.path.join(LIB_DIR, "ptxas.txt")
 SOURCES = [os.path.join(CSRC, name) for name in ("vq_encode.cu", "vq_attn.cu", "vq_scalar.cu",
                                            "vq_append.cu", "vq_paged.cu", "vq_pfew.cu", "vq_pchunk.cu",
-                                           "vq_share.cu", "vq_sappend.cu", "vq_scache.cu", "vq_sfew.cu")]
+                                           "vq_share.cu", "vq_sappend.cu", "vq_scache.cu", "vq_sfew.cu", "vq_schunk.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, name) for name in (
     "vq_kernels.cuh", "vq_filter.cuh", "vq_tc.cuh", "vq_decode.cuh", "vq_attn.cuh", "vq_host.h", "vq_scalar.cuh", "vq_status.cuh", "vq_check.cuh", "vq_umma.cuh",
     "vq_append.cuh", "vq_pages.cuh", "vq_pagescan.cuh", "vq_paged_plan.h", "vq_share.cuh", "vq_sappend.cuh", "vq_nearest.cuh", "vq_sattn.cuh", "vq_sfew.cuh", "vq_pattn.cuh", "vq_pfew.cuh", "vq_pchunk.cuh", "vq_paged_host.h",

@@ -686,7 +686,7 @@ vq_status vq_kernel_status(uint32_t *bits, int32_t clear)
         vqh_status_paged(bits, c) != cudaSuccess || vqh_status_pfew(bits, c) != cudaSuccess ||
         vqh_status_pchunk(bits, c) != cudaSuccess || vqh_status_share(bits, c) != cudaSuccess ||
         vqh_status_sappend(bits, c) != cudaSuccess || vqh_status_scache(bits, c) != cudaSuccess ||
-        vqh_status_sfew(bits, c) != cudaSuccess)
+        vqh_status_sfew(bits, c) != cudaSuccess || vqh_status_schunk(bits, c) != cudaSuccess)
         return vqh_failed();
     return VQ_OK;
 }

@@ -1,7 +1,7 @@
 // vq_pchunk.cuh -- paged attention of chunks of new tokens (prefill beside a
 // cache, long verification runs): tiles of 128 rows (tokens x query heads of one
 // KV head) on the 5th-generation tensor cores, 16-bit types, head sizes 64, 128
-// and 256, sub-vectors of 4 or 8.
+// and 256, sub-vectors of 4 or 8, or (SUB = 2) 4-bit scalar codes with a scale a row.
 //
 // Per block of kKeys cached tokens, with the accumulators in tensor memory:
 //   S (128 x kKeys) = Q K^^T     tcgen05.mma, both operands in shared memory
@@ -43,6 +43,13 @@
 // sets the block's abort word and kStatusWaitGaveUp, the others see it and all
 // leave; the issuer first waits (bounded) for its products in flight, the tensor
 // memory is freed, and the rows that the block has not written become NaN.
+//
+// 4-bit scalar codes: a byte selects a pair of centroids from an image of 256 pairs, 32 copies
+// each (a lane its own: no conflict whatever the codes), and the pair is multiplied by the
+// row's scale, one rounding of K^ and V^ to the type, which the products need.  The rebuild
+// moves as many bytes of shared memory as that of sub-vectors, in words of 4 bytes where
+// those come in 8 or 16, so it issues four times as much: 512 lookups, products of two and
+// address steps a warp and kind of 128 keys.
 #pragma once
 
 #include "vq_pfew.cuh"
@@ -212,6 +219,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     constexpr int kMyCodes = NS / kSplit;        // code bytes of a thread's token
     constexpr int kMyVec = kMyCodes < 16 ? kMyCodes : 16;
     constexpr int kCodeWords = kMyCodes < 4 ? 1 : kMyCodes / 4;
+    constexpr bool kScalar = SUB == 2;
+    // Sets of registers for codes: the next block's are loaded before this one's are used up.
+    // Scalar codes of both kinds would take 64: there one set, each kind's loaded anew as soon
+    // as it is rebuilt, while the other kind is.
+    constexpr int kSets = kScalar && kKinds == 2 ? 1 : 2;
     constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr float kShift = weight_shift<T>();
     extern __shared__ __align__(128) unsigned char chunk_mem[];
@@ -581,7 +593,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         const int in_half = me - vals * kHalf;
         const int tk = in_half % kKeys, part = in_half / kKeys;  // token of the block, which part of its row
         const uint32_t copy = (uint32_t)(lane % (64 / SUB)) * (2 * SUB);
-        const int64_t cb_elems = (int64_t)a.hkv * a.nc * SUB;
+        [[maybe_unused]] const int64_t cb_elems = (int64_t)a.hkv * a.nc * SUB;
         const int64_t code_bytes = (a.num_pages - 1) * a.page_stride + (((int64_t)a.hkv * NS) << a.page_shift);
         uint32_t base_n = 0;  // stages of the segments so far
         uint32_t block = 0;   // key blocks of them
@@ -595,8 +607,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
         };
         while (go && next_seg(seg_n, s)) {
             const int h = s.h;
-            if (h != built) {
-                // the images of this head: only these warps read them
+            if (h != built && !(kScalar && built >= 0)) {
+                // the images of this head (of all heads, of scalar codes): only these warps read them
                 if (!(go = meet())) break;
 #pragma unroll 1
                 for (int kd = 0; kd < kKinds; ++kd) {
@@ -605,7 +617,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 #pragma unroll 1
                     for (int c = in_half; c < 256; c += kHalf) {
                         uint32_t wd[SUB / 2];
-                        book_row<T, SUB>(all + (int64_t)h * a.nc * SUB, c, a.nc, all, cb_elems, wd);
+                        if constexpr (kScalar) wd[0] = scalar_pair<T>(v ? a.v_cent : a.k_cent, c, a.nc);
+                        else book_row<T, SUB>(all + (int64_t)h * a.nc * SUB, c, a.nc, all, cb_elems, wd);
                         image_line<SUB>(v ? v_image : k_image, c, wd);
                     }
                 }
@@ -623,25 +636,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return paged_entry(a, s.r, (int32_t)t);
             };
             const int64_t head_off = ((int64_t)h << a.page_shift) * NS + part * kMyCodes;
-            auto load = [&](int j, int32_t &pg, uint32_t (&codes)[kKinds][kCodeWords]) {
+            // (scales: a pair of the row's scale, of scalar codes)
+            auto load_kind = [&](int j, int32_t &pg, int kd, uint32_t (&codes)[kCodeWords], uint32_t &scale) {
                 if (pg < 0 || pg >= a.num_pages) {
                     pg = -1;
                     return;
                 }
                 const int32_t off = (key0 + j * kKeys + tk) & ((1 << a.page_shift) - 1);
                 const int64_t at = head_off + (int64_t)pg * a.page_stride + off * NS;
-#pragma unroll
-                for (int kd = 0; kd < kKinds; ++kd) {
-                    const uint8_t *all = (kHalves ? vals : kd) ? a.v_codes : a.k_codes;
-                    if (!span_ok(all + at, kMyCodes, all, code_bytes, kMyVec)) continue;
+                const bool v = kHalves ? vals : kd;
+                const uint8_t *all = v ? a.v_codes : a.k_codes;
+                if (span_ok(all + at, kMyCodes, all, code_bytes, kMyVec)) {
 #pragma unroll
                     for (int i = 0; i < kMyCodes / kMyVec; ++i) {
-                        uint32_t v[(kMyVec + 3) / 4];
-                        load_codes<kMyVec>(all + at + i * kMyVec, v);
+                        uint32_t w[(kMyVec + 3) / 4];
+                        load_codes<kMyVec>(all + at + i * kMyVec, w);
 #pragma unroll
-                        for (int k = 0; k < (kMyVec + 3) / 4; ++k) codes[kd][i * (kMyVec / 4) + k] = v[k];
+                        for (int k = 0; k < (kMyVec + 3) / 4; ++k) codes[i * (kMyVec / 4) + k] = w[k];
                     }
                 }
+                if constexpr (kScalar) {
+                    const uint16_t *scales = static_cast<const uint16_t *>(v ? a.v_scales : a.k_scales);
+                    const uint16_t *from = scales + (int64_t)pg * a.scale_stride + ((int64_t)h << a.page_shift) + off;
+                    scale = 0;
+                    if (VQ_SPAN(from, 1, scales, (a.num_pages - 1) * a.scale_stride + ((int64_t)a.hkv << a.page_shift)))
+                        scale = __ldg(from) * 0x10001u;
+                }
+            };
+            auto load = [&](int j, int32_t &pg, uint32_t (&codes)[kKinds][kCodeWords], uint32_t (&scale)[kKinds]) {
+#pragma unroll
+                for (int kd = 0; kd < kKinds; ++kd) load_kind(j, pg, kd, codes[kd], scale[kd]);
             };
             // a block's place in the ring: with two tiles the stages go K0 V0 K1 V1 ..,
             // with one K0 K1 V0 K2 V1 .. (there the scores of a block are issued before
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return base_n + (j > 0 ? 2 * j - 1 : 0);
             };
             // rebuild this thread's part of its token of block j
-            auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords]) -> bool {
+            auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords], uint32_t scale) -> bool {
                 const unsigned char *base = (v ? v_image : k_image) + copy;
                 const uint32_t n = stage_of(j, v), st = n % kChunkStages, round = n / kChunkStages;
                 // (the stages are released in ring order, so that the phase before the one
@@ -666,8 +690,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     if (lane == 0 && part == 0) valid[block & 7][tk / 32] = have;
                 }
                 unsigned char *dst = ring + st * S::kStageBytes + (part * (kPieces / kSplit)) * (16 * kKeys) + tk * 16;
-                // eight pieces at a time, so that their loads overlap
-                constexpr int kMyPieces = kPieces / kSplit, kBatch = kMyPieces < 8 ? kMyPieces : 8;
+                // eight pieces at a time (four of scalar codes), so that their loads overlap
+                constexpr int kMost = kScalar ? 4 : 8, kMyPieces = kPieces / kSplit, kBatch = kMyPieces < kMost ? kMyPieces : kMost;
 #pragma unroll
                 for (int c0 = 0; c0 < kMyPieces; c0 += kBatch) {
                     uint32_t w[kBatch][4];
@@ -675,6 +699,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     for (int c = 0; c < kBatch; ++c) {
                         if constexpr (SUB == 8) {
                             image_row<8>(base, code_at(codes, c0 + c), w[c]);
+                        } else if constexpr (kScalar) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t pair[1];
+                                image_row<2>(base, code_at(codes, 4 * (c0 + c) + i), pair);
+                                w[c][i] = mul2<T>(pair[0], scale);
+                            }
                         } else {
                             uint32_t lo[2], hi[2];
                             image_row<4>(base, code_at(codes, 2 * (c0 + c)), lo);
@@ -700,24 +731,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return true;
             };
             // codes one block ahead, page entries two
-            uint32_t codes[2][kKinds][kCodeWords] = {};
+            uint32_t codes[kSets][kKinds][kCodeWords] = {}, scale[kSets][kKinds] = {};
             int32_t pg[3];
             pg[0] = page_of(0);
             pg[1] = page_of(1);
-            load(0, pg[0], codes[0]);
+            load(0, pg[0], codes[0], scale[0]);
             for (int j = 0; j < nb; ++j, ++block) {
-                load(j + 1, pg[1], codes[1]);
+                if constexpr (kSets == 2) load(j + 1, pg[1], codes[1], scale[1]);
                 pg[2] = page_of(j + 2);
 #pragma unroll
-                for (int kd = 0; kd < kKinds; ++kd)
-                    if (go) go = fill(j, kHalves ? vals : kd, pg[0] >= 0, codes[0][kd]);
+                for (int kd = 0; kd < kKinds; ++kd) {
+                    if (go) go = fill(j, kHalves ? vals : kd, pg[0] >= 0, codes[0][kd], scale[0][kd]);
+                    if constexpr (kSets == 1) load_kind(j + 1, pg[1], kd, codes[0][kd], scale[0][kd]);
+                }
                 if (!go) break;
                 pg[0] = pg[1];
                 pg[1] = pg[2];
+                if constexpr (kSets == 2) {
 #pragma unroll
-                for (int kd = 0; kd < kKinds; ++kd)
+                    for (int kd = 0; kd < kKinds; ++kd) {
 #pragma unroll
-                    for (int i = 0; i < kCodeWords; ++i) codes[0][kd][i] = codes[1][kd][i];
+                        for (int i = 0; i < kCodeWords; ++i) codes[0][kd][i] = codes[1][kd][i];
+                        scale[0][kd] = scale[1][kd];
+                    }
+                }
             }
             base_n += 2 * nb;
         }

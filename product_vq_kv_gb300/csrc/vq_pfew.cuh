@@ -178,10 +178,12 @@ __device__ __forceinline__ void image_row(const unsigned char *base, uint32_t co
         w[1] = v.y;
         w[2] = v.z;
         w[3] = v.w;
-    } else {
+    } else if constexpr (SUB == 4) {
         const uint2 v = *reinterpret_cast<const uint2 *>(at);
         w[0] = v.x;
         w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(at);
     }
 }
 
@@ -199,6 +201,30 @@ __device__ __forceinline__ void book_row(const T *__restrict__ cb, int c, int nc
     }
 }
 
+// The pair of centroids that byte b of two 4-bit codes selects, the low half's first, in the
+// rows' type (0 for a code past them).
+template <typename T>
+__device__ __forceinline__ uint32_t scalar_pair(const float *__restrict__ cent, int b, int nc)
+{
+    float v[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int code = b >> (4 * i) & 15;
+        if (code < nc && VQ_SPAN(cent + code, 1, cent, nc)) v[i] = __ldg(cent + code);
+    }
+    return pack2<T>(v[0], v[1]);
+}
+
+// Two products in the 16-bit type.
+template <typename T>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Line c of a codebook's image: its row 64 / SUB times.  The copies are
 // written in an order that starts at c, so that the lanes of a wavefront meet in
 // no bank.  The caller synchronises.
@@ -211,7 +237,8 @@ __device__ __forceinline__ void image_line(unsigned char *image, int c, const ui
         unsigned char *dst = image + c * 128 + ((c + k) % kCopies) * (2 * SUB);
         if (!dyn_smem_ok(dst, 2 * SUB, 2 * SUB)) continue;
         if constexpr (SUB == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else if constexpr (SUB == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(dst) = w[0];
     }
 }
 

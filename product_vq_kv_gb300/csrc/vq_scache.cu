@@ -38,7 +38,7 @@ bool tensor_layout(const vqk::PagedArgs &a)
 
 TensorKernels tensor_kernels(int32_t dim)
 {
-    const int32_t items = 1 << 20;
+    const int32_t items = dim == 256 ? 2 : 3;
     return TensorKernels{vqh_few_rows(), 1, vqh_chunk_tiles(dim), items, vqh_paged_sfew,
                          vqh_paged_schunk};
 }

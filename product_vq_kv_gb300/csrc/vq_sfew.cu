@@ -39,5 +39,3 @@ vq_status vqh_paged_sfew(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cu
 {
     return dtype == VQ_F16 ? launch_dim<__half>(a, blocks, st) : launch_dim<__nv_bfloat16>(a, blocks, st);
 }
-
-vq_status vqh_paged_schunk(const vqk::PagedArgs &, vq_dtype, int, cudaStream_t) { return VQ_ERR_UNSUPPORTED; }

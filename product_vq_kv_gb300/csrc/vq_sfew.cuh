@@ -215,17 +215,12 @@ __device__ __forceinline__ void each(F f)
 template <typename T, int THREADS>
 __device__ __forceinline__ void scalar_table(const PagedArgs &a, unsigned char *table)
 {
-    auto value = [&](const float *cent, int code) -> uint32_t {
-        float v = 0.f;
-        if (code < a.nc && VQ_SPAN(cent + code, 1, cent, a.nc)) v = __ldg(cent + code);
-        return pack2<T>(v, 0.f) & 0xffffu;
-    };
     // 16 pieces of 16 bytes a line, a thread a piece of its own of every (THREADS / 16)-th
     const int piece = threadIdx.x % 16;
     const float *cent = piece < 8 ? a.k_cent : a.v_cent;
 #pragma unroll 4
     for (int b = threadIdx.x / 16; b < 256; b += THREADS / 16) {
-        const uint32_t pair = value(cent, b & 15) | value(cent, b >> 4) << 16;
+        const uint32_t pair = scalar_pair<T>(cent, b, a.nc);
         unsigned char *dst = table + b * 256 + piece * 16;
         if (dyn_smem_ok(dst, 16, 16)) *reinterpret_cast<uint4 *>(dst) = make_uint4(pair, pair, pair, pair);
     }

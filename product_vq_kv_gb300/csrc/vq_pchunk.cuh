@@ -75,6 +75,11 @@ struct ChunkShape {
     static constexpr int kStageBytes = kKeys * D * 2;
     static constexpr int kQBytes = kQTmem ? 0 : 128 * D * 2;  // a tile
     static constexpr size_t kSmem = (size_t)kTiles * kQBytes + kStages * kStageBytes + 65536;
+    // Scalar codes: their table at a fixed shared address, behind the static memory (and the
+    // system's 1024 bytes), then Q and the ring.  The array starts behind kStatic at least.
+    static constexpr int kTable = 3072;
+    static constexpr int kStatic = 1024 + (int)sizeof(PagedWalk<64>);
+    static constexpr size_t kScalarSmem = kTable - kStatic + kSmem;
 };
 
 // Instruction descriptor: kind::f16, fp32 accumulator, 16-bit operands of one
@@ -233,9 +238,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     __shared__ uint32_t valid[8][4];  // per key block (mod 8): which tokens are in a page
     __shared__ uint32_t tmem_slot;
     __shared__ volatile uint32_t abort_word;
-    unsigned char *q_mem = chunk_mem;
-    unsigned char *ring = chunk_mem + (size_t)kTiles * S::kQBytes;
-    unsigned char *k_image = ring + kChunkStages * S::kStageBytes, *v_image = k_image + 32768;
+    // of scalar codes the table comes first, at its address
+    [[maybe_unused]] unsigned char *lines = chunk_mem + (S::kTable - (int)smem_addr(chunk_mem));
+    static_assert(1024 + sizeof w + sizeof full + sizeof empty + 7 * sizeof q_full + sizeof drain + sizeof segs + sizeof valid + 8 + 256 <= S::kTable,
+                  "static memory below the table");
+    unsigned char *q_mem = kScalar ? lines + 65536 : chunk_mem;
+    unsigned char *ring = q_mem + (size_t)kTiles * S::kQBytes;
+    unsigned char *k_image = ring + kChunkStages * S::kStageBytes, *v_image = k_image + 32768;  // of sub-vectors
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float kNone = __int_as_float(0xff800000);
@@ -613,18 +622,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 #pragma unroll 1
                 for (int kd = 0; kd < kKinds; ++kd) {
                     const bool v = kHalves ? vals : kd;
-                    const T *all = static_cast<const T *>(v ? a.vcb : a.kcb);
+                    [[maybe_unused]] const T *all = static_cast<const T *>(v ? a.vcb : a.kcb);
+                    if constexpr (kScalar) {
+                        scalar_lines<T>(v ? a.v_cent : a.k_cent, a.nc, v, lines, in_half, kHalf);
+                    } else {
 #pragma unroll 1
-                    for (int c = in_half; c < 256; c += kHalf) {
-                        uint32_t wd[SUB / 2];
-                        if constexpr (kScalar) wd[0] = scalar_pair<T>(v ? a.v_cent : a.k_cent, c, a.nc);
-                        else book_row<T, SUB>(all + (int64_t)h * a.nc * SUB, c, a.nc, all, cb_elems, wd);
-                        image_line<SUB>(v ? v_image : k_image, c, wd);
+                        for (int c = in_half; c < 256; c += kHalf) {
+                            uint32_t wd[SUB / 2];
+                            book_row<T, SUB>(all + (int64_t)h * a.nc * SUB, c, a.nc, all, cb_elems, wd);
+                            image_line<SUB>(v ? v_image : k_image, c, wd);
+                        }
                     }
                 }
                 if (!(go = meet())) break;
                 built = h;
             }
+            // (no lookup of scalar codes before this point, where the table is written)
+            uint32_t lane4 = lane * 4;
+            asm volatile("" : "+r"(lane4)::"memory");
             const int32_t key0 = s.key0;
             const int nb = s.nb;
             const int64_t none_lo = a.window == 0 ? -1 : (int64_t)s.pos0 - a.window;  // no row sees at or below
@@ -677,7 +692,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             };
             // rebuild this thread's part of its token of block j
             auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords], uint32_t scale) -> bool {
-                const unsigned char *base = (v ? v_image : k_image) + copy;
+                if (!live) scale = 0;  // (no token: a row of zeros, whatever its scale would be)
+                [[maybe_unused]] const unsigned char *base = (v ? v_image : k_image) + copy;
                 const uint32_t n = stage_of(j, v), st = n % kChunkStages, round = n / kChunkStages;
                 // (the stages are released in ring order, so that the phase before the one
                 // waited for is over)
@@ -701,11 +717,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                             image_row<8>(base, code_at(codes, c0 + c), w[c]);
                         } else if constexpr (kScalar) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t pair[1];
-                                image_row<2>(base, code_at(codes, 4 * (c0 + c) + i), pair);
-                                w[c][i] = mul2<T>(pair[0], scale);
-                            }
+                            for (int i = 0; i < 4; ++i) w[c][i] = mul2<T>(scalar_lookup<S::kTable>(codes[c0 + c], i, lane4 + 128 * v), scale);
                         } else {
                             uint32_t lo[2], hi[2];
                             image_row<4>(base, code_at(codes, 2 * (c0 + c)), lo);
@@ -716,7 +728,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                             w[c][3] = hi[1];
                         }
                     }
-                    if (!live) {  // no token: finite whatever its codes would be
+                    if (!kScalar && !live) {  // no token: finite whatever its codes would be
 #pragma unroll
                         for (int c = 0; c < kBatch; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0;
                     }

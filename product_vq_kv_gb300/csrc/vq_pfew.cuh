@@ -178,12 +178,10 @@ __device__ __forceinline__ void image_row(const unsigned char *base, uint32_t co
         w[1] = v.y;
         w[2] = v.z;
         w[3] = v.w;
-    } else if constexpr (SUB == 4) {
+    } else {
         const uint2 v = *reinterpret_cast<const uint2 *>(at);
         w[0] = v.x;
         w[1] = v.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(at);
     }
 }
 
@@ -215,6 +213,32 @@ __device__ __forceinline__ uint32_t scalar_pair(const float *__restrict__ cent, 
     return pack2<T>(v[0], v[1]);
 }
 
+// The copies of one kind (0 keys, 1 values) in a table of scalar pairs: line b of 256 bytes holds
+// the keys' pair of byte b 32 times, a copy a lane and bank, then the values'.  A word's byte,
+// moved up by 8 bits, beside 4 lane is a lookup's place.  `rank` of `threads` threads call; the
+// caller synchronises.
+template <typename T>
+__device__ __forceinline__ void scalar_lines(const float *__restrict__ cent, int nc, int kind, unsigned char *table, int rank, int threads)
+{
+#pragma unroll 4
+    for (int i = rank; i < 256 * 8; i += threads) {  // 16 bytes at a time
+        const uint32_t pair = scalar_pair<T>(cent, i >> 3, nc);
+        unsigned char *dst = table + (i >> 3) * 256 + kind * 128 + (i & 7) * 16;
+        if (dyn_smem_ok(dst, 16, 16)) *reinterpret_cast<uint4 *>(dst) = make_uint4(pair, pair, pair, pair);
+    }
+}
+
+// The pair of byte i of `word` from the table at shared address TABLE; `copy`: 4 lane, and 128
+// for the values.  In the order of its operands alone (a volatile load would stand in the order
+// of the matrix instructions, a plain one in that of the stores).
+template <int TABLE>
+__device__ __forceinline__ uint32_t scalar_lookup(uint32_t word, int i, uint32_t copy)
+{
+    uint32_t v;
+    asm("ld.shared.b32 %0, [%1 + %2];" : "=r"(v) : "r"(__byte_perm(word, copy, 0x5504 | (i << 4))), "n"(TABLE));
+    return v;
+}
+
 // Two products in the 16-bit type.
 template <typename T>
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
@@ -237,8 +261,7 @@ __device__ __forceinline__ void image_line(unsigned char *image, int c, const ui
         unsigned char *dst = image + c * 128 + ((c + k) % kCopies) * (2 * SUB);
         if (!dyn_smem_ok(dst, 2 * SUB, 2 * SUB)) continue;
         if constexpr (SUB == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        else if constexpr (SUB == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t *>(dst) = w[0];
+        else *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     }
 }
 

@@ -15,9 +15,9 @@
 // close, and the kernel is laid out to issue little:
 //   * A table of 256 lines, one per byte, holds the pair (c[low half], c[high half]) as one
 //     32-bit word 32 times, a copy for each lane in its own bank: no lookup conflicts.  A line
-//     is 256 bytes, the keys' copies then the values', and the table lies at address 2^16 of
-//     shared memory, so that one byte permute of the code word and a lane's constant is the
-//     whole address: 2^16 | byte << 8 | 4 lane.
+//     is 256 bytes, the keys' copies then the values', and the table lies at a fixed address of
+//     shared memory, so that one byte permute of the code word and a lane's constant (byte << 8 |
+//     4 lane) is the whole address but for the load's offset.
 //   * Keys: a byte's two codes are neighbouring columns of a key, one operand register.
 //     The scale multiplies the score, in fp32.
 //   * Values: an operand register takes one column of two tokens.  The nibbles of two
@@ -210,22 +210,6 @@ __device__ __forceinline__ void each(F f)
     }
 }
 
-// The table of both codebooks: line b of 256 bytes holds the keys' pair of byte b 32 times,
-// then the values'.  The caller synchronises.
-template <typename T, int THREADS>
-__device__ __forceinline__ void scalar_table(const PagedArgs &a, unsigned char *table)
-{
-    // 16 pieces of 16 bytes a line, a thread a piece of its own of every (THREADS / 16)-th
-    const int piece = threadIdx.x % 16;
-    const float *cent = piece < 8 ? a.k_cent : a.v_cent;
-#pragma unroll 4
-    for (int b = threadIdx.x / 16; b < 256; b += THREADS / 16) {
-        const uint32_t pair = scalar_pair<T>(cent, b, a.nc);
-        unsigned char *dst = table + b * 256 + piece * 16;
-        if (dyn_smem_ok(dst, 16, 16)) *reinterpret_cast<uint4 *>(dst) = make_uint4(pair, pair, pair, pair);
-    }
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
     paged_attn_sfew(const __grid_constant__ PagedArgs a)
@@ -247,7 +231,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const float kNone = __int_as_float(0xff800000);
-    const uint32_t copy = S::kTable | lane * 4;  // this lane's copies in the table's line 0
+    const uint32_t copy[2] = {(uint32_t)lane * 4, (uint32_t)lane * 4 + 128};  // this lane's copies in a line
     const T *__restrict__ q = static_cast<const T *>(a.q);
     const unsigned char *ks = static_cast<const unsigned char *>(a.k_scales), *vs = static_cast<const unsigned char *>(a.v_scales);
     const bool q_vec = (uintptr_t)a.q % 8 == 0 && a.q_stride % 4 == 0;
@@ -268,7 +252,8 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
         PagedCursor cur;
         cur.init(w, (int32_t)blockIdx.x);
         PagedSegment s;
-        scalar_table<T, kThreads>(a, lines);
+        scalar_lines<T>(a.k_cent, a.nc, 0, lines, tid, kThreads);
+        scalar_lines<T>(a.v_cent, a.nc, 1, lines, tid, kThreads);
         while (cur.next(a, w, l, s, note)) {
             const int h = s.hx / a.gch, g0 = s.hx % a.gch * a.gc;
             const int gc = a.group - g0 < a.gc ? a.group - g0 : a.gc;
@@ -403,15 +388,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                 fetch_values(from, ring + x * S::kSlot);
             }
 
-            // (in the order of its operands alone: a volatile load would stand in the order of
-            // the matrix instructions)
-            auto table = [&](uint32_t word, int i, int kind) -> uint32_t {
-                uint32_t v;
-                const uint32_t at = __byte_perm(word, copy, 0x7604 | (i << 4));
-                if (kind) asm("ld.shared.b32 %0, [%1 + 128];" : "=r"(v) : "r"(at));
-                else asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
-                return v;
-            };
+            auto table = [&](uint32_t word, int i, int kind) { return scalar_lookup<S::kTable>(word, i, copy[kind]); };
             uint32_t slot = ring;
             int n = 0, batches = 0;  // of the warp's runs: in the batch, before it
             for (int run = g_begin; run < g_end; run += kWarps) {

@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return paged_entry(a, s.r, (int32_t)t);
             };
             const int64_t head_off = ((int64_t)h << a.page_shift) * NS + part * kMyCodes;
-            // (scales: a pair of the row's scale, of scalar codes)
+            // (scale: the row's, of scalar codes)
             auto load_kind = [&](int j, int32_t &pg, int kd, uint32_t (&codes)[kCodeWords], uint32_t &scale) {
                 if (pg < 0 || pg >= a.num_pages) {
                     pg = -1;
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     const uint16_t *from = scales + (int64_t)pg * a.scale_stride + ((int64_t)h << a.page_shift) + off;
                     scale = 0;
                     if (VQ_SPAN(from, 1, scales, (a.num_pages - 1) * a.scale_stride + ((int64_t)a.hkv << a.page_shift)))
-                        scale = __ldg(from) * 0x10001u;
+                        scale = __ldg(from);  // (made a pair where it is used: here that would wait for the load)
                 }
             };
             auto load = [&](int j, int32_t &pg, uint32_t (&codes)[kKinds][kCodeWords], uint32_t (&scale)[kKinds]) {
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
             };
             // rebuild this thread's part of its token of block j
             auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords], uint32_t scale) -> bool {
-                if (!live) scale = 0;  // (no token: a row of zeros, whatever its scale would be)
+                scale = live ? scale * 0x10001u : 0;  // a pair of it (no token: a row of zeros, whatever its scale would be)
                 [[maybe_unused]] const unsigned char *base = (v ? v_image : k_image) + copy;
                 const uint32_t n = stage_of(j, v), st = n % kChunkStages, round = n / kChunkStages;
                 // (the stages are released in ring order, so that the phase before the one

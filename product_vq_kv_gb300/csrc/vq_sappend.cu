@@ -20,7 +20,8 @@ vq_status launch(const vqk::ScalarAppendArgs &a, cudaStream_t st)
 {
     constexpr int kRows = vqk::kSAppendThreads / LANES;  // of a block
     const int64_t want = (a.tokens * a.heads + kRows - 1) / kRows;
-    const int64_t most = 4 * (int64_t)(vqh_device_sms() > 0 ? vqh_device_sms() : 152);
+    // three blocks an SM, keys and values: a block's set-up is worth several rows a warp
+    const int64_t most = 3 * (int64_t)(vqh_device_sms() > 0 ? vqh_device_sms() : 152) / 2;
     vqk::scalar_append<T, LANES, CUTS><<<dim3((unsigned)(want < most ? want : most), 2), vqk::kSAppendThreads, 0, st>>>(a);
     return vqh_launched(st, vqh_status_sappend);
 }
@@ -102,8 +103,10 @@ vq_status vq_paged_scalar_append(const void *k, const void *v, int64_t k_stride,
     a.nc = n_centroids;
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
     a.norm = (float)(1.0 / std::sqrt((double)head_dim));
+    a.over_dim = (float)(1.0 / head_dim);
+    a.exact = (head_dim & (head_dim - 1)) == 0;
     // rows of whole runs, each 16-byte aligned
-    const bool runs = head_dim >= vqk::kRowRun && (head_dim & (head_dim - 1)) == 0;
+    const bool runs = head_dim >= vqk::kRowRun && a.exact;
     for (int kv = 0; kv < 2; ++kv)
         a.vec[kv] = runs && (uintptr_t)a.x[kv] % 16 == 0 && a.stride[kv] * (int64_t)es % 16 == 0;
     a.vec_codes = head_dim % vqk::kRowRun == 0 && (uintptr_t)k_codes % 8 == 0 && (uintptr_t)v_codes % 8 == 0 &&

@@ -16,7 +16,7 @@
 // A lane holds kRowRun = 16 consecutive elements, two 16-byte loads of a 16-bit type, so
 // that of the rotation's and the sum's log2 dim steps four stay in registers; a warp takes
 // 32 / lanes rows side by side.  The cut points of the centroids (vq_nearest.cuh) decide a
-// code by four comparisons.
+// code: two comparisons find a quarter of them, whose three one 16-byte load brings.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,6 +44,8 @@ struct ScalarAppendArgs {
     int64_t tokens, num_pages, page_stride, scale_stride;
     int32_t heads, dim, nc, page_shift;
     float norm;                // 1 / sqrt(dim)
+    float over_dim;            // 1 / dim
+    bool exact;                // dim is a power of two: a product with 1 / dim is the quotient
     bool vec[2];               // rows can be read in 16-byte pieces
     bool vec_codes;            // codes can be written in 8-byte pieces
 };
@@ -75,21 +77,14 @@ __device__ __forceinline__ T scale_cap(const float *__restrict__ centroids, int 
 // LANES lanes to a row (LANES x 16 >= dim); CUTS: 16 centroids, through their cut points.
 // blockIdx.y: keys or values.
 template <typename T, int LANES, bool CUTS>
-__global__ void __launch_bounds__(kSAppendThreads) scalar_append(const __grid_constant__ ScalarAppendArgs a)
+__global__ void __launch_bounds__(kSAppendThreads, 3) scalar_append(const __grid_constant__ ScalarAppendArgs a)
 {
     constexpr int kRows = 32 / LANES;  // of a warp
     constexpr int kE = kRowRun;
     __shared__ float sm[4 * 16];
+    __shared__ __align__(16) float quarters[16];
     const int kv = blockIdx.y;
     const int lane = threadIdx.x & 31, sub = lane / LANES, l = lane % LANES;
-    vqs::CutCb<16> cut;
-    if constexpr (CUTS) {
-        vqs::build_cut_cb<16>(a.centroids[kv], sm, cut);
-    } else {
-        if ((int)threadIdx.x < a.nc) sm[16 + threadIdx.x] = __ldg(a.centroids[kv] + threadIdx.x);
-        __syncthreads();
-    }
-    const T cap = scale_cap<T>(a.centroids[kv], a.nc);
     const T *__restrict__ x = static_cast<const T *>(a.x[kv]);
     const int64_t x_elems = (a.tokens - 1) * a.stride[kv] + (int64_t)a.heads * a.dim;
     const bool rotate = kv == 0 && a.signs;
@@ -99,22 +94,64 @@ __global__ void __launch_bounds__(kSAppendThreads) scalar_append(const __grid_co
 #pragma unroll
     for (int j = 0; j < kE; ++j)
         sg[j] = rotate && e0 + j < a.dim && VQ_SPAN(a.signs + e0 + j, 1, a.signs, a.dim) ? __ldg(a.signs + e0 + j) : 0.f;
-    for (int64_t base = ((int64_t)blockIdx.x * (kSAppendThreads / 32) + (threadIdx.x >> 5)) * kRows; base < rows; base += stride) {
-        const int64_t row = base + sub;
-        const int64_t t = row / a.heads;
-        const int h = (int)(row - t * a.heads);
-        int64_t slot = -1;
-        if (row < rows && VQ_SPAN(a.slots + t, 1, a.slots, a.tokens)) slot = __ldg(a.slots + t);
-        const bool live = slot >= 0 && (slot >> a.page_shift) < a.num_pages;
-        const T *src = x + t * a.stride[kv] + (int64_t)h * a.dim + e0;
-        float v[kE];
-        if (live && a.vec[kv] && VQ_VSPAN(src, kE, x, x_elems, 16)) {  // (then LANES x 16 = dim)
-            vqs::load_run<T, kE>(src, v);
+    // a warp's rows of the next pass are loaded before this pass's are worked on
+    constexpr int kLoads = kE * (int)sizeof(T) / 16;
+    const int64_t first = ((int64_t)blockIdx.x * (kSAppendThreads / 32) + (threadIdx.x >> 5)) * kRows;
+    auto place = [&](int64_t row, int64_t *t, int *h) {
+        if (rows <= 0x7fffffff) {  // (32 bits divide in a third of the steps)
+            const uint32_t q = (uint32_t)row / (uint32_t)a.heads;
+            *t = q;
+            *h = (int)((uint32_t)row - q * (uint32_t)a.heads);
         } else {
+            *t = row / a.heads;
+            *h = (int)(row - *t * a.heads);
+        }
+    };
+    uint4 raw[kLoads] = {};
+    int64_t t_next = 0, slot_next = -1;
+    int h_next = 0;
+    auto load = [&](int64_t base) {
+        const int64_t row = base + sub;
+        slot_next = -1;
+        if (row >= rows) return;
+        place(row, &t_next, &h_next);
+        if (VQ_SPAN(a.slots + t_next, 1, a.slots, a.tokens)) slot_next = __ldg(a.slots + t_next);
+        const T *src = x + t_next * a.stride[kv] + (int64_t)h_next * a.dim + e0;
+        if (a.vec[kv] && VQ_VSPAN(src, kE, x, x_elems, 16)) {  // (then LANES x 16 = dim)
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(src) + k);
+        }
+    };
+    if (first < rows) load(first);
+    // the set-up, while the first rows come
+    [[maybe_unused]] vqs::CutCb<16> cut{};
+    if constexpr (CUTS) {
+        vqs::build_cut_cb<16>(a.centroids[kv], sm, cut);
+        if (threadIdx.x < 15) quarters[threadIdx.x] = cut.t[threadIdx.x];
+        __syncthreads();
+    } else {
+        if ((int)threadIdx.x < a.nc) sm[16 + threadIdx.x] = __ldg(a.centroids[kv] + threadIdx.x);
+        __syncthreads();
+    }
+    // cut points 3, 7 and 11; whether the centroids ascend
+    [[maybe_unused]] const float mid[3] = {quarters[3], quarters[7], quarters[11]};
+    [[maybe_unused]] const bool in_order = cut.perm == 0xfedcba9876543210ull;
+    const T cap = scale_cap<T>(a.centroids[kv], a.nc);
+    for (int64_t base = first; base < rows; base += stride) {
+        const int64_t t = t_next, slot = slot_next;
+        const int h = h_next;
+        float v[kE];
+        if (a.vec[kv]) {
+#pragma unroll
+            for (int j = 0; j < kE; ++j) v[j] = vqs::widen_elem(reinterpret_cast<const T *>(raw)[j]);
+        } else {
+            const T *src = x + t * a.stride[kv] + (int64_t)h * a.dim + e0;
 #pragma unroll
             for (int j = 0; j < kE; ++j)
-                v[j] = live && e0 + j < a.dim && VQ_SPAN(src + j, 1, x, x_elems) ? vqs::widen_elem(src[j]) : 0.f;
+                v[j] = base + sub < rows && e0 + j < a.dim && VQ_SPAN(src + j, 1, x, x_elems) ? vqs::widen_elem(src[j]) : 0.f;
         }
+        if (base + stride < rows) load(base + stride);
+        const bool live = base + sub < rows && slot >= 0 && (slot >> a.page_shift) < a.num_pages;
         if (rotate) {  // (dim is a power of two; the padding of a row below 16 stays zero)
 #pragma unroll
             for (int j = 0; j < kE; ++j) v[j] = __fmul_rn(v[j], sg[j]);
@@ -150,7 +187,7 @@ __global__ void __launch_bounds__(kSAppendThreads) scalar_append(const __grid_co
         float total = q[0];
 #pragma unroll
         for (int ls = 1; ls < LANES; ls <<= 1) total = __fadd_rn(total, __shfl_xor_sync(0xffffffffu, total, ls));
-        T scale = scale_of<T>(__fsqrt_rn(__fdiv_rn(total, (float)a.dim)));
+        T scale = scale_of<T>(__fsqrt_rn(a.exact ? __fmul_rn(total, a.over_dim) : __fdiv_rn(total, (float)a.dim)));
         float s = vqs::widen_elem(scale);
         if (!(s <= 3.402823466e38f)) {  // NaN or infinite
             s = 0.f;
@@ -159,29 +196,43 @@ __global__ void __launch_bounds__(kSAppendThreads) scalar_append(const __grid_co
             scale = cap;
             s = vqs::widen_elem(cap);
         }
-        const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-        uint32_t code[kE];
-        bool all = true;
+        const float inv = __frcp_rn(s);  // (infinite for the least scales: the scan decides their codes)
 #pragma unroll
-        for (int j = 0; j < kE; ++j) {
-            const float z = s > 0.f ? __fmul_rn(v[j], inv) : 0.f;
-            v[j] = z;
-            if constexpr (CUTS) {
-                code[j] = vqs::cut_code<16>(z, cut);
-                all = all && vqs::cut_decides<16>(z, cut);
-            } else {
-                code[j] = vqs::nearest(z, sm + 16, a.nc);
-            }
+        for (int j = 0; j < kE; ++j) v[j] = __fmul_rn(v[j], inv);
+        if (s == 0.f) {
+#pragma unroll
+            for (int j = 0; j < kE; ++j) v[j] = 0.f;
         }
-        if (CUTS && !all) {  // values that the cut points do not decide (rare): the rule's scan
+        uint32_t code[kE];
+        if constexpr (CUTS) {
+            float least = v[0], most = v[0];
 #pragma unroll
-            for (int j = 0; j < kE; ++j)
-                if (!vqs::cut_decides<16>(v[j], cut)) code[j] = vqs::nearest(v[j], sm + 16, 16);
+            for (int j = 0; j < kE; ++j) {
+                const bool upper = v[j] >= mid[1], quarter = v[j] >= (upper ? mid[2] : mid[0]);
+                code[j] = (upper ? 8u : 0u) + (quarter ? 4u : 0u);
+                const float4 t = *reinterpret_cast<const float4 *>(quarters + code[j]);
+                code[j] += (v[j] >= t.x ? 1u : 0u) + (v[j] >= t.y ? 1u : 0u) + (v[j] >= t.z ? 1u : 0u);
+                least = fminf(least, v[j]);
+                most = fmaxf(most, v[j]);
+            }
+            if (!in_order) {
+#pragma unroll
+                for (int j = 0; j < kE; ++j) code[j] = (uint32_t)(cut.perm >> (4 * code[j])) & 15u;
+            }
+            // values that the cut points do not decide (rare): the rule's scan
+            if (!(cut.ok && least >= cut.lo && most <= cut.hi && inv <= 3.402823466e38f)) {
+#pragma unroll
+                for (int j = 0; j < kE; ++j)
+                    if (!vqs::cut_decides<16>(v[j], cut)) code[j] = vqs::nearest(v[j], sm + 16, 16);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kE; ++j) code[j] = vqs::nearest(v[j], sm + 16, a.nc);
         }
         if (!live) continue;
         uint32_t w[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < kE; ++j) w[j / 8] |= code[j] << (4 * (j % 8));
+        for (int j = kE - 1; j >= 0; --j) w[j / 8] = w[j / 8] * 16 + code[j];
         const int64_t page = slot >> a.page_shift, off = slot & (((int64_t)1 << a.page_shift) - 1);
         const int64_t in_page = ((int64_t)h << a.page_shift) + off;
         const int ns = a.dim / 2;

@@ -38,7 +38,12 @@ bool tensor_layout(const vqk::PagedArgs &a)
 
 TensorKernels tensor_kernels(int32_t dim)
 {
-    const int32_t items = dim == 256 ? 2 : 3;
+    // Three items of 8 rows, four at dim 64: the chunk kernel takes the time of a tile of 128
+    // rows however few there are, the few-row kernel that of its items.  16 requests of 8000 (2
+    // of 30000), few-row against chunk kernel, us: dim 128 three 130 : 147 (69 : 91), four 165 :
+    // 149 (83 : 93); dim 64 four 124 : 120 (65 : 81), five 149 : 122 (73 : 81); dim 256 three
+    // 118 : 124 (67 : 81), four 147 : 126 (81 : 83).
+    const int32_t items = dim == 64 ? 4 : 3;
     return TensorKernels{vqh_few_rows(), 1, vqh_chunk_tiles(dim), items, vqh_paged_sfew,
                          vqh_paged_schunk};
 }

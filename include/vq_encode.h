@@ -553,13 +553,17 @@ vq_status vq_paged_fork(const int32_t *lens, const int32_t *parents, const int32
  *                   ascending, then -1, -1
  *   page_map        [num_pages]  device, written: the new number of each held page,
  *                   -1 of a free one (for page numbers that are kept elsewhere)
+ *   workspace       >= vq_paged_compact_workspace_bytes(num_pages) bytes, device, 16-byte
+ *                   aligned
  * Asynchronous on `stream`.
  */
+size_t vq_paged_compact_workspace_bytes(int64_t num_pages);
 vq_status vq_paged_compact(const int32_t *lens, int64_t requests, const int32_t *block_table,
                            int64_t max_blocks, int32_t page_size, const int32_t *free_pages,
                            const int32_t *free_count, int64_t num_pages, int32_t *table_out,
                            int32_t *free_pages_out, int32_t *free_count_out, int32_t *moves,
-                           int32_t *page_map, vq_stream_t stream);
+                           int32_t *page_map, void *workspace, size_t workspace_bytes,
+                           vq_stream_t stream);
 
 /*
  * vq_paged_copy -- copy page pairs[i][0] to page pairs[i][1] in every pool.

@@ -118,7 +118,10 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.vq_paged_fork.argtypes = [vp, vp, vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp,
                                   ctypes.c_size_t, vp]
     lib.vq_paged_compact.restype = i32
-    lib.vq_paged_compact.argtypes = [vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    lib.vq_paged_compact.argtypes = [vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp, vp,
+                                     ctypes.c_size_t, vp]
+    lib.vq_paged_compact_workspace_bytes.restype = ctypes.c_size_t
+    lib.vq_paged_compact_workspace_bytes.argtypes = [i64]
     lib.vq_paged_copy.restype = i32
     lib.vq_paged_copy.argtypes = [vp, i64, vp, i32, i64, vp]
     lib.vq_status_string.restype = ctypes.c_char_p
@@ -998,6 +1001,10 @@ def vq_paged_fork_workspace_bytes(num_pages: int) -> int:
     return int(load_library().vq_paged_fork_workspace_bytes(num_pages))
 
 
+def vq_paged_compact_workspace_bytes(num_pages: int) -> int:
+    return int(load_library().vq_paged_compact_workspace_bytes(num_pages))
+
+
 def _workspace_of(workspace, need: int, device, stream) -> tuple:
     """A workspace of at least ``need`` bytes: the given one, checked, or a new one; and
     its size."""
@@ -1055,15 +1062,16 @@ def vq_paged_compact(lens: torch.Tensor, block_table: torch.Tensor, page_size: i
                      free_count: torch.Tensor, table_out: torch.Tensor | None = None,
                      free_pages_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
                      moves: torch.Tensor | None = None, page_map: torch.Tensor | None = None,
-                     stream: torch.cuda.Stream | None = None) -> tuple:
+                     workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> tuple:
     """Number the held pages ``0 .. used - 1``, those not on the free list.
 
     Arguments as in :func:`vq_paged_fork`.  Returns ``(table_out, free_pages_out,
     free_count_out, moves, page_map)``; the first three may be ``block_table``,
     ``free_pages`` and ``free_count`` themselves.  ``moves`` ``[num_pages // 2, 2]`` names
     the pages (from, to) whose contents :func:`vq_paged_copy` brings over, then -1, -1;
-    ``page_map`` ``[num_pages]`` is the new number of every page, -1 of a free one.  New
-    outputs are allocated on ``stream``."""
+    ``page_map`` ``[num_pages]`` is the new number of every page, -1 of a free one.  A
+    workspace of :func:`vq_paged_compact_workspace_bytes` bytes is allocated here (by torch) if
+    none is given; it and new outputs are allocated on ``stream``."""
     n = _extent(lens)
     _i32_tensor(lens, "lens", (n,), None)
     dev, pages = lens.device, _extent(free_pages)
@@ -1075,10 +1083,12 @@ def vq_paged_compact(lens: torch.Tensor, block_table: torch.Tensor, page_size: i
     free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev, stream)
     moves = _out_like(moves, "moves", (pages // 2, 2), torch.int32, dev, stream)
     page_map = _out_like(page_map, "page_map", (pages,), torch.int32, dev, stream)
-    _launch(load_library().vq_paged_compact, "vq_paged_compact", dev, stream, lens.data_ptr(), n,
+    lib = load_library()
+    workspace, nbytes = _workspace_of(workspace, int(lib.vq_paged_compact_workspace_bytes(pages)), dev, stream)
+    _launch(lib.vq_paged_compact, "vq_paged_compact", dev, stream, lens.data_ptr(), n,
             block_table.data_ptr(), blocks, page_size, free_pages.data_ptr(), free_count.data_ptr(), pages,
             table_out.data_ptr(), free_pages_out.data_ptr(), free_count_out.data_ptr(), moves.data_ptr(),
-            page_map.data_ptr())
+            page_map.data_ptr(), workspace.data_ptr(), nbytes)
     return table_out, free_pages_out, free_count_out, moves, page_map
 
 

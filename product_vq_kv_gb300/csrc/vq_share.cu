@@ -45,7 +45,7 @@ int spread(int64_t items, int per)
     return (int)(want < 1 ? 1 : want > 4 * sms ? 4 * sms : want);
 }
 
-// Blocks of the cluster that goes through the pages: one for up to 16 thousand.
+// Blocks of the cluster that goes through the pages: one for up to per_block.
 int page_cluster(int64_t num_pages, int per_block)
 {
     int blocks = 1;
@@ -60,7 +60,8 @@ extern "C" {
 size_t vq_paged_fork_workspace_bytes(int64_t num_pages)
 {
     if (num_pages < 0 || num_pages > INT32_MAX) return 0;
-    return 2 * up256((size_t)num_pages) + up256((size_t)num_pages * 4);
+    const size_t padded = up256((size_t)num_pages);  // (the flags are cleared 16 at a time)
+    return 2 * padded + padded * 4;
 }
 
 vq_status vq_paged_fork(const int32_t *lens, const int32_t *parents, const int32_t *keep_lens, int64_t seats,
@@ -103,9 +104,9 @@ vq_status vq_paged_fork(const int32_t *lens, const int32_t *parents, const int32
     a.num_pages = (int32_t)num_pages;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const size_t smem = vqk::fork_finish_smem(seats);
-    vqk::fork_clear<<<(unsigned)spread(num_pages, vqk::kForkThreads), vqk::kForkThreads, 0, st>>>(a);
-    if ((s = vqh_launched(st, vqh_status_share)) != VQ_OK) return s;
     const int64_t segments = seats * ((max_blocks + vqk::kForkSegment - 1) / vqk::kForkSegment);
+    vqk::fork_clear<<<(unsigned)spread((num_pages + 15) / 16, vqk::kForkThreads), vqk::kForkThreads, 0, st>>>(a);
+    if ((s = vqh_launched(st, vqh_status_share)) != VQ_OK) return s;
     if (!launch_after(vqk::fork_mark, spread(segments, vqk::kForkThreads / 32), vqk::kForkThreads, 0, 1, st, a))
         return vqh_failed();
     if ((s = vqh_launched(st, vqh_status_share)) != VQ_OK) return s;
@@ -114,16 +115,23 @@ vq_status vq_paged_fork(const int32_t *lens, const int32_t *parents, const int32
     return vqh_launched(st, vqh_status_share);
 }
 
+size_t vq_paged_compact_workspace_bytes(int64_t num_pages)
+{
+    return num_pages < 0 || num_pages > INT32_MAX ? 0 : up256((size_t)(num_pages + 31) / 32 * 4);
+}
+
 vq_status vq_paged_compact(const int32_t *lens, int64_t requests, const int32_t *block_table, int64_t max_blocks,
                            int32_t page_size, const int32_t *free_pages, const int32_t *free_count,
                            int64_t num_pages, int32_t *table_out, int32_t *free_pages_out,
-                           int32_t *free_count_out, int32_t *moves, int32_t *page_map, vq_stream_t stream)
+                           int32_t *free_count_out, int32_t *moves, int32_t *page_map, void *workspace,
+                           size_t workspace_bytes, vq_stream_t stream)
 {
     vq_status s = check_pool(requests, max_blocks, page_size, num_pages);
     if (s != VQ_OK) return s;
     if (!free_count || !free_count_out || (num_pages > 0 && (!free_pages || !free_pages_out || !page_map)))
         return VQ_ERR_INVALID_ARG;
-    if (num_pages > 1 && !moves) return VQ_ERR_INVALID_ARG;
+    if ((num_pages > 1 && !moves) || (num_pages > 0 && !workspace)) return VQ_ERR_INVALID_ARG;
+    if ((uintptr_t)workspace % 16 || workspace_bytes < vq_paged_compact_workspace_bytes(num_pages)) return VQ_ERR_INVALID_ARG;
     if (requests > 0 && (!lens || (max_blocks > 0 && (!block_table || !table_out)))) return VQ_ERR_INVALID_ARG;
     for (const void *p : {(const void *)lens, (const void *)block_table, (const void *)free_pages,
                           (const void *)free_count, (const void *)table_out, (const void *)free_pages_out,
@@ -139,13 +147,14 @@ vq_status vq_paged_compact(const int32_t *lens, int64_t requests, const int32_t 
     a.free_count_out = free_count_out;
     a.moves = moves;
     a.map = page_map;
+    a.idle = static_cast<uint32_t *>(workspace);
     a.requests = (int32_t)requests;
     a.max_blocks = (int32_t)max_blocks;
     a.page_shift = page_shift(page_size);
     a.num_pages = (int32_t)num_pages;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
-    const int blocks = page_cluster(num_pages, 4 * vqk::kPageThreads);
+    const int blocks = page_cluster(num_pages, 4 * vqk::kPageThreads);  // (for the lists: the bits would take fewer)
     cudaLaunchConfig_t cfg = cluster_launch(blocks, vqk::kPageThreads, 0, st, attr);
     if (cudaLaunchKernelEx(&cfg, vqk::compact_plan, a) != cudaSuccess) return vqh_failed();
     if ((s = vqh_launched(st, vqh_status_share)) != VQ_OK) return s;

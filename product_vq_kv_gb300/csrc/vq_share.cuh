@@ -17,10 +17,13 @@
 //
 // What bounds it: the table is read twice and written once, at scattered flags of
 // one byte a page.  256 seats of 150 pages move 0.2 MB, so launches and their
-// dependent loads count: three launches, each started while the one before ends.
+// dependent loads count: three launches, each started while the one before ends (26 us on the
+// device with a cold cache, 30 us for 800 seats of up to 577 pages; one launch of a cluster of
+// eight blocks took 13 us where three take 15 for four seats, but 30 and 75 us here).
 //
 // Compact.  used = pages that are not on the free list.  The i-th held page at or
-// past `used` moves to the i-th free page below it.
+// past `used` moves to the i-th free page below it.  Bound by latency too: a bit a page, so that
+// 200,000 pages are one word for each thread of a cluster, and counts of bits.
 //
 // Copy.  Pairs of pages in up to kCopyPools pools, each of any number of layers.
 // Bound by HBM: every byte is read and written once; a warp takes 4 KiB of one page
@@ -84,28 +87,33 @@ __device__ __forceinline__ int32_t fork_blocks(const ForkArgs &a, int32_t tokens
 
 __device__ __forceinline__ bool fork_page(const ForkArgs &a, int32_t pg) { return pg >= 0 && pg < a.num_pages; }
 
+// The flags of all pages, 16 at a time (they are padded to that).
 __global__ void __launch_bounds__(kForkThreads) fork_clear(const __grid_constant__ ForkArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t stride = (int64_t)gridDim.x * kForkThreads;
-    for (int64_t p = (int64_t)blockIdx.x * kForkThreads + threadIdx.x; p < a.num_pages; p += stride) {
-        if (VQ_SPAN(a.before + p, 1, a.before, a.num_pages)) a.before[p] = 0;
-        if (VQ_SPAN(a.whole + p, 1, a.whole, a.num_pages)) a.whole[p] = 0;
-        if (VQ_SPAN(a.first + p, 1, a.first, a.num_pages)) a.first[p] = kNoSeat;
+    const int64_t tiles = ((int64_t)a.num_pages + 15) / 16, threads = (int64_t)gridDim.x * kForkThreads;
+    for (int64_t t = (int64_t)blockIdx.x * kForkThreads + threadIdx.x; t < tiles; t += threads) {
+        if (VQ_VSPAN(a.before + 16 * t, 16, a.before, 16 * tiles, 16)) reinterpret_cast<uint4 *>(a.before)[t] = make_uint4(0, 0, 0, 0);
+        if (VQ_VSPAN(a.whole + 16 * t, 16, a.whole, 16 * tiles, 16)) reinterpret_cast<uint4 *>(a.whole)[t] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (VQ_VSPAN(a.first + 16 * t + 4 * k, 4, a.first, 16 * tiles, 16))
+                reinterpret_cast<int4 *>(a.first)[4 * t + k] = make_int4(kNoSeat, kNoSeat, kNoSeat, kNoSeat);
     }
 }
 
-// A warp per seat and kForkSegment entries: flags of the old row, the new row and
-// its flags.
+// Flags of the old rows, the new rows and their flags: a warp takes a seat and kForkSegment
+// entries at a time.
 __global__ void __launch_bounds__(kForkThreads) fork_mark(const __grid_constant__ ForkArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t me = (int64_t)blockIdx.x * (kForkThreads / 32) + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * (kForkThreads / 32);
     const int lane = threadIdx.x & 31;
     const int32_t per = (a.max_blocks + kForkSegment - 1) / kForkSegment;
     const int64_t entries = (int64_t)a.seats * a.max_blocks;
-    const int64_t all = (int64_t)a.seats * per, stride = (int64_t)gridDim.x * (kForkThreads / 32);
-    for (int64_t i = (int64_t)blockIdx.x * (kForkThreads / 32) + (threadIdx.x >> 5); i < all; i += stride) {
+    const int64_t all = (int64_t)a.seats * per;
+    for (int64_t i = me; i < all; i += warps) {
         const int32_t seat = (int32_t)(i / per);
         const int32_t b0 = (int32_t)(i - (int64_t)seat * per) * kForkSegment + lane;
         const int32_t old = fork_blocks(a, fork_held(a, seat));
@@ -148,9 +156,9 @@ __global__ void __launch_bounds__(kPageThreads) fork_finish(const __grid_constan
     int64_t *scratch = reinterpret_cast<int64_t *>(share_smem);
     int64_t *mine = scratch + 64;                             // pages freed in this block's range
     int32_t *take = reinterpret_cast<int32_t *>(scratch + 80);  // [seats]
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     auto cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, rank = blockIdx.x, blocks = gridDim.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t fc = *a.free_count;
     const int64_t avail = fc < 0 ? 0 : fc > a.num_pages ? a.num_pages : fc;
     // this block's pages, 16 to a thread and pass
@@ -261,11 +269,11 @@ struct CompactArgs {
     int32_t *free_out, *free_count_out;
     int32_t *moves;  // [num_pages / 2][2]
     int32_t *map;    // [num_pages]
+    uint32_t *idle;  // a bit a page: on the free list
     int32_t requests, max_blocks, page_shift, num_pages;
 };
 
-// Launch: one cluster, kPageThreads threads, static shared memory only.  The map first
-// holds flags (0 held, -1 free).
+// Launch: one cluster, kPageThreads threads, static shared memory only.
 __global__ void __launch_bounds__(kPageThreads) compact_plan(const __grid_constant__ CompactArgs a)
 {
     __shared__ int64_t scratch[64];
@@ -274,30 +282,27 @@ __global__ void __launch_bounds__(kPageThreads) compact_plan(const __grid_consta
     auto cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, rank = blockIdx.x, blocks = gridDim.x;
     const int64_t P = a.num_pages, all = (int64_t)blocks * kPageThreads, me = (int64_t)rank * kPageThreads + tid;
+    const int64_t words = (P + 31) / 32;
     const int32_t fc = *a.free_count;
     const int64_t avail = fc < 0 ? 0 : fc > P ? P : fc;
-    for (int64_t p = me; p < P; p += all)
-        if (VQ_SPAN(a.map + p, 1, a.map, P)) a.map[p] = 0;
+    for (int64_t w = me; w < words; w += all)
+        if (VQ_SPAN(a.idle + w, 1, a.idle, words)) a.idle[w] = 0;
     cluster.sync();
     for (int64_t i = me; i < avail; i += all) {
         if (!VQ_SPAN(a.free_pages + i, 1, a.free_pages, P)) continue;
         const int32_t p = a.free_pages[i];
-        if (p >= 0 && p < P && VQ_SPAN(a.map + p, 1, a.map, P)) a.map[p] = -1;
+        if (p >= 0 && p < P && VQ_SPAN(a.idle + (p >> 5), 1, a.idle, words)) atomicOr(a.idle + (p >> 5), 1u << (p & 31));
     }
     cluster.sync();
-    // this block's pages, kPer to a thread and pass
-    constexpr int kPer = 4;
-    const int64_t p0 = (P * rank / blocks + kPer - 1) / kPer * kPer;
-    const int64_t p1 = rank + 1 == blocks ? P : (P * (rank + 1) / blocks + kPer - 1) / kPer * kPer;
-    auto held_of = [&](int64_t p) -> uint32_t {  // bit i: page p + i is held
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (p + i < p1 && VQ_SPAN(a.map + p + i, 1, a.map, P) && __ldcg(a.map + p + i) == 0) bits |= 1u << i;
-        return bits;
+    // this block's words, one to a thread and pass
+    const int64_t w0 = words * rank / blocks, w1 = words * (rank + 1) / blocks;
+    auto held_of = [&](int64_t w) -> uint32_t {  // bit i: page 32 w + i is held
+        if (!VQ_SPAN(a.idle + w, 1, a.idle, words)) return 0;
+        const uint32_t bits = ~__ldcg(a.idle + w);
+        return w == words - 1 && P % 32 ? bits & ((1u << (P % 32)) - 1u) : bits;
     };
     int64_t held = 0, unused = 0;
-    for (int64_t p = p0 + (int64_t)tid * kPer; p < p1; p += (int64_t)kPageThreads * kPer) held += __popc(held_of(p));
+    for (int64_t w = w0 + tid; w < w1; w += kPageThreads) held += __popc(held_of(w));
     block_scan2(held, unused, scratch);
     if (tid == 0) mine[0] = scratch[31];
     cluster.sync();
@@ -308,13 +313,12 @@ __global__ void __launch_bounds__(kPageThreads) compact_plan(const __grid_consta
         used += c;
     }
     // Page p has h held pages before it.  A hole below `used` is number p - h; a held page
-    // at or past it is number h - (held pages below `used`) = h - (used - holes), and there
-    // are as many holes as such pages.
+    // at or past it is number h - (held pages below `used`), and there are as many holes as
+    // such pages.
     int64_t below = 0;  // held pages below `used`, of this block
-    for (int64_t p = p0 + (int64_t)tid * kPer; p < p1; p += (int64_t)kPageThreads * kPer) {
-        const uint32_t bits = held_of(p);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) below += (bits >> i & 1u) && p + i < used;
+    for (int64_t w = w0 + tid; w < w1; w += kPageThreads) {
+        const int64_t left = used - 32 * w;
+        if (left > 0) below += __popc(held_of(w) & (left < 32 ? (1u << left) - 1u : 0xffffffffu));
     }
     __syncthreads();  // scratch is read
     block_scan2(below, unused, scratch);
@@ -324,24 +328,31 @@ __global__ void __launch_bounds__(kPageThreads) compact_plan(const __grid_consta
     for (int b = 0; b < blocks; ++b) kept += *cluster.map_shared_rank(mine + 1, b);
     const int64_t moving = used - kept;
     const int64_t rows = P / 2;
-    for (int64_t base = p0; base < p1; base += (int64_t)kPageThreads * kPer) {
-        const int64_t p = base + (int64_t)tid * kPer;
-        const uint32_t bits = p < p1 ? held_of(p) : 0;
+    const int lane = tid & 31;
+    for (int64_t base = w0; base < w1; base += kPageThreads) {
+        const uint32_t bits = base + tid < w1 ? held_of(base + tid) : 0;
         int64_t s = __popc(bits);
         const int64_t own = s;
         __syncthreads();  // scratch is read
         block_scan2(s, unused, scratch);
-        int64_t h = held_before + s - own;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (p + i >= p1) break;
-            const bool is_held = bits >> i & 1u;
-            const int64_t nth = is_held ? h - kept : p + i - h;
-            const bool listed = is_held == (p + i >= used);
-            int32_t *m = a.moves + 2 * nth + (is_held ? 0 : 1);
-            if (listed && nth < rows && VQ_SPAN(m, 1, a.moves, 2 * rows)) *m = (int32_t)(p + i);
-            if (is_held && p + i < used && VQ_SPAN(a.map + p + i, 1, a.map, P)) a.map[p + i] = (int32_t)(p + i);
-            h += is_held;
+        // the pages of the warp's words, a word at a time: a lane a page
+        const int64_t h0 = held_before + s - own;
+        for (int k = 0; k < 32; ++k) {
+            const int64_t w = base + (tid & ~31) + k;
+            if (w >= w1) break;  // warp-uniform
+            const uint32_t word = __shfl_sync(0xffffffffu, bits, k);
+            const int64_t h = __shfl_sync(0xffffffffu, h0, k) + __popc(word & ((1u << lane) - 1u));
+            const int64_t p = 32 * w + lane;
+            const bool is_held = word >> lane & 1u;
+            if (p >= P) continue;
+            if (is_held != (p >= used)) {  // it stays, or is free past the held ones
+                if (VQ_SPAN(a.map + p, 1, a.map, P)) a.map[p] = is_held ? (int32_t)p : -1;
+            } else {
+                const int64_t nth = is_held ? h - kept : p - h;
+                int32_t *m = a.moves + 2 * nth + (is_held ? 0 : 1);
+                if (nth < rows && VQ_SPAN(m, 1, a.moves, 2 * rows)) *m = (int32_t)p;
+                if (!is_held && VQ_SPAN(a.map + p, 1, a.map, P)) a.map[p] = -1;
+            }
         }
         held_before += scratch[31];
     }

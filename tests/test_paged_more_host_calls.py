@@ -12,7 +12,7 @@ def fork(lib, seats=4, pages=10):  # noqa: F811
 
 
 def compact(lib, requests=4, pages=10):  # noqa: F811
-    return lib.vq_paged_compact(P, requests, P, 8, 16, P, P, pages, P, P, P, P, P, None)
+    return lib.vq_paged_compact(P, requests, P, 8, 16, P, P, pages, P, P, P, P, P, P, 1 << 30, None)
 
 
 def copy(lib, n=3):  # noqa: F811

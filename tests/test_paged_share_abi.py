@@ -12,7 +12,7 @@ FAR = P + (1 << 30)
 FORK = dict(lens=P, parents=P, keep=P, seats=4, table=P, blocks=8, page=16, free=P, count=P, pages=10, lens_out=P,
             table_out=FAR, count_out=P, copies=P, ws=P, ws_bytes=1 << 20)
 COMPACT = dict(lens=P, requests=4, table=P, blocks=8, page=16, free=P, count=P, pages=10, table_out=P, free_out=P,
-               count_out=P, moves=P, map=P)
+               count_out=P, moves=P, map=P, ws=P, ws_bytes=1 << 20)
 
 
 @pytest.mark.parametrize("change, want", [
@@ -35,7 +35,8 @@ def test_fork_refusals(lib, change, want):  # noqa: F811
     (dict(requests=8193), UNSUPPORTED), (dict(pages=-1), INVALID), (dict(blocks=-2), INVALID), (dict(lens=0), INVALID),
     (dict(table=0), INVALID), (dict(table_out=0), INVALID), (dict(free=0), INVALID), (dict(free_out=0), INVALID),
     (dict(count=0), INVALID), (dict(count_out=0), INVALID), (dict(moves=0), INVALID), (dict(map=0), INVALID),
-    (dict(map=P + 3), INVALID), (dict(moves=P + 1), INVALID)])
+    (dict(map=P + 3), INVALID), (dict(moves=P + 1), INVALID), (dict(ws=0), INVALID), (dict(ws=P + 8), INVALID),
+    (dict(pages=1 << 30), INVALID)])
 def test_compact_refusals(lib, change, want):  # noqa: F811
     assert call(lib.vq_paged_compact, COMPACT, **change) == want
 
@@ -63,6 +64,8 @@ def test_copy_refusals(lib, change, pool, want):  # noqa: F811
 def test_workspace_bytes(lib):  # noqa: F811
     assert lib.vq_paged_fork_workspace_bytes(0) == 0
     assert lib.vq_paged_fork_workspace_bytes(1000) >= 6000
+    assert lib.vq_paged_compact_workspace_bytes(0) == lib.vq_paged_compact_workspace_bytes(-1) == 0
+    assert lib.vq_paged_compact_workspace_bytes(33) >= 8
     assert lib.vq_paged_fork_workspace_bytes(-1) == lib.vq_paged_fork_workspace_bytes(1 << 31) == 0
 
 

@@ -231,6 +231,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     constexpr int kSets = kScalar && kKinds == 2 ? 1 : 2;
     constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr float kShift = weight_shift<T>();
+    // A row's maximum may lag by this many powers of two.  Rows of scalar codes differ in scale, so
+    // that maxima rise often, and every rise sends a warp's block down the longer path; where
+    // weights have fp32's range the lag can be longer (scales e^(0.5 z), 2048 tokens on 8192
+    // cached in bf16: 383 -> 304 us).
+    constexpr float kSlack = SUB == 2 && std::is_same<T, __nv_bfloat16>::value ? 32.f : kFewSlack;
     extern __shared__ __align__(128) unsigned char chunk_mem[];
     __shared__ PagedWalk<64> w;
     __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image[2], drain, seg_full[2], seg_empty[2];
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         weights(v, p + c * 16, 32, m, add);
                     }
                     const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.kappa;
-                    if (!__any_sync(0xffffffffu, top > m + (kFewSlack + kShift) || m == kNone)) {
+                    if (!__any_sync(0xffffffffu, top > m + (kSlack + kShift) || m == kNone)) {
                         done = true;
                         sum2 = add2_rn(sum2, add);
 #pragma unroll
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     top *= a.kappa;  // kappa > 0
                     // a row rises for its own scores alone, so that what it computes does
                     // not depend on the rows beside it; the others are scaled by 1
-                    const bool rise = top > m + (kFewSlack + kShift);
+                    const bool rise = top > m + (kSlack + kShift);
                     if (__any_sync(0xffffffffu, rise)) {
                         const float to = rise ? top - kShift : m;
                         const float f = rise ? exp2_fast(m - to) : 1.f;

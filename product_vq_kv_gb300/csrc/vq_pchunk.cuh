@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     // weights have fp32's range the lag can be longer (scales e^(0.5 z), 2048 tokens on 8192
     // cached in bf16: 383 -> 304 us).
     constexpr float kSlack = SUB == 2 && std::is_same<T, __nv_bfloat16>::value ? 32.f : kFewSlack;
+    constexpr bool kRedo = SUB == 2 && std::is_same<T, __half>::value;
     extern __shared__ __align__(128) unsigned char chunk_mem[];
     __shared__ PagedWalk<64> w;
     __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image[2], drain, seg_full[2], seg_empty[2];
@@ -425,6 +426,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     }
                 };
                 bool done = false;
+                // (scalar codes in fp16, whose maxima rise often: a first pass that was not kept has
+                // found the maximum, and there are no masks; 308 -> 284 us at dim 64)
+                [[maybe_unused]] bool known = false;
+                [[maybe_unused]] float known_top = kNone;
                 if (whole && j > 0) {  // the same for all rows of the tile
                     // one pass with the maximum so far, kept if no score of the warp's
                     // rows exceeds it by more than the slack; the scores still stand then
@@ -444,6 +449,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         weights(v, p + c * 16, 32, m, add);
                     }
                     const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.kappa;
+                    if constexpr (kRedo) {
+                        known = true;
+                        known_top = top;
+                    }
                     if (!__any_sync(0xffffffffu, top > m + (kSlack + kShift) || m == kNone)) {
                         done = true;
                         sum2 = add2_rn(sum2, add);
@@ -454,17 +463,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 if (!done) {
                     // first the maximum, then the weights
                     float top = kNone;
+                    if (kRedo && known) {
+                        top = known_top;
+                        saw = 1u;
+                    } else {
 #pragma unroll 1
-                    for (int c = 0; c < kKeys / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_load32_async(s_addr + c * 32, v);
-                        const uint32_t bits = seen_bits(c);
-                        saw |= bits;
-                        tmem_wait_ld(v);
+                        for (int c = 0; c < kKeys / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_load32_async(s_addr + c * 32, v);
+                            const uint32_t bits = seen_bits(c);
+                            saw |= bits;
+                            tmem_wait_ld(v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
+                            for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
+                        }
+                        top *= a.kappa;  // kappa > 0
                     }
-                    top *= a.kappa;  // kappa > 0
                     // a row rises for its own scores alone, so that what it computes does
                     // not depend on the rows beside it; the others are scaled by 1
                     const bool rise = top > m + (kSlack + kShift);
@@ -499,11 +513,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     for (int c = 0; c < kKeys / 32; ++c) {
                         uint32_t v[32], p[16];
                         tmem_load32_async(s_addr + c * 32, v);
-                        const uint32_t bits = seen_bits(c);
+                        const uint32_t bits = kRedo && known ? 0xffffffffu : seen_bits(c);
                         tmem_wait_ld(v);
                         // a score that is not seen is left out as -inf: weight 0, whatever it was
+                        if (!(kRedo && known)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : 0xff800000u;
+                            for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : 0xff800000u;
+                        }
                         weights(v, p, 32, ref, add);
                         tmem_store16(s_addr + c * 16, p);
                     }

@@ -36,7 +36,7 @@ bool tensor_layout(const vqk::PagedArgs &a)
     return a.page_stride % 16 == 0 && a.scale_stride % 8 == 0;
 }
 
-TensorKernels tensor_kernels(int32_t dim)
+TensorKernels tensor_kernels(int32_t dim, int32_t group, int64_t max_new)
 {
     // Three items of 8 rows, four at dim 64: the chunk kernel takes the time of a tile of 128
     // rows however few there are, the few-row kernel that of its items.  16 requests of 8000 (2
@@ -44,7 +44,9 @@ TensorKernels tensor_kernels(int32_t dim)
     // 149 (83 : 93); dim 64 four 124 : 120 (65 : 81), five 149 : 122 (73 : 81); dim 256 three
     // 118 : 124 (67 : 81), four 147 : 126 (81 : 83).
     const int32_t items = dim == 64 ? 4 : 3;
-    return TensorKernels{vqh_few_rows(), 1, vqh_chunk_tiles(dim), items, vqh_paged_sfew,
+    // items of 4 rows where no request has more
+    const int rows = max_new > 0 && group <= 4 && max_new * group <= 4 ? 4 : vqh_few_rows();
+    return TensorKernels{rows, 1, vqh_chunk_tiles(dim), items, vqh_paged_sfew,
                          vqh_paged_schunk};
 }
 
@@ -84,7 +86,7 @@ size_t vq_paged_scalar_attention_workspace_bytes(int64_t requests, int64_t token
     size_t need = simple_part(sms, group, head_dim, 0).end;
     if (tensor_shape(VQ_F16, head_dim, page_size)) {
         AttnPart few, chunk;
-        const TensorKernels k = tensor_kernels(head_dim);
+        const TensorKernels k = tensor_kernels(head_dim, group, max_new);
         const size_t t = tensor_parts(k, tensor_plan(k, requests, tokens, max_new, group), sms, group, head_dim, &few, &chunk);
         if (t > need) need = t;
     }
@@ -164,7 +166,7 @@ vq_status vq_paged_scalar_attention(const void *q, int64_t q_stride, const int32
     a.kappa = (scale > 0.f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
 
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    if (tensor_shape(dtype, head_dim, page_size) && tensor_layout(a)) return launch_tensor(c, tensor_kernels(head_dim), ws);
+    if (tensor_shape(dtype, head_dim, page_size) && tensor_layout(a)) return launch_tensor(c, tensor_kernels(head_dim, a.group, max_new), ws);
     const AttnPart p = simple_part(c.sms, a.group, head_dim, 0);
     switch (dtype) {
     case VQ_F16: return launch_simple<__half>(c, p, ws);

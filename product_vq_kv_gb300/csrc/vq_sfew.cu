@@ -12,14 +12,20 @@ VQH_STATUS_READER(vqh_status_sfew)
 
 namespace {
 
-template <typename T, int D>
-vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
+template <typename T, int D, bool PAIR>
+vq_status launch_rows(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
 {
-    auto kernel = vqk::paged_attn_sfew<T, D>;
+    auto kernel = vqk::paged_attn_sfew<T, D, PAIR>;
     using S = vqk::SFewShape<D>;
     if (!vqh_allow_smem(kernel, S::kSmem)) return vqh_failed();
     kernel<<<(unsigned)blocks, S::kWarps * 32, S::kSmem, st>>>(a);
     return vqh_launched(st, vqh_status_sfew);
+}
+
+template <typename T, int D>
+vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
+{
+    return a.tile_rows <= 4 ? launch_rows<T, D, true>(a, blocks, st) : launch_rows<T, D, false>(a, blocks, st);
 }
 
 template <typename T>

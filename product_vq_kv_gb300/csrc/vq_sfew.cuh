@@ -26,6 +26,9 @@
 //     before their rounding to two pieces, so that no rebuilt value is rounded.
 //   * A warp takes 32 tokens at a time, so that addresses, page lookups, waits and the vote
 //     are paid once and the two groups' chains of dependent instructions overlap.
+//   * Up to 4 rows (one token of up to 4 query heads a KV head) leave half of an instruction's
+//     columns free: there the rows stand twice, and the second pieces of the weights take the
+//     columns that would be idle, one instruction instead of two (PAIRGAIN).
 //   * Codes and scales come by cp.async into two slots a warp, 16-byte pieces exchanged so
 //     that the keys' and the values' reads meet no bank twice; a slot is filled again as
 //     soon as its codes are in registers, two runs ahead of their use.
@@ -53,7 +56,7 @@ struct SFewShape {
     // Addresses in shared memory: static memory, the ring of the first kLow warps from kRing,
     // the table from kTable, the other warps' ring from kUpper.
     static constexpr uint32_t kTable = 65536, kUpper = kTable + 65536;
-    static constexpr uint32_t kRing = 10240;
+    static constexpr uint32_t kRing = D == 64 ? 18432 : 15360;
     static constexpr int kLow = (kTable - kRing) / kWarpRing < kWarps ? (kTable - kRing) / kWarpRing : kWarps;
     static constexpr size_t kAbove = (size_t)(kWarps - kLow) * kWarpRing;
     static constexpr size_t kSmem = kUpper + (kAbove > kMerge ? kAbove : kMerge);  // (of which the array has the part from its start on)
@@ -82,9 +85,10 @@ constexpr float kSFewLess = 7.6293945e-6f;   // 2^-17: p, which stays fp32, may 
 // tokens g and g + 8) folded in.  m follows the scores alone and the factor f the weights alone: a value's scale
 // does not touch the sum, and tokens whose values are large do not push others, of larger
 // weight, out of fp16.
-template <typename T, int H, int MMA>
-__device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const float (&vs)[H][2], float (&m)[2], float (&sum)[2],
-                                             float (&f)[2], float (&o)[MMA][4], uint32_t (&pf)[H][2][2])
+// PAIR: this lane's columns hold the first or (`second`) the second piece of their weights.
+template <typename T, bool PAIR, int H, int MMA>
+__device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const float (&vs)[H][2], bool second, float (&m)[2],
+                                             float (&sum)[2], float (&f)[2], float (&o)[MMA][4], uint32_t (&pf)[H][PAIR ? 1 : 2][2])
 {
     float p[H][4], w[H][4], high = 0.f;
 #pragma unroll
@@ -152,8 +156,9 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const floa
         for (int c = 0; c < 2; ++c) {
             const uint32_t first = pack2<T>(w[h][2 * c], w[h][2 * c + 1]);
             const float2 kept = unpack2<T>(first);
-            pf[h][0][c] = transpose8x8(first);
-            pf[h][1][c] = transpose8x8(pack2<T>(w[h][2 * c] - kept.x, w[h][2 * c + 1] - kept.y));
+            const uint32_t rest = pack2<T>(w[h][2 * c] - kept.x, w[h][2 * c + 1] - kept.y);
+            pf[h][0][c] = transpose8x8(PAIR && second ? rest : first);
+            if constexpr (!PAIR) pf[h][1][c] = transpose8x8(rest);
         }
     }
 }
@@ -210,7 +215,9 @@ __device__ __forceinline__ void each(F f)
     }
 }
 
-template <typename T, int D>
+// PAIR: items of up to 4 rows, which lie in columns 0 to 3 of the instructions and once more in
+// 4 to 7; there the weights' second pieces enter the second product.
+template <typename T, int D, bool PAIR>
 __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
     paged_attn_sfew(const __grid_constant__ PagedArgs a)
 {
@@ -223,7 +230,8 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
     extern __shared__ __align__(128) unsigned char sfew_mem[];
     __shared__ PagedWalk<> w;
     __shared__ float wm[kWarps][kFewRows], wl[kWarps][kFewRows];
-    static_assert(1024 + sizeof w + sizeof wm + sizeof wl + 256 <= S::kRing, "static memory (and the system's) below the ring");
+    __shared__ int32_t batch[kWarps][2][S::kHalves][32];
+    static_assert(1024 + sizeof w + sizeof wm + sizeof wl + sizeof batch + 256 <= S::kRing, "static memory (and the system's) below the ring");
     // (the array begins behind the static memory, which ends below kRing)
     unsigned char *lines = sfew_mem + (S::kTable - smem_addr(sfew_mem));
     float *slots = reinterpret_cast<float *>(lines + (S::kUpper - S::kTable));
@@ -262,7 +270,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
 
             // query fragments: row g, columns t dim/4 + 4 i .. + 3
             uint32_t qf[kMma][2];
-            const int row = g;
+            const int row = PAIR ? g & 3 : g;
             const T *src = q + (s.it.tok0 + row / gc) * a.q_stride + (int64_t)(head0 + row % gc) * D + t * (D / 4);
             const bool ok = row < rows && VQ_SPAN(src, D / 4, q, q_elems);
 #pragma unroll
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
             float o[kMma][4];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int row = 2 * t + c;
+                const int row = PAIR ? (2 * t + c) & 3 : 2 * t + c;
                 const int32_t p = s.it.pos0 + (row < rows ? row / gc : 0);
                 lim[c] = p < s.it.k_hi ? p : s.it.k_hi - 1;
                 // (a row whose limit k_hi cut keeps its own window)
@@ -312,22 +320,23 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                 if (k0 >= s.it.k_hi || k0 + 15 <= none_lo) return -1;
                 return paged_entry(a, cur.r, k0);  // checked when it is used: a check here would wait for the load
             };
-            // The pages of 32 runs of this warp, a run a lane, one batch ahead of its use: a load
-            // for each run is waited for where its register is handed on.
+            // The pages of 32 runs of this warp, a run a lane, kept in shared memory one batch ahead
+            // of their use: a load for each run would be waited for where its register is handed
+            // on.
             struct Pages { int32_t pg[S::kHalves]; };
-            auto batch_of = [&](int n) {  // runs 32 n .. of this warp
-                Pages p;
-                const int run = g_begin + (32 * n + lane) * kWarps;
+            auto keep_batch = [&](int b) {  // runs 32 b .. of this warp
+                const int run = g_begin + (32 * b + lane) * kWarps;
+                __syncwarp();  // the batch that was there is read
 #pragma unroll
-                for (int x = 0; x < S::kHalves; ++x) p.pg[x] = run < g_end ? entry_of(first_of(run) + 16 * x) : -1;
-                return p;
+                for (int x = 0; x < S::kHalves; ++x) batch[warp][b & 1][x][lane] = run < g_end ? entry_of(first_of(run) + 16 * x) : -1;
+                __syncwarp();
             };
-            Pages batch = batch_of(0), batch_next = batch_of(1);
-            auto pages_of = [&](int n) {  // of this warp's n-th run in the batch or the next
+            keep_batch(0);
+            keep_batch(1);
+            auto pages_of = [&](int n) {  // of this warp's n-th run
                 Pages p;
 #pragma unroll
-                for (int x = 0; x < S::kHalves; ++x)
-                    p.pg[x] = __shfl_sync(0xffffffffu, n < 32 ? batch.pg[x] : batch_next.pg[x], n & 31);
+                for (int x = 0; x < S::kHalves; ++x) p.pg[x] = batch[warp][n >> 5 & 1][x][n & 31];
                 return p;
             };
             auto is_page = [&](int32_t pg) { return pg >= 0 && pg < a.num_pages; };
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
 
             auto table = [&](uint32_t word, int i, int kind) { return scalar_lookup<S::kTable>(word, i, copy[kind]); };
             uint32_t slot = ring;
-            int n = 0, batches = 0;  // of the warp's runs: in the batch, before it
+            int n = 0;  // of the warp's runs
             for (int run = g_begin; run < g_end; run += kWarps) {
                 const Pages ahead = pages_of(n + S::kSlots);
                 const Places from = places_of(run + S::kSlots * kWarps, ahead);
@@ -449,8 +458,8 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                                 if (!live[x] || key >= s.it.k_hi || key > last_pos || key <= none_lo) vscale[x][k] = 0.f;
                             }
                     }
-                    uint32_t pf[S::kHalves][2][2];
-                    sfew_weights<T>(st, vscale, m, sum, factor, o, pf);
+                    uint32_t pf[S::kHalves][PAIR ? 1 : 2][2];
+                    sfew_weights<T, PAIR>(st, vscale, t >= 2, m, sum, factor, o, pf);
                     copy_wait<2 * S::kSlots - 1>();  // its values
                     uint32_t vc[S::kHalves][4][VW];
                     each<4 * S::kHalves>([&](auto at) {
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                                 const uint32_t a0 = table(even[0], b, 1), a1 = table(odd[0], b, 1);
                                 const uint32_t a2 = table(even[1], b, 1), a3 = table(odd[1], b, 1);
                                 mma16816<T>(o[4 * i + b], a0, a1, a2, a3, pf[x][0][0], pf[x][0][1]);
-                                mma16816<T>(o[4 * i + b], a0, a1, a2, a3, pf[x][1][0], pf[x][1][1]);
+                                if constexpr (!PAIR) mma16816<T>(o[4 * i + b], a0, a1, a2, a3, pf[x][1][0], pf[x][1][1]);
                             }
                         }
                 } else {
@@ -487,14 +496,15 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
                 }
                 static_assert(S::kSlots == 2, "two slots in turn");
                 slot = slot == ring ? ring + S::kSlot : ring;
-                if (++n == 32) {
-                    n = 0;
-                    ++batches;
-                    batch = batch_next;
-                    batch_next = batch_of(batches + 1);
-                }
+                if ((++n & 31) == 0) keep_batch((n >> 5) + 1);
             }
             copy_wait<0>();
+            if constexpr (PAIR) {  // the two pieces' sums
+#pragma unroll
+                for (int i = 0; i < kMma; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[i][c] += __shfl_xor_sync(0xffffffffu, o[i][c], 2);
+            }
             // to weights without the factors
 #pragma unroll
             for (int c = 0; c < 2; ++c) {

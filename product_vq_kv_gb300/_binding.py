@@ -849,6 +849,23 @@ def vq_paged_attention(q: torch.Tensor, cu_new: torch.Tensor, lens: torch.Tensor
 def _scalar_page_tensors(k_codes, v_codes, k_scales, v_scales, k_centroids, v_centroids, dtype, device):
     """Check the pages and centroids of the cache in 4 bits; returns (num_pages, heads,
     page_size, dim, page stride in bytes, scale stride in elements, n_centroids)."""
+    if (isinstance(k_codes, torch.Tensor) and isinstance(v_codes, torch.Tensor) and isinstance(k_scales, torch.Tensor)
+            and isinstance(v_scales, torch.Tensor) and isinstance(k_centroids, torch.Tensor)
+            and isinstance(v_centroids, torch.Tensor) and k_codes.dim() == 4 and k_scales.dim() == 3
+            and k_centroids.dim() == 1):
+        # the usual case in one test; anything else is told apart below
+        shape, strides, scale_strides = k_codes.shape, k_codes.stride(), k_scales.stride()
+        pages, heads, page_size, ns = shape
+        if (pages > 1 and k_codes.dtype is torch.uint8 and v_codes.dtype is torch.uint8 and k_scales.dtype is dtype
+                and v_scales.dtype is dtype and k_centroids.dtype is torch.float32 and v_centroids.dtype is torch.float32
+                and v_codes.shape == shape and v_codes.stride() == strides and k_scales.shape == shape[:3]
+                and v_scales.shape == shape[:3] and v_scales.stride() == scale_strides
+                and v_centroids.shape == k_centroids.shape and strides[1:] == (page_size * ns, ns, 1)
+                and strides[0] >= heads * page_size * ns and scale_strides[1:] == (page_size, 1)
+                and scale_strides[0] >= heads * page_size and k_centroids.is_contiguous() and v_centroids.is_contiguous()
+                and k_codes.device == device and v_codes.device == device and k_scales.device == device
+                and v_scales.device == device and k_centroids.device == device and v_centroids.device == device):
+            return pages, heads, page_size, 2 * ns, strides[0], scale_strides[0], k_centroids.shape[0]
     named = (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales), ("v_scales", v_scales),
              ("k_centroids", k_centroids), ("v_centroids", v_centroids))
     for name, t in named:
@@ -1050,7 +1067,7 @@ def vq_paged_fork(lens: torch.Tensor, parents: torch.Tensor, block_table: torch.
     free_count_out = _out_like(free_count_out, "free_count_out", (1,), torch.int32, dev, stream)
     copies = _out_like(copies, "copies", (n, 2), torch.int32, dev, stream)
     lib = load_library()
-    workspace, nbytes = _workspace_of(workspace, int(lib.vq_paged_fork_workspace_bytes(pages)), dev, stream)
+    workspace, nbytes = _workspace_of(workspace, lib.vq_paged_fork_workspace_bytes(pages), dev, stream)
     _launch(lib.vq_paged_fork, "vq_paged_fork", dev, stream, lens.data_ptr(), parents.data_ptr(),
             keep_lens.data_ptr() if keep_lens is not None else None, n, block_table.data_ptr(), blocks, page_size,
             free_pages.data_ptr(), free_count.data_ptr(), pages, lens_out.data_ptr(), table_out.data_ptr(),
@@ -1084,7 +1101,7 @@ def vq_paged_compact(lens: torch.Tensor, block_table: torch.Tensor, page_size: i
     moves = _out_like(moves, "moves", (pages // 2, 2), torch.int32, dev, stream)
     page_map = _out_like(page_map, "page_map", (pages,), torch.int32, dev, stream)
     lib = load_library()
-    workspace, nbytes = _workspace_of(workspace, int(lib.vq_paged_compact_workspace_bytes(pages)), dev, stream)
+    workspace, nbytes = _workspace_of(workspace, lib.vq_paged_compact_workspace_bytes(pages), dev, stream)
     _launch(lib.vq_paged_compact, "vq_paged_compact", dev, stream, lens.data_ptr(), n,
             block_table.data_ptr(), blocks, page_size, free_pages.data_ptr(), free_count.data_ptr(), pages,
             table_out.data_ptr(), free_pages_out.data_ptr(), free_count_out.data_ptr(), moves.data_ptr(),

@@ -51,7 +51,9 @@ TensorKernels tensor_kernels(int32_t dim)
     // three 74 : 84 (43 : 56), four 93 : 84 (51 : 56); dim 256 two 72 : 80 (43 : 51), three
     // 99 : 80 (54 : 54).  Other head groups and sub-vectors lie alike.
     const int32_t items = dim == 256 ? 2 : 3;
-    return TensorKernels{vqh_few_rows(), vqh_few_blocks_per_sm(dim), vqh_chunk_tiles(dim), items, vqh_paged_few,
+    // An item's cost: 2 : 3 : 4 : 5 give drafts of 16 requests 60.7 : 57.3 : 56.0 : 55.4 us, 32
+    // uneven decodes 148.8 : 147.7 : 146.9 : 146.5
+    return TensorKernels{vqh_few_rows(), vqh_few_blocks_per_sm(dim), vqh_chunk_tiles(dim), items, 4, vqh_paged_few,
                          vqh_paged_chunk};
 }
 

@@ -103,6 +103,7 @@ struct TensorKernels {
     int few_rows, few_blocks_per_sm;  // the few-row kernel: rows of an item
     int chunk_tiles;                  // the chunk kernel: tiles of 128 rows an item has
     int32_t few_items;                // items of a request up to which the few-row kernel takes it
+    int32_t item_cost;                // set-up, merge of the warps and write of its item, in units
     vq_status (*few)(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);
     vq_status (*chunk)(const vqk::PagedArgs &a, vq_dtype dtype, int blocks, cudaStream_t st);
 };
@@ -133,9 +134,7 @@ inline AttnPart few_part(const TensorKernels &k, int sms, int32_t group, int32_t
     p.gch = (group + p.gc - 1) / p.gc;
     p.tile_tokens = k.few_rows / p.gc;
     p.tile_rows = k.few_rows;
-    // set-up, merge of the warps and write of an item, in units: 2 : 3 : 4 : 5 give drafts of
-    // 16 requests 60.7 : 57.3 : 56.0 : 55.4 us, 32 uneven decodes 148.8 : 147.7 : 146.9 : 146.5
-    p.item_cost = 4;
+    p.item_cost = k.item_cost;
     lay_out(&p, dim, at);
     return p;
 }

@@ -475,9 +475,9 @@ vq_status vq_paged_scalar_append(const void *k, const void *v, int64_t k_stride,
  * page, may be anything.  slots may be NULL.
  * Arithmetic: as vq_paged_attention.  With 16-bit inputs, head_dim 64, 128 or 256,
  * page_size >= 16 and pools whose addresses and strides are multiples of 16 bytes, the
- * tensor kernels take the products.  For a few new tokens the scales multiply scores and
- * weights in fp32, and the weights enter in two pieces, as there; for longer runs K^, V^ and
- * the weights are each rounded once to the input type.
+ * tensor kernels take the products.  The keys' scales multiply the scores and the values'
+ * scales the weights, in fp32.  For a few new tokens the weights enter in two pieces, as
+ * there; for longer runs they are rounded once to the input type.
  * Asynchronous on `stream`.
  */
 vq_status vq_paged_scalar_attention(const void *q, int64_t q_stride, const int32_t *cu_new,

@@ -236,10 +236,10 @@ template <int STAGE>
 struct PagedStage {
     int32_t cu[STAGE], lens[STAGE], start[STAGE];
 };
-template <int STAGE = kStageCu>
+template <int STAGE = kStageCu, int SCRATCH = 33>
 struct PagedWalk {
     PagedStage<STAGE> stage;
-    int64_t scratch[33];
+    int64_t scratch[SCRATCH];  // of the plan alone
     int64_t total;  // the costs of one head group
     int64_t u0, u1; // this block's part of the line
     int32_t blocks; // blocks with work
@@ -250,8 +250,8 @@ struct PagedWalk {
 };
 
 // The lengths as a block reads them: from its stage if they fit there.
-template <int STAGE>
-__device__ __forceinline__ PagedLens paged_lens(const PagedArgs &a, const PagedWalk<STAGE> &w)
+template <int STAGE, int SCRATCH>
+__device__ __forceinline__ PagedLens paged_lens(const PagedArgs &a, const PagedWalk<STAGE, SCRATCH> &w)
 {
     PagedLens l{a.cu, a.lens, nullptr, a.requests, a.tile_tokens, a.tokens};
     if (a.requests + 2 <= STAGE) {
@@ -264,8 +264,8 @@ __device__ __forceinline__ PagedLens paged_lens(const PagedArgs &a, const PagedW
 
 // Lay the items out and find this block's part (all THREADS threads; w in
 // shared memory).  Returns whether the block has any.
-template <int THREADS, int STAGE>
-__device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE> &w, PagedLens &l)
+template <int THREADS, int STAGE, int SCRATCH>
+__device__ __forceinline__ bool paged_plan(const PagedArgs &a, PagedWalk<STAGE, SCRATCH> &w, PagedLens &l)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.requests + 2 <= STAGE) {

@@ -45,11 +45,17 @@
 // memory is freed, and the rows that the block has not written become NaN.
 //
 // 4-bit scalar codes: a byte selects a pair of centroids from an image of 256 pairs, 32 copies
-// each (a lane its own: no conflict whatever the codes), and the pair is multiplied by the
-// row's scale, one rounding of K^ and V^ to the type, which the products need.  The rebuild
-// moves as many bytes of shared memory as that of sub-vectors, in words of 4 bytes where
-// those come in 8 or 16, so it issues four times as much: 512 lookups, products of two and
-// address steps a warp and kind of 128 keys.
+// each (a lane its own: no conflict whatever the codes).  Keys and values stay without their
+// scales: the keys' multiply the scores, the values' the weights, in fp32, and the one rounding
+// to the type is that of the weights, as for sub-vectors.  (K^ rounded to bf16 moved a score of
+// 10 by 0.01; with V^ rounded the output in bf16 is off by 0.0029, without by 0.0023, of which
+// its own rounding is 0.0017.  The values' scales cost 9 % for that: 289 -> 315 us for 16
+// requests, one with 2048 new tokens.)  What a row's maximum bounds is then a score plus log2 of
+// the value's scale (by key block: the largest score, plus the power of two that bounds the
+// scales), so that the weights stay in the type's range whatever the scales are; the sum of
+// weights has fp32's.  The rebuild moves as many bytes of shared memory as that of sub-vectors,
+// in words of 4 bytes where those come in 8 or 16, so it issues more: 512 lookups and address
+// steps a warp and kind of 128 keys.
 #pragma once
 
 #include "vq_pfew.cuh"
@@ -75,11 +81,10 @@ struct ChunkShape {
     static constexpr int kStageBytes = kKeys * D * 2;
     static constexpr int kQBytes = kQTmem ? 0 : 128 * D * 2;  // a tile
     static constexpr size_t kSmem = (size_t)kTiles * kQBytes + kStages * kStageBytes + 65536;
-    // Scalar codes: their table at a fixed shared address, behind the static memory (and the
-    // system's 1024 bytes), then Q and the ring.  The array starts behind kStatic at least.
-    static constexpr int kTable = 3072;
-    static constexpr int kStatic = 1024 + (int)sizeof(PagedWalk<64>);
-    static constexpr size_t kScalarSmem = kTable - kStatic + kSmem;
+    // Scalar codes: the keys' scales of so many key blocks.  A block's are written once the stage
+    // that takes it was released: with three stages by the products of values two blocks back,
+    // with more after the weights of four blocks back (whatever the lengths of the segments).
+    static constexpr int kScaleBlocks = kStages == 3 ? 2 : 4;
 };
 
 // Instruction descriptor: kind::f16, fp32 accumulator, 16-bit operands of one
@@ -205,6 +210,21 @@ struct ChunkSeg {
     int32_t live;      // 0: no more segments
 };
 
+// Scalar codes: their table lies at a fixed shared address, behind the static memory (and the
+// system's 1024 bytes), Q and the ring behind it.  The static memory is at least kStatic, so
+// that the array, which begins behind it, need not be longer than kSmem.  For the scales to fit
+// the values' lie in what the plan used, and its stage of lengths is shorter than elsewhere.
+template <int D, int SUB>
+using ChunkWalk = PagedWalk<SUB == 2 ? 28 : 64, SUB == 2 ? ChunkShape<D>::kScaleBlocks * ChunkShape<D>::kKeys / 2 : 33>;
+template <int D>
+struct ScalarChunk {
+    using S = ChunkShape<D>;
+    static constexpr int kStatic = (int)(sizeof(ChunkWalk<D, 2>) + (2 * S::kStages + 15) * sizeof(uint64_t) + 2 * sizeof(ChunkSeg) +
+                                         128 + S::kScaleBlocks * S::kKeys * sizeof(float) + 8);
+    static constexpr int kTable = (1024 + kStatic + 24 + 127) / 128 * 128;  // (24: for alignment)
+    static constexpr size_t kSmem = kTable - (1024 + kStatic + 127) / 128 * 128 + S::kSmem;
+};
+
 // POLLS: the limit of every wait but the last, kChunkPolls except in a test.
 template <typename T, int D, int SUB, int POLLS = kChunkPolls>
 __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __grid_constant__ PagedArgs a)
@@ -230,24 +250,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     // as it is rebuilt, while the other kind is.
     constexpr int kSets = kScalar && kKinds == 2 ? 1 : 2;
     constexpr uint32_t kBf16 = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-    constexpr float kShift = weight_shift<T>();
-    // A row's maximum may lag by this many powers of two.  Rows of scalar codes differ in scale, so
-    // that maxima rise often, and every rise sends a warp's block down the longer path; where
-    // weights have fp32's range the lag can be longer (scales e^(0.5 z), 2048 tokens on 8192
-    // cached in bf16: 383 -> 304 us).
-    constexpr float kSlack = SUB == 2 && std::is_same<T, __nv_bfloat16>::value ? 32.f : kFewSlack;
-    constexpr bool kRedo = SUB == 2 && std::is_same<T, __half>::value;
+    // A row's maximum may lag by kSlack powers of two, and its weights start at 2^kShift.  Rows of
+    // scalar codes differ in scale, so that maxima rise often, and every rise sends a warp's block
+    // down the longer path: their lag is longer (2048 tokens on 8192 cached, scales e^(0.5 z):
+    // bf16, whose weights have fp32's range, 32 for 8, 383 -> 304 us as measured then; fp16, where
+    // 2^(lag + shift) has to stay below 2^16, 11 and 4 for 8 and 7, 437 -> 396 us, at dim 64 355 -> 321;
+    // a weight is off by 2^-29 of the row's largest then).
+    constexpr bool kHalfScalar = kScalar && std::is_same<T, __half>::value;
+    constexpr float kShift = kHalfScalar ? 4.f : weight_shift<T>();
+    constexpr float kSlack = kHalfScalar ? 11.f : kScalar ? 32.f : kFewSlack;
+    constexpr int kLift = 40;  // (fp16's scales are within 2^-24 .. 2^16)
+    constexpr bool kRedo = kHalfScalar;
     extern __shared__ __align__(128) unsigned char chunk_mem[];
-    __shared__ PagedWalk<64> w;
+    __shared__ __align__(16) ChunkWalk<D, SUB> w;
     __shared__ uint64_t full[kChunkStages], empty[kChunkStages], q_full[2], s_full[2], p_full[2], o_done[2], image[2], drain, seg_full[2], seg_empty[2];
     __shared__ ChunkSeg segs[2];
     __shared__ uint32_t valid[8][4];  // per key block (mod 8): which tokens are in a page
+    // scalar codes: kappa x the keys' scales; the values' lie in w.scratch, which the plan leaves
+    __shared__ __align__(16) float k_scale[SUB == 2 ? S::kScaleBlocks : 1][SUB == 2 ? kKeys : 4];
+    [[maybe_unused]] float (*v_scale)[kKeys] = reinterpret_cast<float (*)[kKeys]>(w.scratch);
     __shared__ uint32_t tmem_slot;
     __shared__ volatile uint32_t abort_word;
     // of scalar codes the table comes first, at its address
-    [[maybe_unused]] unsigned char *lines = chunk_mem + (S::kTable - (int)smem_addr(chunk_mem));
-    static_assert(1024 + sizeof w + sizeof full + sizeof empty + 7 * sizeof q_full + sizeof drain + sizeof segs + sizeof valid + 8 + 256 <= S::kTable,
-                  "static memory below the table");
+    static_assert(SUB != 2 || sizeof w + sizeof full + sizeof empty + 7 * sizeof q_full + sizeof drain + sizeof segs + sizeof valid +
+                                      sizeof k_scale + 8 <= ScalarChunk<D>::kStatic + 24,
+                  "the table lies behind the static memory");
+    [[maybe_unused]] unsigned char *lines = chunk_mem + (ScalarChunk<D>::kTable - (int)smem_addr(chunk_mem));
     unsigned char *q_mem = kScalar ? lines + 65536 : chunk_mem;
     unsigned char *ring = q_mem + (size_t)kTiles * S::kQBytes;
     unsigned char *k_image = ring + kChunkStages * S::kStageBytes, *v_image = k_image + 32768;  // of sub-vectors
@@ -425,6 +453,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         p[i / 2] = pack2<T>(x.x, x.y);
                     }
                 };
+                // scalar codes: two columns' scales, of the keys (kappa among them) and of the values
+                [[maybe_unused]] auto k_pair = [&](int col) { return *reinterpret_cast<const float2 *>(&k_scale[block % S::kScaleBlocks][col]); };
+                [[maybe_unused]] auto v_pair = [&](int col) { return *reinterpret_cast<const float2 *>(&v_scale[block % S::kScaleBlocks][col]); };
+                // .. 32 scores times the keys' scales, less ref (in one step, as below, so that a row's
+                // weights do not depend on the path); one that is not seen becomes -inf, whatever it was
+                [[maybe_unused]] auto scaled = [&](uint32_t (&v)[32], int c, uint32_t bits, float ref) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), k_pair(c * 32 + i),
+                                                 make_float2(-ref, -ref));
+                        v[i] = (bits >> i) & 1u ? __float_as_uint(x.x) : 0xff800000u;
+                        v[i + 1] = (bits >> (i + 1)) & 1u ? __float_as_uint(x.y) : 0xff800000u;
+                    }
+                };
+                // .. scores to weights, nothing masked; the largest of what is raised to a power
+                [[maybe_unused]] auto turn = [&](const auto &v, uint32_t *p, int col, float ref, float2 &add, float (&tops)[4]) {
+#pragma unroll
+                    for (int i = 0; i < (int)(sizeof v / 4); i += 2) {
+                        float2 x = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), k_pair(col + i),
+                                           make_float2(-ref, -ref));
+                        tops[i / 2 % 4] = max3(tops[i / 2 % 4], x.x, x.y);
+                        x.x = exp2_fast(x.x);
+                        x.y = exp2_fast(x.y);
+                        add = add2_rn(add, x);
+                        x = mul2_rn(x, v_pair(col + i));
+                        p[i / 2] = pack2<T>(x.x, x.y);
+                    }
+                };
+                // .. the power of two that bounds the values' scales
+                [[maybe_unused]] auto lift = [](float s) {
+                    const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s >= 0
+                    return (float)(e < -kLift ? -kLift : e > kLift ? kLift : e);
+                };
                 bool done = false;
                 // (scalar codes in fp16, whose maxima rise often: a first pass that was not kept has
                 // found the maximum, and there are no masks; 308 -> 284 us at dim 64)
@@ -436,21 +497,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     uint32_t p[kKeys / 2];
                     float tops[4] = {kNone, kNone, kNone, kNone};
                     float2 add = make_float2(0.f, 0.f);
+                    // (scalar codes at dim 128 by 16 columns: 363 -> 349 us; at 64 and 256 355 -> 362, 400 -> 411)
+                    constexpr int kCols = kScalar && D == 128 ? 16 : 32;
 #pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_load32_async(s_addr + c * 32, v);
+                    for (int c = 0; c < kKeys; c += kCols) {
+                        uint32_t v[kCols];
+                        if constexpr (kCols == 16) tmem_load16_async(s_addr + c, v);
+                        else tmem_load32_async(s_addr + c, v);
                         tmem_wait_ld(v);
+                        if constexpr (kScalar) {
+                            turn(v, p + c / 2, c, m, add, tops);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
+                            for (int i = 0; i < 32; i += 8)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tops[k] = max3(tops[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
-                        weights(v, p + c * 16, 32, m, add);
+                                for (int k = 0; k < 4; ++k)
+                                    tops[k] = max3(tops[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+                            weights(v, p + c / 2, 32, m, add);
+                        }
                     }
-                    const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.kappa;
+                    float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
+                    if constexpr (kScalar) {
+                        uint32_t most = 0;
+#pragma unroll
+                        for (int i = 0; i < kKeys / 64; ++i) {
+                            const float2 two = v_pair(64 * i + 2 * lane);
+                            most = max(most, __float_as_uint(fmaxf(fabsf(two.x), fabsf(two.y))));
+                        }
+                        most = __reduce_max_sync(0xffffffffu, most);
+                        top += m + lift(__uint_as_float(most));  // (of no use where m is -inf)
+                    } else {
+                        top *= a.kappa;
+                    }
                     if constexpr (kRedo) {
-                        known = true;
+                        known = !__any_sync(0xffffffffu, m == kNone);
                         known_top = top;
                     }
                     if (!__any_sync(0xffffffffu, top > m + (kSlack + kShift) || m == kNone)) {
@@ -463,6 +543,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 if (!done) {
                     // first the maximum, then the weights
                     float top = kNone;
+                    [[maybe_unused]] float most = 0.f;
                     if (kRedo && known) {
                         top = known_top;
                         saw = 1u;
@@ -474,10 +555,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                             const uint32_t bits = seen_bits(c);
                             saw |= bits;
                             tmem_wait_ld(v);
+                            if constexpr (kScalar) {
+                                scaled(v, c, bits, m == kNone ? 0.f : m);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
+                                for (int i = 0; i < 32; i += 2) {
+                                    const float2 s = v_pair(c * 32 + i);
+                                    top = max3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                                    most = max3(most, (bits >> i) & 1u ? fabsf(s.x) : 0.f, (bits >> (i + 1)) & 1u ? fabsf(s.y) : 0.f);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
+                            }
                         }
-                        top *= a.kappa;  // kappa > 0
+                        if constexpr (kScalar) top += (m == kNone ? 0.f : m) + lift(most);
+                        else top *= a.kappa;  // kappa > 0
                     }
                     // a row rises for its own scores alone, so that what it computes does
                     // not depend on the rows beside it; the others are scaled by 1
@@ -516,11 +608,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         const uint32_t bits = kRedo && known ? 0xffffffffu : seen_bits(c);
                         tmem_wait_ld(v);
                         // a score that is not seen is left out as -inf: weight 0, whatever it was
-                        if (!(kRedo && known)) {
+                        if (kRedo && known) {
+                            float tops[4] = {};
+                            turn(v, p, c * 32, ref, add, tops);
+                        } else if constexpr (kScalar) {
+                            scaled(v, c, bits, ref);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float2 x = make_float2(exp2_fast(__uint_as_float(v[i])), exp2_fast(__uint_as_float(v[i + 1])));
+                                add = add2_rn(add, x);
+                                const float2 s = v_pair(c * 32 + i);
+                                p[i / 2] = pack2<T>((bits >> i) & 1u ? x.x * s.x : 0.f, (bits >> (i + 1)) & 1u ? x.y * s.y : 0.f);
+                            }
+                        } else {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : 0xff800000u;
+                            weights(v, p, 32, ref, add);
                         }
-                        weights(v, p, 32, ref, add);
                         tmem_store16(s_addr + c * 16, p);
                     }
                     sum2 = add2_rn(sum2, add);
@@ -672,8 +776,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return paged_entry(a, s.r, (int32_t)t);
             };
             const int64_t head_off = ((int64_t)h << a.page_shift) * NS + part * kMyCodes;
-            // (scale: the row's, of scalar codes)
-            auto load_kind = [&](int j, int32_t &pg, int kd, uint32_t (&codes)[kCodeWords], uint32_t &scale) {
+            // (scale: the key's and the value's, of scalar codes, taken with the keys)
+            auto load_kind = [&](int j, int32_t &pg, int kd, uint32_t (&codes)[kCodeWords], uint32_t (&scale)[2]) {
                 if (pg < 0 || pg >= a.num_pages) {
                     pg = -1;
                     return;
@@ -692,16 +796,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     }
                 }
                 if constexpr (kScalar) {
-                    const uint16_t *scales = static_cast<const uint16_t *>(v ? a.v_scales : a.k_scales);
-                    const uint16_t *from = scales + (int64_t)pg * a.scale_stride + ((int64_t)h << a.page_shift) + off;
-                    scale = 0;
-                    if (VQ_SPAN(from, 1, scales, (a.num_pages - 1) * a.scale_stride + ((int64_t)a.hkv << a.page_shift)))
-                        scale = __ldg(from);  // (made a pair where it is used: here that would wait for the load)
+                    if (!v && part == 0) {  // the same for the warp
+                        const int64_t place = (int64_t)pg * a.scale_stride + ((int64_t)h << a.page_shift) + off;
+                        const int64_t most = (a.num_pages - 1) * a.scale_stride + ((int64_t)a.hkv << a.page_shift);
+                        const uint16_t *ks = static_cast<const uint16_t *>(a.k_scales), *vs = static_cast<const uint16_t *>(a.v_scales);
+                        scale[0] = VQ_SPAN(ks + place, 1, ks, most) ? __ldg(ks + place) : 0;
+                        scale[1] = VQ_SPAN(vs + place, 1, vs, most) ? __ldg(vs + place) : 0;
+                    }
                 }
             };
-            auto load = [&](int j, int32_t &pg, uint32_t (&codes)[kKinds][kCodeWords], uint32_t (&scale)[kKinds]) {
+            auto load = [&](int j, int32_t &pg, uint32_t (&codes)[kKinds][kCodeWords], uint32_t (&scale)[2]) {
 #pragma unroll
-                for (int kd = 0; kd < kKinds; ++kd) load_kind(j, pg, kd, codes[kd], scale[kd]);
+                for (int kd = 0; kd < kKinds; ++kd) load_kind(j, pg, kd, codes[kd], scale);
             };
             // a block's place in the ring: with two tiles the stages go K0 V0 K1 V1 ..,
             // with one K0 K1 V0 K2 V1 .. (there the scores of a block are issued before
@@ -712,8 +818,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return base_n + (j > 0 ? 2 * j - 1 : 0);
             };
             // rebuild this thread's part of its token of block j
-            auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords], uint32_t scale) -> bool {
-                scale = live ? scale * 0x10001u : 0;  // a pair of it (no token: a row of zeros, whatever its scale would be)
+            auto fill = [&](int j, int v, bool live, const uint32_t (&codes)[kCodeWords], const uint32_t (&scale)[2]) -> bool {
                 [[maybe_unused]] const unsigned char *base = (v ? v_image : k_image) + copy;
                 const uint32_t n = stage_of(j, v), st = n % kChunkStages, round = n / kChunkStages;
                 // (the stages are released in ring order, so that the phase before the one
@@ -725,6 +830,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     // was released after the weights of the one before that
                     const uint32_t have = __ballot_sync(0xffffffffu, live);
                     if (lane == 0 && part == 0) valid[block & 7][tk / 32] = have;
+                    if (kScalar && part == 0) {
+                        k_scale[block % S::kScaleBlocks][tk] = live ? a.kappa * unpack2<T>(scale[0]).x : 0.f;
+                        v_scale[block % S::kScaleBlocks][tk] = live ? unpack2<T>(scale[1]).x : 0.f;
+                    }
                 }
                 unsigned char *dst = ring + st * S::kStageBytes + (part * (kPieces / kSplit)) * (16 * kKeys) + tk * 16;
                 // eight pieces at a time (four of scalar codes), so that their loads overlap
@@ -738,7 +847,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                             image_row<8>(base, code_at(codes, c0 + c), w[c]);
                         } else if constexpr (kScalar) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) w[c][i] = mul2<T>(scalar_lookup<S::kTable>(codes[c0 + c], i, lane4 + 128 * v), scale);
+                            for (int i = 0; i < 4; ++i) w[c][i] = scalar_lookup<ScalarChunk<D>::kTable>(codes[c0 + c], i, lane4 + 128 * v);
                         } else {
                             uint32_t lo[2], hi[2];
                             image_row<4>(base, code_at(codes, 2 * (c0 + c)), lo);
@@ -749,7 +858,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                             w[c][3] = hi[1];
                         }
                     }
-                    if (!kScalar && !live) {  // no token: finite whatever its codes would be
+                    if (!live) {  // no token: finite whatever its codes would be
 #pragma unroll
                         for (int c = 0; c < kBatch; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0;
                     }
@@ -764,7 +873,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 return true;
             };
             // codes one block ahead, page entries two
-            uint32_t codes[kSets][kKinds][kCodeWords] = {}, scale[kSets][kKinds] = {};
+            uint32_t codes[kSets][kKinds][kCodeWords] = {}, scale[kSets][2] = {};
             int32_t pg[3];
             pg[0] = page_of(0);
             pg[1] = page_of(1);
@@ -774,8 +883,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 pg[2] = page_of(j + 2);
 #pragma unroll
                 for (int kd = 0; kd < kKinds; ++kd) {
-                    if (go) go = fill(j, kHalves ? vals : kd, pg[0] >= 0, codes[0][kd], scale[0][kd]);
-                    if constexpr (kSets == 1) load_kind(j + 1, pg[1], kd, codes[0][kd], scale[0][kd]);
+                    if (go) go = fill(j, kHalves ? vals : kd, pg[0] >= 0, codes[0][kd], scale[0]);
+                    if constexpr (kSets == 1) load_kind(j + 1, pg[1], kd, codes[0][kd], scale[0]);
                 }
                 if (!go) break;
                 pg[0] = pg[1];
@@ -785,8 +894,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     for (int kd = 0; kd < kKinds; ++kd) {
 #pragma unroll
                         for (int i = 0; i < kCodeWords; ++i) codes[0][kd][i] = codes[1][kd][i];
-                        scale[0][kd] = scale[1][kd];
                     }
+                    scale[0][0] = scale[1][0];
+                    scale[0][1] = scale[1][1];
                 }
             }
             base_n += 2 * nb;

@@ -16,7 +16,7 @@ template <typename T, int D>
 vq_status launch(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
 {
     auto kernel = vqk::paged_attn_chunk<T, D, 2>;
-    const size_t smem = vqk::ChunkShape<D>::kScalarSmem;
+    const size_t smem = vqk::ScalarChunk<D>::kSmem;
     if (!vqh_allow_smem(kernel, smem)) return vqh_failed();
     kernel<<<(unsigned)blocks, vqk::kChunkThreads, smem, st>>>(a);
     return vqh_launched(st, vqh_status_schunk);

@@ -23,7 +23,7 @@ template <int D, int POLLS>
 vq_status launch_polls(const vqk::PagedArgs &a, int blocks, cudaStream_t st)
 {
     auto kernel = vqk::paged_attn_chunk<__half, D, 2, POLLS>;
-    const size_t smem = vqk::ChunkShape<D>::kScalarSmem;
+    const size_t smem = vqk::ScalarChunk<D>::kSmem;
     if (!vqh_allow_smem(kernel, smem)) return vqh_failed();
     kernel<<<(unsigned)blocks, vqk::kChunkThreads, smem, st>>>(a);
     return vqh_launched(st, vqh_status_scache);

@@ -84,10 +84,9 @@ def attention(q, cu, lens, table, k_codes, v_codes, k_scales, v_scales, k_cents,
         (after the sum) and a rounded factor kappa and its product;
       * a weight by a relative e_t <= ln 2 (d_t + 2 u (M - S_t + 8)) + 2^-21;
       * the sums add (T + 200) u.
-    `tensor`: the tensor kernels round V^ to the rows' type (h = half its epsilon relative, or
-    half its least step) and, for longer runs, K^ too and the weights: d_t gains h A_t + kappa
-    |q|_1 step, e_t gains h and T times half the least step (as for codes), out gains
-    max|V^| h + step."""
+    `tensor`: the tensor kernels round the weights to the rows' type (h = half its epsilon
+    relative, or half its least step): e_t gains h and T times half the least step (as for
+    codes), out its own rounding, max|V^| h + step."""
     u = 2.0 ** -24
     h = HALF_EPS[dtype] if tensor else 0.0
     step = HALF_STEP[dtype] if tensor else 0.0
@@ -130,7 +129,7 @@ def attention(q, cu, lens, table, k_codes, v_codes, k_scales, v_scales, k_cents,
                     out[row, head] = w @ v / total
                     lse[row, head] = top + math.log(total)
                     n = len(s)
-                    d = ((dim + 6) * u + h) * kappa * (np.abs(k) @ np.abs(q[row, head])) + kappa * np.abs(q[row, head]).sum() * step
+                    d = (dim + 6) * u * kappa * (np.abs(k) @ np.abs(q[row, head]))
                     e = math.log(2) * (d + 2 * u * ((top - s) / math.log(2) + 8)) + 2.0 ** -21 + h
                     most = np.abs(v).max()
                     tol[row, head] = 1.1 * (most * (2 * (w @ e) / total + 2 * n * step + 4 * (n + 200) * u + h) + step)

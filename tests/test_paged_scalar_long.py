@@ -66,12 +66,11 @@ def run(vq, c, window=0, known=True, **kw):
 
 def check(c, out, lse, window=0, chunk=False):
     """Against the definition in 64 bits, with the bounds of scalar_reference.attention; the
-    few-row kernel (not `chunk`) rounds no key or value, and its weights to two pieces."""
+    few-row kernel (not `chunk`) rounds its weights to two pieces."""
     u = 2.0 ** -24
     dtype = c["dtype"]
     eps, tiny = ref.HALF_EPS[dtype], ref.HALF_STEP[dtype]
     h, step = (eps, tiny) if chunk else (eps ** 2, 2.0 ** -31 if dtype is F16 else tiny)
-    kh = eps if chunk else 0.0
     tokens, hq, dim = c["q"].shape
     pages, hkv, page, _ = c["kc"].shape
     scale, cents = 1 / math.sqrt(dim), c["cents"].to(dtype).double()
@@ -107,11 +106,11 @@ def check(c, out, lse, window=0, chunk=False):
                 total = w.sum(1, keepdim=True)
                 want = w @ values / total
                 want_lse = (top + torch.log(total))[:, 0]
-                d = ((dim + 6) * u + kh) * kappa * (q.abs() @ keys.abs().t()) + kappa * q.abs().sum(1, keepdim=True) * (tiny if chunk else 0)
+                d = (dim + 6) * u * kappa * (q.abs() @ keys.abs().t())
                 e = math.log(2) * (d + 2 * u * ((top - s) / math.log(2) + 40)) + 2.0 ** -21 + h
                 e = e.masked_fill(~seen, 0)
                 big = values[seen.any(0)].abs().max()
-                tol = 1.1 * (big * (2 * (w * e).sum(1, keepdim=True) / total + 2 * n * step + 4 * (n + 200) * u + kh) + tiny)
+                tol = 1.1 * (big * (2 * (w * e).sum(1, keepdim=True) / total + 2 * n * step + 4 * (n + 200) * u) + tiny)
                 tol_lse = 1.1 * (e.amax(1) + n[:, 0] * step + (n[:, 0] + 200) * u) + 4 * u * want_lse.abs()
                 off = (out[a:b, head].double() - want).abs() - (tol + eps * (want.abs() + tol) + tiny)
                 assert (off[some] <= 0).all(), f"request {r} head {head}: beyond the bound by {off[some].max():.3g}"
@@ -156,6 +155,30 @@ def test_values_of_every_size(vq):
     c["vs"][page, :, at] = 8192.0
     check(c, *run(vq, c))
     c["vs"].zero_()  # no value at all
+    out, lse = run(vq, c)
+    assert not out.any() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dim, dtype, low, high", [(64, F16, -20, 13), (128, F16, -20, 13), (128, BF16, -90, 90), (256, F16, -20, 13),
+                                                   (256, BF16, -90, 90)])
+def test_values_of_every_size_in_chunks(vq, dim, dtype, low, high):
+    """The same for a chunk, whose rows' references follow the scales block by block."""
+    c = make(dim + 7, dim, dtype, 8, 2, 16, [3000], [700])
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    c["vs"] = torch.exp2(torch.randint(low, high, c["vs"].shape, generator=gen, device="cuda").float()).to(dtype)
+    check(c, *run(vq, c), chunk=True)
+    pages = c["table"][0, :188].long()
+    c["vs"][pages] = torch.exp2(torch.linspace(low, high - 1, 188, device="cuda")).to(dtype)[:, None, None]  # growing
+    check(c, *run(vq, c), chunk=True)
+    c["vs"][pages] = torch.exp2(torch.linspace(high - 1, low, 188, device="cuda")).to(dtype)[:, None, None]
+    check(c, *run(vq, c), chunk=True)
+    # tokens that the first rows do not see, far larger: their results stay those without them
+    c["vs"].fill_(2.0 ** -14)
+    want, want_lse = run(vq, c)
+    c["vs"][c["table"][0, 186].long()] = 8192.0
+    out, lse = run(vq, c)
+    assert torch.equal(out[:600], want[:600]) and torch.equal(lse[:600], want_lse[:600])
+    c["vs"].zero_()
     out, lse = run(vq, c)
     assert not out.any() and torch.isfinite(lse).all()
 

@@ -38,17 +38,16 @@ bool tensor_layout(const vqk::PagedArgs &a)
 
 TensorKernels tensor_kernels(int32_t dim, int32_t group, int64_t max_new)
 {
-    // Three items of 8 rows, four at dim 64: the chunk kernel takes the time of a tile of 128
-    // rows however few there are, the few-row kernel that of its items.  16 requests of 8000 (2
-    // of 30000), few-row against chunk kernel, us: dim 128 three 130 : 147 (69 : 91), four 165 :
-    // 149 (83 : 93); dim 64 four 124 : 120 (65 : 81), five 149 : 122 (73 : 81); dim 256 three
-    // 118 : 124 (67 : 81), four 147 : 126 (81 : 83).
-    const int32_t items = dim == 64 ? 4 : 3;
+    // Four items of 8 rows: the chunk kernel takes the time of a tile of 128 rows however few
+    // there are, the few-row kernel that of its items.  16 requests of 8000 (2 of 30000), few-row
+    // against chunk kernel, us: dim 128 three 128 : 160 (69 : 99), four 163 : 161 (83 : 102), five
+    // 196 : 163 (95 : 104); dim 64 four 122 : 128 (64 : 83), five 147 : 128 (73 : 85); dim 256
+    // three 116 : 143 (65 : 89), four 145 : 145 (77 : 89), five 173 : 145 (89 : 89).
     // items of 4 rows where no request has more
     const int rows = max_new > 0 && group <= 4 && max_new * group <= 4 ? 4 : vqh_few_rows();
     // An item's cost: 2 : 4 : 8 : 12 give drafts of 16 requests 70.8 : 64.6 : 62.6 : 66.7 us, 32
     // uneven decodes 156.8 : 154.8 : 152.7 : 150.7, 64 short ones 56.4 : 54.4 : 52.3 : 52.3
-    return TensorKernels{rows, 1, vqh_chunk_tiles(dim), items, 8, vqh_paged_sfew, vqh_paged_schunk};
+    return TensorKernels{rows, 1, vqh_chunk_tiles(dim), 4, 8, vqh_paged_sfew, vqh_paged_schunk};
 }
 
 template <typename T>

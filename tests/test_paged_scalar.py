@@ -407,3 +407,16 @@ def test_step(vq, dtype, dim):
                     assert np.abs(out[row, h].double().cpu().numpy() - want).max() < 8 * 4 * 2.0 ** -8
                 row += 1
         assert lens.tolist() == [len(a) for a in lines]
+
+
+def test_example_serving_loop_in_4_bits(vq):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_serving.py")
+    spec = importlib.util.spec_from_file_location("paged_serving", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    for requests in ("5", "8"):
+        report = module.main(["--scalar", "--steps", "20", "--requests", requests, "--prompt", "300", "--answer", "30"])
+        assert report["tokens"] > 500

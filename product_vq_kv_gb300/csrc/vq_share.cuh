@@ -23,11 +23,13 @@
 //
 // Compact.  used = pages that are not on the free list.  The i-th held page at or
 // past `used` moves to the i-th free page below it.  Bound by latency too: a bit a page, so that
-// 200,000 pages are one word for each thread of a cluster, and counts of bits.
+// 200,000 pages are one word for each thread of a cluster, and counts of bits (4,096 pages 19 us
+// on the device with a cold cache, 200,000 of 1000 requests 34; with a byte a page 49).
 //
 // Copy.  Pairs of pages in up to kCopyPools pools, each of any number of layers.
 // Bound by HBM: every byte is read and written once; a warp takes 4 KiB of one page
-// at a time, eight 16-byte loads in flight a lane.
+// at a time, eight 16-byte loads in flight a lane (2047 pages of eight layers, 278 MB: 92 us, 89 % of
+// the rate of a plain copy; pieces of 2 and 8 KiB and two to eight blocks an SM are no faster).
 #pragma once
 
 #include <cooperative_groups.h>

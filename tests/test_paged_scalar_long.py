@@ -299,3 +299,14 @@ def test_waits_that_give_up(vq, harness, polls, dim, hq, hkv, new, held):
         assert marked.all() and gave_up
     again, _ = run(vq, c)
     assert torch.equal(again, want) and vq.vq_kernel_status() == 0
+
+
+@pytest.mark.parametrize("dim, dtype, hq, hkv, page", SHAPES)
+def test_many_requests(vq, dim, dtype, hq, hkv, page):
+    """More requests than a block keeps the lengths of, of one token, of none and of chunks."""
+    gen = torch.Generator().manual_seed(dim)
+    lens = torch.randint(1, 900, (61,), generator=gen).tolist()
+    news = [min(n, (0, 1, 3, 40, 150)[i % 5]) for i, n in enumerate(lens)]
+    c = make(dim + 9, dim, dtype, hq, hkv, page, lens, news, holes=True)
+    for known in (True, False):
+        check(c, *run(vq, c, known=known), chunk=True)

@@ -50,10 +50,10 @@
 // to the type is that of the weights, as for sub-vectors.  (K^ rounded to bf16 moved a score of
 // 10 by 0.01; with V^ rounded the output in bf16 is off by 0.0029, without by 0.0023, of which
 // its own rounding is 0.0017.  The values' scales cost 9 % for that: 289 -> 315 us for 16
-// requests, one with 2048 new tokens.)  What a row's maximum bounds is then a score plus log2 of
-// the value's scale (by key block: the largest score, plus the power of two that bounds the
-// scales), so that the weights stay in the type's range whatever the scales are; the sum of
-// weights has fp32's.  The rebuild moves as many bytes of shared memory as that of sub-vectors,
+// requests, one with 2048 new tokens.)  What a row's reference follows is then the largest of its
+// tokens' weights times scales, 2^(score - m) |s|, a token at a time, so that these stay in the type's
+// range whatever the scales are, and a token of a large value and no weight moves nothing; the sum
+// of weights has fp32's range.  The rebuild moves as many bytes of shared memory as that of sub-vectors,
 // in words of 4 bytes where those come in 8 or 16, so it issues more: 512 lookups and address
 // steps a warp and kind of 128 keys.
 #pragma once
@@ -255,11 +255,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
     // down the longer path: their lag is longer (2048 tokens on 8192 cached, scales e^(0.5 z):
     // bf16, whose weights have fp32's range, 32 for 8, 383 -> 304 us as measured then; fp16, where
     // 2^(lag + shift) has to stay below 2^16, 11 and 4 for 8 and 7, 437 -> 396 us, at dim 64 355 -> 321;
-    // a weight is off by 2^-29 of the row's largest then).
+    // a weight times its scale is off by 2^-29 of the row's largest then).
     constexpr bool kHalfScalar = kScalar && std::is_same<T, __half>::value;
     constexpr float kShift = kHalfScalar ? 4.f : weight_shift<T>();
     constexpr float kSlack = kHalfScalar ? 11.f : kScalar ? 32.f : kFewSlack;
-    constexpr int kLift = 40;  // (fp16's scales are within 2^-24 .. 2^16)
+    // How far the values' scales may move a reference, in powers of two.  fp16: its scales, 2^-24 ..
+    // 2^16, move it as far as they reach; what is below stands for scales of 0.  bf16, whose weights have
+    // fp32's range: so that weights times scales stay in it (up to 2^(96 - 60 + 32)), and a sum of
+    // weights too when the reference goes from one end to the other (60 + 10 + 32 < 126).
+    constexpr float kLiftLow = kHalfScalar ? -40.f : -10.f, kLiftHigh = kHalfScalar ? 40.f : 60.f;
+    constexpr float kMostProduct = kHalfScalar ? 32768.f : 4294967296.f;  // 2^(kSlack + kShift)
+    constexpr float kMostSum = 1.2089258e24f;  // 2^80: of one block's weights, for a reference to stay
     constexpr bool kRedo = kHalfScalar;
     extern __shared__ __align__(128) unsigned char chunk_mem[];
     __shared__ __align__(16) ChunkWalk<D, SUB> w;
@@ -467,38 +473,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         v[i + 1] = (bits >> (i + 1)) & 1u ? __float_as_uint(x.y) : 0xff800000u;
                     }
                 };
-                // .. scores to weights, nothing masked; the largest of what is raised to a power
-                [[maybe_unused]] auto turn = [&](const auto &v, uint32_t *p, int col, float ref, float2 &add, float (&tops)[4]) {
+                // .. scores to weights, nothing masked; the largest weight times scale, whatever its sign
+                // (two maxima at a time: four take registers that the pass lacks, 357 -> 366 us at dim 64
+                // and 494 -> 522 at 256, 2048 tokens on 8192 in fp16)
+                [[maybe_unused]] auto turn = [&](const auto &v, uint32_t *p, int col, float ref, float2 &add, float (&most)[2]) {
 #pragma unroll
                     for (int i = 0; i < (int)(sizeof v / 4); i += 2) {
                         float2 x = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), k_pair(col + i),
                                            make_float2(-ref, -ref));
-                        tops[i / 2 % 4] = max3(tops[i / 2 % 4], x.x, x.y);
                         x.x = exp2_fast(x.x);
                         x.y = exp2_fast(x.y);
                         add = add2_rn(add, x);
                         x = mul2_rn(x, v_pair(col + i));
+                        most[i / 2 % 2] = max3(most[i / 2 % 2], fabsf(x.x), fabsf(x.y));
                         p[i / 2] = pack2<T>(x.x, x.y);
                     }
                 };
-                // .. the power of two that bounds the values' scales
-                [[maybe_unused]] auto lift = [](float s) {
-                    const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s >= 0
-                    return (float)(e < -kLift ? -kLift : e > kLift ? kLift : e);
-                };
+                // .. what a value's scale adds to its token's score in a reference
+                [[maybe_unused]] auto lift = [&](float s) { return fminf(fmaxf(log2_fast(fabsf(s)), kLiftLow), kLiftHigh); };
                 bool done = false;
-                // (scalar codes in fp16, whose maxima rise often: a first pass that was not kept has
-                // found the maximum, and there are no masks; 308 -> 284 us at dim 64)
+                // scalar codes: whether the first pass has judged this row, and that its reference has
+                // to rise (for its own tokens alone, whatever path the rows beside it send the warp down)
+                [[maybe_unused]] bool judged = false, over = false;
+                // (in fp16, whose references rise often: a first pass that was not kept has found where
+                // to, and there are no masks; 308 -> 284 us at dim 64)
                 [[maybe_unused]] bool known = false;
                 [[maybe_unused]] float known_top = kNone;
                 if (whole && j > 0) {  // the same for all rows of the tile
                     // one pass with the maximum so far, kept if no score of the warp's
                     // rows exceeds it by more than the slack; the scores still stand then
                     uint32_t p[kKeys / 2];
-                    float tops[4] = {kNone, kNone, kNone, kNone};
+                    [[maybe_unused]] float tops[4] = {kNone, kNone, kNone, kNone};
+                    [[maybe_unused]] float most[2] = {};
                     float2 add = make_float2(0.f, 0.f);
-                    // (scalar codes at dim 128 by 16 columns: 363 -> 349 us; at 64 and 256 355 -> 362, 400 -> 411)
-                    constexpr int kCols = kScalar && D == 128 ? 16 : 32;
+                    // (scalar codes at dim 64 and 128 by 16 columns: 380 -> 357 us, 363 -> 349; at 256 494 -> 563)
+                    constexpr int kCols = kScalar && D <= 128 ? 16 : 32;
 #pragma unroll
                     for (int c = 0; c < kKeys; c += kCols) {
                         uint32_t v[kCols];
@@ -506,7 +515,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                         else tmem_load32_async(s_addr + c, v);
                         tmem_wait_ld(v);
                         if constexpr (kScalar) {
-                            turn(v, p + c / 2, c, m, add, tops);
+                            turn(v, p + c / 2, c, m, add, most);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 32; i += 8)
@@ -516,24 +525,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                             weights(v, p + c / 2, 32, m, add);
                         }
                     }
-                    float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
                     if constexpr (kScalar) {
-                        uint32_t most = 0;
-#pragma unroll
-                        for (int i = 0; i < kKeys / 64; ++i) {
-                            const float2 two = v_pair(64 * i + 2 * lane);
-                            most = max(most, __float_as_uint(fmaxf(fabsf(two.x), fabsf(two.y))));
+                        const float high = fmaxf(most[0], most[1]);
+                        // (a NaN is over, and so is a weight past fp32's largest: the sum tells, for a
+                        // value's scale of 0 makes nothing of it in the product)
+                        const bool sane = add.x + add.y <= kMostSum;
+                        judged = m != kNone;
+                        over = !(sane && high <= kMostProduct);
+                        if constexpr (kRedo) {
+                            known = judged && sane && high <= 3.402823466e38f;
+                            known_top = m + log2_fast(high);
                         }
-                        most = __reduce_max_sync(0xffffffffu, most);
-                        top += m + lift(__uint_as_float(most));  // (of no use where m is -inf)
                     } else {
-                        top *= a.kappa;
+                        const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.kappa;
+                        over = top > m + (kSlack + kShift);
                     }
-                    if constexpr (kRedo) {
-                        known = !__any_sync(0xffffffffu, m == kNone);
-                        known_top = top;
-                    }
-                    if (!__any_sync(0xffffffffu, top > m + (kSlack + kShift) || m == kNone)) {
+                    if (!__any_sync(0xffffffffu, over || m == kNone)) {
                         done = true;
                         sum2 = add2_rn(sum2, add);
 #pragma unroll
@@ -543,9 +550,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                 if (!done) {
                     // first the maximum, then the weights
                     float top = kNone;
-                    [[maybe_unused]] float most = 0.f;
-                    if (kRedo && known) {
-                        top = known_top;
+                    const bool all_known = kRedo && __all_sync(0xffffffffu, known);
+                    if (all_known) {
                         saw = 1u;
                     } else {
 #pragma unroll 1
@@ -560,22 +566,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
 #pragma unroll
                                 for (int i = 0; i < 32; i += 2) {
                                     const float2 s = v_pair(c * 32 + i);
-                                    top = max3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                                    most = max3(most, (bits >> i) & 1u ? fabsf(s.x) : 0.f, (bits >> (i + 1)) & 1u ? fabsf(s.y) : 0.f);
+                                    top = max3(top, __uint_as_float(v[i]) + lift(s.x), __uint_as_float(v[i + 1]) + lift(s.y));
                                 }
                             } else {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) top = fmaxf(top, (bits >> i) & 1u ? __uint_as_float(v[i]) : kNone);
                             }
                         }
-                        if constexpr (kScalar) top += (m == kNone ? 0.f : m) + lift(most);
+                        if constexpr (kScalar) top += m == kNone ? 0.f : m;
                         else top *= a.kappa;  // kappa > 0
                     }
+                    if (kRedo && known) top = known_top;
                     // a row rises for its own scores alone, so that what it computes does
                     // not depend on the rows beside it; the others are scaled by 1
-                    const bool rise = top > m + (kSlack + kShift);
+                    const bool rise = kScalar && judged ? over : top > m + (kSlack + kShift);
                     if (__any_sync(0xffffffffu, rise)) {
-                        const float to = rise ? top - kShift : m;
+                        const float to = rise ? (kScalar ? fmaxf(top - kShift, m) : top - kShift) : m;
                         const float f = rise ? exp2_fast(m - to) : 1.f;
                         m = to;
                         sum2 = make_float2(sum2.x * f, sum2.y * f);
@@ -605,12 +611,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_attn_chunk(const __gri
                     for (int c = 0; c < kKeys / 32; ++c) {
                         uint32_t v[32], p[16];
                         tmem_load32_async(s_addr + c * 32, v);
-                        const uint32_t bits = kRedo && known ? 0xffffffffu : seen_bits(c);
+                        const uint32_t bits = all_known ? 0xffffffffu : seen_bits(c);
                         tmem_wait_ld(v);
                         // a score that is not seen is left out as -inf: weight 0, whatever it was
-                        if (kRedo && known) {
-                            float tops[4] = {};
-                            turn(v, p, c * 32, ref, add, tops);
+                        if (all_known) {
+                            float most[2] = {};
+                            turn(v, p, c * 32, ref, add, most);
                         } else if constexpr (kScalar) {
                             scaled(v, c, bits, ref);
 #pragma unroll

@@ -129,6 +129,14 @@ __device__ __forceinline__ float exp2_fast(float x)
     return r;
 }
 
+// log2 x, -inf for 0 and what rounds to it; error 2^-22.
+__device__ __forceinline__ float log2_fast(float x)
+{
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;

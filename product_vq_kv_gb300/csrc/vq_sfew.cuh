@@ -98,7 +98,7 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const floa
         for (int c = 0; c < 4; ++c) {
             p[h][c] = exp2_fast(st[h][c] - m[c & 1]);
             w[h][c] = p[h][c] * vs[h][c >> 1] * f[c & 1];
-            high = max3(high, p[h][c] * kSFewLess, w[h][c]);
+            high = max3(high, p[h][c] * kSFewLess, fabsf(w[h][c]));
         }
     if (__any_sync(0xffffffffu, high > kSFewTop)) {
         // a row rises for its own scores and weights alone, so that what it computes does not
@@ -128,7 +128,7 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const floa
 #pragma unroll
                 for (int k = c; k < 4; k += 2) {
                     p[h][k] = exp2_fast(st[h][k] - m[c]);
-                    most = fmaxf(most, p[h][k] * vs[h][k >> 1]);
+                    most = fmaxf(most, p[h][k] * fabsf(vs[h][k >> 1]));
                 }
             most = over_lanes(most);
             if (most * f[c] > kSFewTop) {

@@ -99,3 +99,16 @@ def test_large_values_without_weight(vq, dim, dtype, page, new, size):  # noqa: 
     for wrong in (torch.zeros_like(out), out * 0.9):
         with pytest.raises(AssertionError, match="bounds off"):
             check(c, wrong, lse, chunk)
+
+
+@pytest.mark.parametrize("dim, dtype, page", FORMS)
+@pytest.mark.parametrize("new", [1, 3, 200])
+def test_values_of_both_signs(vq, dim, dtype, page, new):  # noqa: F811
+    """Value scales below zero: a caller's cache may hold them."""
+    c = make(dim, dim, dtype, 8, 2, page, [1500, 77], [new, 1])
+    flip = torch.rand(c["vs"].shape, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") < 0.5
+    c["vs"] = torch.where(flip, -c["vs"], c["vs"])
+    check(c, *run(vq, c), new * 4 > 32)
+    c["vs"] = -c["vs"].abs()
+    c["ks"] = torch.where(flip, -c["ks"], c["ks"])
+    check(c, *run(vq, c), new * 4 > 32)

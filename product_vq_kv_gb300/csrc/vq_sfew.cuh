@@ -115,7 +115,15 @@ __device__ __forceinline__ void sfew_weights(const float (&st)[H][4], const floa
             for (int h = 0; h < H; ++h) top = fmaxf(top, fmaxf(st[h][c], st[h][c + 2]));
             top = over_lanes(top);
             float scale = 1.f;  // of the accumulators
-            if (exp2_fast(top - m[c]) * kSFewLess > kSFewTop) {
+            // for its scores, or for a weight whose product with the value's scale passes fp32's
+            // largest (against the largest score none does)
+            bool past = false;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int k = c; k < 4; k += 2) past |= !(p[h][k] * fabsf(vs[h][k >> 1]) <= 3.402823466e38f);
+            past = (__ballot_sync(0xffffffffu, past) & (0x11111111u << (threadIdx.x & 3))) != 0;  // the row's lanes
+            if (past || exp2_fast(top - m[c]) * kSFewLess > kSFewTop) {
                 const float to = f[c] * exp2_fast(top - m[c]);
                 f[c] = fminf(to, kSFewMost);
                 scale = f[c] / to;  // (0 where `to` is infinite: what was is nothing beside it)
@@ -506,14 +514,22 @@ __global__ void __launch_bounds__(SFewShape<D>::kWarps * 32, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[i][c] += __shfl_xor_sync(0xffffffffu, o[i][c], 2);
             }
-            // to weights without the factors
+            // to weights without the factors, and no larger than 1 (a maximum may have lagged): by
+            // powers of two, so that sums of large values stay in fp32 where values do
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float inv = 1.f / factor[c];
+                float all = sum[c];
+                all += __shfl_xor_sync(0xffffffffu, all, 4);
+                all += __shfl_xor_sync(0xffffffffu, all, 8);
+                all += __shfl_xor_sync(0xffffffffu, all, 16);
+                const int lag = all > 1.f && all <= 3.402823466e38f ? (int)(__float_as_uint(all) >> 23) - 127 : 0;
+                const float less = __uint_as_float((uint32_t)(127 - lag) << 23), inv = 1.f / factor[c];
+                m[c] += (float)lag;
+                sum[c] *= less;
 #pragma unroll
                 for (int i = 0; i < kMma; ++i) {
-                    o[i][c] *= inv;
-                    o[i][c + 2] *= inv;
+                    o[i][c] = o[i][c] * less * inv;
+                    o[i][c + 2] = o[i][c + 2] * less * inv;
                 }
             }
             // (what it looks through for tokens that rows see: this warp's groups of 16)

@@ -112,3 +112,21 @@ def test_values_of_both_signs(vq, dim, dtype, page, new):  # noqa: F811
     c["vs"] = -c["vs"].abs()
     c["ks"] = torch.where(flip, -c["ks"], c["ks"])
     check(c, *run(vq, c), new * 4 > 32)
+
+
+@pytest.mark.parametrize("dim, page", [(64, 16), (128, 16), (256, 32), (96, 16)])
+@pytest.mark.parametrize("new", [1, 3, 200])
+@pytest.mark.parametrize("power", [-90, 90, 118])
+def test_values_of_bf16_range(vq, dim, page, new, power):  # noqa: F811
+    """Values near both ends of bf16's range, under scores that rise along the sequence (so that
+    references lag) and that fall."""
+    if power > 90 and (new == 200 or dim == 96):
+        pytest.skip("sums of hundreds of such values pass fp32's largest")
+    for rising in (True, False):
+        c = make(dim + new, dim, BF16, 8, 2, page, [900], [new])
+        held = -(-900 // page)
+        grow = torch.exp(torch.linspace(-3, 1.7, held * page, device="cuda").reshape(held, 1, page))
+        here = c["table"][0, :held].long()
+        c["ks"][here] = (c["ks"][here] * (grow if rising else 1 / grow * math.exp(-1.3))).to(BF16)
+        c["vs"] = (c["vs"].float() * 2.0 ** power).to(BF16)
+        check(c, *run(vq, c), new * 4 > 32)

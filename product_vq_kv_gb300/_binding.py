@@ -1119,7 +1119,8 @@ def vq_paged_copy(pairs: torch.Tensor, pools, layered: bool = False,
     page contiguous; the pages may be strided.  Pages are written in place."""
     rows = pairs.shape[0] if isinstance(pairs, torch.Tensor) and pairs.dim() == 2 else None
     _i32_tensor(pairs, "pairs", (rows, 2), None)
-    if isinstance(pools, torch.Tensor) or not all(isinstance(t, torch.Tensor) for t in pools):
+    pools = None if isinstance(pools, torch.Tensor) else list(pools)  # (a generator can be read once)
+    if pools is None or not all(isinstance(t, torch.Tensor) for t in pools):
         raise TypeError("pools must be a list of torch.Tensor")
     if not 1 <= len(pools) <= PAGED_MAX_POOLS:
         raise ValueError(f"expected 1 to {PAGED_MAX_POOLS} pools, got {len(pools)}")

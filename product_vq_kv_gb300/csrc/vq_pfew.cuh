@@ -247,16 +247,6 @@ __device__ __forceinline__ uint32_t scalar_lookup(uint32_t word, int i, uint32_t
     return v;
 }
 
-// Two products in the 16-bit type.
-template <typename T>
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    if constexpr (std::is_same<T, __half>::value) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // Line c of a codebook's image: its row 64 / SUB times.  The copies are
 // written in an order that starts at c, so that the lanes of a wavefront meet in
 // no bank.  The caller synchronises.

@@ -28,6 +28,8 @@ def check(c, out, lse, chunk=False):
         two (its square): h more.  Their reference is such that the row's largest w_t |s_t| lies at
         2^3 or above in fp16 (2^6 with two pieces), where the least step is 2^-24: half of that
         is `floor` of it.  bf16 has fp32's range: none.
+      * a weight of less than 2^-60 of the row's largest may count as none: powers below 2^-126 have
+        fewer bits or are 0, and a reference lies up to 60 above the largest score.
       * sums of n products are off by 4 (n + 200) u of the sum of magnitudes."""
     u = 2.0 ** -24
     dtype = c["dtype"]
@@ -70,7 +72,8 @@ def check(c, out, lse, chunk=False):
                 e = e.masked_fill(~seen, 0)
                 most = (w * sizes[1].abs()).amax(1, keepdim=True)
                 tol = 1.1 * ((w * (e + h)) @ values.abs() / total + want.abs() * (w * e).sum(1, keepdim=True) / total +
-                             n * floor * most * cents.abs().max() / total + 4 * (n + 200) * u * sums)
+                             n * floor * most * cents.abs().max() / total + 4 * (n + 200) * u * sums +
+                             (w * (w < 2.0 ** -60)) @ values.abs() / total)
                 tol = tol + eps * (want.abs() + tol) + tiny
                 tol_lse = 1.1 * (e.amax(1) + (n[:, 0] + 200) * u) + 4 * u * want_lse.abs()
                 off = (out[a:b, head].double() - want).abs() / tol
@@ -130,3 +133,36 @@ def test_values_of_bf16_range(vq, dim, page, new, power):  # noqa: F811
         c["ks"][here] = (c["ks"][here] * (grow if rising else 1 / grow * math.exp(-1.3))).to(BF16)
         c["vs"] = (c["vs"].float() * 2.0 ** power).to(BF16)
         check(c, *run(vq, c), new * 4 > 32)
+
+
+@pytest.mark.parametrize("dim, dtype, page", FORMS)
+@pytest.mark.parametrize("new", [1, 3, 200])
+def test_scores_that_leap_over_values_of_zero(vq, dim, dtype, page, new):  # noqa: F811
+    """Tokens of no value whose scores pass all others' by up to 2^200 at once: they take the
+    weight, and nothing becomes infinite."""
+    c = make(dim + 3, dim, dtype, 8, 2, page, [1500], [new])
+    c["q"] = c["q"].abs()
+    for at, size in ((300, 0.5), (431, 1.0), (700, 2.0), (701, 2.0), (1100, 3.5)):  # keys that point along every query
+        entry = c["table"][0, at // page].long(), slice(None), at % page
+        c["kc"][entry], c["ks"][entry], c["vs"][entry] = 255, size, 0.0
+    out, lse = run(vq, c)
+    assert torch.isfinite(out).all()
+    check(c, out, lse, new * 4 > 32)
+
+
+@pytest.mark.parametrize("dim, dtype, page", FORMS)
+@pytest.mark.parametrize("new", [3, 300])
+def test_rows_beside_rows_of_nan(vq, dim, dtype, page, new):  # noqa: F811
+    """Uneven scales of both signs: a row has the same bits whatever path the rows beside it take."""
+    c = make(dim + 4, dim, dtype, 8, 2, page, [2000], [new], spread=2.0)
+    flip = torch.rand(c["vs"].shape, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") < 0.5
+    c["vs"] = torch.where(flip, -c["vs"], c["vs"])
+    out, lse = run(vq, c)
+    check(c, out, lse, new * 4 > 32)
+    hit = torch.zeros(c["q"].shape[:2], dtype=torch.bool, device="cuda")
+    hit[::7, 1] = hit[1::9, 6] = hit[2::31] = True
+    for value in (math.nan, math.inf, 300.0):
+        q = c["q"].clone()
+        q[hit] = q[hit] * value
+        got, got_lse = run(vq, {**c, "q": q})
+        assert torch.equal(got[~hit], out[~hit]) and torch.equal(got_lse[~hit], lse[~hit])

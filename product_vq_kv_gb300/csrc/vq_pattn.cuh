@@ -81,7 +81,7 @@ struct PagedArgs {
     PagedNote *notes;      // [N]
     int32_t tile_rows;
     // a cache of 4-bit scalar codes (sub = 2, kcb and vcb unused): codes come in pairs, low
-    // half first, and stand for scale x centroid in the rows' type
+    // half first, and stand for scale x centroid, the centroids in the rows' type
     const void *k_scales, *v_scales;  // page p at p * scale_stride, [heads][page_size], in the rows' type
     const float *k_cent, *v_cent;     // [nc]
     int64_t scale_stride;             // elements between pages of scales

@@ -49,11 +49,12 @@
 // scales: the keys' multiply the scores, the values' the weights, in fp32, and the one rounding
 // to the type is that of the weights, as for sub-vectors.  (K^ rounded to bf16 moved a score of
 // 10 by 0.01; with V^ rounded the output in bf16 is off by 0.0029, without by 0.0023, of which
-// its own rounding is 0.0017.  The values' scales cost 9 % for that: 289 -> 315 us for 16
+// its own rounding is 0.0017.  Scales in scores and weights cost 279 -> 310 us for that, 16
 // requests, one with 2048 new tokens.)  What a row's reference follows is then the largest of its
 // tokens' weights times scales, 2^(score - m) |s|, a token at a time, so that these stay in the type's
-// range whatever the scales are, and a token of a large value and no weight moves nothing; the sum
-// of weights has fp32's range.  The rebuild moves as many bytes of shared memory as that of sub-vectors,
+// range whatever the scales are, and a token of a large value and no weight moves nothing (310 ->
+// 314 us; a bound of a block's largest score and largest scale, once tried, let such a token wipe out
+// the others in fp16); the sum of weights has fp32's range.  The rebuild moves as many bytes of shared memory as that of sub-vectors,
 // in words of 4 bytes where those come in 8 or 16, so it issues more: 512 lookups and address
 // steps a warp and kind of 128 keys.
 #pragma once

@@ -12,7 +12,10 @@
 // pairs of codes is 128 lookups, 4 warp instructions and 4 cycles of shared memory if each
 // lookup of a warp takes one; beside them stand the address of each lookup, 24 matrix
 // instructions per 16 tokens and the softmax, about 5 cycles of issue.  So all three are
-// close, and the kernel is laid out to issue little:
+// close, and the kernel is laid out to issue little.  (As measured no unit is full: 16 x 32768 tokens at
+// dim 128 in fp16 take 142 us, 3.9 TB/s, at 61 % of the issue slots, 22 % of the tensor pipe and a third
+// of the shared-memory port.  Of 359 warp instructions per 16 tokens 128 are the lookups and their
+// addresses; three warps a scheduler wait first for fixed latencies.)
 //   * A table of 256 lines, one per byte, holds the pair (c[low half], c[high half]) as one
 //     32-bit word 32 times, a copy for each lane in its own bank: no lookup conflicts.  A line
 //     is 256 bytes, the keys' copies then the values', and the table lies at a fixed address of
@@ -75,7 +78,7 @@ __device__ __forceinline__ uint32_t sfew_place(uint32_t at)
 
 // A row's state beside its maximum m and its sum of p = 2^(score - m): what the weights
 // p s_v of the second product are multiplied by.  It starts at its most and falls when a
-// weight passes kSFewTop; a rise of m lifts it by as much, so that the accumulators stay as
+// weight's magnitude passes kSFewTop; a rise of m lifts it by as much, so that the accumulators stay as
 // they are.
 constexpr float kSFewMost = 1.2676506e30f;   // 2^100
 constexpr float kSFewTop = 32768.f;          // the largest weight: 2^15, inside fp16

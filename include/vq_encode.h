@@ -473,9 +473,10 @@ vq_status vq_paged_scalar_append(const void *k, const void *v, int64_t k_stride,
  * cached tokens are finite, their products with the centroids too (in dtype), as
  * vq_paged_scalar_append leaves them; those of tokens past a request's length, or in no
  * page, may be anything.  slots may be NULL.
- * Scales have any sign.  Sums are in fp32: with values (scale times centroid) of up to 2^96
- * they hold for every length (vq_paged_scalar_append leaves scales of at most 2^64).  A weight
- * of less than 2^-60 of the row's largest may count as none, however large its value.
+ * Scales have any sign.  Sums are in fp32: with centroids of up to 2^30 and values (scale times
+ * centroid) of up to 2^96 they hold for every length (vq_paged_scalar_append leaves scales of at
+ * most 2^64).  A weight of less than 2^-60 of the row's largest may count as none, however large
+ * its value.
  * Arithmetic: as vq_paged_attention.  With 16-bit inputs, head_dim 64, 128 or 256,
  * page_size >= 16 and pools whose addresses and strides are multiples of 16 bytes, the
  * tensor kernels take the products.  The keys' scales multiply the scores and the values'
